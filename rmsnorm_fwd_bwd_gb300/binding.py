@@ -1,5 +1,6 @@
 """Python front end of ``librmsnorm.so`` (the C ABI in ``include/rmsnorm.h``,
-``include/layernorm.h`` and ``include/rmsnorm_double_backward.h``).
+``include/layernorm.h``, ``include/rmsnorm_double_backward.h`` and
+``include/rmsnorm_fused.h``).
 
 The functions named like the C entry points take the same arguments in the same
 order and only marshal them: a pointer argument may be a torch tensor (its
@@ -82,6 +83,13 @@ def _load():
             "rmsnorm_bwd_bwd_workspace_size": (SZ, [I64, I64, I]),
             "rmsnorm_bwd_bwd": (I, [P, I64, P, P, I64, P, I64, P, P, P, I64, P, I64, P, I64, I64, I, I, P, SZ,
                                     P]),
+            "rmsnorm_add_fwd": (I, [P, I64, P, I64, P, P, I64, P, I64, P, I64, I64, F, I, I, F, P, P, P]),
+            "rmsnorm_add_bwd_workspace_size": (SZ, [I64, I64, I]),
+            "rmsnorm_add_bwd": (I, [P, I64, P, I64, P, I64, P, P, P, I64, P, I64, P, I64, I64, I, I, F, P, P, SZ, P]),
+            "rmsnorm_quant_fwd": (I, [P, I64, P, I64, P, P, I64, P, I64, P, I64, I64, I64, F, I, I, I, I, P]),
+            "rmsnorm_rope_fwd": (I, [P, I, P, I64, I64, I64, P, I, F, F, I, I, P]),
+            "rmsnorm_rope_bwd_workspace_size": (SZ, [I64, I64, I64, I]),
+            "rmsnorm_rope_bwd": (I, [P, I, P, I64, I64, I64, P, I, F, F, I, I, P, SZ, P]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(lib, name)
@@ -202,6 +210,96 @@ def rmsnorm_bwd_bwd(ddx, ldddx, ddgamma, dy, lddy, x, ldx, gamma, rstd, d_dy, ld
                                    int(ldx), _addr(gamma), _addr(rstd), _addr(d_dy), int(ldd_dy), _addr(d_x),
                                    int(ldd_x), _addr(d_gamma), int(M), int(N), _dtype_code(dtype), int(offset),
                                    _addr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def rmsnorm_add_fwd(x, ldx, residual, ldres, gamma, h, ldh, y, ldy, rstd, M, N, eps, dtype, offset, dropout_p=0.0,
+                    rng=None, rng_used=None, stream=None) -> int:
+    return _load().rmsnorm_add_fwd(_addr(x), int(ldx), _addr(residual), int(ldres), _addr(gamma), _addr(h), int(ldh),
+                                   _addr(y), int(ldy), _addr(rstd), int(M), int(N), float(eps), _dtype_code(dtype),
+                                   int(offset), float(dropout_p), _addr(rng), _addr(rng_used), _stream(stream))
+
+
+def rmsnorm_add_bwd_workspace_size(M, N, dtype) -> int:
+    return int(_load().rmsnorm_add_bwd_workspace_size(int(M), int(N), _dtype_code(dtype)))
+
+
+def rmsnorm_add_bwd(dy, lddy, dh, lddh, h, ldh, gamma, rstd, dx, lddx, dresidual, lddres, dgamma, M, N, dtype, offset,
+                    dropout_p, rng, workspace, workspace_bytes, stream=None) -> int:
+    return _load().rmsnorm_add_bwd(_addr(dy), int(lddy), _addr(dh), int(lddh), _addr(h), int(ldh), _addr(gamma),
+                                   _addr(rstd), _addr(dx), int(lddx), _addr(dresidual), int(lddres), _addr(dgamma),
+                                   int(M), int(N), _dtype_code(dtype), int(offset), float(dropout_p), _addr(rng),
+                                   _addr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def rmsnorm_quant_fwd(x, ldx, residual, ldres, gamma, h, ldh, codes, ldcodes, scales, ldscales, M, N, eps, dtype,
+                      offset, group=0, pow2=False, stream=None) -> int:
+    return _load().rmsnorm_quant_fwd(_addr(x), int(ldx), _addr(residual), int(ldres), _addr(gamma), _addr(h), int(ldh),
+                                     _addr(codes), int(ldcodes), _addr(scales), int(ldscales), int(M), int(N),
+                                     float(eps), _dtype_code(dtype), int(offset), int(group), int(pow2),
+                                     _stream(stream))
+
+
+class RopeHeads(ctypes.Structure):
+    """rmsnorm_rope_heads: one kind of heads (see include/rmsnorm_fused.h)."""
+    _fields_ = [("x", ctypes.c_void_p), ("x_token", ctypes.c_int64), ("x_head", ctypes.c_int64),
+                ("gamma", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("y_token", ctypes.c_int64), ("y_head", ctypes.c_int64),
+                ("heads", ctypes.c_int64)]
+
+
+class RopeHeadsBwd(ctypes.Structure):
+    """rmsnorm_rope_heads_bwd: one kind of heads in the backward."""
+    _fields_ = [("dy", ctypes.c_void_p), ("dy_token", ctypes.c_int64), ("dy_head", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("x_token", ctypes.c_int64), ("x_head", ctypes.c_int64),
+                ("gamma", ctypes.c_void_p),
+                ("dx", ctypes.c_void_p), ("dx_token", ctypes.c_int64), ("dx_head", ctypes.c_int64),
+                ("dgamma", ctypes.c_void_p), ("heads", ctypes.c_int64)]
+
+
+def _head_strides(t):
+    """(address, token stride, head stride) of a [T, heads, D] tensor with unit stride in D."""
+    if t is None:
+        return None, 0, 0
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError("heads are [tokens, heads, D] tensors with unit stride in D")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def rope_heads(sets):
+    """The ``sets`` of rmsnorm_rope_fwd from (x, gamma, y) tensors: x and y are
+    [tokens, heads, D], gamma is [D] or None. It holds the tensors' addresses: build
+    it once for buffers that stay, and keep them alive as long as it is used."""
+    return (RopeHeads * len(sets))(*[RopeHeads(*_head_strides(x), _addr(g), *_head_strides(y), x.shape[1])
+                                     for x, g, y in sets])
+
+
+def rope_heads_bwd(sets):
+    """The ``sets`` of rmsnorm_rope_bwd from (dy, x, gamma, dx, dgamma) tensors (x and
+    dgamma may be None where gamma is)."""
+    return (RopeHeadsBwd * len(sets))(*[RopeHeadsBwd(*_head_strides(dy), *_head_strides(x), _addr(g),
+                                                     *_head_strides(dx), _addr(dg), dy.shape[1])
+                                        for dy, x, g, dx, dg in sets])
+
+
+def rmsnorm_rope_fwd(sets, positions, T, D, rotary_dim, inv_freq, interleaved, mscale, eps, dtype, offset,
+                     stream=None) -> int:
+    """sets: what rope_heads returns (the C call's pointer and count)."""
+    return _load().rmsnorm_rope_fwd(ctypes.addressof(sets) if sets else None, len(sets) if sets else 0, _addr(positions),
+                                    int(T), int(D), int(rotary_dim), _addr(inv_freq), int(interleaved), float(mscale),
+                                    float(eps), _dtype_code(dtype), int(offset), _stream(stream))
+
+
+def rmsnorm_rope_bwd_workspace_size(T, heads, D, dtype) -> int:
+    return int(_load().rmsnorm_rope_bwd_workspace_size(int(T), int(heads), int(D), _dtype_code(dtype)))
+
+
+def rmsnorm_rope_bwd(sets, positions, T, D, rotary_dim, inv_freq, interleaved, mscale, eps, dtype, offset, workspace,
+                     workspace_bytes, stream=None) -> int:
+    """sets: what rope_heads_bwd returns (the C call's pointer and count)."""
+    return _load().rmsnorm_rope_bwd(ctypes.addressof(sets) if sets else None, len(sets) if sets else 0, _addr(positions),
+                                    int(T), int(D), int(rotary_dim), _addr(inv_freq), int(interleaved), float(mscale),
+                                    float(eps), _dtype_code(dtype), int(offset), _addr(workspace),
+                                    int(workspace_bytes), _stream(stream))
 
 
 def rmsnorm_status_string(status: int) -> str:

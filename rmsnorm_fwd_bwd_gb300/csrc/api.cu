@@ -26,6 +26,7 @@
 #include "../../include/layernorm.h"
 #include "../../include/rmsnorm.h"
 #include "../../include/rmsnorm_double_backward.h"
+#include "checks.h"
 #include "launch.h"
 #include "tuning.h"
 
@@ -91,10 +92,6 @@ std::atomic<unsigned> g_fwd_slot{0};  // the forward pool's next queue slot
 RowPoolShape g_pool_shape;  // rmsnorm_set_row_pool_shape
 std::map<std::tuple<int, int, int64_t, int, int, int, int, unsigned>, Plan> g_plans;
 std::map<std::pair<const void*, int>, bool> g_attr_done;
-
-int elem_bytes(int dt) { return dt == RMSNORM_F32 ? 4 : 2; }
-int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 const void* kernel_for(int pass, const Plan& p) {
     switch (pass) {
@@ -632,15 +629,6 @@ bool get_plan(int pass, int64_t M, int N, int dt, int offset, int layout, int de
     return true;
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-rmsnorm_status check_common(int64_t M, int64_t N, rmsnorm_dtype dt, int offset) {
-    if (dt != RMSNORM_F32 && dt != RMSNORM_F16 && dt != RMSNORM_BF16) return RMSNORM_ERR_DTYPE;
-    if (offset != 0 && offset != 1) return RMSNORM_ERR_ARG;
-    if (M < 0 || M > RMSNORM_MAX_M || N < 1 || N > RMSNORM_MAX_N) return RMSNORM_ERR_SHAPE;
-    return RMSNORM_OK;
-}
-
 rmsnorm_status current_device(int& dev, DeviceInfo*& di) {
     if (cudaGetDevice(&dev) != cudaSuccess) return RMSNORM_ERR_CUDA;
     if (!device_info(dev, di)) return RMSNORM_ERR_CUDA;
@@ -697,12 +685,6 @@ using namespace rmsnorm;
 
 namespace rmsnorm {
 namespace {
-
-bool pitch_ok(int64_t ld, int64_t N, int64_t M, size_t s) {
-    // ld >= N, and the whole span (M - 1) * ld + N elements addressable
-    return ld >= N && ld <= (int64_t(1) << 40) / static_cast<int64_t>(s) &&
-           (M <= 1 || (M - 1) <= (int64_t(1) << 46) / ld);
-}
 
 rmsnorm_status fwd_impl(const void* x, int64_t ldx, const void* gamma, void* y, int64_t ldy, float* rstd, int64_t M,
                         int64_t N, float eps, rmsnorm_dtype dtype, int offset, rmsnorm_stream_t stream) {

@@ -1,0 +1,492 @@
+// fused_api.cu -- the entry points of include/rmsnorm_fused.h: argument checks,
+// launch shapes and launches of the kernels in add.cu, quant.cu and rope.cu.
+#include <algorithm>
+#include <cmath>
+#include <map>
+#include <mutex>
+#include <utility>
+
+#include "../../include/rmsnorm_fused.h"
+#include "checks.h"
+#include "fused.h"
+#include "launch.h"
+
+namespace rmsnorm {
+namespace {
+
+static_assert(kRopeMaxSets == RMSNORM_ROPE_MAX_SETS, "sets of a rope call");
+
+std::mutex g_fused_mu;
+std::map<int, int> g_fused_sms;                                   // SMs by device
+std::map<std::pair<const void*, std::pair<int, int>>, int> g_fused_fit;  // resident blocks per SM by (kernel, (device, threads))
+
+// SMs of the current device; 0 on failure.
+int current_sms(int& dev) {
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::lock_guard<std::mutex> lock(g_fused_mu);
+    int& n = g_fused_sms[dev];
+    if (n == 0 && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) n = 0;
+    return n;
+}
+
+// Blocks of `threads` that an SM holds, for the persistent kernels; 0 on failure.
+int resident_blocks(const void* k, int dev, int threads, size_t smem) {
+    std::lock_guard<std::mutex> lock(g_fused_mu);
+    int& n = g_fused_fit[{k, {dev, static_cast<int>(smem) * 1024 + threads}}];
+    if (n == 0 && cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, threads, smem) != cudaSuccess) n = 0;
+    return n;
+}
+
+cudaError_t launch(const void* k, int64_t blocks, int threads, size_t smem, void** params, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, k, params);
+}
+
+// Lanes per row and octets per thread: rows of up to 1024 elements by groups of
+// lanes of a 4-warp block (the 8-bit output wants a warp, whose neighbouring lanes
+// hold a group of columns), wider rows by a block of at most kFusedMaxThreads.
+void row_shape(int64_t N, int least_lanes, AddPlan& p) {
+    const int64_t n = ceil_div(N, 8);
+    if (n <= 128) {
+        p.lanes = n <= 16 ? least_lanes : 32;
+        p.octets = 1;
+        while (static_cast<int64_t>(p.lanes) * p.octets < n) p.octets *= 2;
+        p.threads = kFusedGroupThreads;
+        return;
+    }
+    p.lanes = 0;
+    p.octets = 2;
+    if (ceil_div(n, p.octets) > kFusedMaxThreads) p.octets = 4;
+    p.threads = static_cast<int>(round_up(ceil_div(n, p.octets), 32));
+}
+
+int64_t rows_per_block(const AddPlan& p) { return p.lanes ? p.threads / p.lanes : 1; }
+
+struct Operand {
+    const void* p;
+    int64_t ld;
+};
+
+// Every row of every operand on a 16-byte boundary (8 for 1-byte elements), and
+// whole octets.
+bool wide_rows(int64_t N, size_t s, std::initializer_list<Operand> operands) {
+    if (N % 8 != 0) return false;
+    for (const Operand& o : operands)
+        if (o.p && (!aligned(o.p, s == 1 ? 8 : 16) || (o.ld * static_cast<int64_t>(s)) % (s == 1 ? 8 : 16) != 0)) return false;
+    return true;
+}
+
+bool check_dropout(float p, const uint64_t* rng, AddArgs& a, rmsnorm_status& st) {
+    if (!(p >= 0.0f && p <= 1.0f)) {
+        st = RMSNORM_ERR_ARG;
+        return false;
+    }
+    a.threshold = static_cast<uint32_t>(std::lround(65536.0 * static_cast<double>(p)));
+    a.scale = a.threshold < 65536u ? static_cast<float>(65536.0 / (65536 - static_cast<int>(a.threshold))) : 0.0f;
+    a.rng = reinterpret_cast<const unsigned long long*>(rng);
+    return true;
+}
+
+rmsnorm_status check_rng(const AddArgs& a) {
+    if (a.threshold && !a.rng) return RMSNORM_ERR_NULL;
+    if (a.threshold && (!aligned(a.rng, 8) || !aligned(a.rng_used, 8))) return RMSNORM_ERR_ALIGN;
+    return RMSNORM_OK;
+}
+
+// Persistent grid of the backward and its partial rows.
+bool add_bwd_plan(int64_t M, int64_t N, int dtype, bool wide, AddPlan& p) {
+    int dev = 0;
+    const int sms = current_sms(dev);
+    if (!sms) return false;
+    p.dtype = dtype;
+    p.aligned = wide;
+    row_shape(N, 8, p);
+    p.smem = p.lanes ? static_cast<size_t>(rows_per_block(p)) * N * 4 : 0;
+    const void* k = add_bwd_kernel(p);
+    const int fit = k ? resident_blocks(k, dev, p.threads, p.smem) : 0;
+    if (fit < 1) return false;
+    p.blocks = std::min<int64_t>(static_cast<int64_t>(std::min(fit, 8)) * sms, ceil_div(M, rows_per_block(p)));
+    return true;
+}
+
+rmsnorm_status run(const void* k, const AddPlan& p, AddArgs& a, rmsnorm_stream_t stream) {
+    if (!k) return RMSNORM_ERR_UNSUPPORTED;
+    void* params[] = {&a};
+    if (launch(k, p.blocks, p.threads, p.smem, params, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return RMSNORM_ERR_CUDA;
+    }
+    return RMSNORM_OK;
+}
+
+// ---------------------------------------------------------------------------
+// rope
+// ---------------------------------------------------------------------------
+bool strides_ok(int64_t token, int64_t head, int64_t heads, int64_t T, int64_t D) {
+    if ((T > 1 && token < D) || (heads > 1 && head < D) || token < 0 || head < 0) return false;
+    const int64_t most = int64_t(1) << 40;
+    return (T <= 1 || token <= most / (T - 1)) && (heads <= 1 || head <= most / (heads - 1));
+}
+
+rmsnorm_status check_rope(int nsets, int64_t T, int64_t D, int64_t R, int interleaved, float mscale, float eps,
+                          rmsnorm_dtype dtype, int offset) {
+    const rmsnorm_status st = check_common(T, D, dtype, offset);
+    if (st != RMSNORM_OK) return st;
+    if (D > RMSNORM_ROPE_MAX_D || R < 2 || R > D || R % 2 != 0) return RMSNORM_ERR_SHAPE;
+    if (!std::isfinite(eps) || !(eps > 0.0f)) return RMSNORM_ERR_EPS;
+    if (nsets < 1 || nsets > RMSNORM_ROPE_MAX_SETS || (interleaved != 0 && interleaved != 1) || !std::isfinite(mscale))
+        return RMSNORM_ERR_ARG;
+    return RMSNORM_OK;
+}
+
+bool rope_wide(const RopeSet& s, size_t e) {
+    const int64_t w = 16 / static_cast<int64_t>(e);
+    return aligned(s.x, 16) && aligned(s.gamma, 16) && aligned(s.dy, 16) && aligned(s.y, 16) && s.x_token % w == 0 &&
+           s.x_head % w == 0 && s.dy_token % w == 0 && s.dy_head % w == 0 && s.y_token % w == 0 && s.y_head % w == 0;
+}
+
+// Lanes per head row, and the heads of a token that a group of lanes takes: all of
+// them where the tokens alone fill the GPU (a token's cosines and sines are then
+// computed once), fewer where they do not.
+rmsnorm_status rope_plan(RopeArgs& a, int dtype, int interleaved, bool wide, bool bwd, RopePlan& p) {
+    int dev = 0;
+    const int sms = current_sms(dev);
+    if (!sms) return RMSNORM_ERR_CUDA;
+    p.dtype = dtype;
+    p.interleaved = interleaved != 0;
+    p.aligned = wide && a.D % 8 == 0 && (interleaved || a.R % 16 == 0);
+    p.threads = kFusedGroupThreads;
+    int group = 32;  // lanes that share an item
+    if (p.aligned) {
+        const int64_t units = interleaved ? ceil_div(a.D, 16) : a.R / 16 + ceil_div(a.D - a.R, 16);
+        for (p.lanes = 4; p.lanes < units;) p.lanes *= 2;
+        group = p.lanes;
+    } else {
+        p.lanes = static_cast<int>(ceil_div(a.R / 2 + ceil_div(a.D - a.R, 2), 32));
+    }
+    const int64_t full = static_cast<int64_t>(sms) * 2048 / group;  // groups that fill the GPU
+    int64_t nchunk = std::min<int64_t>(ceil_div(full, a.T), a.heads);
+    a.chunk = static_cast<int>(ceil_div(a.heads, nchunk));
+    a.nchunk = static_cast<int>(ceil_div(a.heads, a.chunk));
+    const int64_t blocks = ceil_div(a.T * a.nchunk, p.threads / group);
+    p.smem = bwd ? static_cast<size_t>(p.threads / group) * a.D * 4 : 0;
+    p.blocks = bwd ? std::min<int64_t>(blocks, static_cast<int64_t>(sms) * 8) : blocks;
+    if (!p.aligned) p.blocks = std::min<int64_t>(blocks, static_cast<int64_t>(sms) * (bwd ? 8 : 64));
+    a.units = p.blocks;
+    a.ldws = workspace_pitch(a.D);
+    return RMSNORM_OK;
+}
+
+rmsnorm_status rope_run(RopeArgs& a, const RopePlan& p, int interleaved, bool bwd, cudaStream_t s) {
+    const void* k = rope_kernel(p, bwd);
+    if (!k) return RMSNORM_ERR_UNSUPPORTED;
+    int last = p.aligned ? p.lanes : interleaved;
+    void* params[] = {&a, &last};
+    if (launch(k, p.blocks, p.threads, p.smem, params, s) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return RMSNORM_ERR_CUDA;
+    }
+    return RMSNORM_OK;
+}
+
+}  // namespace
+}  // namespace rmsnorm
+
+using namespace rmsnorm;
+
+extern "C" rmsnorm_status rmsnorm_add_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldres,
+                                          const void* gamma, void* h, int64_t ldh, void* y, int64_t ldy, float* rstd,
+                                          int64_t M, int64_t N, float eps, rmsnorm_dtype dtype, int offset,
+                                          float dropout_p, const uint64_t* rng, uint64_t* rng_used,
+                                          rmsnorm_stream_t stream) {
+    rmsnorm_status st = check_common(M, N, dtype, offset);
+    if (st != RMSNORM_OK) return st;
+    if (!std::isfinite(eps) || !(eps > 0.0f)) return RMSNORM_ERR_EPS;
+    const size_t s = elem_bytes(dtype);
+    if (!pitch_ok(ldx, N, M, s) || !pitch_ok(ldy, N, M, s) || (residual && !pitch_ok(ldres, N, M, s)) ||
+        (h && !pitch_ok(ldh, N, M, s)))
+        return RMSNORM_ERR_SHAPE;
+    AddArgs a = {};
+    if (!check_dropout(dropout_p, rng, a, st)) return st;
+    if (M == 0) return RMSNORM_OK;
+    if (!x || !gamma || !y) return RMSNORM_ERR_NULL;
+    if (!aligned(x, s) || !aligned(residual, s) || !aligned(gamma, s) || !aligned(h, s) || !aligned(y, s) ||
+        !aligned(rstd, 4))
+        return RMSNORM_ERR_ALIGN;
+    a.rng_used = reinterpret_cast<unsigned long long*>(rng_used);
+    if ((st = check_rng(a)) != RMSNORM_OK) return st;
+    a.x = x;
+    a.res = residual;
+    a.gamma = gamma;
+    a.h = h;
+    a.y = y;
+    a.rstd = rstd;
+    a.ldx = ldx;
+    a.ldres = ldres;
+    a.ldh = ldh;
+    a.ldy = ldy;
+    a.M = M;
+    a.N = static_cast<int>(N);
+    a.eps = eps;
+    a.one = static_cast<float>(offset);
+    AddPlan p;
+    p.dtype = dtype;
+    p.aligned = wide_rows(N, s, {{x, ldx}, {residual, ldres}, {gamma, 0}, {h, ldh}, {y, ldy}});
+    row_shape(N, 8, p);
+    p.blocks = ceil_div(M, rows_per_block(p));
+    return run(add_fwd_kernel(p), p, a, stream);
+}
+
+extern "C" size_t rmsnorm_add_bwd_workspace_size(int64_t M, int64_t N, rmsnorm_dtype dtype) {
+    if (check_common(M, N, dtype, 0) != RMSNORM_OK || M == 0) return 0;
+    int64_t units = 0;
+    for (const bool wide : {false, true}) {
+        AddPlan p;
+        if (add_bwd_plan(M, N, dtype, wide, p)) units = std::max(units, p.blocks);
+    }
+    (void)cudaGetLastError();
+    return static_cast<size_t>(units) * static_cast<size_t>(workspace_pitch(N)) * sizeof(float);
+}
+
+extern "C" rmsnorm_status rmsnorm_add_bwd(const void* dy, int64_t lddy, const void* dh, int64_t lddh, const void* h,
+                                          int64_t ldh, const void* gamma, const float* rstd, void* dx, int64_t lddx,
+                                          void* dresidual, int64_t lddres, void* dgamma, int64_t M, int64_t N,
+                                          rmsnorm_dtype dtype, int offset, float dropout_p, const uint64_t* rng,
+                                          void* workspace, size_t workspace_bytes, rmsnorm_stream_t stream) {
+    rmsnorm_status st = check_common(M, N, dtype, offset);
+    if (st != RMSNORM_OK) return st;
+    const size_t s = elem_bytes(dtype);
+    if (!pitch_ok(lddy, N, M, s) || !pitch_ok(ldh, N, M, s) || (dh && !pitch_ok(lddh, N, M, s)) ||
+        (dx && !pitch_ok(lddx, N, M, s)) || (dresidual && !pitch_ok(lddres, N, M, s)))
+        return RMSNORM_ERR_SHAPE;
+    AddArgs a = {};
+    if (!check_dropout(dropout_p, rng, a, st)) return st;
+    if (!dgamma) return RMSNORM_ERR_NULL;
+    if (!aligned(dgamma, s)) return RMSNORM_ERR_ALIGN;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (M == 0)
+        return launch_dgamma_reduce(dtype, nullptr, 0, static_cast<int>(N), workspace_pitch(N), dgamma, cs) == cudaSuccess
+                   ? RMSNORM_OK
+                   : RMSNORM_ERR_CUDA;
+    if (!dy || !h || !gamma || !rstd || !workspace) return RMSNORM_ERR_NULL;
+    if (!aligned(dy, s) || !aligned(dh, s) || !aligned(h, s) || !aligned(gamma, s) || !aligned(dx, s) ||
+        !aligned(dresidual, s) || !aligned(rstd, 4) || !aligned(workspace, 16))
+        return RMSNORM_ERR_ALIGN;
+    if ((st = check_rng(a)) != RMSNORM_OK) return st;
+    AddPlan p;
+    const bool wide = wide_rows(N, s, {{dy, lddy}, {dh, lddh}, {h, ldh}, {gamma, 0}, {dx, lddx}, {dresidual, lddres}});
+    if (!add_bwd_plan(M, N, dtype, wide, p)) {
+        (void)cudaGetLastError();
+        return RMSNORM_ERR_CUDA;
+    }
+    a.ldws = workspace_pitch(N);
+    if (workspace_bytes < static_cast<size_t>(p.blocks) * static_cast<size_t>(a.ldws) * sizeof(float))
+        return RMSNORM_ERR_WORKSPACE;
+    a.dy = dy;
+    a.dh = dh;
+    a.x = h;
+    a.gamma = gamma;
+    a.rstd = const_cast<float*>(rstd);
+    a.dx = dx;
+    a.dres = dresidual;
+    a.ws = static_cast<float*>(workspace);
+    a.lddy = lddy;
+    a.lddh = lddh;
+    a.ldx = ldh;
+    a.lddx = lddx;
+    a.lddres = lddres;
+    a.M = M;
+    a.N = static_cast<int>(N);
+    a.one = static_cast<float>(offset);
+    if ((st = run(add_bwd_kernel(p), p, a, stream)) != RMSNORM_OK) return st;
+    return launch_dgamma_reduce(dtype, a.ws, p.blocks, a.N, a.ldws, dgamma, cs) == cudaSuccess ? RMSNORM_OK
+                                                                                              : RMSNORM_ERR_CUDA;
+}
+
+extern "C" rmsnorm_status rmsnorm_quant_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldres,
+                                            const void* gamma, void* h, int64_t ldh, void* codes, int64_t ldcodes,
+                                            float* scales, int64_t ldscales, int64_t M, int64_t N, float eps,
+                                            rmsnorm_dtype dtype, int offset, int group, int pow2,
+                                            rmsnorm_stream_t stream) {
+    rmsnorm_status st = check_common(M, N, dtype, offset);
+    if (st != RMSNORM_OK) return st;
+    if (!std::isfinite(eps) || !(eps > 0.0f)) return RMSNORM_ERR_EPS;
+    if ((group != 0 && group != 32 && group != 64 && group != 128) || (pow2 != 0 && pow2 != 1)) return RMSNORM_ERR_ARG;
+    const size_t s = elem_bytes(dtype);
+    if (!pitch_ok(ldx, N, M, s) || !pitch_ok(ldcodes, N, M, 1) || (residual && !pitch_ok(ldres, N, M, s)) ||
+        (h && !pitch_ok(ldh, N, M, s)) || !pitch_ok(ldscales, group ? ceil_div(N, group) : 1, M, 4))
+        return RMSNORM_ERR_SHAPE;
+    if (M == 0) return RMSNORM_OK;
+    if (!x || !gamma || !codes || !scales) return RMSNORM_ERR_NULL;
+    if (!aligned(x, s) || !aligned(residual, s) || !aligned(gamma, s) || !aligned(h, s) || !aligned(scales, 4))
+        return RMSNORM_ERR_ALIGN;
+    AddArgs a = {};
+    a.x = x;
+    a.res = residual;
+    a.gamma = gamma;
+    a.h = h;
+    a.y = codes;
+    a.scales = scales;
+    a.ldx = ldx;
+    a.ldres = ldres;
+    a.ldh = ldh;
+    a.ldy = ldcodes;
+    a.ldscales = ldscales;
+    a.M = M;
+    a.N = static_cast<int>(N);
+    a.eps = eps;
+    a.one = static_cast<float>(offset);
+    a.group = group;
+    a.pow2 = pow2;
+    AddPlan p;
+    p.dtype = dtype;
+    p.aligned = wide_rows(N, s, {{x, ldx}, {residual, ldres}, {gamma, 0}, {h, ldh}}) &&
+                wide_rows(N, 1, {{codes, ldcodes}});
+    row_shape(N, 32, p);
+    p.blocks = ceil_div(M, rows_per_block(p));
+    return run(quant_kernel(p), p, a, stream);
+}
+
+extern "C" rmsnorm_status rmsnorm_rope_fwd(const rmsnorm_rope_heads* sets, int nsets, const int64_t* positions,
+                                           int64_t T, int64_t D, int64_t rotary_dim, const double* inv_freq,
+                                           int interleaved, float mscale, float eps, rmsnorm_dtype dtype, int offset,
+                                           rmsnorm_stream_t stream) {
+    rmsnorm_status st = check_rope(nsets, T, D, rotary_dim, interleaved, mscale, eps, dtype, offset);
+    if (st != RMSNORM_OK) return st;
+    if (!sets) return RMSNORM_ERR_NULL;
+    const size_t s = elem_bytes(dtype);
+    RopeArgs a = {};
+    bool wide = true;
+    int64_t heads = 0;
+    for (int i = 0; i < nsets; ++i) {
+        const rmsnorm_rope_heads& q = sets[i];
+        if (q.heads < 1 || q.heads > RMSNORM_ROPE_MAX_HEADS || !strides_ok(q.x_token, q.x_head, q.heads, T, D) ||
+            !strides_ok(q.y_token, q.y_head, q.heads, T, D))
+            return RMSNORM_ERR_SHAPE;
+        heads += q.heads;
+        if (T > 0 && (!q.x || !q.y)) return RMSNORM_ERR_NULL;
+        if (!aligned(q.x, s) || !aligned(q.y, s) || !aligned(q.gamma, s)) return RMSNORM_ERR_ALIGN;
+        RopeSet& t = a.set[i];
+        t.x = q.x;
+        t.gamma = q.gamma;
+        t.y = q.y;
+        t.x_token = q.x_token;
+        t.x_head = q.x_head;
+        t.y_token = q.y_token;
+        t.y_head = q.y_head;
+        t.heads = static_cast<int>(q.heads);
+        wide = wide && rope_wide(t, s);
+    }
+    if (heads > RMSNORM_ROPE_MAX_HEADS) return RMSNORM_ERR_SHAPE;
+    if (T == 0) return RMSNORM_OK;
+    if (!positions || !inv_freq) return RMSNORM_ERR_NULL;
+    if (!aligned(positions, 8) || !aligned(inv_freq, 8)) return RMSNORM_ERR_ALIGN;
+    a.nsets = nsets;
+    a.heads = static_cast<int>(heads);
+    a.pos = positions;
+    a.inv_freq = inv_freq;
+    a.T = T;
+    a.D = static_cast<int>(D);
+    a.R = static_cast<int>(rotary_dim);
+    a.mscale = mscale;
+    a.eps = eps;
+    a.one = static_cast<float>(offset);
+    RopePlan p;
+    if ((st = rope_plan(a, dtype, interleaved, wide, false, p)) != RMSNORM_OK) return st;
+    return rope_run(a, p, interleaved, false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t rmsnorm_rope_bwd_workspace_size(int64_t T, int64_t heads, int64_t D, rmsnorm_dtype dtype) {
+    if (check_common(T, D, dtype, 0) != RMSNORM_OK || D > RMSNORM_ROPE_MAX_D || T == 0 || heads < 1 ||
+        heads > RMSNORM_ROPE_MAX_HEADS)
+        return 0;
+    int dev = 0;
+    const int sms = current_sms(dev);
+    // the backward's most blocks, a partial row each and set
+    return static_cast<size_t>(RMSNORM_ROPE_MAX_SETS) * static_cast<size_t>(std::min<int64_t>(T * heads, int64_t(sms) * 8)) *
+           static_cast<size_t>(workspace_pitch(D)) * sizeof(float);
+}
+
+extern "C" rmsnorm_status rmsnorm_rope_bwd(const rmsnorm_rope_heads_bwd* sets, int nsets, const int64_t* positions,
+                                           int64_t T, int64_t D, int64_t rotary_dim, const double* inv_freq,
+                                           int interleaved, float mscale, float eps, rmsnorm_dtype dtype, int offset,
+                                           void* workspace, size_t workspace_bytes, rmsnorm_stream_t stream) {
+    rmsnorm_status st = check_rope(nsets, T, D, rotary_dim, interleaved, mscale, eps, dtype, offset);
+    if (st != RMSNORM_OK) return st;
+    if (!sets) return RMSNORM_ERR_NULL;
+    const size_t s = elem_bytes(dtype);
+    RopeArgs a = {};
+    bool wide = true;
+    int64_t heads = 0;
+    bool weights = false;
+    for (int i = 0; i < nsets; ++i) {
+        const rmsnorm_rope_heads_bwd& q = sets[i];
+        if (q.heads < 1 || q.heads > RMSNORM_ROPE_MAX_HEADS || !strides_ok(q.dy_token, q.dy_head, q.heads, T, D) ||
+            (q.gamma && !strides_ok(q.x_token, q.x_head, q.heads, T, D)) ||
+            !strides_ok(q.dx_token, q.dx_head, q.heads, T, D))
+            return RMSNORM_ERR_SHAPE;
+        heads += q.heads;
+        weights = weights || q.gamma;
+        if ((T > 0 && (!q.dy || !q.dx || (q.gamma && !q.x))) || (q.gamma && !q.dgamma)) return RMSNORM_ERR_NULL;
+        if (!aligned(q.dy, s) || !aligned(q.dx, s) || !aligned(q.gamma, s) || (q.gamma && (!aligned(q.x, s) || !aligned(q.dgamma, s))))
+            return RMSNORM_ERR_ALIGN;
+        RopeSet& t = a.set[i];
+        t.dy = q.dy;
+        t.gamma = q.gamma;
+        t.y = q.dx;
+        t.dy_token = q.dy_token;
+        t.dy_head = q.dy_head;
+        if (q.gamma) {
+            t.x = q.x;
+            t.x_token = q.x_token;
+            t.x_head = q.x_head;
+        }
+        t.y_token = q.dx_token;
+        t.y_head = q.dx_head;
+        t.heads = static_cast<int>(q.heads);
+        wide = wide && rope_wide(t, s);
+    }
+    if (heads > RMSNORM_ROPE_MAX_HEADS) return RMSNORM_ERR_SHAPE;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    a.nsets = nsets;
+    a.heads = static_cast<int>(heads);
+    a.pos = positions;
+    a.inv_freq = inv_freq;
+    a.T = T;
+    a.D = static_cast<int>(D);
+    a.R = static_cast<int>(rotary_dim);
+    a.mscale = mscale;
+    a.eps = eps;
+    a.one = static_cast<float>(offset);
+    if (T > 0) {
+        if (!positions || !inv_freq || (weights && !workspace)) return RMSNORM_ERR_NULL;
+        if (!aligned(positions, 8) || !aligned(inv_freq, 8) || !aligned(workspace, 16)) return RMSNORM_ERR_ALIGN;
+        RopePlan p;
+        if ((st = rope_plan(a, dtype, interleaved, wide, true, p)) != RMSNORM_OK) return st;
+        const size_t need = static_cast<size_t>(nsets) * static_cast<size_t>(a.units) * static_cast<size_t>(a.ldws) * sizeof(float);
+        if (weights && workspace_bytes < need) return RMSNORM_ERR_WORKSPACE;
+        a.ws = static_cast<float*>(workspace);
+        if ((st = rope_run(a, p, interleaved, true, cs)) != RMSNORM_OK) return st;
+    }
+    // a set's partials are a plane of `units` rows; two sets take one launch
+    const int64_t plane = a.units * a.ldws;
+    if (nsets == 2 && sets[0].gamma && sets[1].gamma)
+        return launch_dgamma_reduce(dtype, a.ws, a.units, a.D, workspace_pitch(D), sets[0].dgamma, cs, sets[1].dgamma) ==
+                       cudaSuccess
+                   ? RMSNORM_OK
+                   : RMSNORM_ERR_CUDA;
+    for (int i = 0; i < nsets; ++i)
+        if (sets[i].gamma && launch_dgamma_reduce(dtype, a.ws ? a.ws + i * plane : nullptr, a.units, a.D, workspace_pitch(D),
+                                                  sets[i].dgamma, cs) != cudaSuccess)
+            return RMSNORM_ERR_CUDA;
+    return RMSNORM_OK;
+}

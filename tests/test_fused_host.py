@@ -1,0 +1,275 @@
+"""The operators of include/rmsnorm_fused.h without a GPU: refusals (all before the
+library touches CUDA), the formulas of the 64-bit oracle, Philox, the rotation's
+frequencies, and the checks of the torch front end."""
+import numpy as np
+import pytest
+import torch
+
+from rmsnorm_fwd_bwd_gb300 import binding as B
+from rmsnorm_fwd_bwd_gb300 import build as build_mod
+from rmsnorm_fwd_bwd_gb300 import fused
+from tests import fused_ref as ref
+
+OK, NULL, SHAPE, DTYPE, EPS, ALIGN, WORKSPACE, ARG = 0, 1, 2, 3, 4, 5, 6, 9
+
+
+@pytest.fixture(scope="module", autouse=True)
+def library():
+    build_mod.build()
+
+
+def add_fwd(**kw):
+    a = dict(x=0x1000, ldx=8, residual=0x2000, ldres=8, gamma=0x3000, h=0x4000, ldh=8, y=0x5000, ldy=8, rstd=0x6000,
+             M=4, N=8, eps=1e-6, dtype=2, offset=0, dropout_p=0.0, rng=None, rng_used=None, stream=0)
+    a.update(kw)
+    return B.rmsnorm_add_fwd(**a)
+
+
+@pytest.mark.parametrize("want,kw", [
+    (DTYPE, dict(dtype=3)), (ARG, dict(offset=2)), (SHAPE, dict(M=-1)), (SHAPE, dict(N=0)), (SHAPE, dict(N=16385)),
+    (EPS, dict(eps=0.0)), (EPS, dict(eps=float("nan"))), (SHAPE, dict(ldx=7)), (SHAPE, dict(ldres=7)),
+    (SHAPE, dict(ldh=7)), (SHAPE, dict(ldy=7)), (ARG, dict(dropout_p=-0.1)), (ARG, dict(dropout_p=1.5)),
+    (ARG, dict(dropout_p=float("nan"))), (OK, dict(M=0, x=None, y=None)), (NULL, dict(x=None)), (NULL, dict(gamma=None)),
+    (NULL, dict(y=None)), (ALIGN, dict(x=0x1001)), (ALIGN, dict(residual=0x2001)), (ALIGN, dict(h=0x4001)),
+    (ALIGN, dict(rstd=0x6002)), (NULL, dict(dropout_p=0.5)), (ALIGN, dict(dropout_p=0.5, rng=0x7004)),
+    (ALIGN, dict(dropout_p=0.5, rng=0x7000, rng_used=0x7014)),
+])
+def test_add_fwd_refusals(want, kw):
+    assert add_fwd(**kw) == want
+
+
+def add_bwd(**kw):
+    a = dict(dy=0x1000, lddy=8, dh=0x2000, lddh=8, h=0x3000, ldh=8, gamma=0x4000, rstd=0x5000, dx=0x6000, lddx=8,
+             dresidual=0x7000, lddres=8, dgamma=0x8000, M=4, N=8, dtype=2, offset=0, dropout_p=0.0, rng=None,
+             workspace=0x9000, workspace_bytes=1 << 20, stream=0)
+    a.update(kw)
+    return B.rmsnorm_add_bwd(**a)
+
+
+@pytest.mark.parametrize("want,kw", [
+    (DTYPE, dict(dtype=-1)), (ARG, dict(offset=-1)), (SHAPE, dict(N=16385)), (SHAPE, dict(lddy=7)), (SHAPE, dict(lddh=7)),
+    (SHAPE, dict(ldh=7)), (SHAPE, dict(lddx=7)), (SHAPE, dict(lddres=7)), (ARG, dict(dropout_p=2.0)),
+    (NULL, dict(dgamma=None)), (ALIGN, dict(dgamma=0x8001)), (NULL, dict(dy=None)), (NULL, dict(h=None)),
+    (NULL, dict(gamma=None)), (NULL, dict(rstd=None)), (NULL, dict(workspace=None)), (ALIGN, dict(workspace=0x9008)),
+    (ALIGN, dict(dx=0x6001)), (NULL, dict(dropout_p=0.5)),
+])
+def test_add_bwd_refusals(want, kw):
+    assert add_bwd(**kw) == want
+
+
+def quant(**kw):
+    a = dict(x=0x1000, ldx=64, residual=0x2000, ldres=64, gamma=0x3000, h=0x4000, ldh=64, codes=0x5000, ldcodes=64,
+             scales=0x6000, ldscales=2, M=4, N=64, eps=1e-6, dtype=1, offset=0, group=32, pow2=0, stream=0)
+    a.update(kw)
+    return B.rmsnorm_quant_fwd(**a)
+
+
+@pytest.mark.parametrize("want,kw", [
+    (DTYPE, dict(dtype=7)), (ARG, dict(offset=3)), (EPS, dict(eps=-1.0)), (ARG, dict(group=16)), (ARG, dict(group=-32)),
+    (ARG, dict(pow2=2)), (SHAPE, dict(ldcodes=63)), (SHAPE, dict(ldscales=1)), (SHAPE, dict(ldh=63)),
+    (OK, dict(M=0, x=None)), (NULL, dict(x=None)), (NULL, dict(codes=None)), (NULL, dict(scales=None)),
+    (ALIGN, dict(scales=0x6002)), (ALIGN, dict(x=0x1001)),
+])
+def test_quant_refusals(want, kw):
+    assert quant(**kw) == want
+
+
+def rope(bwd=False, drop=(), **kw):
+    s = dict(x=0x1000, x_token=128, x_head=64, gamma=0x2000, y=0x3000, y_token=128, y_head=64, heads=2)
+    if bwd:
+        s = dict(dy=0x1000, dy_token=128, dy_head=64, x=0x2000, x_token=128, x_head=64, gamma=0x3000, dx=0x4000,
+                 dx_token=128, dx_head=64, dgamma=0x5000, heads=2)
+    a = dict(sets=1, positions=0x6000, T=4, D=64, rotary_dim=64, inv_freq=0x7000, interleaved=0, mscale=1.0, eps=1e-6,
+             dtype=2, offset=0, stream=0)
+    if bwd:
+        a.update(workspace=0x9000, workspace_bytes=1 << 24)
+    for k, v in kw.items():
+        (s if k in s and k not in ("heads_total",) else a)[k] = v
+    cls = B.RopeHeadsBwd if bwd else B.RopeHeads
+    n = a.pop("sets")
+    sets = (cls * n)(*[cls(**s) for _ in range(n)]) if n else None
+    return (B.rmsnorm_rope_bwd if bwd else B.rmsnorm_rope_fwd)(sets, **a)
+
+
+@pytest.mark.parametrize("want,kw", [
+    (DTYPE, dict(dtype=4)), (ARG, dict(offset=2)), (SHAPE, dict(D=513)), (SHAPE, dict(D=0)), (SHAPE, dict(rotary_dim=0)),
+    (SHAPE, dict(rotary_dim=3)), (SHAPE, dict(rotary_dim=66)), (EPS, dict(eps=0.0)), (ARG, dict(interleaved=2)),
+    (ARG, dict(mscale=float("inf"))), (ARG, dict(sets=0)), (ARG, dict(sets=3)), (SHAPE, dict(heads=0)),
+    (SHAPE, dict(heads=65537, x_token=1 << 30)), (SHAPE, dict(x_token=63)), (SHAPE, dict(x_head=63)), (SHAPE, dict(x_token=-64)),
+    (SHAPE, dict(sets=2, heads=40000)), (NULL, dict(positions=None)), (NULL, dict(inv_freq=None)),
+    (ALIGN, dict(positions=0x6004)), (ALIGN, dict(inv_freq=0x7004)), (ALIGN, dict(gamma=0x2001)),
+])
+def test_rope_refusals(want, kw):
+    assert rope(**kw) == want
+    if "y" not in kw:
+        kw = {{"x_token": "dy_token", "x_head": "dy_head"}.get(k, k): v for k, v in kw.items()}
+        assert rope(bwd=True, **kw) == want
+
+
+def test_rope_refusals_of_each_direction():
+    assert rope(x=None) == NULL
+    assert rope(y=None) == NULL
+    assert rope(x=0x1001) == ALIGN
+    assert rope(y_head=1) == SHAPE
+    assert rope(T=0, positions=None, inv_freq=None, x=None, y=None) == OK
+    assert rope(bwd=True, dy=None) == NULL
+    assert rope(bwd=True, x=None) == NULL
+    assert rope(bwd=True, dx=None) == NULL
+    assert rope(bwd=True, dgamma=None) == NULL
+    assert rope(bwd=True, workspace=None) == NULL
+    assert rope(bwd=True, workspace=0x9008) == ALIGN
+    assert rope(bwd=True, x_token=1) == SHAPE
+
+
+def test_workspace_sizes_of_invalid_arguments():
+    assert B.rmsnorm_add_bwd_workspace_size(0, 8, 0) == 0
+    assert B.rmsnorm_add_bwd_workspace_size(4, 0, 0) == 0
+    assert B.rmsnorm_add_bwd_workspace_size(4, 8, 9) == 0
+    assert B.rmsnorm_rope_bwd_workspace_size(0, 1, 64, 0) == 0
+    assert B.rmsnorm_rope_bwd_workspace_size(4, 0, 64, 0) == 0
+    assert B.rmsnorm_rope_bwd_workspace_size(4, 1, 513, 0) == 0
+    assert B.rmsnorm_rope_bwd_workspace_size(4, 1, 64, 5) == 0
+
+
+# --------------------------------------------------------------------------- #
+# the oracle
+# --------------------------------------------------------------------------- #
+def test_philox_known_answers():
+    # the test vectors of Philox4x32-10 that its authors give
+    for ctr, key, out in (
+            ([0] * 4, (0, 0), [0x6627E8D5, 0xE169C58D, 0xBC57AC4C, 0x9B00DBD8]),
+            ([0xFFFFFFFF] * 4, (0xFFFFFFFF, 0xFFFFFFFF), [0x408F276D, 0x41C83B0E, 0xA20BC7C6, 0x6D5451FD]),
+            ([0x243F6A88, 0x85A308D3, 0x13198A2E, 0x03707344], (0xA4093822, 0x299F31D0),
+             [0xD16CFE09, 0x94FDCCEB, 0x5001E420, 0x24126EA1])):
+        assert ref.philox(np.array([ctr], dtype=np.uint32), key).tolist() == [out]
+
+
+def test_dropout_share_and_streams():
+    a = ref.kept(5, 7, 64, 512, 0.25)
+    n = a.numel()
+    assert abs(a.double().mean().item() - 0.75) < 5 * (0.75 * 0.25 / n) ** 0.5
+    for other in (ref.kept(6, 7, 64, 512, 0.25), ref.kept(5, 8, 64, 512, 0.25), ref.kept(5, 7 + (1 << 32), 64, 512, 0.25)):
+        # independent streams agree on 0.75^2 + 0.25^2 of the elements
+        assert abs((a == other).double().mean().item() - 0.625) < 5 * (0.625 * 0.375 / n) ** 0.5
+    # a row's numbers do not depend on the matrix around it
+    assert torch.equal(ref.kept(5, 7, 3, 21, 0.25), a[:3, :21])
+
+
+def _difference(f, v, t, step=1e-5):
+    return (f(v + step * t) - f(v - step * t)) / (2 * step)
+
+
+@pytest.mark.parametrize("offset", [False, True])
+def test_add_bwd_formula_against_differences(offset):
+    g = torch.Generator().manual_seed(3)
+    M, N, p = 5, 23, 0.3
+    x, res, dy, dh = (torch.randn(M, N, generator=g, dtype=torch.float64) for _ in range(4))
+    w = torch.randn(N, generator=g, dtype=torch.float64)
+    keep = ref.kept(11, 2, M, N, p)
+
+    def loss(x, res, w):
+        h = ref.add_sum(x, res, p, 11, 2)[0]
+        return ((ref.norm(h, w, 1e-6, offset)[0] * dy).sum() + (h * dh).sum()).item()
+    h = ref.add_sum(x, res, p, 11, 2)[0]
+    r = ref.norm(h, w, 1e-6, offset)[1].squeeze(-1)
+    (dres, dx, dw), _ = ref.add_bwd(dy, dh, h, r, w, offset, keep, p)
+    for k in range(3):
+        t, tw = torch.randn(M, N, generator=g, dtype=torch.float64), torch.randn(N, generator=g, dtype=torch.float64)
+        # central differences: truncation step^2 and rounding 2^-53 / step, both near 1e-10 of the loss
+        assert _difference(lambda v: loss(v, res, w), x, t) == pytest.approx((dx * t).sum().item(), rel=1e-6, abs=1e-7)
+        assert _difference(lambda v: loss(x, v, w), res, t) == pytest.approx((dres * t).sum().item(), rel=1e-6, abs=1e-7)
+        assert _difference(lambda v: loss(x, res, v), w, tw) == pytest.approx((dw * tw).sum().item(), rel=1e-6, abs=1e-7)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("weight", [False, True])
+def test_rope_bwd_formula_against_differences(interleaved, weight):
+    g = torch.Generator().manual_seed(4)
+    T, H, D, R = 3, 2, 14, 10
+    x, dy, t = (torch.randn(T, H, D, generator=g, dtype=torch.float64) for _ in range(3))
+    w, tw = (torch.randn(D, generator=g, dtype=torch.float64) for _ in range(2))
+    w = w if weight else None
+    pos, freq = torch.tensor([0, 5, 1000]), torch.rand(R // 2, generator=g, dtype=torch.float64)
+
+    def loss(x, w):
+        return (ref.rope_fwd(x, w, pos, freq, interleaved, 1.1, 1e-6)[0] * dy).sum().item()
+    (dx, dw), _ = ref.rope_bwd(dy, x, w, pos, freq, interleaved, 1.1, 1e-6)
+    assert _difference(lambda v: loss(v, w), x, t) == pytest.approx((dx * t).sum().item(), rel=1e-6, abs=1e-7)
+    if weight:
+        assert _difference(lambda v: loss(x, v), w, tw) == pytest.approx((dw * tw).sum().item(), rel=1e-6, abs=1e-7)
+
+
+# --------------------------------------------------------------------------- #
+# frequencies
+# --------------------------------------------------------------------------- #
+def test_rope_frequencies():
+    f, m = fused.rope_frequencies(8, device="cpu")
+    assert m == 1.0 and f.dtype == torch.float64
+    assert f.tolist() == pytest.approx([1.0, 0.1, 0.01, 0.001], rel=1e-15)
+    lin, _ = fused.rope_frequencies(8, scaling="linear", factor=4.0, device="cpu")
+    assert lin.tolist() == pytest.approx([v / 4.0 for v in f.tolist()], rel=1e-15)
+    ntk, _ = fused.rope_frequencies(8, scaling="ntk", factor=4.0, device="cpu")
+    assert ntk[0].item() == 1.0 and ntk[-1].item() == pytest.approx(f[-1].item() / 4.0, rel=1e-14)
+    y, m = fused.rope_frequencies(128, scaling="yarn", factor=4.0, original_length=4096, device="cpu")
+    f, _ = fused.rope_frequencies(128, device="cpu")
+    assert m == pytest.approx(0.1 * np.log(4.0) + 1.0)
+    turns = 4096 * f / (2 * np.pi)
+    ratio = f / y
+    assert torch.all(ratio[turns > 64] == 1.0)
+    # below one turn, but for the pair that the rounding of the band's end takes in
+    assert ratio[turns < 0.8].min().item() == pytest.approx(4.0, rel=1e-12)
+    assert torch.all(ratio.diff() >= -1e-12) and ratio.min() >= 1.0
+    one, _ = fused.rope_frequencies(2, scaling="ntk", factor=8.0, device="cpu")
+    assert one.tolist() == [1.0]
+
+
+@pytest.mark.parametrize("args,kw", [((7,), {}), ((0,), {}), ((8,), dict(base=0.0)), ((8,), dict(factor=0.5)),
+                                     ((8,), dict(scaling="other")), ((8,), dict(scaling="yarn", factor=2.0))])
+def test_rope_frequencies_refusals(args, kw):
+    with pytest.raises(ValueError):
+        fused.rope_frequencies(*args, device="cpu", **kw)
+
+
+# --------------------------------------------------------------------------- #
+# the torch front end's checks (before any call)
+# --------------------------------------------------------------------------- #
+def test_front_end_refusals():
+    x, w = torch.zeros(4, 8), torch.ones(8)
+    h = torch.zeros(4, 2, 8)
+    pos, freq = torch.zeros(4, dtype=torch.int64), torch.ones(4, dtype=torch.float64)
+    for call in (
+            lambda: fused.rms_norm_add(x, torch.zeros(4, 7), w),
+            lambda: fused.rms_norm_add(x, x, torch.ones(7)),
+            lambda: fused.rms_norm_add(x, x, w.half()),
+            lambda: fused.rms_norm_add(x, x.half(), w),
+            lambda: fused.rms_norm_add(x, x, w, p=1.5),
+            lambda: fused.rms_norm_add(x, x, w, p=0.1),
+            lambda: fused.rms_norm_add(x, x, w, p=0.1, rng=torch.zeros(2)),
+            lambda: fused.rms_norm_add(x, x, w, p=0.1, rng=torch.zeros(3, dtype=torch.int64)),
+            lambda: fused.rms_norm_add_(x, torch.zeros(8, 4).t(), w),
+            lambda: fused.rms_norm_add_(x, x, w),
+            lambda: fused.rms_norm_add_(x, torch.zeros(4, 8, requires_grad=True), w),
+            lambda: fused.rms_norm_quant(x, w, group=48),
+            lambda: fused.rms_norm_quant(x, torch.ones(4, 8)),
+            lambda: fused.rms_norm_rope(h, torch.zeros(3, 2, 8), w, w, pos, freq),
+            lambda: fused.rms_norm_rope(h, torch.zeros(4, 2, 6), w, w, pos, freq),
+            lambda: fused.rms_norm_rope(h, h, torch.ones(7), w, pos, freq),
+            lambda: fused.rms_norm_rope(h, h, w, w, pos.int(), freq),
+            lambda: fused.rms_norm_rope(h, h, w, w, pos[:3], freq),
+            lambda: fused.rms_norm_rope(h, h, w, w, pos, freq.float()),
+            lambda: fused.rms_norm_rope(h, None, w, w, pos, freq),
+            lambda: fused.rms_norm_rope(torch.zeros(4, 0, 8), None, w, None, pos, freq)):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_dropout_state_holds_64_bits():
+    s = fused.dropout_state((1 << 64) - 1, 1 << 63, device="cpu")
+    assert s.tolist() == [-1, -(1 << 63)]
+
+
+def test_rope_module_keeps_its_frequencies_in_64_bits():
+    m = fused.RMSNormRope(16, 8, base=500.0).to(torch.bfloat16) if torch.cuda.is_available() else \
+        fused.RMSNormRope(16, 8, base=500.0, device="cpu").to(torch.bfloat16)
+    assert m.inv_freq.dtype == torch.float64 and m.q_weight.dtype == torch.bfloat16
+    assert m.inv_freq.cpu().tolist() == fused.rope_frequencies(8, 500.0, device="cpu")[0].tolist()
