@@ -1,18 +1,12 @@
-// add.cu -- residual addition with dropout and the RMSNorm of the sum, forward and
-// backward.
+// add.cu -- residual addition with dropout and the RMSNorm of the sum: the forward.
 //
 // Per row, with D(x) = x * scale where the dropout keeps an element and 0 where it
 // drops it (D(x) = x without dropout):
 //     h = D(x) + residual, rounded to the I/O dtype: the residual stream
 //     r = 1 / sqrt(sum(h^2) / N + eps);   y = (h * r) * g
-// and for the cotangents dy of y and dh of h, n = h * r, u = dy * g:
-//     dresidual = dh + r * (u - n * (sum(u * n) / N))
-//     dx = D'(dresidual)  (the same elements kept, the same scale, before rounding)
-//     dgamma = sum over rows of dy * n
 // The norm is taken of the rounded h, so that y is the RMSNorm of what the caller
 // holds and the backward, which reads h, differentiates the forward at the point
-// where it was evaluated. Arithmetic is fp32; h, y, dresidual and dx are rounded
-// once.
+// where it was evaluated. Arithmetic is fp32; h and y are rounded once.
 //
 // The dropout mask is never stored: each direction draws an octet's numbers from
 // its row and column (octet.cuh).
@@ -22,222 +16,99 @@
 
 namespace rmsnorm {
 
-// Forward. G lanes per row (several rows per block), or a block per row (G == 0);
-// KB octets per thread, thread t of a row owning octets t, t + threads, ... Each
-// block does its rows and ends: the hardware balances the rows over the SMs.
-template <int DT, bool AL, int G, int KB>
+// G lanes per row (several rows per block), or a block per row (G == 0); KB octets
+// per thread, thread t of a row owning octets t, t + threads, ... Each block does its
+// rows and ends: the hardware balances the rows over the SMs, and a row's loads are
+// all in flight at once.
+template <int DT, int MODE, int G, int KB, bool DROP>
 __global__ void __launch_bounds__(G ? kFusedGroupThreads : kFusedMaxThreads) add_fwd_rows(const AddArgs a) {
-    using O = Oct<DT>;
-    constexpr int W = O::kWords;
+    constexpr bool AL = MODE == kRowsAligned;
+    constexpr int W = Oct<DT>::kWords;
     constexpr int EB = Elem<DT>::kBytes;
     __shared__ float part[32];
     const int per_row = G ? G : blockDim.x;
     const int t = G ? threadIdx.x % G : threadIdx.x;
     const int64_t row = G ? static_cast<int64_t>(blockIdx.x) * (blockDim.x / G) + threadIdx.x / G : blockIdx.x;
-    const bool first = G ? t == 0 : (t & 31) == 0;
     griddep_wait();
     const bool live = row < a.M;
     const char* xr = static_cast<const char*>(a.x) + row * a.ldx * EB;
     const char* rr = static_cast<const char*>(a.res) + row * a.ldres * EB;
+    char* hr = static_cast<char*>(a.h) + row * a.ldh * EB;
+    char* yr = static_cast<char*>(a.y) + row * a.ldy * EB;
     const char* gr = static_cast<const char*>(a.gamma);
+    const bool on_word = MODE == kRowsOnePhase || a.same_phase != 0;
+    const int phase = !AL && on_word ? word_phase<DT>(yr) : 0;
 
     uint32_t xw[KB][W], rw[KB][W], gw[KB][W];
-    int valid[KB];
+    Cut cut[KB];
 #pragma unroll
     for (int v = 0; v < KB; ++v) {
-        const int o = v * per_row + t;
-        valid[v] = live ? octet_valid(o, a.N) : 0;
+        cut[v] = Cut(v * per_row + t, phase, a.N);
+        if (!live) cut[v].hi = 0;
 #pragma unroll
         for (int i = 0; i < W; ++i) xw[v][i] = 0u;
-        if (valid[v] > 0) octet_load<DT, AL>(xr + o * O::kBytes, valid[v], xw[v]);
+        if (cut[v].live()) row_load<DT, MODE>(xr + cut[v].col * EB, cut[v].lo, cut[v].hi, xw[v]);
     }
     if (a.res) {
 #pragma unroll
         for (int v = 0; v < KB; ++v)
-            if (valid[v] > 0) octet_load<DT, AL>(rr + (v * per_row + t) * O::kBytes, valid[v], rw[v]);
+            if (cut[v].live()) row_load<DT, MODE>(rr + cut[v].col * EB, cut[v].lo, cut[v].hi, rw[v]);
     }
 #pragma unroll
     for (int v = 0; v < KB; ++v)
-        if (valid[v] > 0) octet_load<DT, AL>(gr + (v * per_row + t) * O::kBytes, valid[v], gw[v]);
+        if (cut[v].live()) octet_load<DT, AL>(gr + cut[v].col * EB, cut[v].lo, cut[v].hi, gw[v]);
 
     const Dropout drop = {a.rng, a.threshold, a.scale};
     PhiloxKey key = {};
-    if (a.threshold) {
+    if (DROP) {
         key = philox_key(drop);
         if (a.rng_used && blockIdx.x == 0 && threadIdx.x == 0) {
             a.rng_used[0] = a.rng[0];
             a.rng_used[1] = a.rng[1];
         }
     }
-    float ss = 0.f;
+    uint64_t ss = f2_pack(0.f, 0.f);
 #pragma unroll
     for (int v = 0; v < KB; ++v) {
-        const int o = v * per_row + t;
-        if (valid[v] > 0) {
-            float f[8];
-            O::unpack(xw[v], f);
-            if (a.threshold) dropout_octet(drop, key, o, static_cast<uint32_t>(row), f);
+        if (cut[v].live()) {
+            uint64_t f[4];
+            octet_pairs<DT>(xw[v], f);
+            if (DROP) dropout_octet<!AL>(drop, key, cut[v].col, static_cast<uint32_t>(row), f);
             if (a.res) {
-                float b[8];
-                O::unpack(rw[v], b);
+                uint64_t b[4];
+                octet_pairs<DT>(rw[v], b);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] += b[e];
+                for (int e = 0; e < 4; ++e) f[e] = f2_add(f[e], b[e]);
             }
-            O::pack(f, xw[v]);  // h from here on
-            O::unpack(xw[v], f);
+            pairs_octet<DT>(f, xw[v]);  // h from here on
+            octet_pairs<DT>(xw[v], f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
+            for (int e = 0; e < 4; ++e) ss = f2_fma(f[e], f[e], ss);
         }
-        if (a.h && (!AL || valid[v] > 0))
-            octet_store<EB, W, AL>(static_cast<char*>(a.h) + row * a.ldh * EB + o * O::kBytes, xw[v], valid[v] * EB,
-                                   first, t % 32 == 31 || (G && t == G - 1) || 8 * (o + 1) >= a.N);
     }
-    ss = row_sum<G>(ss, part);
-    const float r = 1.0f / sqrtf(ss / static_cast<float>(a.N) + a.eps);
+    if (a.h) {
+#pragma unroll
+        for (int v = 0; v < KB; ++v)
+            octet_put<DT, AL>(hr + cut[v].col * EB, xw[v], cut[v].lo, cut[v].hi, on_word, G ? t == 0 : t % 32 == 0,
+                              t % 32 == 31 || (G && t == G - 1) || cut[v].col + 8 >= a.N);
+    }
+    float s0, s1;
+    f2_unpack(ss, s0, s1);
+    const float r = row_rsqrt(row_sum<G>(s0 + s1, part), a.inv_n, a.eps);
     if (live && t == 0 && a.rstd) a.rstd[row] = r;
+    const uint64_t r2 = f2_pack(r, r), one2 = f2_pack(a.one, a.one);
 #pragma unroll
     for (int v = 0; v < KB; ++v) {
-        const int o = v * per_row + t;
-        if (valid[v] > 0) {
-            float f[8], g[8];
-            O::unpack(xw[v], f);
-            O::unpack(gw[v], g);
+        if (cut[v].live()) {
+            uint64_t f[4], g[4];
+            octet_pairs<DT>(xw[v], f);
+            octet_pairs<DT>(gw[v], g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = (f[e] * r) * (g[e] + a.one);
-            O::pack(f, xw[v]);
+            for (int e = 0; e < 4; ++e) f[e] = f2_mul(f2_mul(f[e], r2), f2_add(g[e], one2));
+            pairs_octet<DT>(f, xw[v]);
         }
-        if (!AL || valid[v] > 0)
-            octet_store<EB, W, AL>(static_cast<char*>(a.y) + row * a.ldy * EB + o * O::kBytes, xw[v], valid[v] * EB,
-                                   first, t % 32 == 31 || (G && t == G - 1) || 8 * (o + 1) >= a.N);
-    }
-    griddep_launch_dependents();
-}
-
-// Backward: persistent, so that a thread, which owns the same columns in all its
-// rows, adds their share of dgamma up in registers. A block's rows (G == 0) or its
-// groups' rows are a fixed set in a fixed order, and each block writes one row of
-// partial sums for the fixed-order column reduce: dgamma is deterministic.
-template <int DT, bool AL, int G, int KB>
-__global__ void __launch_bounds__(G ? kFusedGroupThreads : kFusedMaxThreads) add_bwd_rows(const AddArgs a) {
-    using O = Oct<DT>;
-    constexpr int W = O::kWords;
-    constexpr int EB = Elem<DT>::kBytes;
-    __shared__ float part[2][32];
-    extern __shared__ float sums[];  // G > 0: [groups of the block][N]
-    const int per_row = G ? G : blockDim.x;
-    const int rows_block = G ? blockDim.x / G : 1;
-    const int t = G ? threadIdx.x % G : threadIdx.x;
-    const bool first = G ? t == 0 : (t & 31) == 0;
-    const char* gr = static_cast<const char*>(a.gamma);
-    griddep_wait();
-
-    uint32_t gw[KB][W];
-    float acc[KB][8];
-    int valid[KB];
-#pragma unroll
-    for (int v = 0; v < KB; ++v) {
-        const int o = v * per_row + t;
-        valid[v] = octet_valid(o, a.N);
-        if (valid[v] > 0) octet_load<DT, AL>(gr + o * O::kBytes, valid[v], gw[v]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[v][e] = 0.f;
-    }
-    const Dropout drop = {a.rng, a.threshold, a.scale};
-    PhiloxKey key = {};
-    if (a.threshold) key = philox_key(drop);
-    const float inv_n = 1.0f / static_cast<float>(a.N);
-
-    int parity = 0;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * rows_block;
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * rows_block; base < a.M; base += step, parity ^= 1) {
-        const int64_t row = base + (G ? threadIdx.x / G : 0);
-        const bool live = row < a.M;
-        const char* dyr = static_cast<const char*>(a.dy) + row * a.lddy * EB;
-        const char* hr = static_cast<const char*>(a.x) + row * a.ldx * EB;
-        const char* dhr = static_cast<const char*>(a.dh) + row * a.lddh * EB;
-        const float r = live ? a.rstd[row] : 0.f;
-        uint32_t yw[KB][W], hw[KB][W], ew[KB][W];
-#pragma unroll
-        for (int v = 0; v < KB; ++v) {
-            const int o = v * per_row + t;
-            const int n = live ? valid[v] : 0;
-#pragma unroll
-            for (int i = 0; i < W; ++i) yw[v][i] = hw[v][i] = ew[v][i] = 0u;
-            if (n > 0) {
-                octet_load<DT, AL>(dyr + o * O::kBytes, n, yw[v]);
-                octet_load<DT, AL>(hr + o * O::kBytes, n, hw[v]);
-                if (a.dh) octet_load<DT, AL>(dhr + o * O::kBytes, n, ew[v]);
-            }
-        }
-        float c = 0.f;
-#pragma unroll
-        for (int v = 0; v < KB; ++v) {
-            if (valid[v] > 0) {
-                float d[8], h[8], g[8];
-                O::unpack(yw[v], d);
-                O::unpack(hw[v], h);
-                O::unpack(gw[v], g);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float n = h[e] * r;
-                    const float w = d[e] * n;
-                    acc[v][e] += w;
-                    c = fmaf(w, g[e] + a.one, c);
-                }
-            }
-        }
-        c = row_sum<G>(c, part[parity]) * inv_n;
-#pragma unroll
-        for (int v = 0; v < KB; ++v) {
-            const int o = v * per_row + t;
-            const int n = live ? valid[v] : 0;
-            const bool last = t % 32 == 31 || (G && t == G - 1) || 8 * (o + 1) >= a.N;
-            float d[8], h[8], g[8];
-            if (n > 0) {
-                float q[8];
-                O::unpack(yw[v], d);
-                O::unpack(hw[v], h);
-                O::unpack(gw[v], g);
-                O::unpack(ew[v], q);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    d[e] = fmaf(r, fmaf(-(h[e] * r), c, d[e] * (g[e] + a.one)), q[e]);
-                O::pack(d, yw[v]);
-            }
-            if (a.dres && (!AL || n > 0))
-                octet_store<EB, W, AL>(static_cast<char*>(a.dres) + row * a.lddres * EB + o * O::kBytes, yw[v], n * EB,
-                                       first, last);
-            if (a.dx) {
-                if (n > 0 && a.threshold) {
-                    dropout_octet(drop, key, o, static_cast<uint32_t>(row), d);
-                    O::pack(d, yw[v]);
-                }
-                if (!AL || n > 0)
-                    octet_store<EB, W, AL>(static_cast<char*>(a.dx) + row * a.lddx * EB + o * O::kBytes, yw[v], n * EB,
-                                           first, last);
-            }
-        }
-    }
-    // this block's partial row
-    float* out = a.ws + static_cast<int64_t>(blockIdx.x) * a.ldws;
-    if constexpr (G > 0) {
-#pragma unroll
-        for (int v = 0; v < KB; ++v)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e < valid[v]) sums[(threadIdx.x / G) * a.N + 8 * (v * per_row + t) + e] = acc[v][e];
-        __syncthreads();
-        for (int col = threadIdx.x; col < a.N; col += blockDim.x) {
-            float s = sums[col];
-            for (int k = 1; k < rows_block; ++k) s += sums[k * a.N + col];
-            out[col] = s;
-        }
-    } else {
-#pragma unroll
-        for (int v = 0; v < KB; ++v)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e < valid[v]) out[8 * (v * per_row + t) + e] = acc[v][e];
+        octet_put<DT, AL>(yr + cut[v].col * EB, xw[v], cut[v].lo, cut[v].hi, on_word, G ? t == 0 : t % 32 == 0,
+                          t % 32 == 31 || (G && t == G - 1) || cut[v].col + 8 >= a.N);
     }
     griddep_launch_dependents();
 }
@@ -245,34 +116,41 @@ __global__ void __launch_bounds__(G ? kFusedGroupThreads : kFusedMaxThreads) add
 // ---------------------------------------------------------------------------
 // dispatch
 // ---------------------------------------------------------------------------
-template <int DT, bool AL, bool BWD>
-static const void* add_rows_for(int lanes, int octets) {
-#define RMSNORM_ADD_ROWS(G, KB)                                                          \
-    if (lanes == G && octets == KB)                                                      \
-        return BWD ? reinterpret_cast<const void*>(&add_bwd_rows<DT, AL, G, KB>)         \
-                   : reinterpret_cast<const void*>(&add_fwd_rows<DT, AL, G, KB>);
-    RMSNORM_ADD_ROWS(8, 1)
-    RMSNORM_ADD_ROWS(8, 2)
-    RMSNORM_ADD_ROWS(32, 1)
-    RMSNORM_ADD_ROWS(32, 2)
-    RMSNORM_ADD_ROWS(32, 4)
-    RMSNORM_ADD_ROWS(0, 1)
-    RMSNORM_ADD_ROWS(0, 2)
-    RMSNORM_ADD_ROWS(0, 4)
-#undef RMSNORM_ADD_ROWS
+template <int DT, int MODE, bool DROP>
+static const void* add_fwd_for(int lanes, int octets) {
+#define RMSNORM_ADD_FWD(G, KB) \
+    if (lanes == G && octets == KB) return reinterpret_cast<const void*>(&add_fwd_rows<DT, MODE, G, KB, DROP>);
+    RMSNORM_ADD_FWD(8, 1)
+    RMSNORM_ADD_FWD(8, 2)
+    RMSNORM_ADD_FWD(32, 1)
+    RMSNORM_ADD_FWD(32, 2)
+    RMSNORM_ADD_FWD(32, 4)
+    RMSNORM_ADD_FWD(0, 1)
+    RMSNORM_ADD_FWD(0, 2)
+    RMSNORM_ADD_FWD(0, 3)
+    RMSNORM_ADD_FWD(0, 4)
+    if constexpr (MODE != kRowsAligned) {
+        RMSNORM_ADD_FWD(0, 5)
+    }
+#undef RMSNORM_ADD_FWD
     return nullptr;
 }
-template <bool BWD>
-static const void* add_rows(const AddPlan& p) {
-    switch (p.dtype) {
-    case kF32: return p.aligned ? add_rows_for<kF32, true, BWD>(p.lanes, p.octets) : add_rows_for<kF32, false, BWD>(p.lanes, p.octets);
-    case kF16: return p.aligned ? add_rows_for<kF16, true, BWD>(p.lanes, p.octets) : add_rows_for<kF16, false, BWD>(p.lanes, p.octets);
-    case kBF16: return p.aligned ? add_rows_for<kBF16, true, BWD>(p.lanes, p.octets) : add_rows_for<kBF16, false, BWD>(p.lanes, p.octets);
-    default: return nullptr;
+template <int DT, bool DROP>
+static const void* add_fwd_mode(const AddPlan& p) {
+    switch (p.mode) {
+    case kRowsAligned: return add_fwd_for<DT, kRowsAligned, DROP>(p.lanes, p.octets);
+    case kRowsOnePhase: return add_fwd_for<DT, kRowsOnePhase, DROP>(p.lanes, p.octets);
+    default: return add_fwd_for<DT, kRowsAny, DROP>(p.lanes, p.octets);
     }
 }
 
-const void* add_fwd_kernel(const AddPlan& p) { return add_rows<false>(p); }
-const void* add_bwd_kernel(const AddPlan& p) { return add_rows<true>(p); }
+const void* add_fwd_kernel(const AddPlan& p) {
+    switch (p.dtype) {
+    case kF32: return p.drop ? add_fwd_mode<kF32, true>(p) : add_fwd_mode<kF32, false>(p);
+    case kF16: return p.drop ? add_fwd_mode<kF16, true>(p) : add_fwd_mode<kF16, false>(p);
+    case kBF16: return p.drop ? add_fwd_mode<kBF16, true>(p) : add_fwd_mode<kBF16, false>(p);
+    default: return nullptr;
+    }
+}
 
 }  // namespace rmsnorm

@@ -14,6 +14,13 @@ constexpr int kRopeMaxSets = 2;
 constexpr int kFusedMaxThreads = 512;
 constexpr int kFusedGroupThreads = 128;
 
+// How a kernel's rows lie. kRowsAligned: every row on a 16-byte boundary and of whole
+// octets (blocks of 8 columns, octet.cuh). kRowsOnePhase: the rows of all its tensors
+// (but for gamma) start at one offset from a 16-byte boundary, as dense tensors of any
+// width do: octets start on the boundaries, and only a row's two ends are masked.
+// kRowsAny: anything.
+enum RowMode : int { kRowsAny = 0, kRowsAligned = 1, kRowsOnePhase = 2 };
+
 // Residual addition (with dropout), norm and, in quant.cu, 8-bit output.
 struct AddArgs {
     const void* x;
@@ -32,6 +39,7 @@ struct AddArgs {
     int64_t M;
     int N;
     float eps;
+    float inv_n;                    // 1 / N
     float one;                      // 1 with the offset variant (g = 1 + gamma), else 0
     const unsigned long long* rng;  // dropout: {seed, offset} in device memory
     unsigned long long* rng_used;   // forward: a copy of them, may be null
@@ -39,17 +47,26 @@ struct AddArgs {
     float scale;
     int group;                      // quant: columns per scale, 0 for the row
     int pow2;                       // quant: scales rounded up to a power of two
+    int stages;                     // ring: rows staged
+    uint32_t slot;                  // bytes of a row's place in a stage
+    int same_phase;                 // outputs at one offset from a 16-byte boundary
+    uint32_t* err;                  // device error word
 };
 
 // A launch shape. lanes: lanes per row (0: a block per row).
 struct AddPlan {
     int dtype = 0;
     bool aligned = false;
+    int mode = 0;      // RowMode (forward)
     int lanes = 0;
     int octets = 1;  // per thread
     int threads = 0;
     int64_t blocks = 0;
     size_t smem = 0;
+    bool drop = false;
+    bool ring = false;  // add_bwd.cu's ring
+    int stages = 0;
+    uint32_t slot = 0;
 };
 
 const void* add_fwd_kernel(const AddPlan& p);

@@ -16,6 +16,9 @@ namespace {
 
 static_assert(kRopeMaxSets == RMSNORM_ROPE_MAX_SETS, "sets of a rope call");
 
+// Fewest rows that the backward's ring takes: fewer do not fill it.
+constexpr int64_t kRingLeastRows = 1024;
+
 std::mutex g_fused_mu;
 std::map<int, int> g_fused_sms;                                   // SMs by device
 std::map<std::pair<const void*, std::pair<int, int>>, int> g_fused_fit;  // resident blocks per SM by (kernel, (device, threads))
@@ -29,11 +32,26 @@ int current_sms(int& dev) {
     return n;
 }
 
+// Allow the kernel the device's whole shared memory; the attribute belongs to the
+// context, so it is set again where a launch fails (run).
+bool allow_shared_memory(const void* k, int dev) {
+    int optin = 0;
+    cudaFuncAttributes fa;
+    return cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) == cudaSuccess &&
+           cudaFuncGetAttributes(&fa, k) == cudaSuccess &&
+           cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, optin - static_cast<int>(fa.sharedSizeBytes)) ==
+               cudaSuccess &&
+           cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) ==
+               cudaSuccess;
+}
+
 // Blocks of `threads` that an SM holds, for the persistent kernels; 0 on failure.
 int resident_blocks(const void* k, int dev, int threads, size_t smem) {
     std::lock_guard<std::mutex> lock(g_fused_mu);
     int& n = g_fused_fit[{k, {dev, static_cast<int>(smem) * 1024 + threads}}];
-    if (n == 0 && cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, threads, smem) != cudaSuccess) n = 0;
+    if (n == 0 && ((smem > 48 * 1024 && !allow_shared_memory(k, dev)) ||
+                   cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, threads, smem) != cudaSuccess))
+        n = 0;
     return n;
 }
 
@@ -51,22 +69,36 @@ cudaError_t launch(const void* k, int64_t blocks, int threads, size_t smem, void
     return cudaLaunchKernelExC(&cfg, k, params);
 }
 
-// Lanes per row and octets per thread: rows of up to 1024 elements by groups of
+// Octets of a row that may start off a 16-byte boundary (`wide`: it does not).
+int64_t octets_of(int64_t N, int dtype, bool wide) { return wide ? N / 8 : ceil_div(N + (dtype == RMSNORM_F32 ? 3 : 7), 8); }
+
+// The fewest threads, a multiple of 32, that hold n octets, times their octets, over
+// the given choices of octets per thread; the first of equals.
+bool block_shape(int64_t n, std::initializer_list<int> choices, AddPlan& p) {
+    int64_t best = 0;
+    for (const int octets : choices) {
+        const int64_t threads = round_up(ceil_div(n, octets), 32);
+        if (threads > kFusedMaxThreads || (best && threads * octets >= best)) continue;
+        best = threads * octets;
+        p.octets = octets;
+        p.threads = static_cast<int>(threads);
+    }
+    return best > 0;
+}
+
+// Lanes per row and octets per thread for rows of n octets: up to 128 by groups of
 // lanes of a 4-warp block (the 8-bit output wants a warp, whose neighbouring lanes
 // hold a group of columns), wider rows by a block of at most kFusedMaxThreads.
-void row_shape(int64_t N, int least_lanes, AddPlan& p) {
-    const int64_t n = ceil_div(N, 8);
+bool row_shape(int64_t n, int least_lanes, std::initializer_list<int> choices, AddPlan& p) {
     if (n <= 128) {
         p.lanes = n <= 16 ? least_lanes : 32;
         p.octets = 1;
         while (static_cast<int64_t>(p.lanes) * p.octets < n) p.octets *= 2;
         p.threads = kFusedGroupThreads;
-        return;
+        return true;
     }
     p.lanes = 0;
-    p.octets = 2;
-    if (ceil_div(n, p.octets) > kFusedMaxThreads) p.octets = 4;
-    p.threads = static_cast<int>(round_up(ceil_div(n, p.octets), 32));
+    return block_shape(n, choices, p) || block_shape(n, {5}, p);
 }
 
 int64_t rows_per_block(const AddPlan& p) { return p.lanes ? p.threads / p.lanes : 1; }
@@ -102,30 +134,86 @@ rmsnorm_status check_rng(const AddArgs& a) {
     return RMSNORM_OK;
 }
 
-// Persistent grid of the backward and its partial rows.
-bool add_bwd_plan(int64_t M, int64_t N, int dtype, bool wide, AddPlan& p) {
+// The ring's shape; false where it does not apply.
+bool ring_plan(int64_t M, int64_t N, int dtype, bool wide, bool drop, bool has_dh, int dev, int sms, AddPlan& p) {
+    if (N <= 1024 || M < kRingLeastRows) return false;
+    p.dtype = dtype;
+    p.aligned = wide;
+    p.drop = drop;
+    p.ring = true;
+    const int64_t eb = elem_bytes(dtype);
+    if (!block_shape(octets_of(N, dtype, wide), {2, 3, 4}, p)) return false;
+    // whole octets for every thread that has one: rows off 16 bytes are copied from the
+    // word they start in to the one they end in
+    const int64_t octet = 8 * eb;
+    p.slot = static_cast<uint32_t>(wide ? N * eb : octets_of(N, dtype, wide) * octet);
+    const int64_t stage = (has_dh ? 3 : 2) * static_cast<int64_t>(p.slot);
+    const int64_t fixed = p.threads * p.octets * (p.octets == 2 ? 32 : octet) + 64 * 4;
+    const int64_t room = 227 * 1024;
+    const void* k = add_bwd_kernel(p);
+    const int by_registers = k ? resident_blocks(k, dev, p.threads, 1024) : 0;
+    if (by_registers < 1) return false;
+    // three stages, and two blocks an SM; three blocks with dropout, whose numbers take
+    // as many instructions as the rest (then of two stages, where three do not fit)
+    int bps = std::min(by_registers, drop ? 3 : 2);
+    int64_t stages = 3;
+    while (stages > 2 && bps * (stages * (stage + 8) + fixed + 1024) > room) --stages;
+    while (bps > 1 && bps * (stages * (stage + 8) + fixed + 1024) > room) --bps;
+    if (stages * (stage + 8) + fixed > room) return false;
+    p.stages = static_cast<int>(stages);
+    p.smem = static_cast<size_t>(stages * (stage + 8) + fixed);
+    const int fit = resident_blocks(k, dev, p.threads, p.smem);
+    if (fit < 1) return false;
+    p.blocks = std::min<int64_t>(static_cast<int64_t>(std::min(fit, bps)) * sms, M);
+    if (!wide) p.blocks = std::min<int64_t>(p.blocks / 8 * 8, round_up(M, 8));
+    return true;
+}
+
+// Persistent grid of the backward and its partial rows. Rows off 16 bytes want a grid
+// that is a multiple of 8; blocks without a row write a row of zeros.
+bool add_bwd_plan(int64_t M, int64_t N, int dtype, bool wide, bool ring, bool drop, bool has_dh, AddPlan& p) {
     int dev = 0;
     const int sms = current_sms(dev);
     if (!sms) return false;
+    if (ring && ring_plan(M, N, dtype, wide, drop, has_dh, dev, sms, p)) return true;
+    p = AddPlan();
     p.dtype = dtype;
     p.aligned = wide;
-    row_shape(N, 8, p);
+    if (!row_shape(octets_of(N, dtype, wide), 8, {2, 4}, p)) return false;
     p.smem = p.lanes ? static_cast<size_t>(rows_per_block(p)) * N * 4 : 0;
     const void* k = add_bwd_kernel(p);
     const int fit = k ? resident_blocks(k, dev, p.threads, p.smem) : 0;
     if (fit < 1) return false;
-    p.blocks = std::min<int64_t>(static_cast<int64_t>(std::min(fit, 8)) * sms, ceil_div(M, rows_per_block(p)));
+    const int64_t most = static_cast<int64_t>(std::min(fit, 8)) * sms, need = ceil_div(M, rows_per_block(p));
+    p.blocks = wide ? std::min(most, need) : std::min(most / 8 * 8, round_up(need, 8));
     return true;
+}
+
+// Whether the rows of two outputs start at one offset from a 16-byte boundary each.
+bool same_offset(const void* p, int64_t ldp, const void* q, int64_t ldq, size_t s) {
+    return !p || !q ||
+           (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15) == 0 && (ldp - ldq) * static_cast<int64_t>(s) % 16 == 0);
 }
 
 rmsnorm_status run(const void* k, const AddPlan& p, AddArgs& a, rmsnorm_stream_t stream) {
     if (!k) return RMSNORM_ERR_UNSUPPORTED;
-    void* params[] = {&a};
-    if (launch(k, p.blocks, p.threads, p.smem, params, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return RMSNORM_ERR_CUDA;
+    if (p.ring) {
+        a.stages = p.stages;
+        a.slot = p.slot;
+        a.err = device_error_word();
+        if (!a.err) return RMSNORM_ERR_CUDA;
     }
-    return RMSNORM_OK;
+    void* params[] = {&a};
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (launch(k, p.blocks, p.threads, p.smem, params, s) == cudaSuccess) return RMSNORM_OK;
+    (void)cudaGetLastError();
+    // a device reset since the attribute was set discards it
+    int dev = 0;
+    if (p.smem > 48 * 1024 && cudaGetDevice(&dev) == cudaSuccess && allow_shared_memory(k, dev) &&
+        launch(k, p.blocks, p.threads, p.smem, params, s) == cudaSuccess)
+        return RMSNORM_OK;
+    (void)cudaGetLastError();
+    return RMSNORM_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------------------
@@ -236,12 +324,19 @@ extern "C" rmsnorm_status rmsnorm_add_fwd(const void* x, int64_t ldx, const void
     a.ldy = ldy;
     a.M = M;
     a.N = static_cast<int>(N);
+    a.inv_n = 1.0f / static_cast<float>(N);
     a.eps = eps;
     a.one = static_cast<float>(offset);
+    const bool wide = wide_rows(N, s, {{x, ldx}, {residual, ldres}, {gamma, 0}, {h, ldh}, {y, ldy}});
+    a.same_phase = same_offset(h, ldh, y, ldy, s);
     AddPlan p;
     p.dtype = dtype;
-    p.aligned = wide_rows(N, s, {{x, ldx}, {residual, ldres}, {gamma, 0}, {h, ldh}, {y, ldy}});
-    row_shape(N, 8, p);
+    p.aligned = wide;
+    p.drop = a.threshold != 0;
+    p.mode = wide ? kRowsAligned : same_offset(x, ldx, y, ldy, s) && same_offset(residual, ldres, y, ldy, s) && a.same_phase
+                 ? kRowsOnePhase
+                 : kRowsAny;
+    if (!row_shape(octets_of(N, dtype, wide), 8, {4, 2, 3}, p)) return RMSNORM_ERR_UNSUPPORTED;
     p.blocks = ceil_div(M, rows_per_block(p));
     return run(add_fwd_kernel(p), p, a, stream);
 }
@@ -249,10 +344,13 @@ extern "C" rmsnorm_status rmsnorm_add_fwd(const void* x, int64_t ldx, const void
 extern "C" size_t rmsnorm_add_bwd_workspace_size(int64_t M, int64_t N, rmsnorm_dtype dtype) {
     if (check_common(M, N, dtype, 0) != RMSNORM_OK || M == 0) return 0;
     int64_t units = 0;
-    for (const bool wide : {false, true}) {
-        AddPlan p;
-        if (add_bwd_plan(M, N, dtype, wide, p)) units = std::max(units, p.blocks);
-    }
+    for (const bool wide : {false, true})
+        for (const bool ring : {false, true})
+            for (const bool drop : {false, true})
+                for (const bool has_dh : {false, true}) {
+                    AddPlan p;
+                    if (add_bwd_plan(M, N, dtype, wide, ring, drop, has_dh, p)) units = std::max(units, p.blocks);
+                }
     (void)cudaGetLastError();
     return static_cast<size_t>(units) * static_cast<size_t>(workspace_pitch(N)) * sizeof(float);
 }
@@ -284,7 +382,9 @@ extern "C" rmsnorm_status rmsnorm_add_bwd(const void* dy, int64_t lddy, const vo
     if ((st = check_rng(a)) != RMSNORM_OK) return st;
     AddPlan p;
     const bool wide = wide_rows(N, s, {{dy, lddy}, {dh, lddh}, {h, ldh}, {gamma, 0}, {dx, lddx}, {dresidual, lddres}});
-    if (!add_bwd_plan(M, N, dtype, wide, p)) {
+    const bool one_offset = same_offset(dy, lddy, h, ldh, s) && same_offset(dy, lddy, dh, lddh, s) &&
+                            same_offset(dy, lddy, dx, lddx, s) && same_offset(dy, lddy, dresidual, lddres, s);
+    if (!add_bwd_plan(M, N, dtype, wide, wide || one_offset, a.threshold != 0, dh != nullptr, p)) {
         (void)cudaGetLastError();
         return RMSNORM_ERR_CUDA;
     }
@@ -307,6 +407,7 @@ extern "C" rmsnorm_status rmsnorm_add_bwd(const void* dy, int64_t lddy, const vo
     a.M = M;
     a.N = static_cast<int>(N);
     a.one = static_cast<float>(offset);
+    a.same_phase = same_offset(dx, lddx, dresidual, lddres, s);
     if ((st = run(add_bwd_kernel(p), p, a, stream)) != RMSNORM_OK) return st;
     return launch_dgamma_reduce(dtype, a.ws, p.blocks, a.N, a.ldws, dgamma, cs) == cudaSuccess ? RMSNORM_OK
                                                                                               : RMSNORM_ERR_CUDA;
@@ -343,15 +444,17 @@ extern "C" rmsnorm_status rmsnorm_quant_fwd(const void* x, int64_t ldx, const vo
     a.ldscales = ldscales;
     a.M = M;
     a.N = static_cast<int>(N);
+    a.inv_n = 1.0f / static_cast<float>(N);
     a.eps = eps;
     a.one = static_cast<float>(offset);
     a.group = group;
     a.pow2 = pow2;
+    const bool wide = wide_rows(N, s, {{x, ldx}, {residual, ldres}, {gamma, 0}, {h, ldh}}) &&
+                      wide_rows(N, 1, {{codes, ldcodes}});
     AddPlan p;
     p.dtype = dtype;
-    p.aligned = wide_rows(N, s, {{x, ldx}, {residual, ldres}, {gamma, 0}, {h, ldh}}) &&
-                wide_rows(N, 1, {{codes, ldcodes}});
-    row_shape(N, 32, p);
+    p.aligned = wide;
+    if (!row_shape(ceil_div(N, 8), 32, {4, 2}, p)) return RMSNORM_ERR_UNSUPPORTED;
     p.blocks = ceil_div(M, rows_per_block(p));
     return run(quant_kernel(p), p, a, stream);
 }

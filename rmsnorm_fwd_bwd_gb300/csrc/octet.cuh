@@ -10,6 +10,7 @@
 #pragma once
 
 #include "device.cuh"
+#include "fused.h"
 
 namespace rmsnorm {
 
@@ -36,33 +37,62 @@ template <int DT> struct Oct {
     }
 };
 
-// Elements of octet `o` that lie in a row of N.
-__device__ __forceinline__ int octet_valid(int o, int N) {
-    const int left = N - 8 * o;
-    return left < 0 ? 0 : (left > 8 ? 8 : left);
+// An octet as four packed pairs of fp32 values (f2_*: one instruction for two).
+template <int DT>
+__device__ __forceinline__ void octet_pairs(const uint32_t (&w)[Oct<DT>::kWords], uint64_t (&f)[4]) {
+    float e[8];
+    Oct<DT>::unpack(w, e);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f2_pack(e[2 * i], e[2 * i + 1]);
+}
+template <int DT>
+__device__ __forceinline__ void pairs_octet(const uint64_t (&f)[4], uint32_t (&w)[Oct<DT>::kWords]) {
+    float e[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f2_unpack(f[i], e[2 * i], e[2 * i + 1]);
+    Oct<DT>::pack(e, w);
 }
 
-// Zero the elements from `valid` on.
+// Keep elements [lo, hi) of an octet, the others become zero.
 template <int DT>
-__device__ __forceinline__ void octet_mask(uint32_t (&w)[Oct<DT>::kWords], int valid) {
+__device__ __forceinline__ void octet_keep(uint32_t (&w)[Oct<DT>::kWords], int lo, int hi) {
 #pragma unroll
     for (int i = 0; i < Oct<DT>::kWords; ++i) {
         if constexpr (DT == kF32) {
-            if (i >= valid) w[i] = 0u;
+            if (i < lo || i >= hi) w[i] = 0u;
         } else {
-            if (2 * i >= valid) w[i] = 0u;
-            else if (2 * i + 1 >= valid) w[i] &= 0xffffu;
+            if (2 * i < lo || 2 * i >= hi) w[i] &= 0xffff0000u;
+            if (2 * i + 1 < lo || 2 * i + 1 >= hi) w[i] &= 0xffffu;
         }
     }
 }
 
-// Words of the octet at `p` (its first element), of which `valid` elements are
-// the row's; the others read as zero. ALIGNED: p is a multiple of 16 and valid is
-// 8. Otherwise every 16-byte word that is read holds at least one byte of a valid
-// element, so no read leaves the 16-byte words of the tensor.
-template <int DT, bool ALIGNED>
-__device__ __forceinline__ void octet_load(const char* p, int valid, uint32_t (&w)[Oct<DT>::kWords]) {
+// The octet that starts `sh` bytes (a multiple of the element size, below 16) into the
+// words s.
+template <int DT>
+__device__ __forceinline__ void octet_shift(uint32_t (&s)[Oct<DT>::kWords + 5], uint32_t sh, uint32_t (&w)[Oct<DT>::kWords]) {
     constexpr int W = Oct<DT>::kWords;
+    if (sh & 8u) {
+#pragma unroll
+        for (int i = 0; i < W + 3; ++i) s[i] = s[i + 2];
+    }
+    if (sh & 4u) {
+#pragma unroll
+        for (int i = 0; i < W + 2; ++i) s[i] = s[i + 1];
+    }
+    const uint32_t bits = 8u * (sh & 3u);
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = __funnelshift_r(s[i], s[i + 1], bits);
+}
+
+// The octet at `p` (where its first element is or would be), of which elements
+// [lo, hi) are the row's; the others read as zero. ALIGNED: p is a multiple of 16, lo
+// is 0 and hi 8. Otherwise every 16-byte word that is read holds at least one byte of
+// one of the elements, so no read leaves the 16-byte words of the tensor.
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ void octet_load(const char* p, int lo, int hi, uint32_t (&w)[Oct<DT>::kWords]) {
+    constexpr int W = Oct<DT>::kWords;
+    constexpr int EB = Elem<DT>::kBytes;
     if constexpr (ALIGNED) {
 #pragma unroll
         for (int c = 0; c < W / 4; ++c) {
@@ -71,28 +101,23 @@ __device__ __forceinline__ void octet_load(const char* p, int valid, uint32_t (&
         }
     } else {
         const uint32_t sh = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15);
-        const int need = static_cast<int>(sh) + valid * Elem<DT>::kBytes;  // bytes from the first aligned word on
+        const int from = static_cast<int>(sh) + lo * EB, to = static_cast<int>(sh) + hi * EB;  // bytes after p - sh
         const uint4* q = reinterpret_cast<const uint4*>(p - sh);
         uint32_t s[W + 5];
         s[W + 4] = 0u;
 #pragma unroll
         for (int c = 0; c < W / 4 + 1; ++c) {
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (valid > 0 && need > 16 * c) v = q[c];
+            if (from < 16 * c + 16 && to > 16 * c) v = q[c];
             s[4 * c] = v.x; s[4 * c + 1] = v.y; s[4 * c + 2] = v.z; s[4 * c + 3] = v.w;
         }
-        if (sh & 8u) {
+        if (sh != 0u) {
+            octet_shift<DT>(s, sh, w);
+        } else {
 #pragma unroll
-            for (int i = 0; i < W + 3; ++i) s[i] = s[i + 2];
+            for (int i = 0; i < W; ++i) w[i] = s[i];
         }
-        if (sh & 4u) {
-#pragma unroll
-            for (int i = 0; i < W + 2; ++i) s[i] = s[i + 1];
-        }
-        const uint32_t bits = 8u * (sh & 3u);
-#pragma unroll
-        for (int i = 0; i < W; ++i) w[i] = __funnelshift_r(s[i], s[i + 1], bits);
-        if (valid < 8) octet_mask<DT>(w, valid);
+        if (lo > 0 || hi < 8) octet_keep<DT>(w, lo, hi);
     }
 }
 
@@ -178,6 +203,65 @@ __device__ __forceinline__ void octet_store(char* p, const uint32_t (&w)[W], int
     }
 }
 
+// Load an octet of a row: whole 16-byte words (and the ends masked), or octet_load.
+template <int DT, int MODE>
+__device__ __forceinline__ void row_load(const char* p, int lo, int hi, uint32_t (&w)[Oct<DT>::kWords]) {
+    constexpr int W = Oct<DT>::kWords;
+    constexpr int EB = Elem<DT>::kBytes;
+    if constexpr (MODE == kRowsOnePhase) {
+#pragma unroll
+        for (int c = 0; c < W / 4; ++c) {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (W == 4 || (lo * EB < 16 * c + 16 && hi * EB > 16 * c)) v = reinterpret_cast<const uint4*>(p)[c];
+            w[4 * c] = v.x; w[4 * c + 1] = v.y; w[4 * c + 2] = v.z; w[4 * c + 3] = v.w;
+        }
+        if (lo > 0 || hi < 8) octet_keep<DT>(w, lo, hi);
+    } else {
+        octet_load<DT, MODE == kRowsAligned>(p, lo, hi, w);
+    }
+}
+
+// Store an octet at p, of which elements [lo, hi) are the row's. ALIGNED as above.
+// on_word: p is a multiple of 16 (the octets follow this tensor's rows); else octet_store,
+// called by the whole warp, with lo 0.
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ void octet_put(char* p, const uint32_t (&w)[Oct<DT>::kWords], int lo, int hi, bool on_word,
+                                          bool first, bool last) {
+    constexpr int W = Oct<DT>::kWords;
+    constexpr int EB = Elem<DT>::kBytes;
+    if (ALIGNED || on_word) {
+        if (ALIGNED ? hi > 0 : lo == 0 && hi == 8) {
+#pragma unroll
+            for (int c = 0; c < W / 4; ++c) store_chunk<4>(p + 16 * c, &w[4 * c]);
+        } else if (hi > lo) {
+            store_part<EB, W>(p, w, lo * EB, hi * EB);
+        }
+    } else {
+        octet_store<EB, W, false>(p, w, hi > 0 ? hi * EB : 0, first, last);
+    }
+}
+
+// How a row is cut into octets. They start at the columns 8 * o - phase, phase being
+// the elements that the outputs' row starts after a 16-byte boundary (0 for aligned
+// rows): the outputs, and the inputs that share the offset, then move in whole
+// 16-byte words, and only a row's two ends are masked.
+struct Cut {
+    int col, lo, hi;  // first column, and the octet's elements in the row
+    __device__ __forceinline__ Cut() {}
+    __device__ __forceinline__ Cut(int o, int phase, int N) {
+        col = 8 * o - phase;
+        lo = col < 0 ? -col : 0;
+        const int left = N - col;
+        hi = left < 0 ? 0 : (left > 8 ? 8 : left);
+    }
+    __device__ __forceinline__ bool live() const { return hi > 0; }
+};
+
+// The elements that p starts after a 16-byte boundary.
+template <int DT> __device__ __forceinline__ int word_phase(const void* p) {
+    return static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / Elem<DT>::kBytes);
+}
+
 // ---------------------------------------------------------------------------
 // dropout: Philox4x32 with 10 rounds (Salmon, Moraes, Dror and Shaw, "Parallel
 // random numbers: as easy as 1, 2, 3", 2011). Counter {octet, row, offset low,
@@ -190,6 +274,9 @@ struct Dropout {
     const unsigned long long* rng;  // {seed, offset} in device memory
     uint32_t threshold;             // an element is dropped when its number is below; 0: no dropout
     float scale;                    // 65536 / (65536 - threshold)
+    // A number in the upper half of a word is at least the threshold where the word is
+    // above this, whatever its lower half (with a threshold of 65536: nowhere).
+    __device__ __forceinline__ uint32_t below() const { return (threshold << 16) - 1u; }
 };
 
 struct PhiloxKey {
@@ -205,6 +292,9 @@ __device__ __forceinline__ PhiloxKey philox_key(const Dropout& d) {
 __device__ __forceinline__ void philox_octet(const PhiloxKey& key, uint32_t octet, uint32_t row, uint32_t (&c)[4]) {
     c[0] = octet; c[1] = row; c[2] = key.o0; c[3] = key.o1;
     uint32_t k0 = key.k0, k1 = key.k1;
+    // opaque, so that the rounds' keys are added up here: hoisted out of a loop over
+    // rows they would hold 20 registers
+    asm volatile("" : "+r"(k0), "+r"(k1));
 #pragma unroll
     for (int i = 0; i < 10; ++i) {
         const uint64_t a = static_cast<uint64_t>(c[0]) * 0xD2511F53u;
@@ -218,15 +308,43 @@ __device__ __forceinline__ void philox_octet(const PhiloxKey& key, uint32_t octe
     }
 }
 
-// f scaled where its number keeps it, 0 (whatever f was) where it is dropped.
-__device__ __forceinline__ void dropout_octet(const Dropout& d, const PhiloxKey& key, uint32_t octet, uint32_t row,
-                                              float (&f)[8]) {
-    uint32_t c[4];
-    philox_octet(key, octet, row, c);
+// The octet whose first column is col: f scaled where its number keeps it, 0 (whatever f
+// was) where it is dropped. ANY: the octet may start inside a counter's eight columns,
+// and takes two calls then.
+template <bool ANY>
+__device__ __forceinline__ void dropout_octet(const Dropout& d, const PhiloxKey& key, int col, uint32_t row, uint64_t (&f)[4]) {
+    uint32_t s[9];
+    {
+        uint32_t c[4];
+        philox_octet(key, static_cast<uint32_t>(col >> 3), row, c);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t u = (e & 1) ? c[e / 2] >> 16 : c[e / 2] & 0xffffu;
-        f[e] = u >= d.threshold ? f[e] * d.scale : 0.f;
+        for (int i = 0; i < 4; ++i) s[i] = c[i];
+    }
+    if (ANY && (col & 7) != 0) {
+        uint32_t c[4];
+        philox_octet(key, static_cast<uint32_t>((col >> 3) + 1), row, c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[4 + i] = c[i];
+        s[8] = 0u;
+        if (col & 4) {
+#pragma unroll
+            for (int i = 0; i < 7; ++i) s[i] = s[i + 2];
+        }
+        if (col & 2) {
+#pragma unroll
+            for (int i = 0; i < 6; ++i) s[i] = s[i + 1];
+        }
+        const uint32_t bits = (col & 1) ? 16u : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = __funnelshift_r(s[i], s[i + 1], bits);
+    }
+    const uint32_t below = d.below();
+    const uint64_t scale = f2_pack(d.scale, d.scale);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        f2_unpack(f2_mul(f[i], scale), lo, hi);
+        f[i] = f2_pack((s[i] << 16) > below ? lo : 0.f, s[i] > below ? hi : 0.f);
     }
 }
 
@@ -235,6 +353,18 @@ __device__ __forceinline__ void dropout_octet(const Dropout& d, const PhiloxKey&
 // the whole block: one barrier, `part` (32 floats) not reused before the next one.
 // Every thread of the row gets the same bits.
 // ---------------------------------------------------------------------------
+// The largest of the 32 lanes' values. By shuffles: behind a branch that not all lanes
+// take, __reduce_max_sync was seen to be run by the two sides apart (nvcc 13.0).
+__device__ __forceinline__ uint32_t warp_allmax(uint32_t v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// 1 / sqrt(sum / N + eps): rsqrtf is off by at most 2 units in the last place, and the
+// IEEE root and quotients would cost some forty instructions per thread and row.
+__device__ __forceinline__ float row_rsqrt(float sum, float inv_n, float eps) { return rsqrtf(fmaf(sum, inv_n, eps)); }
+
 template <int G>
 __device__ __forceinline__ float row_sum(float v, float* part) {
     if constexpr (G > 0) {

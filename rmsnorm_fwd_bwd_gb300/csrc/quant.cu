@@ -10,30 +10,9 @@
 #include "fused.h"
 #include "launch.h"
 #include "octet.cuh"
+#include "quant.cuh"
 
 namespace rmsnorm {
-
-// Two fp32 values as e4m3, a in the low byte.
-__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
-    uint16_t v;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(b), "f"(a));
-    return v;
-}
-
-// |y| as an integer: ordered as the value, with NaN above infinity.
-__device__ __forceinline__ uint32_t magnitude(float y) { return __float_as_uint(y) & 0x7fffffffu; }
-
-__device__ __forceinline__ float quant_scale(uint32_t amax, int pow2) {
-    float s = __uint_as_float(amax) / 448.0f;
-    if (s < 1.17549435e-38f) s = 1.17549435e-38f;  // 2^-126; a NaN stays
-    if (pow2) {
-        // up to the next power of two: a carry out of the fraction raises the exponent
-        // (infinity and NaN stay)
-        const uint32_t b = __float_as_uint(s);
-        if (b < 0x7f800000u) s = __uint_as_float((b + 0x007fffffu) & 0x7f800000u);
-    }
-    return s;
-}
 
 // A block (G == 0) or a warp (G == 32) per row; KB octets per thread. The lanes of a
 // group of 32, 64 or 128 columns are 4, 8 or 16 neighbours.
@@ -59,71 +38,71 @@ __global__ void __launch_bounds__(G ? kFusedGroupThreads : kFusedMaxThreads) qua
 #pragma unroll
     for (int v = 0; v < KB; ++v) {
         const int o = v * per_row + t;
-        valid[v] = live ? octet_valid(o, a.N) : 0;
+        valid[v] = live ? Cut(o, 0, a.N).hi : 0;
 #pragma unroll
         for (int i = 0; i < W; ++i) xw[v][i] = 0u;
-        if (valid[v] > 0) octet_load<DT, AL>(xr + o * O::kBytes, valid[v], xw[v]);
+        if (valid[v] > 0) octet_load<DT, AL>(xr + o * O::kBytes, 0, valid[v], xw[v]);
     }
     if (a.res) {
 #pragma unroll
         for (int v = 0; v < KB; ++v)
-            if (valid[v] > 0) octet_load<DT, AL>(rr + (v * per_row + t) * O::kBytes, valid[v], rw[v]);
+            if (valid[v] > 0) octet_load<DT, AL>(rr + (v * per_row + t) * O::kBytes, 0, valid[v], rw[v]);
     }
 #pragma unroll
     for (int v = 0; v < KB; ++v)
-        if (valid[v] > 0) octet_load<DT, AL>(gr + (v * per_row + t) * O::kBytes, valid[v], gw[v]);
+        if (valid[v] > 0) octet_load<DT, AL>(gr + (v * per_row + t) * O::kBytes, 0, valid[v], gw[v]);
 
-    float ss = 0.f;
+    uint64_t ss = f2_pack(0.f, 0.f);
 #pragma unroll
     for (int v = 0; v < KB; ++v) {
         const int o = v * per_row + t;
         if (valid[v] > 0) {
-            float f[8];
-            O::unpack(xw[v], f);
+            uint64_t f[4];
+            octet_pairs<DT>(xw[v], f);
             if (a.res) {
-                float b[8];
-                O::unpack(rw[v], b);
+                uint64_t b[4];
+                octet_pairs<DT>(rw[v], b);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] += b[e];
-                O::pack(f, xw[v]);
-                O::unpack(xw[v], f);
+                for (int e = 0; e < 4; ++e) f[e] = f2_add(f[e], b[e]);
+                pairs_octet<DT>(f, xw[v]);
+                octet_pairs<DT>(xw[v], f);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
+            for (int e = 0; e < 4; ++e) ss = f2_fma(f[e], f[e], ss);
         }
         if (a.h && (!AL || valid[v] > 0))
             octet_store<EB, W, AL>(static_cast<char*>(a.h) + row * a.ldh * EB + o * O::kBytes, xw[v], valid[v] * EB,
                                    lane == 0, lane == 31 || 8 * (o + 1) >= a.N);
     }
-    ss = row_sum<G>(ss, part);
-    const float r = 1.0f / sqrtf(ss / static_cast<float>(a.N) + a.eps);
-    float y[KB][8];
+    float s0, s1;
+    f2_unpack(ss, s0, s1);
+    const float r = row_rsqrt(row_sum<G>(s0 + s1, part), a.inv_n, a.eps);
+    const uint64_t r2 = f2_pack(r, r), one2 = f2_pack(a.one, a.one);
+    uint64_t y[KB][4];
     uint32_t m[KB];
 #pragma unroll
     for (int v = 0; v < KB; ++v) {
         m[v] = 0u;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[v][e] = 0.f;
+        for (int e = 0; e < 4; ++e) y[v][e] = 0ull;
         if (valid[v] > 0) {
-            float g[8];
-            O::unpack(xw[v], y[v]);
-            O::unpack(gw[v], g);
+            uint64_t g[4];
+            octet_pairs<DT>(xw[v], y[v]);
+            octet_pairs<DT>(gw[v], g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                y[v][e] = (y[v][e] * r) * (g[e] + a.one);
-                if (AL || e < valid[v]) m[v] = max(m[v], magnitude(y[v][e]));
-            }
+            for (int e = 0; e < 4; ++e) y[v][e] = f2_mul(f2_mul(y[v][e], r2), f2_add(g[e], one2));
+            m[v] = octet_amax(y[v], AL ? 8 : valid[v]);
         }
     }
     if (a.group == 0) {
         uint32_t all = m[0];
 #pragma unroll
         for (int v = 1; v < KB; ++v) all = max(all, m[v]);
-        all = __reduce_max_sync(0xffffffffu, all);
+        all = warp_allmax(all);
         if constexpr (G == 0) {
             if (lane == 0) top[threadIdx.x >> 5] = all;
             __syncthreads();
-            all = __reduce_max_sync(0xffffffffu, lane < static_cast<int>(blockDim.x >> 5) ? top[lane] : 0u);
+            all = warp_allmax(lane < static_cast<int>(blockDim.x >> 5) ? top[lane] : 0u);
         }
 #pragma unroll
         for (int v = 0; v < KB; ++v) m[v] = all;
@@ -136,24 +115,7 @@ __global__ void __launch_bounds__(G ? kFusedGroupThreads : kFusedMaxThreads) qua
 #pragma unroll
     for (int v = 0; v < KB; ++v) {
         const int o = v * per_row + t;
-        const float s = quant_scale(m[v], a.pow2);
-        const float inv = 1.0f / s;
-        uint32_t code[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            code[i] = e4m3_pair(y[v][4 * i] * inv, y[v][4 * i + 1] * inv) |
-                      e4m3_pair(y[v][4 * i + 2] * inv, y[v][4 * i + 3] * inv) << 16;
-        if (!AL || valid[v] > 0)
-            octet_store<1, 2, AL>(static_cast<char*>(a.y) + row * a.ldy + o * 8, code, valid[v], lane == 0,
-                                  lane == 31 || 8 * (o + 1) >= a.N);
-        if (valid[v] > 0) {
-            float* sr = a.scales + row * a.ldscales;
-            if (a.group == 0) {
-                if (o == 0) sr[0] = s;
-            } else if (o % (a.group / 8) == 0) {
-                sr[o / (a.group / 8)] = s;
-            }
-        }
+        quant_store<AL>(a, row, o, valid[v], y[v], m[v], lane == 0, lane == 31 || 8 * (o + 1) >= a.N);
     }
     griddep_launch_dependents();
 }

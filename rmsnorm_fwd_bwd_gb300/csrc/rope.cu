@@ -92,8 +92,8 @@ template <int DT>
 __device__ __forceinline__ void load16(const char* row, int a, int b, bool live, uint32_t (&w)[2][Oct<DT>::kWords]) {
 #pragma unroll
     for (int i = 0; i < Oct<DT>::kWords; ++i) w[0][i] = w[1][i] = 0u;
-    if (live && a >= 0) octet_load<DT, true>(row + a * Oct<DT>::kBytes, 8, w[0]);
-    if (live && b >= 0) octet_load<DT, true>(row + b * Oct<DT>::kBytes, 8, w[1]);
+    if (live && a >= 0) octet_load<DT, true>(row + a * Oct<DT>::kBytes, 0, 8, w[0]);
+    if (live && b >= 0) octet_load<DT, true>(row + b * Oct<DT>::kBytes, 0, 8, w[1]);
 }
 template <int DT>
 __device__ __forceinline__ void unpack16(const uint32_t (&w)[2][Oct<DT>::kWords], float (&f)[16]) {
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kFusedGroupThreads) rope_fwd_octets(const Rope
         // every lane of the warp runs the longest of its groups' counts (the sums
         // see the whole warp); all groups but a token's last have the same
         const int n = to > from ? to - from : 0;
-        const int most = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(n)));
+        const int most = static_cast<int>(warp_allmax(static_cast<uint32_t>(n)));
         uint32_t gw[2][W];
         load16<DT>(static_cast<const char*>(set.gamma), oa, ob, set.gamma != nullptr, gw);
         const char* xb = static_cast<const char*>(set.x) + (token * set.x_token + from * set.x_head) * EB;
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kFusedGroupThreads) rope_bwd_octets(const Rope
             heads_of(set, at, lo, hi, from, to);
             at += set.heads;
             const int n = to > from ? to - from : 0;
-            const int most = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(n)));
+            const int most = static_cast<int>(warp_allmax(static_cast<uint32_t>(n)));
             uint32_t gw[2][W];
             load16<DT>(static_cast<const char*>(set.gamma), oa, ob, set.gamma != nullptr, gw);
             const char* db = static_cast<const char*>(set.dy) + (token * set.dy_token + from * set.dy_head) * EB;

@@ -145,9 +145,15 @@ def test_add_fwd_without_residual_or_h(dtype):
 def test_add_fwd_in_place(N):
     for dtype in DTYPES:
         x, res, w = randn(6, N, dtype=dtype, seed=8), randn(6, N, dtype=dtype, seed=9), weight(N, dtype, False)
-        y, h, _, _ = run_add_fwd(x, res, w, dtype)
-        xr, rr = Rows(6, N, x.dtype, 1, 3, data=x), Rows(6, N, x.dtype, 0, 0, data=res)
         wt = w.cuda()
+
+        def buffers():
+            return Rows(6, N, x.dtype, 1, 3, data=x), Rows(6, N, x.dtype, 0, 0, data=res)
+        (xr, rr), (yr, hr) = buffers(), buffers()           # outputs laid out as the inputs: the same sums, the same bits
+        assert B.rmsnorm_add_fwd(xr, xr.ld, rr, rr.ld, wt, hr, hr.ld, yr, yr.ld, None, 6, N, EPS, dtype, 0) == 0
+        y, h = yr.get(), hr.get()
+        r = ref.norm(h, w, EPS)[1].squeeze(-1)
+        check_add_fwd(x, res, w, dtype, y, h, r)
         assert B.rmsnorm_add_fwd(xr, xr.ld, rr, rr.ld, wt, rr, rr.ld, xr, xr.ld, None, 6, N, EPS, dtype, 0) == 0
         assert torch.equal(rr.get(), h) and torch.equal(xr.get(), y)
 
@@ -259,15 +265,22 @@ def test_add_bwd_optional_tensors(N):
         assert torch.equal(only[1], full[1]) and torch.equal(only[2], full[2])
         only = run_add_bwd(dy, dh, h, r, w, dtype, want=())
         assert torch.equal(only[2], full[2])
-        # in place on dy, and on dh
-        for k in (0, 1):
+        # in place on dy, and on dh, against an output laid out as they are: the same sums, the same bits
+        need = B.rmsnorm_add_bwd_workspace_size(30, N, dtype)
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        wt, rt = w.cuda(), r.cuda()
+        want = None
+        for k in (None, 0, 1):
             t = [Rows(30, N, dy.dtype, 0, 3, data=v) for v in (dy, dh, h)]
-            dw, ws = torch.empty(N, dtype=dy.dtype, device="cuda"), None
-            need = B.rmsnorm_add_bwd_workspace_size(30, N, dtype)
-            ws = torch.empty(need, dtype=torch.uint8, device="cuda")
-            assert B.rmsnorm_add_bwd(t[0], t[0].ld, t[1], t[1].ld, t[2], t[2].ld, w.cuda(), r.cuda(), None, 0, t[k], t[k].ld,
-                                     dw, 30, N, dtype, 0, 0.0, None, ws, need) == 0
-            assert torch.equal(t[k].get(), full[0]) and torch.equal(dw.cpu(), full[2])
+            out = Rows(30, N, dy.dtype, 0, 3) if k is None else t[k]
+            dw = torch.empty(N, dtype=dy.dtype, device="cuda")
+            assert B.rmsnorm_add_bwd(t[0], t[0].ld, t[1], t[1].ld, t[2], t[2].ld, wt, rt, None, 0, out, out.ld, dw, 30, N,
+                                     dtype, 0, 0.0, None, ws, need) == 0
+            got = (out.get(), dw.cpu())
+            if k is None:
+                want = got
+                check_add_bwd(dy, dh, h, r, w, dtype, got[0], None, got[1])
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_add_bwd_workspace_contents_do_not_matter_and_it_is_checked():
