@@ -91,8 +91,10 @@ struct RopeArgs {
     const double* inv_freq;    // [R / 2]
     int64_t T;
     int D, R;
+    int interleaved;
     int chunk;                 // heads that a group of lanes takes of a token
     int nchunk;                // chunks per token
+    int chunks0;               // of them of the first set (octet kernels)
     float mscale;
     float eps;
     float one;
@@ -105,11 +107,16 @@ struct RopePlan {
     int dtype = 0;
     bool aligned = false;      // 16-byte octets; else element by element
     bool interleaved = false;
-    int lanes = 0;             // per head row
+    int lanes = 0;             // per head row, where aligned
+    int pairs = 0;             // per lane, elsewhere
     int threads = 0;
     int64_t blocks = 0;
     size_t smem = 0;
 };
+
+// Most heads that a group of lanes takes at a time in the forward: their loads are in
+// flight together (128 bytes a lane).
+constexpr int rope_fwd_batch(int dtype) { return dtype == 0 ? 2 : 4; }
 
 const void* rope_kernel(const RopePlan& p, bool bwd);
 

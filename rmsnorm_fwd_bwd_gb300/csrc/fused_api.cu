@@ -19,6 +19,11 @@ static_assert(kRopeMaxSets == RMSNORM_ROPE_MAX_SETS, "sets of a rope call");
 // Fewest rows that the backward's ring takes: fewer do not fill it.
 constexpr int64_t kRingLeastRows = 1024;
 
+// The rotation's backward: heads for which a group computes a token's cosines and sines
+// once, and blocks per SM (what its registers leave).
+constexpr int kRopeBwdRun = 8;
+constexpr int kRopeBwdBlocks = 3;
+
 std::mutex g_fused_mu;
 std::map<int, int> g_fused_sms;                                   // SMs by device
 std::map<std::pair<const void*, std::pair<int, int>>, int> g_fused_fit;  // resident blocks per SM by (kernel, (device, threads))
@@ -259,16 +264,23 @@ rmsnorm_status rope_plan(RopeArgs& a, int dtype, int interleaved, bool wide, boo
         for (p.lanes = 4; p.lanes < units;) p.lanes *= 2;
         group = p.lanes;
     } else {
-        p.lanes = static_cast<int>(ceil_div(a.R / 2 + ceil_div(a.D - a.R, 2), 32));
+        p.pairs = static_cast<int>(ceil_div(a.R / 2 + ceil_div(a.D - a.R, 2), 32));
     }
     const int64_t full = static_cast<int64_t>(sms) * 2048 / group;  // groups that fill the GPU
-    int64_t nchunk = std::min<int64_t>(ceil_div(full, a.T), a.heads);
-    a.chunk = static_cast<int>(ceil_div(a.heads, nchunk));
-    a.nchunk = static_cast<int>(ceil_div(a.heads, a.chunk));
-    const int64_t blocks = ceil_div(a.T * a.nchunk, p.threads / group);
     p.smem = bwd ? static_cast<size_t>(p.threads / group) * a.D * 4 : 0;
-    p.blocks = bwd ? std::min<int64_t>(blocks, static_cast<int64_t>(sms) * 8) : blocks;
-    if (!p.aligned) p.blocks = std::min<int64_t>(blocks, static_cast<int64_t>(sms) * (bwd ? 8 : 64));
+    if (p.aligned) {
+        const int batch = bwd ? kRopeBwdRun : rope_fwd_batch(dtype);
+        a.chunk = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(batch, a.T * a.heads / full)));
+        a.chunks0 = static_cast<int>(ceil_div(a.set[0].heads, a.chunk));
+        a.nchunk = a.chunks0 + static_cast<int>(a.nsets > 1 ? ceil_div(a.set[1].heads, a.chunk) : 0);
+        p.blocks = ceil_div(a.T * a.nchunk, p.threads / group);
+        if (bwd) p.blocks = std::min<int64_t>(p.blocks, static_cast<int64_t>(sms) * kRopeBwdBlocks);
+    } else {
+        const int64_t nchunk = std::min<int64_t>(ceil_div(full, a.T), a.heads);
+        a.chunk = static_cast<int>(ceil_div(a.heads, nchunk));
+        a.nchunk = static_cast<int>(ceil_div(a.heads, a.chunk));
+        p.blocks = std::min<int64_t>(ceil_div(a.T * a.nchunk, p.threads / group), static_cast<int64_t>(sms) * (bwd ? 8 : 64));
+    }
     a.units = p.blocks;
     a.ldws = workspace_pitch(a.D);
     return RMSNORM_OK;
@@ -277,8 +289,8 @@ rmsnorm_status rope_plan(RopeArgs& a, int dtype, int interleaved, bool wide, boo
 rmsnorm_status rope_run(RopeArgs& a, const RopePlan& p, int interleaved, bool bwd, cudaStream_t s) {
     const void* k = rope_kernel(p, bwd);
     if (!k) return RMSNORM_ERR_UNSUPPORTED;
-    int last = p.aligned ? p.lanes : interleaved;
-    void* params[] = {&a, &last};
+    a.interleaved = interleaved;
+    void* params[] = {&a};
     if (launch(k, p.blocks, p.threads, p.smem, params, s) != cudaSuccess) {
         (void)cudaGetLastError();
         return RMSNORM_ERR_CUDA;

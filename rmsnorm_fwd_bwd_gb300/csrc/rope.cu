@@ -37,17 +37,57 @@ __device__ __forceinline__ uint64_t turns_per_position(double f) {
     return (b >> 63) ? 0ull - t : t;
 }
 
-__device__ __forceinline__ void turn_at(uint64_t per_position, int64_t pos, float mscale, float& c, float& s) {
-    const uint64_t phase = per_position * static_cast<uint64_t>(pos);
-    const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f;  // 2^-31
-    sincospif(half_turns, &s, &c);
-    c *= mscale;
-    s *= mscale;
+// The turn's fraction at a position, in units of 2^-32 (a signed half turn either way).
+__device__ __forceinline__ int32_t phase_at(uint64_t per_position, int64_t pos) {
+    return static_cast<int32_t>((per_position * static_cast<uint64_t>(pos)) >> 32);
 }
 
-__device__ __forceinline__ float lanes_sum(float v, int lanes) {
-    for (int o = lanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+// cos and sin, times m, of two angles given as phases. The nearest quarter turn is taken
+// off, and the rest, below pi / 4, goes through the Taylor series: sin to t^9 (the next
+// term is below 2^-28 there), cos to t^10 (below 2^-32), both angles in one packed
+// instruction. About half the instructions of two sincospif calls.
+__device__ __forceinline__ void turn_pair(int32_t p0, int32_t p1, float m0, float m1, uint64_t& c, uint64_t& s) {
+    const uint32_t q0 = static_cast<uint32_t>(p0) + 0x20000000u, q1 = static_cast<uint32_t>(p1) + 0x20000000u;
+    const float unit = 1.4629180792671596e-9f;  // 2 pi / 2^32
+    const float t0 = static_cast<float>(static_cast<int32_t>(q0 & 0x3fffffffu) - 0x20000000) * unit;
+    const float t1 = static_cast<float>(static_cast<int32_t>(q1 & 0x3fffffffu) - 0x20000000) * unit;
+    auto both = [](float v) { return f2_pack(v, v); };
+    const uint64_t t = f2_pack(t0, t1), z = f2_mul(t, t);
+    uint64_t p = f2_fma(z, both(1.f / 362880), both(-1.f / 5040));
+    p = f2_fma(p, z, both(1.f / 120));
+    p = f2_fma(p, z, both(-1.f / 6));
+    const uint64_t sn = f2_fma(f2_mul(t, z), p, t);
+    p = f2_fma(z, both(-1.f / 3628800), both(1.f / 40320));
+    p = f2_fma(p, z, both(-1.f / 720));
+    p = f2_fma(p, z, both(1.f / 24));
+    p = f2_fma(p, z, both(-1.f / 2));
+    const uint64_t cs = f2_fma(p, z, both(1.f));
+    float s0, s1, c0, c1;
+    f2_unpack(sn, s0, s1);
+    f2_unpack(cs, c0, c1);
+    // quarter turns: 1 swaps (cos, sin) to (-sin, cos), 2 turns both signs
+    auto turned = [](uint32_t q, float& a, float& b) {
+        const float x = (q & 0x40000000u) ? b : a, y = (q & 0x40000000u) ? a : b;
+        a = __uint_as_float(__float_as_uint(x) ^ ((q + 0x40000000u) & 0x80000000u));
+        b = __uint_as_float(__float_as_uint(y) ^ (q & 0x80000000u));
+    };
+    turned(q0, c0, s0);
+    turned(q1, c1, s1);
+    const uint64_t m = f2_pack(m0, m1);
+    c = f2_mul(f2_pack(c0, c1), m);
+    s = f2_mul(f2_pack(s0, s1), m);
+}
+
+// item = token * n + chunk, by a 32-bit division where it fits.
+__device__ __forceinline__ int64_t split_item(int64_t item, int n, int& chunk) {
+    if (item < (int64_t(1) << 32)) {
+        const uint32_t t = static_cast<uint32_t>(item) / static_cast<uint32_t>(n);
+        chunk = static_cast<int>(static_cast<uint32_t>(item) - t * static_cast<uint32_t>(n));
+        return t;
+    }
+    const int64_t t = item / n;
+    chunk = static_cast<int>(item - t * n);
+    return t;
 }
 
 // The heads of a set among the heads [lo, hi) of all sets, the set's first being
@@ -76,16 +116,33 @@ __device__ __forceinline__ void lane_octets(int li, int D, int R, int& a, int& b
     if (b >= n) b = -1;
 }
 
-template <bool INTER>
-__device__ __forceinline__ void rotate(float (&f)[16], const float (&c)[8], const float (&s)[8]) {
+// The octets as the pairs' first entries p and second entries q, packed two pairs to a
+// word; and back.
+template <int DT, bool INTER>
+__device__ __forceinline__ void to_pairs(const uint32_t (&w)[2][Oct<DT>::kWords], uint64_t (&p)[4], uint64_t (&q)[4]) {
+    float f[16];
+    Oct<DT>::unpack(w[0], *reinterpret_cast<float(*)[8]>(&f[0]));
+    Oct<DT>::unpack(w[1], *reinterpret_cast<float(*)[8]>(&f[8]));
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        float& p = f[INTER ? 2 * k : k];
-        float& q = f[INTER ? 2 * k + 1 : k + 8];
-        const float x = p, y = q;
-        p = x * c[k] - y * s[k];
-        q = y * c[k] + x * s[k];
+    for (int i = 0; i < 4; ++i) {
+        p[i] = INTER ? f2_pack(f[4 * i], f[4 * i + 2]) : f2_pack(f[2 * i], f[2 * i + 1]);
+        q[i] = INTER ? f2_pack(f[4 * i + 1], f[4 * i + 3]) : f2_pack(f[8 + 2 * i], f[9 + 2 * i]);
     }
+}
+template <int DT, bool INTER>
+__device__ __forceinline__ void store_pairs(char* row, int a, int b, const uint64_t (&p)[4], const uint64_t (&q)[4]) {
+    float f[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f2_unpack(p[i], INTER ? f[4 * i] : f[2 * i], INTER ? f[4 * i + 2] : f[2 * i + 1]);
+        f2_unpack(q[i], INTER ? f[4 * i + 1] : f[8 + 2 * i], INTER ? f[4 * i + 3] : f[9 + 2 * i]);
+    }
+    uint32_t w[Oct<DT>::kWords];
+    constexpr int EB = Elem<DT>::kBytes, B = Oct<DT>::kBytes;
+    Oct<DT>::pack(*reinterpret_cast<const float(*)[8]>(&f[0]), w);
+    octet_store<EB, Oct<DT>::kWords, true>(row + a * B, w, a >= 0 ? B : 0, false, false);
+    Oct<DT>::pack(*reinterpret_cast<const float(*)[8]>(&f[8]), w);
+    octet_store<EB, Oct<DT>::kWords, true>(row + b * B, w, b >= 0 ? B : 0, false, false);
 }
 
 template <int DT>
@@ -95,182 +152,256 @@ __device__ __forceinline__ void load16(const char* row, int a, int b, bool live,
     if (live && a >= 0) octet_load<DT, true>(row + a * Oct<DT>::kBytes, 0, 8, w[0]);
     if (live && b >= 0) octet_load<DT, true>(row + b * Oct<DT>::kBytes, 0, 8, w[1]);
 }
-template <int DT>
-__device__ __forceinline__ void unpack16(const uint32_t (&w)[2][Oct<DT>::kWords], float (&f)[16]) {
-    Oct<DT>::unpack(w[0], *reinterpret_cast<float(*)[8]>(&f[0]));
-    Oct<DT>::unpack(w[1], *reinterpret_cast<float(*)[8]>(&f[8]));
-}
-template <int DT>
-__device__ __forceinline__ void store16(char* row, int a, int b, const float (&f)[16]) {
-    uint32_t w[Oct<DT>::kWords];
-    Oct<DT>::pack(*reinterpret_cast<const float(*)[8]>(&f[0]), w);
-    octet_store<Elem<DT>::kBytes, Oct<DT>::kWords, true>(row + a * Oct<DT>::kBytes, w, a >= 0 ? Oct<DT>::kBytes : 0, false,
-                                                         false);
-    Oct<DT>::pack(*reinterpret_cast<const float(*)[8]>(&f[8]), w);
-    octet_store<Elem<DT>::kBytes, Oct<DT>::kWords, true>(row + b * Oct<DT>::kBytes, w, b >= 0 ? Oct<DT>::kBytes : 0, false,
-                                                         false);
+
+// A lane's gains g or 1 + g (1 without a weight), as pairs.
+template <int DT, bool INTER>
+__device__ __forceinline__ void load_gains(const RopeSet& set, float one, int oa, int ob, uint64_t (&gp)[4], uint64_t (&gq)[4]) {
+    uint32_t w[2][Oct<DT>::kWords];
+    load16<DT>(static_cast<const char*>(set.gamma), oa, ob, set.gamma != nullptr, w);
+    to_pairs<DT, INTER>(w, gp, gq);
+    const float add = set.gamma ? one : 1.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        gp[i] = f2_add(gp[i], f2_pack(add, add));
+        gq[i] = f2_add(gq[i], f2_pack(add, add));
+    }
 }
 
-// Rows of whole octets: a group of `lanes` lanes (4 to 32) takes a chunk of a
-// token's heads, its cosines and sines computed once and kept in registers; the
-// loads of several heads go out together.
-template <int DT, bool INTER>
-__global__ void __launch_bounds__(kFusedGroupThreads) rope_fwd_octets(const RopeArgs a, int lanes) {
+// The turns per position of a row's pairs, in shared memory: lane li's eight at [k][li],
+// 0 from entry R on (to be followed by a block barrier).
+struct Turns {
+    uint64_t at[8][32];
+    __device__ __forceinline__ void fill(const RopeArgs& a, int lanes) {
+        for (int i = threadIdx.x; i < 8 * lanes; i += blockDim.x) {
+            const int li = i / 8, k = i % 8;
+            at[k][li] = i < a.R / 2 ? turns_per_position(a.inv_freq[i]) : 0ull;
+        }
+    }
+    // cos and sin (times mscale) of a lane's pairs at a position; 1 and 0 from entry R on
+    __device__ __forceinline__ void of_lane(const RopeArgs& a, int li, int64_t pos, uint64_t (&c)[4], uint64_t (&s)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = 8 * li + 2 * i;
+            turn_pair(phase_at(at[2 * i][li], pos), phase_at(at[2 * i + 1][li], pos), k < a.R / 2 ? a.mscale : 1.f,
+                      k + 1 < a.R / 2 ? a.mscale : 1.f, c[i], s[i]);
+        }
+    }
+};
+
+__device__ __forceinline__ uint64_t f2_neg(uint64_t v) { return v ^ 0x8000000080000000ull; }
+
+__device__ __forceinline__ float f2_sum(uint64_t v) {
+    float a, b;
+    f2_unpack(v, a, b);
+    return a + b;
+}
+
+// Rows of whole octets: a group of L lanes (4 to 32, the fewest that hold a row at 16
+// entries each) takes up to BATCH heads of a token; neighbouring groups take
+// neighbouring heads. The heads' loads go out first, and the cosines and sines are
+// computed while they are under way and folded into the weight:
+// out_a = r * (x_a * (g_a cos) - x_b * (g_b sin)), out_b = r * (x_b * (g_b cos) + x_a *
+// (g_a sin)).
+template <int DT, bool INTER, int L>
+__global__ void __maxnreg__(96) rope_fwd_octets(const RopeArgs a) {
     constexpr int W = Oct<DT>::kWords;
     constexpr int EB = Elem<DT>::kBytes;
-    constexpr int BATCH = DT == kF32 ? 2 : 4;
-    const int li = threadIdx.x % lanes;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * (blockDim.x / lanes) + threadIdx.x / lanes;
+    constexpr int BATCH = rope_fwd_batch(DT);
+    __shared__ Turns turns;
+    const int li = threadIdx.x % L;
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * (blockDim.x / L) + threadIdx.x / L;
     griddep_wait();
     const bool live = item < a.T * a.nchunk;
-    const int64_t token = live ? item / a.nchunk : 0;
-    const int lo = live ? static_cast<int>(item % a.nchunk) * a.chunk : 0;
-    const int hi = live ? min(lo + a.chunk, a.heads) : 0;
+    int chunk;
+    const int64_t token = split_item(live ? item : 0, a.nchunk, chunk);
+    const int which = chunk >= a.chunks0 ? 1 : 0;
+    if (which) chunk -= a.chunks0;
+    const RopeSet& set = a.set[which];
+    const int from = chunk * a.chunk;
+    const int n = live ? min(a.chunk, set.heads - from) : 0;
     int oa, ob;
     lane_octets<INTER>(li, a.D, a.R, oa, ob);
-    float c[8], s[8];
-    const int64_t pos = a.pos[token];
+    const char* xb = static_cast<const char*>(set.x) + (token * set.x_token + from * set.x_head) * EB;
+    char* yb = static_cast<char*>(set.y) + (token * set.y_token + from * set.y_head) * EB;
+    const int64_t x_step = set.x_head * EB, y_step = set.y_head * EB;
+    uint32_t xw[BATCH][2][W];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        c[k] = 1.f;
-        s[k] = 0.f;
-        if (8 * li + k < a.R / 2) turn_at(turns_per_position(a.inv_freq[8 * li + k]), pos, a.mscale, c[k], s[k]);
+    for (int j = 0; j < BATCH; ++j) load16<DT>(xb + j * x_step, oa, ob, j < n, xw[j]);
+    uint64_t pc[4], ps[4], qc[4], qs[4];
+    load_gains<DT, INTER>(set, a.one, oa, ob, pc, qc);
+    const int64_t pos = a.pos[token];
+    turns.fill(a, L);
+    __syncthreads();
+    {
+        uint64_t c[4], s[4];
+        turns.of_lane(a, li, pos, c, s);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            ps[k] = f2_mul(pc[k], s[k]);
+            pc[k] = f2_mul(pc[k], c[k]);
+            qs[k] = f2_neg(f2_mul(qc[k], s[k]));
+            qc[k] = f2_mul(qc[k], c[k]);
+        }
     }
     const float inv_d = 1.0f / static_cast<float>(a.D);
-    int at = 0;
-    for (int i = 0; i < a.nsets; ++i) {
-        const RopeSet& set = a.set[i];
-        int from, to;
-        heads_of(set, at, lo, hi, from, to);
-        at += set.heads;
-        // every lane of the warp runs the longest of its groups' counts (the sums
-        // see the whole warp); all groups but a token's last have the same
-        const int n = to > from ? to - from : 0;
-        const int most = static_cast<int>(warp_allmax(static_cast<uint32_t>(n)));
-        uint32_t gw[2][W];
-        load16<DT>(static_cast<const char*>(set.gamma), oa, ob, set.gamma != nullptr, gw);
-        const char* xb = static_cast<const char*>(set.x) + (token * set.x_token + from * set.x_head) * EB;
-        char* yb = static_cast<char*>(set.y) + (token * set.y_token + from * set.y_head) * EB;
-        for (int h = 0; h < most; h += BATCH) {
-            uint32_t xw[BATCH][2][W];
+    // chunk is the same everywhere: the whole warp goes round as often (the sums see it)
 #pragma unroll
-            for (int j = 0; j < BATCH; ++j) load16<DT>(xb + (h + j) * set.x_head * EB, oa, ob, h + j < n, xw[j]);
+    for (int j = 0; j < BATCH; ++j) {
+        if (j >= a.chunk) break;
+        uint64_t p[4], q[4];
+        to_pairs<DT, INTER>(xw[j], p, q);
+        uint64_t ss = f2_mul(p[0], p[0]);
 #pragma unroll
-            for (int j = 0; j < BATCH; ++j) {
-                float f[16];
-                unpack16<DT>(xw[j], f);
-                if (set.gamma) {
-                    float g[16], ss = 0.f;
-                    unpack16<DT>(gw, g);
+        for (int k = 1; k < 4; ++k) ss = f2_fma(p[k], p[k], ss);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) ss = fmaf(f[e], f[e], ss);
-                    const float r = 1.0f / sqrtf(lanes_sum(ss, lanes) * inv_d + a.eps);
+        for (int k = 0; k < 4; ++k) ss = f2_fma(q[k], q[k], ss);
+        float r = row_rsqrt(row_sum<L>(f2_sum(ss), nullptr), inv_d, a.eps);
+        if (!set.gamma) r = 1.f;
+        const uint64_t r2 = f2_pack(r, r);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) f[e] = (f[e] * r) * (g[e] + a.one);
-                }
-                rotate<INTER>(f, c, s);
-                if (h + j < n) store16<DT>(yb + (h + j) * set.y_head * EB, oa, ob, f);
-            }
+        for (int k = 0; k < 4; ++k) {
+            const uint64_t x = p[k], y = q[k];
+            p[k] = f2_mul(f2_fma(x, pc[k], f2_mul(y, qs[k])), r2);
+            q[k] = f2_mul(f2_fma(y, qc[k], f2_mul(x, ps[k])), r2);
         }
+        if (j < n) store_pairs<DT, INTER>(yb + j * y_step, oa, ob, p, q);
     }
     griddep_launch_dependents();
 }
 
 // The backward on the same rows: persistent, so that a lane, which owns the same
 // columns of every head, adds its share of dgamma up in registers; each block
-// writes one row of partials per set for the fixed-order column reduce.
-template <int DT, bool INTER>
-__global__ void __launch_bounds__(kFusedGroupThreads) rope_bwd_octets(const RopeArgs a, int lanes) {
+// writes one row of partials per set for the fixed-order column reduce. The sets are
+// done one after the other, so that one set's sums and weight are held at a time.
+// A group takes a run of a token's heads, for which the cosines and sines are computed
+// once; as soon as a head's words are widened, the loads of the head BATCH further on
+// take their registers.
+// With u = v * g and xr = x * r: mean(u * n) = r * sum(u * x) / D, dgamma += v * xr, and
+// dx = r * u - xr * mean(u * n) * r.
+template <int DT, bool INTER, int L>
+__global__ void __maxnreg__((DT == kF32 ? 168 : 144)) rope_bwd_octets(const RopeArgs a) {
     constexpr int W = Oct<DT>::kWords;
     constexpr int EB = Elem<DT>::kBytes;
+    constexpr int BATCH = 2;
     extern __shared__ float sums[];  // [groups of the block][D]
-    const int li = threadIdx.x % lanes;
-    const int groups = blockDim.x / lanes;
-    const int group = threadIdx.x / lanes;
+    __shared__ Turns turns;
+    const int li = threadIdx.x % L;
+    const int groups = blockDim.x / L;
+    const int group = threadIdx.x / L;
     griddep_wait();
     int oa, ob;
     lane_octets<INTER>(li, a.D, a.R, oa, ob);
-    uint64_t turn[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) turn[k] = 8 * li + k < a.R / 2 ? turns_per_position(a.inv_freq[8 * li + k]) : 0ull;
-    float acc[kRopeMaxSets][16];
-#pragma unroll
-    for (int i = 0; i < kRopeMaxSets; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][e] = 0.f;
+    turns.fill(a, L);
+    __syncthreads();
     const float inv_d = 1.0f / static_cast<float>(a.D);
-    const int64_t items = a.T * a.nchunk;
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * groups; base < items;
-         base += static_cast<int64_t>(gridDim.x) * groups) {
-        const int64_t item = base + group;
-        const bool live = item < items;
-        const int64_t token = live ? item / a.nchunk : 0;
-        const int lo = live ? static_cast<int>(item % a.nchunk) * a.chunk : 0;
-        const int hi = live ? min(lo + a.chunk, a.heads) : 0;
-        const int64_t pos = a.pos[token];
-        float c[8], s[8];
+#pragma unroll 1
+    for (int i = 0; i < a.nsets; ++i) {
+        const RopeSet& set = a.set[i];
+        const bool norm = set.gamma != nullptr;
+        uint64_t gp[4], gq[4], ap[4], aq[4];
+        load_gains<DT, INTER>(set, a.one, oa, ob, gp, gq);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            c[k] = 1.f;
-            s[k] = 0.f;
-            if (8 * li + k < a.R / 2) {
-                turn_at(turn[k], pos, a.mscale, c[k], s[k]);
-                s[k] = -s[k];
-            }
-        }
-        int at = 0;
-#pragma unroll
-        for (int i = 0; i < kRopeMaxSets; ++i) {
-            if (i >= a.nsets) break;
-            const RopeSet& set = a.set[i];
-            int from, to;
-            heads_of(set, at, lo, hi, from, to);
-            at += set.heads;
-            const int n = to > from ? to - from : 0;
-            const int most = static_cast<int>(warp_allmax(static_cast<uint32_t>(n)));
-            uint32_t gw[2][W];
-            load16<DT>(static_cast<const char*>(set.gamma), oa, ob, set.gamma != nullptr, gw);
+        for (int k = 0; k < 4; ++k) ap[k] = aq[k] = f2_pack(0.f, 0.f);
+        const int run = min(a.chunk, set.heads);
+        const int nchunk = (set.heads + run - 1) / run;
+        const int64_t items = a.T * nchunk;
+        const int64_t d_step = set.dy_head * EB, x_step = set.x_head * EB, y_step = set.y_head * EB;
+        for (int64_t base = static_cast<int64_t>(blockIdx.x) * groups; base < items;
+             base += static_cast<int64_t>(gridDim.x) * groups) {
+            const int64_t item = base + group;
+            const bool live = item < items;
+            int chunk;
+            const int64_t token = split_item(live ? item : 0, nchunk, chunk);
+            const int from = chunk * run;
+            const int n = live ? min(run, set.heads - from) : 0;
+            const int64_t pos = a.pos[token];
             const char* db = static_cast<const char*>(set.dy) + (token * set.dy_token + from * set.dy_head) * EB;
             const char* xb = static_cast<const char*>(set.x) + (token * set.x_token + from * set.x_head) * EB;
             char* yb = static_cast<char*>(set.y) + (token * set.y_token + from * set.y_head) * EB;
-            for (int h = 0; h < most; ++h) {
-                uint32_t dw[2][W], xw[2][W];
-                load16<DT>(db + h * set.dy_head * EB, oa, ob, h < n, dw);
-                load16<DT>(xb + h * set.x_head * EB, oa, ob, h < n && set.gamma != nullptr, xw);
-                float v[16];
-                unpack16<DT>(dw, v);
-                rotate<INTER>(v, c, s);
-                if (set.gamma) {
-                    float x[16], g[16], ss = 0.f, q = 0.f;
-                    unpack16<DT>(xw, x);
-                    unpack16<DT>(gw, g);
+            uint32_t dw[BATCH][2][W], xw[BATCH][2][W];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        ss = fmaf(x[e], x[e], ss);
-                        q = fmaf(v[e] * (g[e] + a.one), x[e], q);
-                    }
-                    const float r = 1.0f / sqrtf(lanes_sum(ss, lanes) * inv_d + a.eps);
-                    const float m = lanes_sum(q, lanes) * inv_d * r;  // mean(u * n)
+            for (int j = 0; j < BATCH; ++j) {
+                load16<DT>(db, oa, ob, j < n, dw[j]);
+                load16<DT>(xb, oa, ob, norm && j < n, xw[j]);
+                db += d_step;
+                xb += x_step;
+            }
+            uint64_t c[4], sn[4], ns[4];
+            turns.of_lane(a, li, pos, c, sn);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float nv = x[e] * r;
-                        acc[i][e] = fmaf(v[e], nv, acc[i][e]);
-                        v[e] = r * (v[e] * (g[e] + a.one) - nv * m);
+            for (int k = 0; k < 4; ++k) ns[k] = f2_neg(sn[k]);
+            // run is the same everywhere: the whole warp goes round as often (the sums see it)
+            for (int h = 0; h < run; h += BATCH) {
+#pragma unroll
+                for (int j = 0; j < BATCH; ++j) {
+                    uint64_t p[4], q[4], xp[4], xq[4];
+                    to_pairs<DT, INTER>(dw[j], p, q);
+                    to_pairs<DT, INTER>(xw[j], xp, xq);
+                    const bool more = h + j + BATCH < n;
+                    load16<DT>(db, oa, ob, more, dw[j]);
+                    load16<DT>(xb, oa, ob, norm && more, xw[j]);
+                    db += d_step;
+                    xb += x_step;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint64_t x = p[k], y = q[k];
+                        p[k] = f2_fma(x, c[k], f2_mul(y, sn[k]));
+                        q[k] = f2_fma(y, c[k], f2_mul(x, ns[k]));
                     }
+                    if (norm) {
+                        uint64_t ss = f2_pack(0.f, 0.f), ux = f2_pack(0.f, 0.f);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            ss = f2_fma(xq[k], xq[k], f2_fma(xp[k], xp[k], ss));
+                            ux = f2_fma(f2_mul(q[k], gq[k]), xq[k], f2_fma(f2_mul(p[k], gp[k]), xp[k], ux));
+                        }
+                        const float r = row_rsqrt(row_sum<L>(f2_sum(ss), nullptr), inv_d, a.eps);
+                        const float m = row_sum<L>(f2_sum(ux), nullptr) * inv_d * r;
+                        const float e = -(r * m);
+                        const uint64_t r2 = f2_pack(r, r), e2 = f2_pack(e, e);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            xp[k] = f2_mul(xp[k], r2);
+                            xq[k] = f2_mul(xq[k], r2);
+                            ap[k] = f2_fma(p[k], xp[k], ap[k]);
+                            aq[k] = f2_fma(q[k], xq[k], aq[k]);
+                            p[k] = f2_fma(xp[k], e2, f2_mul(f2_mul(p[k], gp[k]), r2));
+                            q[k] = f2_fma(xq[k], e2, f2_mul(f2_mul(q[k], gq[k]), r2));
+                        }
+                    }
+                    if (h + j < n) store_pairs<DT, INTER>(yb, oa, ob, p, q);
+                    yb += y_step;
                 }
-                if (h < n) store16<DT>(yb + h * set.y_head * EB, oa, ob, v);
             }
         }
-    }
-#pragma unroll
-    for (int i = 0; i < kRopeMaxSets; ++i) {
-        if (i >= a.nsets) break;
-        if (!a.set[i].gamma) continue;
+        if (!norm) continue;
         __syncthreads();
+        // the lane's columns: its octets' entries, in the pairs' order
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (oa >= 0) sums[group * a.D + 8 * oa + e] = acc[i][e];
-            if (ob >= 0) sums[group * a.D + 8 * ob + e] = acc[i][8 + e];
+        for (int k = 0; k < 4; ++k) {
+            float p0, p1, q0, q1;
+            f2_unpack(ap[k], p0, p1);
+            f2_unpack(aq[k], q0, q1);
+            float* row = sums + group * a.D;
+            if (INTER) {
+                const int o = k < 2 ? oa : ob;
+                if (o >= 0) {
+                    float* w = row + 8 * o + 4 * (k & 1);
+                    w[0] = p0;
+                    w[1] = q0;
+                    w[2] = p1;
+                    w[3] = q1;
+                }
+            } else {
+                if (oa >= 0) {
+                    row[8 * oa + 2 * k] = p0;
+                    row[8 * oa + 2 * k + 1] = p1;
+                }
+                if (ob >= 0) {
+                    row[8 * ob + 2 * k] = q0;
+                    row[8 * ob + 2 * k + 1] = q1;
+                }
+            }
         }
         __syncthreads();
         float* out = a.ws + (i * a.units + blockIdx.x) * a.ldws;
@@ -312,7 +443,7 @@ template <int DT> __device__ __forceinline__ float entry(const char* p, int64_t 
 }
 
 template <int DT, int PK, bool BWD>
-__global__ void __launch_bounds__(kFusedGroupThreads) rope_pairs(const RopeArgs a, int inter) {
+__global__ void __launch_bounds__(kFusedGroupThreads) rope_pairs(const RopeArgs a) {
     constexpr int EB = Elem<DT>::kBytes;
     extern __shared__ float sums[];  // backward: [warps of the block][D]
     const int li = threadIdx.x & 31;
@@ -320,7 +451,7 @@ __global__ void __launch_bounds__(kFusedGroupThreads) rope_pairs(const RopeArgs 
     const int warps = blockDim.x >> 5;
     griddep_wait();
     int ca[PK], cb[PK];
-    lane_pairs<PK>(li, a, inter != 0, ca, cb);
+    lane_pairs<PK>(li, a, a.interleaved != 0, ca, cb);
     float acc[BWD ? kRopeMaxSets : 1][2 * PK];
 #pragma unroll
     for (int i = 0; i < (BWD ? kRopeMaxSets : 1); ++i)
@@ -340,7 +471,12 @@ __global__ void __launch_bounds__(kFusedGroupThreads) rope_pairs(const RopeArgs 
             c[k] = 1.f;
             s[k] = 0.f;
             if (li + 32 * k < a.R / 2) {
-                turn_at(turns_per_position(a.inv_freq[li + 32 * k]), pos, a.mscale, c[k], s[k]);
+                const int32_t phase = phase_at(turns_per_position(a.inv_freq[li + 32 * k]), pos);
+                uint64_t c2, s2;
+                turn_pair(phase, phase, a.mscale, a.mscale, c2, s2);
+                float other;
+                f2_unpack(c2, c[k], other);
+                f2_unpack(s2, s[k], other);
                 if (BWD) s[k] = -s[k];
             }
         }
@@ -387,7 +523,7 @@ __global__ void __launch_bounds__(kFusedGroupThreads) rope_pairs(const RopeArgs 
                 }
                 float r = 1.f, m = 0.f;
                 if (gb) {
-                    r = 1.0f / sqrtf(warp_allsum(ss) * inv_d + a.eps);
+                    r = row_rsqrt(warp_allsum(ss), inv_d, a.eps);
                     if (BWD) m = warp_allsum(q) * inv_d * r;
                 }
 #pragma unroll
@@ -438,30 +574,35 @@ __global__ void __launch_bounds__(kFusedGroupThreads) rope_pairs(const RopeArgs 
 }
 
 // ---------------------------------------------------------------------------
-// dispatch: `lanes` is the lanes per row of the octet kernels, the pairs per lane of
-// the others
+// dispatch
 // ---------------------------------------------------------------------------
-template <int DT>
-static const void* rope_kernel_for(const RopePlan& p, bool bwd) {
-    if (p.aligned) {
-        if (p.interleaved)
-            return bwd ? reinterpret_cast<const void*>(&rope_bwd_octets<DT, true>)
-                       : reinterpret_cast<const void*>(&rope_fwd_octets<DT, true>);
-        return bwd ? reinterpret_cast<const void*>(&rope_bwd_octets<DT, false>)
-                   : reinterpret_cast<const void*>(&rope_fwd_octets<DT, false>);
+template <int DT, bool INTER, bool BWD>
+static const void* rope_octets_for(int lanes) {
+#define RMSNORM_ROPE(L)                                                                              \
+    if (lanes == L) {                                                                                \
+        if constexpr (BWD) return reinterpret_cast<const void*>(&rope_bwd_octets<DT, INTER, L>);     \
+        else return reinterpret_cast<const void*>(&rope_fwd_octets<DT, INTER, L>);                   \
     }
-    if (p.lanes <= 2)
-        return bwd ? reinterpret_cast<const void*>(&rope_pairs<DT, 2, true>)
-                   : reinterpret_cast<const void*>(&rope_pairs<DT, 2, false>);
-    return bwd ? reinterpret_cast<const void*>(&rope_pairs<DT, 8, true>)
-               : reinterpret_cast<const void*>(&rope_pairs<DT, 8, false>);
+    RMSNORM_ROPE(4)
+    RMSNORM_ROPE(8)
+    RMSNORM_ROPE(16)
+    RMSNORM_ROPE(32)
+#undef RMSNORM_ROPE
+    return nullptr;
+}
+template <int DT, bool BWD>
+static const void* rope_kernel_for(const RopePlan& p) {
+    if (p.aligned)
+        return p.interleaved ? rope_octets_for<DT, true, BWD>(p.lanes) : rope_octets_for<DT, false, BWD>(p.lanes);
+    return p.pairs <= 2 ? reinterpret_cast<const void*>(&rope_pairs<DT, 2, BWD>)
+                        : reinterpret_cast<const void*>(&rope_pairs<DT, 8, BWD>);
 }
 
 const void* rope_kernel(const RopePlan& p, bool bwd) {
     switch (p.dtype) {
-    case kF32: return rope_kernel_for<kF32>(p, bwd);
-    case kF16: return rope_kernel_for<kF16>(p, bwd);
-    case kBF16: return rope_kernel_for<kBF16>(p, bwd);
+    case kF32: return bwd ? rope_kernel_for<kF32, true>(p) : rope_kernel_for<kF32, false>(p);
+    case kF16: return bwd ? rope_kernel_for<kF16, true>(p) : rope_kernel_for<kF16, false>(p);
+    case kBF16: return bwd ? rope_kernel_for<kBF16, true>(p) : rope_kernel_for<kBF16, false>(p);
     default: return nullptr;
     }
 }
