@@ -131,10 +131,21 @@ def _dtype_code(dt) -> int:
     return DTYPE_CODES[name]
 
 
+_raw_stream = None  # () -> the current stream's handle on the current device
+
+
 def _stream(s):
+    global _raw_stream
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        if _raw_stream is None:
+            import torch
+            if not torch.cuda.is_available():
+                return None
+            raw, dev = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+            # the handle without building a torch.cuda.Stream (3 us a call)
+            _raw_stream = (lambda: raw(dev())) if raw and dev else (lambda: torch.cuda.current_stream().cuda_stream)
+            torch.cuda.current_stream()  # initialises CUDA
+        return _raw_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream

@@ -10,12 +10,16 @@
   rotation's frequencies, also for scaled contexts.
 
 They are the custom ops ``rmsnorm_gb300::add_fwd`` and so on, with fake-tensor shapes
-and autograd formulas, as those of ``autograd``; rows that a view spaces out are
-passed with their pitch. Everything runs on torch's current stream of the inputs'
-device. They have no second order: differentiating a backward raises.
+and autograd formulas, as those of ``autograd``, which tracing and compilation use.
+Eager calls run the same code through ``torch.autograd.Function`` (or, where nothing
+asks for a gradient, at once): the custom ops' dispatch takes some 300 us of host time
+per forward and backward. Rows that a view spaces out are passed with their pitch.
+Everything runs on torch's current stream of the inputs' device. They have no second
+order: differentiating a backward raises.
 """
 from __future__ import annotations
 
+import contextlib
 import math
 from typing import Optional
 
@@ -57,6 +61,23 @@ def _check_dropout(where: str, x, p: float, rng) -> None:
         raise ValueError(f"{where}: dropout needs rng, an int64 tensor {{seed, offset}} on x's device")
 
 
+def _eager(*tensors) -> bool:
+    """Plain tensors outside of tracing and compilation."""
+    return not torch.compiler.is_compiling() and all(
+        t is None or type(t) is torch.Tensor or type(t) is torch.nn.Parameter for t in tensors)
+
+
+def _wants_grad(*tensors) -> bool:
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def _on(t: torch.Tensor):
+    """The tensor's device as the current one."""
+    if t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
 def _pitched(t: Optional[torch.Tensor]):
     return (None, 0) if t is None else _row_view(t)
 
@@ -74,16 +95,14 @@ def dropout_state(seed: int, offset: int = 0, device="cuda") -> torch.Tensor:
     return torch.tensor([signed(int(seed)), signed(int(offset))], dtype=torch.int64, device=device)
 
 
-@torch.library.custom_op("rmsnorm_gb300::add_fwd", mutates_args=())
-def _add_fwd(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torch.Tensor, eps: float, offset: bool,
-             p: float, rng: Optional[torch.Tensor]) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
-    with torch.cuda.device(x.device):
+def _add_fwd_run(x, residual, weight, eps, offset, p, rng, want_rstd=True):
+    with _on(x):
         xr, ldx = _row_view(x)
         rr, ldr = _pitched(residual)
         M, N = _rows(x)
         h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if want_rstd else None
         used = torch.empty(2 if p > 0.0 else 0, dtype=torch.int64, device=x.device)
         if p > 0.0 and M == 0:
             used.copy_(rng)
@@ -93,17 +112,21 @@ def _add_fwd(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torch.Te
     return y, h, rstd, used
 
 
+@torch.library.custom_op("rmsnorm_gb300::add_fwd", mutates_args=())
+def _add_fwd(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torch.Tensor, eps: float, offset: bool,
+             p: float, rng: Optional[torch.Tensor]) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    return _add_fwd_run(x, residual, weight, eps, offset, p, rng)
+
+
 @_add_fwd.register_fake
 def _(x, residual, weight, eps, offset, p, rng):
     return (x.new_empty(x.shape), x.new_empty(x.shape), x.new_empty(x.shape[:-1], dtype=torch.float32),
             x.new_empty((2 if p > 0.0 else 0,), dtype=torch.int64))
 
 
-@torch.library.custom_op("rmsnorm_gb300::add_bwd", mutates_args=())
-def _add_bwd(dy: torch.Tensor, dh: Optional[torch.Tensor], h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
-             offset: bool, p: float, rng: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+def _add_bwd_run(dy, dh, h, weight, rstd, offset, p, rng):
     """(dresidual, dx, dweight); dx is empty without dropout, where it is dresidual."""
-    with torch.cuda.device(h.device):
+    with _on(h):
         dyr, lddy = _row_view(dy)
         dhr, lddh = _pitched(dh)
         hr, ldh = _row_view(h)
@@ -118,6 +141,12 @@ def _add_bwd(dy: torch.Tensor, dh: Optional[torch.Tensor], h: torch.Tensor, weig
                                       rng if p > 0.0 else None, ws, ws.numel()),
               "rmsnorm_add_bwd", "add_backward")
     return dres, dx, dw
+
+
+@torch.library.custom_op("rmsnorm_gb300::add_bwd", mutates_args=())
+def _add_bwd(dy: torch.Tensor, dh: Optional[torch.Tensor], h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+             offset: bool, p: float, rng: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    return _add_bwd_run(dy, dh, h, weight, rstd, offset, p, rng)
 
 
 @_add_bwd.register_fake
@@ -145,6 +174,26 @@ def _add_backward(ctx, dy, dh, drstd, dused):
 _add_fwd.register_autograd(_add_backward, setup_context=_add_setup)
 
 
+class _AddFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, eps, offset, p, rng):
+        y, h, rstd, used = _add_fwd_run(x, residual, weight, eps, offset, p, rng)
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(h, weight, rstd, used)
+        ctx.how = (offset, p, residual is not None)
+        return y, h
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dh):
+        h, weight, rstd, used = ctx.saved_tensors
+        offset, p, has_residual = ctx.how
+        if dy is None:
+            dy = torch.zeros_like(h)
+        dres, dx, dw = _add_bwd_run(dy, dh, h, weight, rstd, offset, p, used)
+        return dx if p > 0.0 else dres, dres if has_residual else None, dw, None, None, None, None
+
+
 def rms_norm_add(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torch.Tensor, eps: float = 1e-6,
                  offset: bool = False, p: float = 0.0,
                  rng: Optional[torch.Tensor] = None) -> tuple[torch.Tensor, torch.Tensor]:
@@ -153,18 +202,26 @@ def rms_norm_add(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torc
     elements, whatever happens to ``rng`` in between."""
     _check_rows("rms_norm_add", x, residual, weight)
     _check_dropout("rms_norm_add", x, p, rng)
-    y, h, _, _ = torch.ops.rmsnorm_gb300.add_fwd(x, residual, weight, float(eps), bool(offset), float(p), rng)
-    return y, h
+    args = (x, residual, weight, float(eps), bool(offset), float(p), rng)
+    if _eager(x, residual, weight, rng):
+        if _wants_grad(x, residual, weight):
+            return _AddFunction.apply(*args)
+        return _add_fwd_run(*args, want_rstd=False)[:2]
+    return torch.ops.rmsnorm_gb300.add_fwd(*args)[:2]
 
 
-@torch.library.custom_op("rmsnorm_gb300::add_fwd_", mutates_args=("x", "residual"))
-def _add_fwd_(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor, eps: float, offset: bool) -> None:
-    with torch.cuda.device(x.device):
+def _add_in_place(x, residual, weight, eps, offset):
+    with _on(x):
         M, N = _rows(x)
         ldx = x.stride(0) if x.dim() == 2 and M > 0 else N
         ldr = residual.stride(0) if x.dim() == 2 and M > 0 else N
         _done(binding.rmsnorm_add_fwd(x, ldx, residual, ldr, weight.contiguous(), residual, ldr, x, ldx, None, M, N, eps,
                                       x.dtype, int(offset)), "rmsnorm_add_fwd", "add_forward")
+
+
+@torch.library.custom_op("rmsnorm_gb300::add_fwd_", mutates_args=("x", "residual"))
+def _add_fwd_(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor, eps: float, offset: bool) -> None:
+    _add_in_place(x, residual, weight, eps, offset)
 
 
 @_add_fwd_.register_fake
@@ -184,6 +241,7 @@ def rms_norm_add_(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor,
             raise ValueError("rms_norm_add_ needs contiguous tensors, or 2-D ones with unit column stride")
     if x.data_ptr() == residual.data_ptr() and x.numel():
         raise ValueError("rms_norm_add_: x and residual must not share memory")
+    # always the op, which marks both as changed for whoever saved them for a backward
     torch.ops.rmsnorm_gb300.add_fwd_(x, residual, weight, float(eps), bool(offset))
     return x, residual
 
@@ -207,10 +265,8 @@ class RMSNormAdd(torch.nn.Module):
 # --------------------------------------------------------------------------- #
 # 8-bit output
 # --------------------------------------------------------------------------- #
-@torch.library.custom_op("rmsnorm_gb300::quant_fwd", mutates_args=())
-def _quant_fwd(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torch.Tensor, eps: float, offset: bool,
-               group: int, pow2: bool) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
-    with torch.cuda.device(x.device):
+def _quant_run(x, residual, weight, eps, offset, group, pow2):
+    with _on(x):
         xr, ldx = _row_view(x)
         rr, ldr = _pitched(residual)
         M, N = _rows(x)
@@ -222,6 +278,12 @@ def _quant_fwd(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torch.
                                         codes, N, scales, n, M, N, eps, x.dtype, int(offset), group, int(pow2)),
               "rmsnorm_quant_fwd", "quant")
     return codes, scales, h
+
+
+@torch.library.custom_op("rmsnorm_gb300::quant_fwd", mutates_args=())
+def _quant_fwd(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torch.Tensor, eps: float, offset: bool,
+               group: int, pow2: bool) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    return _quant_run(x, residual, weight, eps, offset, group, pow2)
 
 
 @_quant_fwd.register_fake
@@ -241,9 +303,9 @@ def rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, off
     _check_rows("rms_norm_quant", x, residual, weight)
     if group not in (0, 32, 64, 128):
         raise ValueError("rms_norm_quant: group must be 0 (the row), 32, 64 or 128")
-    codes, scales, h = torch.ops.rmsnorm_gb300.quant_fwd(x.detach(), None if residual is None else residual.detach(),
-                                                         weight.detach(), float(eps), bool(offset), int(group),
-                                                         bool(pow2))
+    args = (x.detach(), None if residual is None else residual.detach(), weight.detach(), float(eps), bool(offset),
+            int(group), bool(pow2))
+    codes, scales, h = _quant_run(*args) if _eager(x, residual, weight) else torch.ops.rmsnorm_gb300.quant_fwd(*args)
     return codes, scales, x if residual is None else h
 
 
@@ -308,11 +370,8 @@ def _tokens(t: torch.Tensor) -> torch.Tensor:
     return t
 
 
-@torch.library.custom_op("rmsnorm_gb300::rope_fwd", mutates_args=())
-def _rope_fwd(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor],
-              k_weight: Optional[torch.Tensor], positions: torch.Tensor, inv_freq: torch.Tensor, interleaved: bool,
-              mscale: float, eps: float, offset: bool) -> tuple[torch.Tensor, torch.Tensor]:
-    with torch.cuda.device(q.device):
+def _rope_fwd_run(q, k, q_weight, k_weight, positions, inv_freq, interleaved, mscale, eps, offset):
+    with _on(q):
         qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         ko = torch.empty(k.shape if k is not None else (0,), dtype=q.dtype, device=q.device)
         D = q.shape[-1]
@@ -326,17 +385,20 @@ def _rope_fwd(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optional[tor
     return qo, ko
 
 
+@torch.library.custom_op("rmsnorm_gb300::rope_fwd", mutates_args=())
+def _rope_fwd(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor],
+              k_weight: Optional[torch.Tensor], positions: torch.Tensor, inv_freq: torch.Tensor, interleaved: bool,
+              mscale: float, eps: float, offset: bool) -> tuple[torch.Tensor, torch.Tensor]:
+    return _rope_fwd_run(q, k, q_weight, k_weight, positions, inv_freq, interleaved, mscale, eps, offset)
+
+
 @_rope_fwd.register_fake
 def _(q, k, q_weight, k_weight, positions, inv_freq, interleaved, mscale, eps, offset):
     return q.new_empty(q.shape), q.new_empty(k.shape if k is not None else (0,))
 
 
-@torch.library.custom_op("rmsnorm_gb300::rope_bwd", mutates_args=())
-def _rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], q: torch.Tensor, k: Optional[torch.Tensor],
-              q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor], positions: torch.Tensor,
-              inv_freq: torch.Tensor, interleaved: bool, mscale: float, eps: float,
-              offset: bool) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
-    with torch.cuda.device(q.device):
+def _rope_bwd_run(dq, dk, q, k, q_weight, k_weight, positions, inv_freq, interleaved, mscale, eps, offset):
+    with _on(q):
         D = q.shape[-1]
         pos, freq = positions.contiguous(), inv_freq.contiguous()
         outs, keep, heads = [], [], 0
@@ -356,6 +418,14 @@ def _rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], q: torch.Tensor, k: 
     return outs[0][0], outs[1][0], outs[0][1], outs[1][1]
 
 
+@torch.library.custom_op("rmsnorm_gb300::rope_bwd", mutates_args=())
+def _rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], q: torch.Tensor, k: Optional[torch.Tensor],
+              q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor], positions: torch.Tensor,
+              inv_freq: torch.Tensor, interleaved: bool, mscale: float, eps: float,
+              offset: bool) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    return _rope_bwd_run(dq, dk, q, k, q_weight, k_weight, positions, inv_freq, interleaved, mscale, eps, offset)
+
+
 @_rope_bwd.register_fake
 def _(dq, dk, q, k, q_weight, k_weight, positions, inv_freq, interleaved, mscale, eps, offset):
     D = q.shape[-1]
@@ -370,7 +440,7 @@ def _rope_setup(ctx, inputs, output):
     ctx.how = (interleaved, mscale, eps, offset)
 
 
-def _rope_backward(ctx, dq, dk):
+def _rope_grads(ctx, dq, dk, run):
     q, k, q_weight, k_weight, positions, inv_freq = ctx.saved_tensors
     if dq is None:
         dq = torch.zeros_like(q)
@@ -378,12 +448,30 @@ def _rope_backward(ctx, dq, dk):
         dk = None
     elif dk is None:
         dk = torch.zeros_like(k)
-    gq, gk, gqw, gkw = _rope_bwd(dq, dk, q, k, q_weight, k_weight, positions, inv_freq, *ctx.how)
+    gq, gk, gqw, gkw = run(dq, dk, q, k, q_weight, k_weight, positions, inv_freq, *ctx.how)
     return (gq, gk if k is not None else None, gqw if q_weight is not None else None,
             gkw if k_weight is not None else None, None, None, None, None, None, None)
 
 
+def _rope_backward(ctx, dq, dk):
+    return _rope_grads(ctx, dq, dk, _rope_bwd)
+
+
 _rope_fwd.register_autograd(_rope_backward, setup_context=_rope_setup)
+
+
+class _RopeFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, positions, inv_freq, *how):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(q, k, q_weight, k_weight, positions, inv_freq)
+        ctx.how = how
+        return _rope_fwd_run(q, k, q_weight, k_weight, positions, inv_freq, *how)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq, dk):
+        return _rope_grads(ctx, dq, dk, _rope_bwd_run)
 
 
 def rms_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor],
@@ -413,8 +501,13 @@ def rms_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optional
         raise ValueError("rms_norm_rope: positions must be int64 with q's leading shape, on its device")
     if inv_freq.dim() != 1 or inv_freq.dtype != torch.float64 or inv_freq.device != q.device:
         raise ValueError("rms_norm_rope: inv_freq must be a 1-D float64 tensor on q's device")
-    qo, ko = torch.ops.rmsnorm_gb300.rope_fwd(q, k, q_weight, k_weight, positions, inv_freq, bool(interleaved),
-                                              float(mscale), float(eps), bool(offset))
+    args = (q, k, q_weight, k_weight, positions, inv_freq, bool(interleaved), float(mscale), float(eps), bool(offset))
+    if not _eager(q, k, q_weight, k_weight, positions, inv_freq):
+        qo, ko = torch.ops.rmsnorm_gb300.rope_fwd(*args)
+    elif _wants_grad(q, k, q_weight, k_weight):
+        qo, ko = _RopeFunction.apply(*args)
+    else:
+        qo, ko = _rope_fwd_run(*args)
     return qo, ko if k is not None else None
 
 
