@@ -184,13 +184,14 @@ class _AddFunction(torch.autograd.Function):
         return y, h
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, dy, dh):
         h, weight, rstd, used = ctx.saved_tensors
         offset, p, has_residual = ctx.how
         if dy is None:
             dy = torch.zeros_like(h)
-        dres, dx, dw = _add_bwd_run(dy, dh, h, weight, rstd, offset, p, used)
+        # with a graph of the backward asked for: the op, which refuses to be differentiated
+        run = _add_bwd if torch.is_grad_enabled() else _add_bwd_run
+        dres, dx, dw = run(dy, dh, h, weight, rstd, offset, p, used)
         return dx if p > 0.0 else dres, dres if has_residual else None, dw, None, None, None, None
 
 
@@ -469,9 +470,8 @@ class _RopeFunction(torch.autograd.Function):
         return _rope_fwd_run(q, k, q_weight, k_weight, positions, inv_freq, *how)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, dq, dk):
-        return _rope_grads(ctx, dq, dk, _rope_bwd_run)
+        return _rope_grads(ctx, dq, dk, _rope_bwd if torch.is_grad_enabled() else _rope_bwd_run)
 
 
 def rms_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor],

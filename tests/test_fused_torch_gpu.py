@@ -74,6 +74,12 @@ def test_rms_norm_add_unused_outputs_views_and_no_residual():
     (g,) = torch.autograd.grad(y.sum(), xt, create_graph=True)
     with pytest.raises(RuntimeError):
         g.sum().backward()
+    q = leaf(randn(4, 2, 16, dtype="float32", seed=27))
+    out, _ = fused.rms_norm_rope(q, None, leaf(weight(16, "float32", False)), None, torch.arange(4, device="cuda"),
+                                 freqs(16).cuda())
+    (g,) = torch.autograd.grad(out.sum(), q, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
 
 
 def test_rms_norm_add_in_place():
