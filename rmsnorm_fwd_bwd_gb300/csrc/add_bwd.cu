@@ -24,11 +24,11 @@ namespace rmsnorm {
 
 // G lanes per row, or a block per row (G == 0), loads straight into registers: rows
 // of up to 1024 elements, wider ones where they are few, and those too wide for the
-// ring.
-template <int DT, bool AL, int G, int KB>
+// ring or not of one offset.
+template <int DT, int MODE, int G, int KB>
 __global__ void __launch_bounds__(G ? kFusedGroupThreads : kFusedMaxThreads) add_bwd_rows(const AddArgs a) {
-    using O = Oct<DT>;
-    constexpr int W = O::kWords;
+    constexpr bool AL = MODE == kRowsAligned;
+    constexpr int W = Oct<DT>::kWords;
     constexpr int EB = Elem<DT>::kBytes;
     __shared__ float part[2][32];
     extern __shared__ float sums[];  // G > 0: [groups of the block][N]
@@ -39,25 +39,28 @@ __global__ void __launch_bounds__(G ? kFusedGroupThreads : kFusedMaxThreads) add
     const bool first = G ? t == 0 : (t & 31) == 0;
     const char* gr = static_cast<const char*>(a.gamma);
     griddep_wait();
-    const bool same = a.same_phase != 0;
-    const int phase = AL || !same ? 0
-                      : a.dres    ? word_phase<DT>(static_cast<char*>(a.dres) + row0 * a.lddres * EB)
-                                  : word_phase<DT>(static_cast<char*>(a.dx) + row0 * a.lddx * EB);
+    const bool on_word = MODE == kRowsOnePhase || a.same_phase != 0;
+    // the offset that octets follow: the one of all tensors, or that of the outputs (of
+    // which there may be none)
+    const char* follow = static_cast<const char*>(MODE == kRowsOnePhase ? a.dy : a.dres ? a.dres : a.dx);
+    const int64_t pitch = MODE == kRowsOnePhase ? a.lddy : a.dres ? a.lddres : a.lddx;
+    const int phase = AL || !on_word || !follow ? 0 : word_phase<DT>(follow + row0 * pitch * EB);
 
     uint32_t gw[KB][W];
-    float acc[KB][8];
+    uint64_t acc[KB][4];
     Cut cut[KB];
 #pragma unroll
     for (int v = 0; v < KB; ++v) {
         cut[v] = Cut(v * per_row + t, phase, a.N);
         if (cut[v].live()) octet_load<DT, AL>(gr + cut[v].col * EB, cut[v].lo, cut[v].hi, gw[v]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[v][e] = 0.f;
+        for (int e = 0; e < 4; ++e) acc[v][e] = f2_pack(0.f, 0.f);
     }
     const Dropout drop = {a.rng, a.threshold, a.scale};
     PhiloxKey key = {};
     if (a.threshold) key = philox_key(drop);
     const float inv_n = 1.0f / static_cast<float>(a.N);
+    const uint64_t one2 = f2_pack(a.one, a.one);
 
     int parity = 0;
     const int64_t step = static_cast<int64_t>(gridDim.x) * rows_block;
@@ -68,88 +71,87 @@ __global__ void __launch_bounds__(G ? kFusedGroupThreads : kFusedMaxThreads) add
         const char* hr = static_cast<const char*>(a.x) + row * a.ldx * EB;
         const char* dhr = static_cast<const char*>(a.dh) + row * a.lddh * EB;
         const float r = live ? a.rstd[row] : 0.f;
+        const uint64_t r2 = f2_pack(r, r);
         uint32_t yw[KB][W], hw[KB][W], ew[KB][W];
 #pragma unroll
         for (int v = 0; v < KB; ++v) {
 #pragma unroll
             for (int i = 0; i < W; ++i) yw[v][i] = hw[v][i] = ew[v][i] = 0u;
             if (live && cut[v].live()) {
-                octet_load<DT, AL>(dyr + cut[v].col * EB, cut[v].lo, cut[v].hi, yw[v]);
-                octet_load<DT, AL>(hr + cut[v].col * EB, cut[v].lo, cut[v].hi, hw[v]);
-                if (a.dh) octet_load<DT, AL>(dhr + cut[v].col * EB, cut[v].lo, cut[v].hi, ew[v]);
+                row_load<DT, MODE>(dyr + cut[v].col * EB, cut[v].lo, cut[v].hi, yw[v]);
+                row_load<DT, MODE>(hr + cut[v].col * EB, cut[v].lo, cut[v].hi, hw[v]);
+                if (a.dh) row_load<DT, MODE>(dhr + cut[v].col * EB, cut[v].lo, cut[v].hi, ew[v]);
             }
         }
-        float c = 0.f;
+        uint64_t c2 = f2_pack(0.f, 0.f);
 #pragma unroll
         for (int v = 0; v < KB; ++v) {
             if (cut[v].live()) {
-                float d[8], h[8], g[8];
-                O::unpack(yw[v], d);
-                O::unpack(hw[v], h);
-                O::unpack(gw[v], g);
+                uint64_t d[4], h[4], g[4];
+                octet_pairs<DT>(yw[v], d);
+                octet_pairs<DT>(hw[v], h);
+                octet_pairs<DT>(gw[v], g);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float n = h[e] * r;
-                    const float w = d[e] * n;
-                    acc[v][e] += w;
-                    c = fmaf(w, g[e] + a.one, c);
+                for (int e = 0; e < 4; ++e) {
+                    const uint64_t w = f2_mul(d[e], f2_mul(h[e], r2));
+                    acc[v][e] = f2_add(acc[v][e], w);
+                    c2 = f2_fma(w, f2_add(g[e], one2), c2);
                 }
             }
         }
-        c = row_sum<G>(c, part[parity]) * inv_n;
+        float ca, cb;
+        f2_unpack(c2, ca, cb);
+        const float m = -(row_sum<G>(ca + cb, part[parity]) * inv_n);  // -mean(u * n)
+        const uint64_t m2 = f2_pack(m, m);
 #pragma unroll
         for (int v = 0; v < KB; ++v) {
             const bool has = live && cut[v].live();
             const int hi = live ? cut[v].hi : 0;
             const bool last = t % 32 == 31 || (G && t == G - 1) || cut[v].col + 8 >= a.N;
-            float d[8];
+            uint64_t d[4];
             if (has) {
-                float h[8], g[8], q[8];
-                O::unpack(yw[v], d);
-                O::unpack(hw[v], h);
-                O::unpack(gw[v], g);
-                O::unpack(ew[v], q);
+                uint64_t h[4], g[4], q[4];
+                octet_pairs<DT>(yw[v], d);
+                octet_pairs<DT>(hw[v], h);
+                octet_pairs<DT>(gw[v], g);
+                octet_pairs<DT>(ew[v], q);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    d[e] = fmaf(r, fmaf(-(h[e] * r), c, d[e] * (g[e] + a.one)), q[e]);
-                O::pack(d, yw[v]);
+                for (int e = 0; e < 4; ++e)
+                    d[e] = f2_fma(f2_fma(f2_mul(h[e], r2), m2, f2_mul(d[e], f2_add(g[e], one2))), r2, q[e]);
+                pairs_octet<DT>(d, yw[v]);
             }
             if (a.dres)
-                octet_put<DT, AL>(static_cast<char*>(a.dres) + (row * a.lddres + cut[v].col) * EB, yw[v], cut[v].lo, hi, same,
-                                  first, last);
+                octet_put<DT, AL>(static_cast<char*>(a.dres) + (row * a.lddres + cut[v].col) * EB, yw[v], cut[v].lo, hi,
+                                  on_word, first, last);
             if (a.dx) {
                 if (has && a.threshold) {
-                    uint64_t f[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) f[e] = f2_pack(d[2 * e], d[2 * e + 1]);
-                    dropout_octet<!AL>(drop, key, cut[v].col, static_cast<uint32_t>(row), f);
-                    pairs_octet<DT>(f, yw[v]);
+                    dropout_octet<!AL>(drop, key, cut[v].col, static_cast<uint32_t>(row), d);
+                    pairs_octet<DT>(d, yw[v]);
                 }
-                octet_put<DT, AL>(static_cast<char*>(a.dx) + (row * a.lddx + cut[v].col) * EB, yw[v], cut[v].lo, hi, same,
+                octet_put<DT, AL>(static_cast<char*>(a.dx) + (row * a.lddx + cut[v].col) * EB, yw[v], cut[v].lo, hi, on_word,
                                   first, last);
             }
         }
     }
     // this block's partial row
     float* out = a.ws + static_cast<int64_t>(blockIdx.x) * a.ldws;
+    float* mine = G ? sums + (threadIdx.x / G) * a.N : out;
+#pragma unroll
+    for (int v = 0; v < KB; ++v)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float x, y;
+            f2_unpack(acc[v][e], x, y);
+            if (2 * e >= cut[v].lo && 2 * e < cut[v].hi) mine[cut[v].col + 2 * e] = x;
+            if (2 * e + 1 >= cut[v].lo && 2 * e + 1 < cut[v].hi) mine[cut[v].col + 2 * e + 1] = y;
+        }
     if constexpr (G > 0) {
-#pragma unroll
-        for (int v = 0; v < KB; ++v)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e >= cut[v].lo && e < cut[v].hi) sums[(threadIdx.x / G) * a.N + cut[v].col + e] = acc[v][e];
         __syncthreads();
         for (int col = threadIdx.x; col < a.N; col += blockDim.x) {
             float s = sums[col];
             for (int k = 1; k < rows_block; ++k) s += sums[k * a.N + col];
             out[col] = s;
         }
-    } else {
-#pragma unroll
-        for (int v = 0; v < KB; ++v)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e >= cut[v].lo && e < cut[v].hi) out[cut[v].col + e] = acc[v][e];
     }
     griddep_launch_dependents();
 }
@@ -411,20 +413,20 @@ __global__ void __maxnreg__((RingRegisters<KB>::value)) add_bwd_ring(const AddAr
 // ---------------------------------------------------------------------------
 // dispatch
 // ---------------------------------------------------------------------------
-template <int DT, bool AL>
+template <int DT, int MODE>
 static const void* bwd_rows_for(int lanes, int octets) {
 #define RMSNORM_ADD_BWD(G, KB) \
-    if (lanes == G && octets == KB) return reinterpret_cast<const void*>(&add_bwd_rows<DT, AL, G, KB>);
+    if (lanes == G && octets == KB) return reinterpret_cast<const void*>(&add_bwd_rows<DT, MODE, G, KB>);
     RMSNORM_ADD_BWD(8, 1)
     RMSNORM_ADD_BWD(8, 2)
     RMSNORM_ADD_BWD(32, 1)
     RMSNORM_ADD_BWD(32, 2)
     RMSNORM_ADD_BWD(32, 4)
-    RMSNORM_ADD_BWD(0, 1)
     RMSNORM_ADD_BWD(0, 2)
-    RMSNORM_ADD_BWD(0, 3)
     RMSNORM_ADD_BWD(0, 4)
-    RMSNORM_ADD_BWD(0, 5)
+    if constexpr (MODE != kRowsAligned) {
+        RMSNORM_ADD_BWD(0, 5)
+    }
 #undef RMSNORM_ADD_BWD
     return nullptr;
 }
@@ -439,9 +441,15 @@ static const void* bwd_ring_for(int octets) {
 }
 template <int DT>
 static const void* bwd_dtype(const AddPlan& p) {
-    if (!p.ring) return p.aligned ? bwd_rows_for<DT, true>(p.lanes, p.octets) : bwd_rows_for<DT, false>(p.lanes, p.octets);
-    if (p.drop) return p.aligned ? bwd_ring_for<DT, true, true>(p.octets) : bwd_ring_for<DT, false, true>(p.octets);
-    return p.aligned ? bwd_ring_for<DT, true, false>(p.octets) : bwd_ring_for<DT, false, false>(p.octets);
+    if (!p.ring) {
+        switch (p.mode) {
+        case kRowsAligned: return bwd_rows_for<DT, kRowsAligned>(p.lanes, p.octets);
+        case kRowsOnePhase: return bwd_rows_for<DT, kRowsOnePhase>(p.lanes, p.octets);
+        default: return bwd_rows_for<DT, kRowsAny>(p.lanes, p.octets);
+        }
+    }
+    if (p.drop) return p.mode == kRowsAligned ? bwd_ring_for<DT, true, true>(p.octets) : bwd_ring_for<DT, false, true>(p.octets);
+    return p.mode == kRowsAligned ? bwd_ring_for<DT, true, false>(p.octets) : bwd_ring_for<DT, false, false>(p.octets);
 }
 
 const void* add_bwd_kernel(const AddPlan& p) {

@@ -56,8 +56,7 @@ struct AddArgs {
 // A launch shape. lanes: lanes per row (0: a block per row).
 struct AddPlan {
     int dtype = 0;
-    bool aligned = false;
-    int mode = 0;      // RowMode (forward)
+    int mode = kRowsAny;
     int lanes = 0;
     int octets = 1;  // per thread
     int threads = 0;

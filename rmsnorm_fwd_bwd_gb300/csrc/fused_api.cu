@@ -113,6 +113,22 @@ struct Operand {
     int64_t ld;
 };
 
+// Whether the rows of all operands start at one offset from a 16-byte boundary, row by
+// row.
+bool one_offset(size_t s, std::initializer_list<Operand> operands) {
+    const Operand* q = nullptr;
+    for (const Operand& o : operands) {
+        if (!o.p) continue;
+        if (q && (((reinterpret_cast<uintptr_t>(o.p) ^ reinterpret_cast<uintptr_t>(q->p)) & 15) != 0 ||
+                  (o.ld - q->ld) * static_cast<int64_t>(s) % 16 != 0))
+            return false;
+        q = &o;
+    }
+    return true;
+}
+
+RowMode row_mode(bool wide, bool one) { return wide ? kRowsAligned : one ? kRowsOnePhase : kRowsAny; }
+
 // Every row of every operand on a 16-byte boundary (8 for 1-byte elements), and
 // whole octets.
 bool wide_rows(int64_t N, size_t s, std::initializer_list<Operand> operands) {
@@ -140,10 +156,11 @@ rmsnorm_status check_rng(const AddArgs& a) {
 }
 
 // The ring's shape; false where it does not apply.
-bool ring_plan(int64_t M, int64_t N, int dtype, bool wide, bool drop, bool has_dh, int dev, int sms, AddPlan& p) {
+bool ring_plan(int64_t M, int64_t N, int dtype, RowMode mode, bool drop, bool has_dh, int dev, int sms, AddPlan& p) {
     if (N <= 1024 || M < kRingLeastRows) return false;
+    const bool wide = mode == kRowsAligned;
     p.dtype = dtype;
-    p.aligned = wide;
+    p.mode = mode;
     p.drop = drop;
     p.ring = true;
     const int64_t eb = elem_bytes(dtype);
@@ -160,7 +177,7 @@ bool ring_plan(int64_t M, int64_t N, int dtype, bool wide, bool drop, bool has_d
     if (by_registers < 1) return false;
     // three stages, and two blocks an SM; three blocks with dropout, whose numbers take
     // as many instructions as the rest (then of two stages, where three do not fit)
-    int bps = std::min(by_registers, drop ? 3 : 2);
+    int bps = std::min(by_registers, drop || !wide ? 3 : 2);
     int64_t stages = 3;
     while (stages > 2 && bps * (stages * (stage + 8) + fixed + 1024) > room) --stages;
     while (bps > 1 && bps * (stages * (stage + 8) + fixed + 1024) > room) --bps;
@@ -176,14 +193,15 @@ bool ring_plan(int64_t M, int64_t N, int dtype, bool wide, bool drop, bool has_d
 
 // Persistent grid of the backward and its partial rows. Rows off 16 bytes want a grid
 // that is a multiple of 8; blocks without a row write a row of zeros.
-bool add_bwd_plan(int64_t M, int64_t N, int dtype, bool wide, bool ring, bool drop, bool has_dh, AddPlan& p) {
+bool add_bwd_plan(int64_t M, int64_t N, int dtype, RowMode mode, bool drop, bool has_dh, AddPlan& p) {
     int dev = 0;
     const int sms = current_sms(dev);
     if (!sms) return false;
-    if (ring && ring_plan(M, N, dtype, wide, drop, has_dh, dev, sms, p)) return true;
+    if (mode != kRowsAny && ring_plan(M, N, dtype, mode, drop, has_dh, dev, sms, p)) return true;
     p = AddPlan();
+    const bool wide = mode == kRowsAligned;
     p.dtype = dtype;
-    p.aligned = wide;
+    p.mode = mode;
     if (!row_shape(octets_of(N, dtype, wide), 8, {2, 4}, p)) return false;
     p.smem = p.lanes ? static_cast<size_t>(rows_per_block(p)) * N * 4 : 0;
     const void* k = add_bwd_kernel(p);
@@ -192,12 +210,6 @@ bool add_bwd_plan(int64_t M, int64_t N, int dtype, bool wide, bool ring, bool dr
     const int64_t most = static_cast<int64_t>(std::min(fit, 8)) * sms, need = ceil_div(M, rows_per_block(p));
     p.blocks = wide ? std::min(most, need) : std::min(most / 8 * 8, round_up(need, 8));
     return true;
-}
-
-// Whether the rows of two outputs start at one offset from a 16-byte boundary each.
-bool same_offset(const void* p, int64_t ldp, const void* q, int64_t ldq, size_t s) {
-    return !p || !q ||
-           (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15) == 0 && (ldp - ldq) * static_cast<int64_t>(s) % 16 == 0);
 }
 
 rmsnorm_status run(const void* k, const AddPlan& p, AddArgs& a, rmsnorm_stream_t stream) {
@@ -340,14 +352,11 @@ extern "C" rmsnorm_status rmsnorm_add_fwd(const void* x, int64_t ldx, const void
     a.eps = eps;
     a.one = static_cast<float>(offset);
     const bool wide = wide_rows(N, s, {{x, ldx}, {residual, ldres}, {gamma, 0}, {h, ldh}, {y, ldy}});
-    a.same_phase = same_offset(h, ldh, y, ldy, s);
+    a.same_phase = one_offset(s, {{h, ldh}, {y, ldy}});
     AddPlan p;
     p.dtype = dtype;
-    p.aligned = wide;
     p.drop = a.threshold != 0;
-    p.mode = wide ? kRowsAligned : same_offset(x, ldx, y, ldy, s) && same_offset(residual, ldres, y, ldy, s) && a.same_phase
-                 ? kRowsOnePhase
-                 : kRowsAny;
+    p.mode = row_mode(wide, one_offset(s, {{x, ldx}, {residual, ldres}, {h, ldh}, {y, ldy}}));
     if (!row_shape(octets_of(N, dtype, wide), 8, {4, 2, 3}, p)) return RMSNORM_ERR_UNSUPPORTED;
     p.blocks = ceil_div(M, rows_per_block(p));
     return run(add_fwd_kernel(p), p, a, stream);
@@ -356,13 +365,12 @@ extern "C" rmsnorm_status rmsnorm_add_fwd(const void* x, int64_t ldx, const void
 extern "C" size_t rmsnorm_add_bwd_workspace_size(int64_t M, int64_t N, rmsnorm_dtype dtype) {
     if (check_common(M, N, dtype, 0) != RMSNORM_OK || M == 0) return 0;
     int64_t units = 0;
-    for (const bool wide : {false, true})
-        for (const bool ring : {false, true})
-            for (const bool drop : {false, true})
-                for (const bool has_dh : {false, true}) {
-                    AddPlan p;
-                    if (add_bwd_plan(M, N, dtype, wide, ring, drop, has_dh, p)) units = std::max(units, p.blocks);
-                }
+    for (const RowMode mode : {kRowsAny, kRowsAligned, kRowsOnePhase})
+        for (const bool drop : {false, true})
+            for (const bool has_dh : {false, true}) {
+                AddPlan p;
+                if (add_bwd_plan(M, N, dtype, mode, drop, has_dh, p)) units = std::max(units, p.blocks);
+            }
     (void)cudaGetLastError();
     return static_cast<size_t>(units) * static_cast<size_t>(workspace_pitch(N)) * sizeof(float);
 }
@@ -394,9 +402,9 @@ extern "C" rmsnorm_status rmsnorm_add_bwd(const void* dy, int64_t lddy, const vo
     if ((st = check_rng(a)) != RMSNORM_OK) return st;
     AddPlan p;
     const bool wide = wide_rows(N, s, {{dy, lddy}, {dh, lddh}, {h, ldh}, {gamma, 0}, {dx, lddx}, {dresidual, lddres}});
-    const bool one_offset = same_offset(dy, lddy, h, ldh, s) && same_offset(dy, lddy, dh, lddh, s) &&
-                            same_offset(dy, lddy, dx, lddx, s) && same_offset(dy, lddy, dresidual, lddres, s);
-    if (!add_bwd_plan(M, N, dtype, wide, wide || one_offset, a.threshold != 0, dh != nullptr, p)) {
+    const RowMode mode =
+        row_mode(wide, one_offset(s, {{dy, lddy}, {dh, lddh}, {h, ldh}, {dx, lddx}, {dresidual, lddres}}));
+    if (!add_bwd_plan(M, N, dtype, mode, a.threshold != 0, dh != nullptr, p)) {
         (void)cudaGetLastError();
         return RMSNORM_ERR_CUDA;
     }
@@ -419,7 +427,7 @@ extern "C" rmsnorm_status rmsnorm_add_bwd(const void* dy, int64_t lddy, const vo
     a.M = M;
     a.N = static_cast<int>(N);
     a.one = static_cast<float>(offset);
-    a.same_phase = same_offset(dx, lddx, dresidual, lddres, s);
+    a.same_phase = one_offset(s, {{dx, lddx}, {dresidual, lddres}});
     if ((st = run(add_bwd_kernel(p), p, a, stream)) != RMSNORM_OK) return st;
     return launch_dgamma_reduce(dtype, a.ws, p.blocks, a.N, a.ldws, dgamma, cs) == cudaSuccess ? RMSNORM_OK
                                                                                               : RMSNORM_ERR_CUDA;
@@ -465,8 +473,9 @@ extern "C" rmsnorm_status rmsnorm_quant_fwd(const void* x, int64_t ldx, const vo
                       wide_rows(N, 1, {{codes, ldcodes}});
     AddPlan p;
     p.dtype = dtype;
-    p.aligned = wide;
-    if (!row_shape(ceil_div(N, 8), 32, {4, 2}, p)) return RMSNORM_ERR_UNSUPPORTED;
+    // groups of columns want octets that start at column 0
+    p.mode = row_mode(wide, group == 0 && one_offset(s, {{x, ldx}, {residual, ldres}, {h, ldh}}));
+    if (!row_shape(p.mode == kRowsOnePhase ? octets_of(N, dtype, false) : ceil_div(N, 8), 32, {4, 2}, p)) return RMSNORM_ERR_UNSUPPORTED;
     p.blocks = ceil_div(M, rows_per_block(p));
     return run(quant_kernel(p), p, a, stream);
 }

@@ -147,15 +147,16 @@ __device__ __forceinline__ void store_chunk(char* p, const uint32_t* w) {
     else *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Store an octet of W words at `p`, of which the first `bytes` are the row's (0 for
-// a lane without one). ALIGNED: p is a multiple of the vector store and bytes is
-// 4 * W or 0. Otherwise all 32 lanes call it together: consecutive lanes hold
+// Store an octet of W words at `p`, of which the bytes up to `bytes` are the row's (0 for
+// a lane without one). `skip`: the bytes before the row's start in the octet, or, for a
+// lane that is not `first`, in the octet before. ALIGNED: p is a multiple of the vector
+// store, bytes is 4 * W or 0 and skip 0. Otherwise all 32 lanes call it together: consecutive lanes hold
 // consecutive octets of a row; `first` marks a lane whose predecessor does not,
 // `last` one whose successor does not (another row, another warp, the row's end).
 // Each lane then stores the aligned words that end in its octet, the bytes before
 // its octet coming from the lane before.
 template <int ELEM, int W, bool ALIGNED>
-__device__ __forceinline__ void octet_store(char* p, const uint32_t (&w)[W], int bytes, bool first, bool last) {
+__device__ __forceinline__ void octet_store(char* p, const uint32_t (&w)[W], int bytes, bool first, bool last, int skip = 0) {
     constexpr int AW = W == 2 ? 2 : 4;  // words of a vector store
     constexpr int A = 4 * AW;
     if constexpr (ALIGNED) {
@@ -190,7 +191,7 @@ __device__ __forceinline__ void octet_store(char* p, const uint32_t (&w)[W], int
         const uint32_t bits = 8u * (static_cast<uint32_t>(d) & 3u);
 #pragma unroll
         for (int i = 0; i < W + AW; ++i) s[i] = __funnelshift_r(s[i], s[i + 1], bits);
-        const int from = first ? sh : 0;
+        const int from = first ? sh + skip : (sh + skip > 4 * W ? sh + skip - 4 * W : 0);
         const int to = last ? sh + bytes : 4 * W;
         char* base = p - sh;
 #pragma unroll
@@ -353,11 +354,15 @@ __device__ __forceinline__ void dropout_octet(const Dropout& d, const PhiloxKey&
 // the whole block: one barrier, `part` (32 floats) not reused before the next one.
 // Every thread of the row gets the same bits.
 // ---------------------------------------------------------------------------
-// The largest of the 32 lanes' values. By shuffles: behind a branch that not all lanes
-// take, __reduce_max_sync was seen to be run by the two sides apart (nvcc 13.0).
-__device__ __forceinline__ uint32_t warp_allmax(uint32_t v) {
+// The largest of the 32 lanes' non-negative values, a NaN before any number. By shuffles:
+// behind a branch that not all lanes take, __reduce_max_sync was seen to be run by the
+// two sides apart (nvcc 13.0).
+__device__ __forceinline__ float warp_allmax(float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = 16; o > 0; o >>= 1) {
+        const float w = __shfl_xor_sync(0xffffffffu, v, o);
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(w));
+    }
     return v;
 }
 

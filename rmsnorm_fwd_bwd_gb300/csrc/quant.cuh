@@ -15,50 +15,67 @@ __device__ __forceinline__ uint32_t e4m3_pair(uint64_t y, float inv) {
     return v;
 }
 
-// |y| as an integer: ordered as the value, with NaN above infinity.
-__device__ __forceinline__ uint32_t magnitude(float y) { return __float_as_uint(y) & 0x7fffffffu; }
+// The larger of a and |b|; a NaN of either stays (fmaxf drops it).
+__device__ __forceinline__ float max_magnitude(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(fabsf(b)));
+    return m;
+}
 
-// The largest magnitude of elements [0, valid) of an octet.
-__device__ __forceinline__ uint32_t octet_amax(const uint64_t (&y)[4], int valid) {
-    uint32_t m = 0u;
+// The largest magnitude of elements [lo, hi) of an octet.
+template <bool ALIGNED>
+__device__ __forceinline__ float octet_amax(const uint64_t (&z)[4], int lo, int hi) {
+    float m = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float a, b;
-        f2_unpack(y[i], a, b);
-        m = max(m, 2 * i < valid ? magnitude(a) : 0u);
-        m = max(m, 2 * i + 1 < valid ? magnitude(b) : 0u);
+        f2_unpack(z[i], a, b);
+        m = max_magnitude(m, ALIGNED || (2 * i >= lo && 2 * i < hi) ? a : 0.f);
+        m = max_magnitude(m, ALIGNED || (2 * i + 1 >= lo && 2 * i + 1 < hi) ? b : 0.f);
     }
     return m;
 }
 
-__device__ __forceinline__ float quant_scale(uint32_t amax, int pow2) {
-    float s = __uint_as_float(amax) * (1.0f / 448.0f);
-    if (s < 1.17549435e-38f) s = 1.17549435e-38f;  // 2^-126; a NaN stays
+// The scale of a group whose largest |z| is amax, with y = z * r; and the factors by which
+// z becomes codes, in this order: 1 and r / scale, the r of y and of the scale having
+// cancelled, or, at the least scale, where that may overflow, r and 1 / scale.
+__device__ __forceinline__ float quant_scale(float amax, float r, int pow2, float& f0, float& f1) {
+    float s = amax * r * (1.0f / 448.0f);
+    const bool least = s < 1.17549435e-38f;  // 2^-126; a NaN stays
+    if (least) s = 1.17549435e-38f;
     if (pow2) {
         // up to the next power of two: a carry out of the fraction raises the exponent
         // (infinity and NaN stay)
         const uint32_t b = __float_as_uint(s);
         if (b < 0x7f800000u) s = __uint_as_float((b + 0x007fffffu) & 0x7f800000u);
     }
-    return s;
-}
-
-// Codes of octet `o` of a row (`valid` elements of y), and its group's scale from the
-// group's largest magnitude, by the group's first octet. Unless ALIGNED every lane of a
-// warp calls it (octet_store).
-template <bool ALIGNED>
-__device__ __forceinline__ void quant_store(const AddArgs& a, int64_t row, int o, int valid, const uint64_t (&y)[4],
-                                            uint32_t amax, bool first, bool last) {
-    const float s = quant_scale(amax, a.pow2);
     // the scale is a normal number and its inverse too: off by at most 1 unit in the last place
     float inv;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    f0 = least ? r : 1.f;
+    f1 = least ? inv : r * inv;
+    return s;
+}
+
+// Codes of octet `o` of a row, and its group's scale from the group's largest |z|, by
+// the group's first octet (groups of columns want octets that start at column 0). Unless ALIGNED every lane of a
+// warp calls it (octet_store).
+template <bool ALIGNED>
+__device__ __forceinline__ void quant_store(const AddArgs& a, int64_t row, int o, const Cut& cut, uint64_t (&z)[4], float amax,
+                                            float r, bool first, bool last) {
+    float f0, f1;
+    const float s = quant_scale(amax, r, a.pow2, f0, f1);
+    if (f0 != 1.f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = f2_mul(z[i], f2_pack(f0, f0));
+    }
     uint32_t code[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) code[i] = e4m3_pair(y[2 * i], inv) | e4m3_pair(y[2 * i + 1], inv) << 16;
-    if (!ALIGNED || valid > 0)
-        octet_store<1, 2, ALIGNED>(static_cast<char*>(a.y) + row * a.ldy + o * 8, code, valid, first, last);
-    if (valid > 0) {
+    for (int i = 0; i < 2; ++i) code[i] = e4m3_pair(z[2 * i], f1) | e4m3_pair(z[2 * i + 1], f1) << 16;
+    if (!ALIGNED || cut.live())
+        octet_store<1, 2, ALIGNED>(static_cast<char*>(a.y) + row * a.ldy + cut.col, code, cut.hi, first, last,
+                                   first ? cut.lo : (cut.col < 8 ? 8 - cut.col : 0));
+    if (cut.live()) {
         float* sr = a.scales + row * a.ldscales;
         if (a.group == 0) {
             if (o == 0) sr[0] = s;

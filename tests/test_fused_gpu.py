@@ -131,6 +131,19 @@ def test_add_fwd_dropout(M, N, layout, p, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N,p", [(4500, 1027, 0.0), (4099, 1035, 0.3), (4100, 2051, 0.0)])
+def test_add_fwd_many_odd_rows(M, N, p, dtype):
+    # blocks of several rows, the last ones without a full share
+    x, res, w = randn(M, N, dtype=dtype, seed=91), randn(M, N, dtype=dtype, seed=92), weight(N, dtype, True)
+    y, h, r, _ = run_add_fwd(x, res, w, dtype, offset=True, p=p, rng=state(3, 9))
+    check_add_fwd(x, res, w, dtype, y, h, r, offset=True, p=p, seed=3, ctr=9)
+    xr, rr = Rows(M, N, x.dtype, data=x), Rows(M, N, x.dtype, data=res)
+    wt = w.cuda()
+    assert B.rmsnorm_add_fwd(xr, N, rr, N, wt, rr, N, xr, N, None, M, N, EPS, dtype, 1, p, state(3, 9)) == 0
+    assert torch.equal(rr.get(), h) and torch.equal(xr.get(), y)      # in place: the same bits
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_add_fwd_without_residual_or_h(dtype):
     for N in (72, 4096, 4099):
         x, w = randn(5, N, dtype=dtype, seed=7), weight(N, dtype, False)
