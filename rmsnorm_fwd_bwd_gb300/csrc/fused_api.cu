@@ -91,11 +91,11 @@ bool block_shape(int64_t n, std::initializer_list<int> choices, AddPlan& p) {
     return best > 0;
 }
 
-// Lanes per row and octets per thread for rows of n octets: up to 128 by groups of
-// lanes of a 4-warp block (the 8-bit output wants a warp, whose neighbouring lanes
+// Lanes per row and octets per thread for rows of n octets: up to 128 (64 off 16 bytes,
+// where a row's ends cost a warp more) by groups of lanes of a 4-warp block (the 8-bit output wants a warp, whose neighbouring lanes
 // hold a group of columns), wider rows by a block of at most kFusedMaxThreads.
 bool row_shape(int64_t n, int least_lanes, std::initializer_list<int> choices, AddPlan& p) {
-    if (n <= 128) {
+    if (n <= (p.mode == kRowsOnePhase ? 64 : 128)) {
         p.lanes = n <= 16 ? least_lanes : 32;
         p.octets = 1;
         while (static_cast<int64_t>(p.lanes) * p.octets < n) p.octets *= 2;
@@ -157,7 +157,7 @@ rmsnorm_status check_rng(const AddArgs& a) {
 
 // The ring's shape; false where it does not apply.
 bool ring_plan(int64_t M, int64_t N, int dtype, RowMode mode, bool drop, bool has_dh, int dev, int sms, AddPlan& p) {
-    if (N <= 1024 || M < kRingLeastRows) return false;
+    if (N <= (mode == kRowsAligned ? 1024 : 256) || M < kRingLeastRows) return false;
     const bool wide = mode == kRowsAligned;
     p.dtype = dtype;
     p.mode = mode;
@@ -175,9 +175,10 @@ bool ring_plan(int64_t M, int64_t N, int dtype, RowMode mode, bool drop, bool ha
     const void* k = add_bwd_kernel(p);
     const int by_registers = k ? resident_blocks(k, dev, p.threads, 1024) : 0;
     if (by_registers < 1) return false;
-    // three stages, and two blocks an SM; three blocks with dropout, whose numbers take
-    // as many instructions as the rest (then of two stages, where three do not fit)
-    int bps = std::min(by_registers, drop || !wide ? 3 : 2);
+    // three stages, and blocks of 512 threads an SM together; of 768 with dropout, whose
+    // numbers take as many instructions as the rest, and for rows off 16 bytes (then of two
+    // stages, where three do not fit)
+    int bps = std::min(by_registers, static_cast<int>(ceil_div(drop || !wide ? 768 : 512, p.threads)));
     int64_t stages = 3;
     while (stages > 2 && bps * (stages * (stage + 8) + fixed + 1024) > room) --stages;
     while (bps > 1 && bps * (stages * (stage + 8) + fixed + 1024) > room) --bps;
