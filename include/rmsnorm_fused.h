@@ -16,7 +16,8 @@
  *
  * In place: every row is read before it is written, so an output may be an input
  * of the same shape, dtype, pointer and pitch (h on residual, y on x, dresidual on
- * dy or dh, rotated heads on the heads). No other overlap is allowed.
+ * dy or dh, rotated heads on the heads). No other overlap is allowed; two outputs at
+ * one address whose values differ are refused.
  */
 #ifndef RMSNORM_FUSED_H
 #define RMSNORM_FUSED_H

@@ -332,6 +332,7 @@ extern "C" rmsnorm_status rmsnorm_add_fwd(const void* x, int64_t ldx, const void
     if (!check_dropout(dropout_p, rng, a, st)) return st;
     if (M == 0) return RMSNORM_OK;
     if (!x || !gamma || !y) return RMSNORM_ERR_NULL;
+    if (h == y) return RMSNORM_ERR_ARG;
     if (!aligned(x, s) || !aligned(residual, s) || !aligned(gamma, s) || !aligned(h, s) || !aligned(y, s) ||
         !aligned(rstd, 4))
         return RMSNORM_ERR_ALIGN;
@@ -401,6 +402,7 @@ extern "C" rmsnorm_status rmsnorm_add_bwd(const void* dy, int64_t lddy, const vo
         !aligned(dresidual, s) || !aligned(rstd, 4) || !aligned(workspace, 16))
         return RMSNORM_ERR_ALIGN;
     if ((st = check_rng(a)) != RMSNORM_OK) return st;
+    if (a.threshold && dx && dx == dresidual) return RMSNORM_ERR_ARG;
     AddPlan p;
     const bool wide = wide_rows(N, s, {{dy, lddy}, {dh, lddh}, {h, ldh}, {gamma, 0}, {dx, lddx}, {dresidual, lddres}});
     const RowMode mode =

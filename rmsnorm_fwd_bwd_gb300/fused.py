@@ -214,8 +214,7 @@ def rms_norm_add(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torc
 def _add_in_place(x, residual, weight, eps, offset):
     with _on(x):
         M, N = _rows(x)
-        ldx = x.stride(0) if x.dim() == 2 and M > 0 else N
-        ldr = residual.stride(0) if x.dim() == 2 and M > 0 else N
+        ldx, ldr = (t.stride(0) if t.dim() == 2 and M > 1 else N for t in (x, residual))
         _done(binding.rmsnorm_add_fwd(x, ldx, residual, ldr, weight.contiguous(), residual, ldr, x, ldx, None, M, N, eps,
                                       x.dtype, int(offset)), "rmsnorm_add_fwd", "add_forward")
 

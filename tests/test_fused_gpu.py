@@ -265,6 +265,53 @@ def test_add_bwd_dropout(M, N, layout, p, dtype):
     assert torch.all(dx[~keep] == 0)
 
 
+RING = [(1100, 1032), (1500, 2048), (1030, 4099), (1040, 5120), (1100, 8192), (1025, 8193), (1030, 12288), (1027, 301),
+        (1500, 1001), (1029, 16384), (1024, 16381)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N", RING)
+@pytest.mark.parametrize("p", [0.0, 0.3])
+def test_add_bwd_many_rows(M, N, p, dtype):
+    # enough rows for the ring of staged rows, where one fits; few blocks have equally many
+    a = add_bwd_inputs(M, N, dtype, True)
+    keep = ref.kept(17, 3, M, N, p) if p else None
+    dres, dx, dw = run_add_bwd(*a, dtype, offset=True, p=p, rng=state(17, 3))
+    check_add_bwd(*a, dtype, dres, dx, dw, offset=True, keep=keep, p=p)
+    again = run_add_bwd(*a, dtype, offset=True, p=p, rng=state(17, 3), ws_fill=0)
+    assert all(torch.equal(u, v) for u, v in zip((dres, dx, dw), again))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("layout", ["shifted", "mixed", "wide pitch"])
+def test_add_bwd_many_rows_layouts(layout, dtype):
+    for M, N, p in ((1100, 1032, 0.0), (1030, 2051, 0.3), (1030, 4096, 0.0)):
+        a = add_bwd_inputs(M, N, dtype, False)
+        keep = ref.kept(17, 3, M, N, p) if p else None
+        dres, dx, dw = run_add_bwd(*a, dtype, p=p, rng=state(17, 3), layout=layout)
+        check_add_bwd(*a, dtype, dres, dx, dw, keep=keep, p=p)
+
+
+@pytest.mark.parametrize("M,N", [(1030, 4096), (1031, 1001)])
+def test_add_bwd_many_rows_optional_tensors_and_in_place(M, N):
+    dy, dh, h, r, w = add_bwd_inputs(M, N, "bfloat16", False)
+    none = run_add_bwd(dy, None, h, r, w, "bfloat16")
+    check_add_bwd(dy, None, h, r, w, "bfloat16", *none)
+    full = run_add_bwd(dy, dh, h, r, w, "bfloat16")
+    for want in (("dres",), ("dx",), ()):
+        got = run_add_bwd(dy, dh, h, r, w, "bfloat16", want=want)
+        assert all(v is None or torch.equal(u, v) for u, v in zip(full, got))
+    wt, rt = w.cuda(), r.cuda()
+    need = B.rmsnorm_add_bwd_workspace_size(M, N, "bfloat16")
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    for k in (0, 1):
+        t = [Rows(M, N, dy.dtype, data=v) for v in (dy, dh, h)]
+        dw = torch.empty(N, dtype=dy.dtype, device="cuda")
+        assert B.rmsnorm_add_bwd(t[0], N, t[1], N, t[2], N, wt, rt, None, 0, t[k], N, dw, M, N, "bfloat16", 0, 0.0, None, ws,
+                                 need) == 0
+        assert torch.equal(t[k].get(), full[0]) and torch.equal(dw.cpu(), full[2])
+
+
 @pytest.mark.parametrize("N", [40, 4096, 4099])
 def test_add_bwd_optional_tensors(N):
     for dtype in DTYPES:
@@ -717,6 +764,31 @@ def test_captured_forward_and_backward_draw_new_numbers(M, N):
         torch.cuda.synchronize()
         check_add_fwd(x, res, w, dtype, y.cpu(), h.cpu(), rstd.cpu(), p=p, seed=5, ctr=k)
         check_add_bwd(dy, dh, h.cpu(), rstd.cpu(), w, dtype, dres.cpu(), dx.cpu(), dw.cpu(), keep=ref.kept(5, k, M, N, p), p=p)
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Calls that may overlap, each with a workspace of its own, and other kernels between them."""
+    M, N = 2000, 4096
+    a = add_bwd_inputs(M, N, "bfloat16", False)
+    want = run_add_bwd(*a, "bfloat16", p=0.1, rng=state(1, 2))
+    t = [v.cuda() for v in a]
+    need = B.rmsnorm_add_bwd_workspace_size(M, N, "bfloat16")
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    rng = state(1, 2)
+    torch.cuda.synchronize()
+    for s in streams:
+        with torch.cuda.stream(s):
+            o = [torch.empty_like(t[0]), torch.empty_like(t[0]), torch.empty(N, dtype=torch.bfloat16, device="cuda"),
+                 torch.empty(need, dtype=torch.uint8, device="cuda")]
+            for _ in range(5):
+                o[3].fill_(255)
+                assert B.rmsnorm_add_bwd(t[0], N, t[1], N, t[2], N, t[4], t[3], o[1], N, o[0], N, o[2], M, N, "bfloat16", 0, 0.1,
+                                         rng, o[3], need) == 0
+            outs.append(o)
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o[0].cpu(), want[0]) and torch.equal(o[1].cpu(), want[1]) and torch.equal(o[2].cpu(), want[2])
 
 
 def test_rows_beyond_32_bit_offsets():

@@ -32,7 +32,7 @@ def add_fwd(**kw):
     (ARG, dict(dropout_p=float("nan"))), (OK, dict(M=0, x=None, y=None)), (NULL, dict(x=None)), (NULL, dict(gamma=None)),
     (NULL, dict(y=None)), (ALIGN, dict(x=0x1001)), (ALIGN, dict(residual=0x2001)), (ALIGN, dict(h=0x4001)),
     (ALIGN, dict(rstd=0x6002)), (NULL, dict(dropout_p=0.5)), (ALIGN, dict(dropout_p=0.5, rng=0x7004)),
-    (ALIGN, dict(dropout_p=0.5, rng=0x7000, rng_used=0x7014)),
+    (ALIGN, dict(dropout_p=0.5, rng=0x7000, rng_used=0x7014)), (ARG, dict(h=0x5000)),
 ])
 def test_add_fwd_refusals(want, kw):
     assert add_fwd(**kw) == want
@@ -51,7 +51,7 @@ def add_bwd(**kw):
     (SHAPE, dict(ldh=7)), (SHAPE, dict(lddx=7)), (SHAPE, dict(lddres=7)), (ARG, dict(dropout_p=2.0)),
     (NULL, dict(dgamma=None)), (ALIGN, dict(dgamma=0x8001)), (NULL, dict(dy=None)), (NULL, dict(h=None)),
     (NULL, dict(gamma=None)), (NULL, dict(rstd=None)), (NULL, dict(workspace=None)), (ALIGN, dict(workspace=0x9008)),
-    (ALIGN, dict(dx=0x6001)), (NULL, dict(dropout_p=0.5)),
+    (ALIGN, dict(dx=0x6001)), (NULL, dict(dropout_p=0.5)), (ARG, dict(dropout_p=0.5, rng=0x100, dx=0x7000)),
 ])
 def test_add_bwd_refusals(want, kw):
     assert add_bwd(**kw) == want
