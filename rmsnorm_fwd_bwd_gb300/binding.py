@@ -51,6 +51,8 @@ class RMSNormError(RuntimeError):
 
 def _load():
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -113,13 +115,12 @@ def header_functions() -> list:
 
 
 def _addr(p):
-    if p is None:
-        return None
-    if isinstance(p, int):
+    if p is None or isinstance(p, int):
         return p
-    if hasattr(p, "data_ptr"):
+    try:
         return p.data_ptr()
-    raise TypeError(f"cannot take the address of {type(p)}")
+    except AttributeError:
+        raise TypeError(f"cannot take the address of {type(p)}") from None
 
 
 def _dtype_code(dt) -> int:

@@ -46,6 +46,7 @@ struct AddArgs {
     uint32_t threshold;             // dropout: 0 for none
     float scale;
     int group;                      // quant: columns per scale, 0 for the row
+    int group_shift;                // log2 of a group's octets
     int pow2;                       // quant: scales rounded up to a power of two
     int stages;                     // ring: rows staged
     uint32_t slot;                  // bytes of a row's place in a stage

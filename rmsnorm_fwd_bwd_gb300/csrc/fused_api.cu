@@ -471,6 +471,7 @@ extern "C" rmsnorm_status rmsnorm_quant_fwd(const void* x, int64_t ldx, const vo
     a.eps = eps;
     a.one = static_cast<float>(offset);
     a.group = group;
+    a.group_shift = group == 128 ? 4 : group == 64 ? 3 : 2;
     a.pow2 = pow2;
     const bool wide = wide_rows(N, s, {{x, ldx}, {residual, ldres}, {gamma, 0}, {h, ldh}}) &&
                       wide_rows(N, 1, {{codes, ldcodes}});

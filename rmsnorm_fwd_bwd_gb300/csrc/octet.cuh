@@ -258,6 +258,15 @@ struct Cut {
     __device__ __forceinline__ bool live() const { return hi > 0; }
 };
 
+// Aligned rows: octets are whole or missing.
+__device__ __forceinline__ Cut whole_cut(int o, int N) {
+    Cut c;
+    c.col = 8 * o;
+    c.lo = 0;
+    c.hi = c.col < N ? 8 : 0;
+    return c;
+}
+
 // The elements that p starts after a 16-byte boundary.
 template <int DT> __device__ __forceinline__ int word_phase(const void* p) {
     return static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / Elem<DT>::kBytes);

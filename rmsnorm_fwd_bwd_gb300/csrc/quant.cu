@@ -43,10 +43,12 @@ __global__ void __launch_bounds__(G ? kFusedGroupThreads : kFusedMaxThreads) qua
     Cut cut[KB];
 #pragma unroll
     for (int v = 0; v < KB; ++v) {
-        cut[v] = Cut(v * per_row + t, phase, a.N);
-        if (!live) cut[v].hi = 0;
+        cut[v] = AL ? whole_cut(v * per_row + t, live ? a.N : 0) : Cut(v * per_row + t, phase, a.N);
+        if (!AL && !live) cut[v].hi = 0;
+        if constexpr (!AL) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) xw[v][i] = 0u;
+            for (int i = 0; i < W; ++i) xw[v][i] = 0u;
+        }
         if (cut[v].live()) row_load<DT, MODE>(xr + cut[v].col * EB, cut[v].lo, cut[v].hi, xw[v]);
     }
     if (a.res) {
@@ -65,8 +67,10 @@ __global__ void __launch_bounds__(G ? kFusedGroupThreads : kFusedMaxThreads) qua
 #pragma unroll
     for (int v = 0; v < KB; ++v) {
         m[v] = 0.f;
+        if constexpr (!AL) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[v][e] = 0ull;
+            for (int e = 0; e < 4; ++e) z[v][e] = 0ull;
+        }
         if (cut[v].live()) {
             uint64_t g[4];
             octet_pairs<DT>(xw[v], z[v]);
@@ -86,7 +90,7 @@ __global__ void __launch_bounds__(G ? kFusedGroupThreads : kFusedMaxThreads) qua
             }
             m[v] = octet_amax<AL>(z[v], cut[v].lo, cut[v].hi);
         }
-        if (a.h)
+        if (a.h && (!AL || cut[v].live()))
             octet_put<DT, AL>(hr + cut[v].col * EB, xw[v], cut[v].lo, cut[v].hi, MODE == kRowsOnePhase, lane == 0,
                               lane == 31 || cut[v].col + 8 >= a.N);
     }
@@ -99,7 +103,7 @@ __global__ void __launch_bounds__(G ? kFusedGroupThreads : kFusedMaxThreads) qua
 #pragma unroll
         for (int v = 0; v < KB; ++v) m[v] = all;
     } else {
-        for (int o = 1; o < a.group / 8; o <<= 1) {
+        for (int o = 1; o < 1 << a.group_shift; o <<= 1) {
 #pragma unroll
             for (int v = 0; v < KB; ++v) m[v] = max_magnitude(m[v], __shfl_xor_sync(0xffffffffu, m[v], o));
         }

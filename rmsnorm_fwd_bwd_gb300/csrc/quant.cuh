@@ -63,6 +63,7 @@ __device__ __forceinline__ float quant_scale(float amax, float r, int pow2, floa
 template <bool ALIGNED>
 __device__ __forceinline__ void quant_store(const AddArgs& a, int64_t row, int o, const Cut& cut, uint64_t (&z)[4], float amax,
                                             float r, bool first, bool last) {
+    if (ALIGNED && !cut.live()) return;
     float f0, f1;
     const float s = quant_scale(amax, r, a.pow2, f0, f1);
     if (f0 != 1.f) {
@@ -72,15 +73,14 @@ __device__ __forceinline__ void quant_store(const AddArgs& a, int64_t row, int o
     uint32_t code[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) code[i] = e4m3_pair(z[2 * i], f1) | e4m3_pair(z[2 * i + 1], f1) << 16;
-    if (!ALIGNED || cut.live())
-        octet_store<1, 2, ALIGNED>(static_cast<char*>(a.y) + row * a.ldy + cut.col, code, cut.hi, first, last,
-                                   first ? cut.lo : (cut.col < 8 ? 8 - cut.col : 0));
+    octet_store<1, 2, ALIGNED>(static_cast<char*>(a.y) + row * a.ldy + cut.col, code, cut.hi, first, last,
+                               first ? cut.lo : (cut.col < 8 ? 8 - cut.col : 0));
     if (cut.live()) {
         float* sr = a.scales + row * a.ldscales;
         if (a.group == 0) {
             if (o == 0) sr[0] = s;
-        } else if (o % (a.group / 8) == 0) {
-            sr[o / (a.group / 8)] = s;
+        } else if ((o & ((1 << a.group_shift) - 1)) == 0) {
+            sr[o >> a.group_shift] = s;
         }
     }
 }
