@@ -21,14 +21,14 @@ namespace rmsnorm {
 // rows and ends: the hardware balances the rows over the SMs, and a row's loads are
 // all in flight at once.
 template <int DT, int MODE, int G, int KB, bool DROP>
-__global__ void __launch_bounds__(G ? kFusedGroupThreads : kFusedMaxThreads) add_fwd_rows(const AddArgs a) {
+__global__ void __launch_bounds__(G > 0 ? kFusedGroupThreads : G < 0 ? kFusedWideThreads : kFusedMaxThreads) add_fwd_rows(const AddArgs a) {
     constexpr bool AL = MODE == kRowsAligned;
     constexpr int W = Oct<DT>::kWords;
     constexpr int EB = Elem<DT>::kBytes;
     __shared__ float part[32];
-    const int per_row = G ? G : blockDim.x;
-    const int t = G ? threadIdx.x % G : threadIdx.x;
-    const int64_t row = G ? static_cast<int64_t>(blockIdx.x) * (blockDim.x / G) + threadIdx.x / G : blockIdx.x;
+    const int per_row = G > 0 ? G : blockDim.x;
+    const int t = G > 0 ? threadIdx.x % G : threadIdx.x;
+    const int64_t row = G > 0 ? static_cast<int64_t>(blockIdx.x) * (blockDim.x / G) + threadIdx.x / G : blockIdx.x;
     griddep_wait();
     const bool live = row < a.M;
     const char* xr = static_cast<const char*>(a.x) + row * a.ldx * EB;
@@ -89,8 +89,8 @@ __global__ void __launch_bounds__(G ? kFusedGroupThreads : kFusedMaxThreads) add
     if (a.h) {
 #pragma unroll
         for (int v = 0; v < KB; ++v)
-            octet_put<DT, AL>(hr + cut[v].col * EB, xw[v], cut[v].lo, cut[v].hi, on_word, G ? t == 0 : t % 32 == 0,
-                              t % 32 == 31 || (G && t == G - 1) || cut[v].col + 8 >= a.N);
+            octet_put<DT, AL>(hr + cut[v].col * EB, xw[v], cut[v].lo, cut[v].hi, on_word, G > 0 ? t == 0 : t % 32 == 0,
+                              t % 32 == 31 || (G > 0 && t == G - 1) || cut[v].col + 8 >= a.N);
     }
     float s0, s1;
     f2_unpack(ss, s0, s1);
@@ -107,8 +107,8 @@ __global__ void __launch_bounds__(G ? kFusedGroupThreads : kFusedMaxThreads) add
             for (int e = 0; e < 4; ++e) f[e] = f2_mul(f2_mul(f[e], r2), f2_add(g[e], one2));
             pairs_octet<DT>(f, xw[v]);
         }
-        octet_put<DT, AL>(yr + cut[v].col * EB, xw[v], cut[v].lo, cut[v].hi, on_word, G ? t == 0 : t % 32 == 0,
-                          t % 32 == 31 || (G && t == G - 1) || cut[v].col + 8 >= a.N);
+        octet_put<DT, AL>(yr + cut[v].col * EB, xw[v], cut[v].lo, cut[v].hi, on_word, G > 0 ? t == 0 : t % 32 == 0,
+                          t % 32 == 31 || (G > 0 && t == G - 1) || cut[v].col + 8 >= a.N);
     }
     griddep_launch_dependents();
 }
@@ -125,12 +125,12 @@ static const void* add_fwd_for(int lanes, int octets) {
     RMSNORM_ADD_FWD(32, 1)
     RMSNORM_ADD_FWD(32, 2)
     RMSNORM_ADD_FWD(32, 4)
-    RMSNORM_ADD_FWD(0, 1)
     RMSNORM_ADD_FWD(0, 2)
-    RMSNORM_ADD_FWD(0, 3)
-    RMSNORM_ADD_FWD(0, 4)
-    if constexpr (MODE != kRowsAligned) {
-        RMSNORM_ADD_FWD(0, 5)
+    if constexpr (MODE == kRowsAligned) {
+        RMSNORM_ADD_FWD(0, 4)
+    } else {
+        RMSNORM_ADD_FWD(-1, 2)
+        RMSNORM_ADD_FWD(-1, 3)
     }
 #undef RMSNORM_ADD_FWD
     return nullptr;

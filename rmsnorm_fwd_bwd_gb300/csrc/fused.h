@@ -12,6 +12,8 @@ namespace rmsnorm {
 constexpr int kRopeMaxSets = 2;
 // Threads of a block that holds one row, at most; of one that holds several.
 constexpr int kFusedMaxThreads = 512;
+// The forwards' blocks for the widest rows off 16 bytes.
+constexpr int kFusedWideThreads = 1024;
 constexpr int kFusedGroupThreads = 128;
 
 // How a kernel's rows lie. kRowsAligned: every row on a 16-byte boundary and of whole
@@ -54,7 +56,7 @@ struct AddArgs {
     uint32_t* err;                  // device error word
 };
 
-// A launch shape. lanes: lanes per row (0: a block per row).
+// A launch shape. lanes: lanes per row (0: a block per row, -1: a wide block).
 struct AddPlan {
     int dtype = 0;
     int mode = kRowsAny;

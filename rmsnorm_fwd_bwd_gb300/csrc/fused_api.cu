@@ -79,11 +79,11 @@ int64_t octets_of(int64_t N, int dtype, bool wide) { return wide ? N / 8 : ceil_
 
 // The fewest threads, a multiple of 32, that hold n octets, times their octets, over
 // the given choices of octets per thread; the first of equals.
-bool block_shape(int64_t n, std::initializer_list<int> choices, AddPlan& p) {
+bool block_shape(int64_t n, std::initializer_list<int> choices, int most, AddPlan& p) {
     int64_t best = 0;
     for (const int octets : choices) {
         const int64_t threads = round_up(ceil_div(n, octets), 32);
-        if (threads > kFusedMaxThreads || (best && threads * octets >= best)) continue;
+        if (threads > most || (best && threads * octets >= best)) continue;
         best = threads * octets;
         p.octets = octets;
         p.threads = static_cast<int>(threads);
@@ -92,8 +92,9 @@ bool block_shape(int64_t n, std::initializer_list<int> choices, AddPlan& p) {
 }
 
 // Lanes per row and octets per thread for rows of n octets: up to 128 (64 off 16 bytes,
-// where a row's ends cost a warp more) by groups of lanes of a 4-warp block (the 8-bit output wants a warp, whose neighbouring lanes
-// hold a group of columns), wider rows by a block of at most kFusedMaxThreads.
+// where a row's ends cost a warp more) by groups of lanes of a 4-warp block (the 8-bit
+// output wants a warp, whose neighbouring lanes hold a group of columns), wider rows by
+// a block.
 bool row_shape(int64_t n, int least_lanes, std::initializer_list<int> choices, AddPlan& p) {
     if (n <= (p.mode == kRowsOnePhase ? 64 : 128)) {
         p.lanes = n <= 16 ? least_lanes : 32;
@@ -103,10 +104,21 @@ bool row_shape(int64_t n, int least_lanes, std::initializer_list<int> choices, A
         return true;
     }
     p.lanes = 0;
-    return block_shape(n, choices, p) || block_shape(n, {5}, p);
+    return block_shape(n, choices, kFusedMaxThreads, p);
 }
 
-int64_t rows_per_block(const AddPlan& p) { return p.lanes ? p.threads / p.lanes : 1; }
+// The forwards' shape: four octets a thread of aligned rows (two with as few threads
+// idle); two of others, whose shifting and masking hold registers, in wide blocks where
+// kFusedMaxThreads do not hold the row (16384 x 14278 bf16 with dropout: 667 us with three
+// octets of 608 threads, 534 us so).
+bool fwd_shape(int64_t n, int least_lanes, AddPlan& p) {
+    if (p.mode == kRowsAligned) return row_shape(n, least_lanes, {4, 2}, p);
+    if (row_shape(n, least_lanes, {2}, p)) return true;
+    p.lanes = -1;
+    return block_shape(n, {2, 3}, kFusedWideThreads, p);
+}
+
+int64_t rows_per_block(const AddPlan& p) { return p.lanes > 0 ? p.threads / p.lanes : 1; }
 
 struct Operand {
     const void* p;
@@ -164,7 +176,7 @@ bool ring_plan(int64_t M, int64_t N, int dtype, RowMode mode, bool drop, bool ha
     p.drop = drop;
     p.ring = true;
     const int64_t eb = elem_bytes(dtype);
-    if (!block_shape(octets_of(N, dtype, wide), {2, 3, 4}, p)) return false;
+    if (!block_shape(octets_of(N, dtype, wide), {2, 3, 4}, kFusedMaxThreads, p)) return false;
     // whole octets for every thread that has one: rows off 16 bytes are copied from the
     // word they start in to the one they end in
     const int64_t octet = 8 * eb;
@@ -203,7 +215,9 @@ bool add_bwd_plan(int64_t M, int64_t N, int dtype, RowMode mode, bool drop, bool
     const bool wide = mode == kRowsAligned;
     p.dtype = dtype;
     p.mode = mode;
-    if (!row_shape(octets_of(N, dtype, wide), 8, {2, 4}, p)) return false;
+    if (!(wide ? row_shape(octets_of(N, dtype, wide), 8, {2, 4}, p)
+              : row_shape(octets_of(N, dtype, wide), 8, {2, 4, 5}, p)))
+        return false;
     p.smem = p.lanes ? static_cast<size_t>(rows_per_block(p)) * N * 4 : 0;
     const void* k = add_bwd_kernel(p);
     const int fit = k ? resident_blocks(k, dev, p.threads, p.smem) : 0;
@@ -359,7 +373,7 @@ extern "C" rmsnorm_status rmsnorm_add_fwd(const void* x, int64_t ldx, const void
     p.dtype = dtype;
     p.drop = a.threshold != 0;
     p.mode = row_mode(wide, one_offset(s, {{x, ldx}, {residual, ldres}, {h, ldh}, {y, ldy}}));
-    if (!row_shape(octets_of(N, dtype, wide), 8, {4, 2, 3}, p)) return RMSNORM_ERR_UNSUPPORTED;
+    if (!fwd_shape(octets_of(N, dtype, wide), 8, p)) return RMSNORM_ERR_UNSUPPORTED;
     p.blocks = ceil_div(M, rows_per_block(p));
     return run(add_fwd_kernel(p), p, a, stream);
 }
@@ -479,7 +493,8 @@ extern "C" rmsnorm_status rmsnorm_quant_fwd(const void* x, int64_t ldx, const vo
     p.dtype = dtype;
     // groups of columns want octets that start at column 0
     p.mode = row_mode(wide, group == 0 && one_offset(s, {{x, ldx}, {residual, ldres}, {h, ldh}}));
-    if (!row_shape(p.mode == kRowsOnePhase ? octets_of(N, dtype, false) : ceil_div(N, 8), 32, {4, 2}, p)) return RMSNORM_ERR_UNSUPPORTED;
+    const int64_t n = p.mode == kRowsOnePhase ? octets_of(N, dtype, false) : ceil_div(N, 8);
+    if (!fwd_shape(n, 32, p)) return RMSNORM_ERR_UNSUPPORTED;
     p.blocks = ceil_div(M, rows_per_block(p));
     return run(quant_kernel(p), p, a, stream);
 }

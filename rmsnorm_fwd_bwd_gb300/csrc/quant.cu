@@ -19,16 +19,16 @@ namespace rmsnorm {
 // largest |y| is r times its largest |z|, so the sum of squares and, for a whole row,
 // the maximum are reduced together, with one barrier.
 template <int DT, int MODE, int G, int KB>
-__global__ void __launch_bounds__(G ? kFusedGroupThreads : kFusedMaxThreads) quant_rows(const AddArgs a) {
+__global__ void __launch_bounds__(G > 0 ? kFusedGroupThreads : G < 0 ? kFusedWideThreads : kFusedMaxThreads) quant_rows(const AddArgs a) {
     constexpr bool AL = MODE == kRowsAligned;
     constexpr int W = Oct<DT>::kWords;
     constexpr int EB = Elem<DT>::kBytes;
     __shared__ float part[32];
     __shared__ float top[32];
-    const int per_row = G ? G : blockDim.x;
-    const int t = G ? threadIdx.x % G : threadIdx.x;
+    const int per_row = G > 0 ? G : blockDim.x;
+    const int t = G > 0 ? threadIdx.x % G : threadIdx.x;
     const int lane = threadIdx.x & 31;
-    const int64_t row = G ? static_cast<int64_t>(blockIdx.x) * (blockDim.x / G) + threadIdx.x / G : blockIdx.x;
+    const int64_t row = G > 0 ? static_cast<int64_t>(blockIdx.x) * (blockDim.x / G) + threadIdx.x / G : blockIdx.x;
     griddep_wait();
     const bool live = row < a.M;
     const char* xr = static_cast<const char*>(a.x) + row * a.ldx * EB;
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(G ? kFusedGroupThreads : kFusedMaxThreads) qua
 #pragma unroll
         for (int v = 1; v < KB; ++v) all = max_magnitude(all, m[v]);
         all = warp_allmax(all);
-        if (G == 0 && lane == 0) top[threadIdx.x >> 5] = all;  // read after row_sum's barrier
+        if (G <= 0 && lane == 0) top[threadIdx.x >> 5] = all;  // read after row_sum's barrier
 #pragma unroll
         for (int v = 0; v < KB; ++v) m[v] = all;
     } else {
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(G ? kFusedGroupThreads : kFusedMaxThreads) qua
     float s0, s1;
     f2_unpack(ss, s0, s1);
     const float r = row_rsqrt(row_sum<G>(s0 + s1, part), a.inv_n, a.eps);
-    if (G == 0 && a.group == 0) {
+    if (G <= 0 && a.group == 0) {
         const float all = warp_allmax(lane < static_cast<int>(blockDim.x >> 5) ? top[lane] : 0.f);
 #pragma unroll
         for (int v = 0; v < KB; ++v) m[v] = all;
@@ -132,9 +132,11 @@ static const void* quant_rows_for(int lanes, int octets) {
     RMSNORM_QUANT_ROWS(32, 2)
     RMSNORM_QUANT_ROWS(32, 4)
     RMSNORM_QUANT_ROWS(0, 2)
-    RMSNORM_QUANT_ROWS(0, 4)
-    if constexpr (MODE != kRowsAligned) {
-        RMSNORM_QUANT_ROWS(0, 5)
+    if constexpr (MODE == kRowsAligned) {
+        RMSNORM_QUANT_ROWS(0, 4)
+    } else {
+        RMSNORM_QUANT_ROWS(-1, 2)
+        RMSNORM_QUANT_ROWS(-1, 3)
     }
 #undef RMSNORM_QUANT_ROWS
     return nullptr;
