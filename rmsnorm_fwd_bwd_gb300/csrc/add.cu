@@ -10,13 +10,22 @@
 //
 // The dropout mask is never stored: each direction draws an octet's numbers from
 // its row and column (octet.cuh).
+//
+// Bound by HBM: x and residual in, h and y out, 4 M N elements. A row's loads go out at
+// once and nothing is staged: with some 30-60 registers a thread the SM holds enough
+// rows to keep the memory busy, and blocks that end balance themselves over the SMs.
+// Measured on GB300, where a device copy moves 6.77 TB/s: 16384 x 4096 bf16 77 us (6.95
+// TB/s), 78.3 us with dropout (four octets a thread; two: 84.4); the same through a
+// TMA ring of persistent blocks, 83.6 us. 8192 x 4099 fp16, every row at another offset:
+// 52.7 us (5.1 TB/s, bound by instructions: the weight has to be shifted to each row; the
+// ring 71-107 us, several rows a block 60 us). 8 x 4096: 1.8 us a call in a graph.
 #include "fused.h"
 #include "launch.h"
 #include "octet.cuh"
 
 namespace rmsnorm {
 
-// G lanes per row (several rows per block), or a block per row (G == 0); KB octets
+// G lanes per row (several rows per block), or a block per row (0, wide -1); KB octets
 // per thread, thread t of a row owning octets t, t + threads, ... Each block does its
 // rows and ends: the hardware balances the rows over the SMs, and a row's loads are
 // all in flight at once.

@@ -16,6 +16,12 @@
 // Rows off 16 bytes: the grid is a multiple of 8, and rows 8 apart start at the same
 // offset from a 16-byte boundary (a pitch is a whole number of 2-byte elements at
 // least), so all rows of a thread share theirs and its columns stay the same.
+//
+// Bound by HBM: dy, dh and h in, dresidual (and dx) out, 4 or 5 M N elements. Measured on
+// GB300 (a device copy moves 6.77 TB/s), the column reduction of 5 us in each figure:
+// 65536 x 4096 bf16 with dropout 422 us (6.35 TB/s), 16384 x 4096 without 91 us (5.9 TB/s),
+// 8192 x 4099 58 us (4.6 TB/s), 65536 x 1000 by lanes 89 us (5.9 TB/s). Without the ring
+// the first took 536 us: loads waited for at every row.
 #include "fused.h"
 #include "launch.h"
 #include "octet.cuh"
@@ -163,7 +169,10 @@ __global__ void __launch_bounds__(G ? kFusedGroupThreads : kFusedMaxThreads) add
 // flight all the time, which the ring gives without holding them in registers.
 //
 // A stage is read twice (the row sum, then the gradients) and refilled one row later,
-// when the next row's one block barrier shows that every thread is done with it.
+// when the next row's one block barrier shows that every thread is done with it. Reading
+// twice keeps dy and h out of the registers, and packed pairs halve the instructions:
+// three blocks of 256 threads fit an SM, where 120 registers left two (bf16 65536 x 4096
+// with dropout: 489 -> 423 us).
 //
 // AL: rows of whole octets on 16-byte boundaries. Otherwise the rows of all tensors
 // start at one offset from a 16-byte boundary (the usual dense tensors of any width):

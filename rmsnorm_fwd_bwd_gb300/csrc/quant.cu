@@ -7,6 +7,13 @@
 // With pow2 the scale is rounded up to a power of two. The floor keeps 1 / scale
 // finite for rows of zeros. A NaN anywhere in a group makes its scale NaN; an
 // infinity makes the scale infinite, so the group's codes are 0 or NaN.
+//
+// Bound by HBM (x, residual in; h out; a byte a code), without a residual by
+// instructions: converting, scaling and packing 8 columns takes some 100. Measured on
+// GB300 (a device copy moves 6.77 TB/s): 16384 x 8192 bf16 with residual 134.5 us (7.0
+// TB/s), 8192 x 5120 fp16 without 29.2 us (4.3 TB/s), 64 x 8192 2.7 us a call in a graph.
+// Four octets a thread, 139 us against 148 with two, before the sum and the maximum were
+// reduced together.
 #include "fused.h"
 #include "launch.h"
 #include "octet.cuh"
