@@ -17,7 +17,7 @@
  * In place: every row is read before it is written, so an output may be an input
  * of the same shape, dtype, pointer and pitch (h on residual, y on x, dresidual on
  * dy or dh, rotated heads on the heads). No other overlap is allowed; two outputs at
- * one address whose values differ are refused.
+ * one address whose values differ are refused, and so are an output's rows that overlap.
  */
 #ifndef RMSNORM_FUSED_H
 #define RMSNORM_FUSED_H
@@ -91,7 +91,8 @@ rmsnorm_status rmsnorm_add_bwd(const void* dy, int64_t lddy, const void* dh, int
  * codes: uint8[M rows, pitch ldcodes]; scales: float32[M rows, pitch ldscales],
  * one per row or ceil(N / group). residual and h may be NULL, each on its own. A
  * group with a NaN gets a NaN scale; one with an infinity an infinite scale and
- * codes of 0 and NaN.
+ * codes of 0 and NaN. h * g is formed before r is known: where that passes fp32's
+ * range (2^128), y counts as infinite.
  */
 rmsnorm_status rmsnorm_quant_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldres, const void* gamma,
                                  void* h, int64_t ldh, void* codes, int64_t ldcodes, float* scales, int64_t ldscales,
@@ -105,7 +106,8 @@ rmsnorm_status rmsnorm_quant_fwd(const void* x, int64_t ldx, const void* residua
 /*
  * Heads of one kind (a model's query heads, its key heads): entry d of head j of
  * token t is at x[t * x_token + j * x_head + d], strides in elements, each at least
- * D where there is more than one token or head. gamma[D], shared by the heads, or
+ * D where there is more than one token or head; of an output (y, dx) also all heads of
+ * a token within a token's stride, or all tokens of a head within a head's. gamma[D], shared by the heads, or
  * NULL for the rotation without a norm. y: the output, with its own strides.
  */
 typedef struct {
@@ -142,8 +144,9 @@ typedef struct {
  * entries from rotary_dim on are z. One to RMSNORM_ROPE_MAX_SETS sets, rotated
  * alike, in one launch. positions: int64[T], any values; inv_freq:
  * float64[rotary_dim / 2], finite, in radians per position: a scaled context is a
- * matter of the frequencies (and mscale) given. Angles are reduced exactly (64-bit
- * fixed point), so far positions lose nothing. 1 <= D <= RMSNORM_ROPE_MAX_D,
+ * matter of the frequencies (and mscale) given. Angles are reduced in 64-bit fixed
+ * point: with frequencies below 4 an angle is off by less than 2^-31 of a turn at any
+ * position up to 2^32 (and by some position * 2^-64 of a turn beyond). x * g is formed before r, as above. 1 <= D <= RMSNORM_ROPE_MAX_D,
  * rotary_dim even, 2 <= rotary_dim <= D; T may be 0; at most
  * RMSNORM_ROPE_MAX_HEADS heads in all sets.
  */

@@ -32,10 +32,14 @@ std::map<std::pair<const void*, std::pair<int, int>>, int> g_fused_fit;  // resi
 // SMs of the current device; 0 on failure.
 int current_sms(int& dev) {
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    std::lock_guard<std::mutex> lock(g_fused_mu);
-    int& n = g_fused_sms[dev];
-    if (n == 0 && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) n = 0;
-    return n;
+    try {
+        std::lock_guard<std::mutex> lock(g_fused_mu);
+        int& n = g_fused_sms[dev];
+        if (n == 0 && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) n = 0;
+        return n;
+    } catch (...) {  // no memory for the entry: nothing is thrown through the C entry points
+        return 0;
+    }
 }
 
 // Allow the kernel the device's whole shared memory; the attribute belongs to the
@@ -53,12 +57,16 @@ bool allow_shared_memory(const void* k, int dev) {
 
 // Blocks of `threads` that an SM holds, for the persistent kernels; 0 on failure.
 int resident_blocks(const void* k, int dev, int threads, size_t smem) {
-    std::lock_guard<std::mutex> lock(g_fused_mu);
-    int& n = g_fused_fit[{k, {dev, static_cast<int>(smem) * 1024 + threads}}];
-    if (n == 0 && ((smem > 48 * 1024 && !allow_shared_memory(k, dev)) ||
-                   cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, threads, smem) != cudaSuccess))
-        n = 0;
-    return n;
+    try {
+        std::lock_guard<std::mutex> lock(g_fused_mu);
+        int& n = g_fused_fit[{k, {dev, static_cast<int>(smem) * 1024 + threads}}];
+        if (n == 0 && ((smem > 48 * 1024 && !allow_shared_memory(k, dev)) ||
+                       cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, threads, smem) != cudaSuccess))
+            n = 0;
+        return n;
+    } catch (...) {
+        return 0;
+    }
 }
 
 cudaError_t launch(const void* k, int64_t blocks, int threads, size_t smem, void** params, cudaStream_t s) {
@@ -139,6 +147,14 @@ bool one_offset(size_t s, std::initializer_list<Operand> operands) {
             return false;
         q = &o;
     }
+    return true;
+}
+
+// No two of the given outputs (NULL: not written) at one address.
+bool distinct(std::initializer_list<const void*> outputs) {
+    for (auto p = outputs.begin(); p != outputs.end(); ++p)
+        for (auto q = outputs.begin(); *p && q != p; ++q)
+            if (*p == *q) return false;
     return true;
 }
 
@@ -263,6 +279,12 @@ bool strides_ok(int64_t token, int64_t head, int64_t heads, int64_t T, int64_t D
     return (T <= 1 || token <= most / (T - 1)) && (heads <= 1 || head <= most / (heads - 1));
 }
 
+// Output rows must not overlap: tokens outside heads, or heads outside tokens.
+bool output_strides_ok(int64_t token, int64_t head, int64_t heads, int64_t T, int64_t D) {
+    return strides_ok(token, head, heads, T, D) &&
+           (T <= 1 || heads <= 1 || token >= (heads - 1) * head + D || head >= (T - 1) * token + D);
+}
+
 rmsnorm_status check_rope(int nsets, int64_t T, int64_t D, int64_t R, int interleaved, float mscale, float eps,
                           rmsnorm_dtype dtype, int offset) {
     const rmsnorm_status st = check_common(T, D, dtype, offset);
@@ -308,6 +330,7 @@ rmsnorm_status rope_plan(RopeArgs& a, int dtype, int interleaved, bool wide, boo
         a.nchunk = a.chunks0 + static_cast<int>(a.nsets > 1 ? ceil_div(a.set[1].heads, a.chunk) : 0);
         p.blocks = ceil_div(a.T * a.nchunk, p.threads / group);
         if (bwd) p.blocks = std::min<int64_t>(p.blocks, static_cast<int64_t>(sms) * kRopeBwdBlocks);
+        if (p.blocks > INT32_MAX) return RMSNORM_ERR_SHAPE;
     } else {
         const int64_t nchunk = std::min<int64_t>(ceil_div(full, a.T), a.heads);
         a.chunk = static_cast<int>(ceil_div(a.heads, nchunk));
@@ -352,7 +375,7 @@ extern "C" rmsnorm_status rmsnorm_add_fwd(const void* x, int64_t ldx, const void
     if (!check_dropout(dropout_p, rng, a, st)) return st;
     if (M == 0) return RMSNORM_OK;
     if (!x || !gamma || !y) return RMSNORM_ERR_NULL;
-    if (h == y) return RMSNORM_ERR_ARG;
+    if (!distinct({h, y, rstd})) return RMSNORM_ERR_ARG;
     if (!aligned(x, s) || !aligned(residual, s) || !aligned(gamma, s) || !aligned(h, s) || !aligned(y, s) ||
         !aligned(rstd, 4))
         return RMSNORM_ERR_ALIGN;
@@ -422,7 +445,9 @@ extern "C" rmsnorm_status rmsnorm_add_bwd(const void* dy, int64_t lddy, const vo
         !aligned(dresidual, s) || !aligned(rstd, 4) || !aligned(workspace, 16))
         return RMSNORM_ERR_ALIGN;
     if ((st = check_rng(a)) != RMSNORM_OK) return st;
-    if (a.threshold && dx && dx == dresidual) return RMSNORM_ERR_ARG;
+    if (!distinct({dx, dgamma, workspace}) || !distinct({dresidual, dgamma, workspace}) ||
+        (a.threshold && !distinct({dx, dresidual})))
+        return RMSNORM_ERR_ARG;
     AddPlan p;
     const bool wide = wide_rows(N, s, {{dy, lddy}, {dh, lddh}, {h, ldh}, {gamma, 0}, {dx, lddx}, {dresidual, lddres}});
     const RowMode mode =
@@ -471,6 +496,7 @@ extern "C" rmsnorm_status rmsnorm_quant_fwd(const void* x, int64_t ldx, const vo
         return RMSNORM_ERR_SHAPE;
     if (M == 0) return RMSNORM_OK;
     if (!x || !gamma || !codes || !scales) return RMSNORM_ERR_NULL;
+    if (!distinct({h, codes, scales})) return RMSNORM_ERR_ARG;
     if (!aligned(x, s) || !aligned(residual, s) || !aligned(gamma, s) || !aligned(h, s) || !aligned(scales, 4))
         return RMSNORM_ERR_ALIGN;
     AddArgs a = {};
@@ -519,7 +545,7 @@ extern "C" rmsnorm_status rmsnorm_rope_fwd(const rmsnorm_rope_heads* sets, int n
     for (int i = 0; i < nsets; ++i) {
         const rmsnorm_rope_heads& q = sets[i];
         if (q.heads < 1 || q.heads > RMSNORM_ROPE_MAX_HEADS || !strides_ok(q.x_token, q.x_head, q.heads, T, D) ||
-            !strides_ok(q.y_token, q.y_head, q.heads, T, D))
+            !output_strides_ok(q.y_token, q.y_head, q.heads, T, D))
             return RMSNORM_ERR_SHAPE;
         heads += q.heads;
         if (T > 0 && (!q.x || !q.y)) return RMSNORM_ERR_NULL;
@@ -537,6 +563,7 @@ extern "C" rmsnorm_status rmsnorm_rope_fwd(const rmsnorm_rope_heads* sets, int n
     }
     if (heads > RMSNORM_ROPE_MAX_HEADS) return RMSNORM_ERR_SHAPE;
     if (T == 0) return RMSNORM_OK;
+    if (!distinct({a.set[0].y, a.set[1].y})) return RMSNORM_ERR_ARG;
     if (!positions || !inv_freq) return RMSNORM_ERR_NULL;
     if (!aligned(positions, 8) || !aligned(inv_freq, 8)) return RMSNORM_ERR_ALIGN;
     a.nsets = nsets;
@@ -581,7 +608,7 @@ extern "C" rmsnorm_status rmsnorm_rope_bwd(const rmsnorm_rope_heads_bwd* sets, i
         const rmsnorm_rope_heads_bwd& q = sets[i];
         if (q.heads < 1 || q.heads > RMSNORM_ROPE_MAX_HEADS || !strides_ok(q.dy_token, q.dy_head, q.heads, T, D) ||
             (q.gamma && !strides_ok(q.x_token, q.x_head, q.heads, T, D)) ||
-            !strides_ok(q.dx_token, q.dx_head, q.heads, T, D))
+            !output_strides_ok(q.dx_token, q.dx_head, q.heads, T, D))
             return RMSNORM_ERR_SHAPE;
         heads += q.heads;
         weights = weights || q.gamma;
@@ -605,6 +632,8 @@ extern "C" rmsnorm_status rmsnorm_rope_bwd(const rmsnorm_rope_heads_bwd* sets, i
         wide = wide && rope_wide(t, s);
     }
     if (heads > RMSNORM_ROPE_MAX_HEADS) return RMSNORM_ERR_SHAPE;
+    if (nsets == 2 && sets[0].gamma && sets[1].gamma && sets[0].dgamma == sets[1].dgamma) return RMSNORM_ERR_ARG;
+    if (T > 0 && !distinct({a.set[0].y, a.set[1].y})) return RMSNORM_ERR_ARG;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     a.nsets = nsets;
     a.heads = static_cast<int>(heads);

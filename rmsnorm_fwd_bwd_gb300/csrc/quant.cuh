@@ -38,11 +38,12 @@ __device__ __forceinline__ float octet_amax(const uint64_t (&z)[4], int lo, int 
 
 // The scale of a group whose largest |z| is amax, with y = z * r; and the factors by which
 // z becomes codes, in this order: 1 and r / scale, the r of y and of the scale having
-// cancelled, or, at the least scale, where that may overflow, r and 1 / scale.
+// cancelled, or, at the least scale and for the smallest z, where that may overflow, r
+// and 1 / scale.
 __device__ __forceinline__ float quant_scale(float amax, float r, int pow2, float& f0, float& f1) {
     float s = amax * r * (1.0f / 448.0f);
-    const bool least = s < 1.17549435e-38f;  // 2^-126; a NaN stays
-    if (least) s = 1.17549435e-38f;
+    const bool apart = s < 1.17549435e-38f || amax < 7.8886091e-31f;  // 2^-126 and 2^-100
+    if (s < 1.17549435e-38f) s = 1.17549435e-38f;                   // a NaN stays
     if (pow2) {
         // up to the next power of two: a carry out of the fraction raises the exponent
         // (infinity and NaN stay)
@@ -52,8 +53,8 @@ __device__ __forceinline__ float quant_scale(float amax, float r, int pow2, floa
     // the scale is a normal number and its inverse too: off by at most 1 unit in the last place
     float inv;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-    f0 = least ? r : 1.f;
-    f1 = least ? inv : r * inv;
+    f0 = apart ? r : 1.f;
+    f1 = apart ? inv : r * inv;
     return s;
 }
 

@@ -198,6 +198,73 @@ struct Turns {
 
 __device__ __forceinline__ uint64_t f2_neg(uint64_t v) { return v ^ 0x8000000080000000ull; }
 
+// How many of a lane's eight pairs are rotated, the first ones: all or none of them but
+// where neighbours are paired.
+__device__ __forceinline__ int rotated_pairs(const RopeArgs& a, int li) { return max(0, min(8, a.R / 2 - 8 * li)); }
+
+// Plain (not read-only-cache) loads: an output may be its input.
+template <int DT> __device__ __forceinline__ float entry(const char* p, int64_t i) {
+    if constexpr (DT == kF32) return reinterpret_cast<const float*>(p)[i];
+    else if constexpr (DT == kF16) return __half2float(reinterpret_cast<const __half*>(p)[i]);
+    else return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+// The lane's pairs (p, q) to p * cp + q * sp and q * cq + p * sq.
+__device__ __forceinline__ void turn_pairs(uint64_t (&p)[4], uint64_t (&q)[4], const uint64_t (&cp)[4], const uint64_t (&sp)[4],
+                                           const uint64_t (&cq)[4], const uint64_t (&sq)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint64_t x = p[k], y = q[k];
+        p[k] = f2_fma(x, cp[k], f2_mul(y, sp[k]));
+        q[k] = f2_fma(y, cq[k], f2_mul(x, sq[k]));
+    }
+}
+
+// The same for the first `rotated` pairs, the others to p * cp and q * cq.
+template <bool INTER>
+__device__ __forceinline__ void turn_first_pairs(int rotated, uint64_t (&p)[4], uint64_t (&q)[4], const uint64_t (&cp)[4],
+                                                 const uint64_t (&sp)[4], const uint64_t (&cq)[4], const uint64_t (&sq)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint64_t x = p[k], y = q[k];
+        const uint64_t keep = (2 * k < rotated ? 0xffffffffull : 0ull) |
+                              ((INTER ? 2 * k + 1 : 2 * k) < rotated ? 0xffffffffull << 32 : 0ull);
+        p[k] = f2_fma(x, cp[k], f2_mul(y & keep, sp[k]));
+        q[k] = f2_fma(y, cq[k], f2_mul(x & keep, sq[k]));
+    }
+}
+
+// The same again from the row in memory, entry by entry, with few registers. An infinity or
+// a NaN behind the rotated entries times a sine of 0 would be a NaN in its neighbour: a
+// row where that happened is done again, but for the fp32 backward, whose registers have no
+// room for it and whose entries are masked. (bf16 forward, half of 128 entries
+// rotated: 101.4 us without, 102.7 so, 114 with two ways for every row; fp32 backward 81.5
+// without, 90.4 masked, 97-107 done again, 104 masked behind a branch on R < D.)
+template <int DT, bool INTER>
+__device__ __forceinline__ void turn_again(const char* row, int oa, int ob, int rotated, uint64_t (&p)[4], uint64_t (&q)[4],
+                                           const uint64_t (&cp)[4], const uint64_t (&sp)[4], const uint64_t (&cq)[4],
+                                           const uint64_t (&sq)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float a[2], b[2], ca[2], sa[2], cb[2], sb[2];
+        f2_unpack(cp[k], ca[0], ca[1]);
+        f2_unpack(sp[k], sa[0], sa[1]);
+        f2_unpack(cq[k], cb[0], cb[1]);
+        f2_unpack(sq[k], sb[0], sb[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = 2 * k + h;
+            const int o = INTER && i >= 4 ? ob : oa, o2 = INTER ? o : ob;
+            const float x = o >= 0 ? entry<DT>(row, 8 * o + (INTER ? 2 * (i & 3) : i)) : 0.f;
+            const float y = o2 >= 0 ? entry<DT>(row, 8 * o2 + (INTER ? 2 * (i & 3) + 1 : i)) : 0.f;
+            a[h] = i < rotated ? fmaf(x, ca[h], y * sa[h]) : x * ca[h];
+            b[h] = i < rotated ? fmaf(y, cb[h], x * sb[h]) : y * cb[h];
+        }
+        p[k] = f2_pack(a[0], a[1]);
+        q[k] = f2_pack(b[0], b[1]);
+    }
+}
+
 __device__ __forceinline__ float f2_sum(uint64_t v) {
     float a, b;
     f2_unpack(v, a, b);
@@ -229,6 +296,7 @@ __global__ void __maxnreg__(96) rope_fwd_octets(const RopeArgs a) {
     const int n = live ? min(a.chunk, set.heads - from) : 0;
     int oa, ob;
     lane_octets<INTER>(li, a.D, a.R, oa, ob);
+    const int rotated = rotated_pairs(a, li);
     const char* xb = static_cast<const char*>(set.x) + (token * set.x_token + from * set.x_head) * EB;
     char* yb = static_cast<char*>(set.y) + (token * set.y_token + from * set.y_head) * EB;
     const int64_t x_step = set.x_head * EB, y_step = set.y_head * EB;
@@ -263,14 +331,16 @@ __global__ void __maxnreg__(96) rope_fwd_octets(const RopeArgs a) {
         for (int k = 1; k < 4; ++k) ss = f2_fma(p[k], p[k], ss);
 #pragma unroll
         for (int k = 0; k < 4; ++k) ss = f2_fma(q[k], q[k], ss);
-        float r = row_rsqrt(row_sum<L>(f2_sum(ss), nullptr), inv_d, a.eps);
-        if (!set.gamma) r = 1.f;
+        const float sum = row_sum<L>(f2_sum(ss), nullptr);
+        const float r = set.gamma ? row_rsqrt(sum, inv_d, a.eps) : 1.f;
         const uint64_t r2 = f2_pack(r, r);
+        turn_pairs(p, q, pc, qs, qc, ps);
+        if (rotated < 8 && j < n && !(sum < __int_as_float(0x7f800000)))
+            turn_again<DT, INTER>(xb + j * x_step, oa, ob, rotated, p, q, pc, qs, qc, ps);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const uint64_t x = p[k], y = q[k];
-            p[k] = f2_mul(f2_fma(x, pc[k], f2_mul(y, qs[k])), r2);
-            q[k] = f2_mul(f2_fma(y, qc[k], f2_mul(x, ps[k])), r2);
+            p[k] = f2_mul(p[k], r2);
+            q[k] = f2_mul(q[k], r2);
         }
         if (j < n) store_pairs<DT, INTER>(yb + j * y_step, oa, ob, p, q);
     }
@@ -299,6 +369,7 @@ __global__ void __maxnreg__((DT == kF32 ? 168 : 144)) rope_bwd_octets(const Rope
     griddep_wait();
     int oa, ob;
     lane_octets<INTER>(li, a.D, a.R, oa, ob);
+    const int rotated = rotated_pairs(a, li);
     turns.fill(a, L);
     __syncthreads();
     const float inv_d = 1.0f / static_cast<float>(a.D);
@@ -350,21 +421,28 @@ __global__ void __maxnreg__((DT == kF32 ? 168 : 144)) rope_bwd_octets(const Rope
                     load16<DT>(xb, oa, ob, norm && more, xw[j]);
                     db += d_step;
                     xb += x_step;
+                    if constexpr (DT == kF32) turn_first_pairs<INTER>(rotated, p, q, c, sn, c, ns);
+                    else turn_pairs(p, q, c, sn, c, ns);
+                    const bool some = DT != kF32 && rotated < 8 && h + j < n;
+                    if (!norm) {
+                        uint64_t all = f2_add(p[0], q[0]);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint64_t x = p[k], y = q[k];
-                        p[k] = f2_fma(x, c[k], f2_mul(y, sn[k]));
-                        q[k] = f2_fma(y, c[k], f2_mul(x, ns[k]));
-                    }
-                    if (norm) {
+                        for (int k = 1; k < 4; ++k) all = f2_add(all, f2_add(p[k], q[k]));
+                        const float u = f2_sum(all);
+                        if (some && u != u)
+                            turn_again<DT, INTER>(db - (BATCH + 1) * d_step, oa, ob, rotated, p, q, c, sn, c, ns);
+                    } else {
                         uint64_t ss = f2_pack(0.f, 0.f), ux = f2_pack(0.f, 0.f);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             ss = f2_fma(xq[k], xq[k], f2_fma(xp[k], xp[k], ss));
                             ux = f2_fma(f2_mul(q[k], gq[k]), xq[k], f2_fma(f2_mul(p[k], gp[k]), xp[k], ux));
                         }
+                        const float u = f2_sum(ux);
+                        if (some && u != u)
+                            turn_again<DT, INTER>(db - (BATCH + 1) * d_step, oa, ob, rotated, p, q, c, sn, c, ns);
                         const float r = row_rsqrt(row_sum<L>(f2_sum(ss), nullptr), inv_d, a.eps);
-                        const float m = row_sum<L>(f2_sum(ux), nullptr) * inv_d * r;
+                        const float m = row_sum<L>(u, nullptr) * inv_d * r;
                         const float e = -(r * m);
                         const uint64_t r2 = f2_pack(r, r), e2 = f2_pack(e, e);
 #pragma unroll
@@ -443,13 +521,6 @@ __device__ __forceinline__ void lane_pairs(int li, const RopeArgs& a, bool inter
     }
 }
 
-// Plain (not read-only-cache) loads: an output may be its input.
-template <int DT> __device__ __forceinline__ float entry(const char* p, int64_t i) {
-    if constexpr (DT == kF32) return reinterpret_cast<const float*>(p)[i];
-    else if constexpr (DT == kF16) return __half2float(reinterpret_cast<const __half*>(p)[i]);
-    else return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
-}
-
 template <int DT, int PK, bool BWD>
 __global__ void __launch_bounds__(kFusedGroupThreads) rope_pairs(const RopeArgs a) {
     constexpr int EB = Elem<DT>::kBytes;
@@ -517,7 +588,7 @@ __global__ void __launch_bounds__(kFusedGroupThreads) rope_pairs(const RopeArgs 
                             if (gb) g[j] = entry<DT>(gb, col) + a.one;
                         }
                     }
-                    if (BWD) {
+                    if (BWD && li + 32 * k < a.R / 2) {
                         const float p = v[2 * k], z = v[2 * k + 1];
                         v[2 * k] = p * c[k] - z * s[k];
                         v[2 * k + 1] = z * c[k] + p * s[k];
@@ -549,8 +620,9 @@ __global__ void __launch_bounds__(kFusedGroupThreads) rope_pairs(const RopeArgs 
                         }
                     } else {
                         const float z0 = (x[2 * k] * r) * g[2 * k], z1 = (x[2 * k + 1] * r) * g[2 * k + 1];
-                        o0 = z0 * c[k] - z1 * s[k];
-                        o1 = z1 * c[k] + z0 * s[k];
+                        const bool rotated = li + 32 * k < a.R / 2;
+                        o0 = rotated ? z0 * c[k] - z1 * s[k] : z0;
+                        o1 = rotated ? z1 * c[k] + z0 * s[k] : z1;
                     }
                     if (ca[k] >= 0) Elem<DT>::st(yr, ca[k], o0);
                     if (cb[k] >= 0) Elem<DT>::st(yr, cb[k], o1);

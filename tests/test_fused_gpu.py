@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from rmsnorm_fwd_bwd_gb300 import binding as B
+from rmsnorm_fwd_bwd_gb300 import fused
 from tests import fused_ref as ref
 
 pytestmark = pytest.mark.gpu
@@ -514,6 +515,21 @@ def test_quant_special_values():
         ref.assert_close(got[:, ok], y[:, ok], bound[:, ok], "codes")
 
 
+@pytest.mark.parametrize("group", [0, 32])
+def test_quant_of_the_smallest_products(group):
+    # h * g = 2^-140 k, k whole: exact in fp32, and r (2^40) restores y = 2^-100 k / 1.25 or so
+    N = 64
+    k = torch.tensor([0.0, 1.0, -1.0, 1.5] * 16)
+    x, w = (k * 2.0 ** -40).unsqueeze(0), torch.full((N,), 2.0 ** -100)
+    codes, scales, _ = (t.cpu() for t in fused.rms_norm_quant(x.cuda(), w.cuda(), 2.0 ** -100, group=group))
+    y = x.double() * w.double() / (x.double().square().mean() + 2.0 ** -100).sqrt()
+    s = scales.double().repeat_interleave(group or N, 1)
+    # the largest value's code is 448; a code is off by half a step (2^-4 relative), the scale by
+    # a few roundings
+    assert torch.all((codes.float().double() * s - y).abs() <= y.abs() * (2.0 ** -4 + 2.0 ** -20))
+    assert codes[0, 3].float().item() == 448.0 and codes[0, 0].float().item() == 0.0
+
+
 def test_quant_rounds_to_even_and_uses_the_whole_range():
     # y is exactly x here up to r: rows scaled so that the codes before rounding are known
     N = 4096
@@ -709,6 +725,36 @@ def test_rope_bwd_is_deterministic():
     first = run_rope_bwd(dys, xs, ws, pos, 64, "bfloat16", False)
     again = run_rope_bwd(dys, xs, ws, pos, 64, "bfloat16", False)
     assert torch.equal(first[0][0], again[0][0]) and torch.equal(first[1][0], again[1][0])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("D,R", [(64, 32), (64, 6), (128, 64), (50, 20), (128, 24)])
+def test_rope_infinities_behind_the_rotated_entries_stay_where_they_are(D, R, inter, dtype):
+    x, pos = randn(5, 3, D, dtype=dtype, seed=90), torch.arange(5) * 9 + 1
+    bad = x.clone()
+    for col, v in ((R, float("inf")), (D - 1, float("nan")), ((R + D) // 2, float("-inf"))):
+        bad[2, 1, col] = v
+    put = ~torch.isfinite(bad)
+    for run in (lambda t: run_rope([t], [None], pos, R, dtype, inter)[0],
+                lambda t: run_rope_bwd([t], [None], [None], pos, R, dtype, inter)[0][0]):
+        want, got = run(x), run(bad)
+        assert torch.equal(got[~put], want[~put])
+        assert torch.equal(got[put].isnan(), bad[put].isnan())
+        assert torch.equal(got[put][~bad[put].isnan()], bad[put][~bad[put].isnan()])
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_rope_weight_gradient_of_infinite_cotangents(inter):
+    # dgamma's columns add up products of their own column (and its pair's) alone
+    D, R = 64, 16
+    dy, x = randn(4, 2, D, dtype="float32", seed=91), randn(4, 2, D, dtype="float32", seed=92)
+    w, pos = weight(D, "float32", False), torch.arange(4)
+    bad = dy.clone()
+    bad[1, 1, 40] = float("inf")
+    want, got = (run_rope_bwd([d], [x], [w], pos, R, "float32", inter)[1][0] for d in (dy, bad))
+    rest = torch.arange(D) != 40
+    assert torch.equal(got[rest], want[rest]) and not torch.isfinite(got[40])
 
 
 # --------------------------------------------------------------------------- #
