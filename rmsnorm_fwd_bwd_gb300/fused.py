@@ -15,7 +15,9 @@ Eager calls run the same code through ``torch.autograd.Function`` (or, where not
 asks for a gradient, at once): the custom ops' dispatch takes some 300 us of host time
 per forward and backward. Rows that a view spaces out are passed with their pitch.
 Everything runs on torch's current stream of the inputs' device. They have no second
-order: differentiating a backward raises.
+order and no forward-mode derivative: differentiating a backward, or tensors with
+tangents, raises. A captured training step wants leaves whose eager graphs are gone, as
+with any op: torch accumulates a leaf's gradient on the stream of its first graph.
 """
 from __future__ import annotations
 
@@ -24,6 +26,7 @@ import math
 from typing import Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from . import binding
 from .autograd import _after_op, _row_view, _rows
@@ -62,9 +65,17 @@ def _check_dropout(where: str, x, p: float, rng) -> None:
 
 
 def _eager(*tensors) -> bool:
-    """Plain tensors outside of tracing and compilation."""
-    return not torch.compiler.is_compiling() and all(
+    """Plain tensors outside of tracing, compilation, dispatch modes and function transforms."""
+    return not (torch.compiler.is_compiling() or torch._C._len_torch_dispatch_stack()
+                or torch._C._are_functorch_transforms_active() or torch._C._get_tracing_state()) and all(
         t is None or type(t) is torch.Tensor or type(t) is torch.nn.Parameter for t in tensors)
+
+
+def _no_tangents(where: str, *tensors) -> None:
+    """Forward-mode derivatives would be dropped in silence."""
+    if forward_ad._current_level >= 0 and any(
+            t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise RuntimeError(f"{where} has no forward-mode derivative")
 
 
 def _wants_grad(*tensors) -> bool:
@@ -203,12 +214,27 @@ def rms_norm_add(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torc
     elements, whatever happens to ``rng`` in between."""
     _check_rows("rms_norm_add", x, residual, weight)
     _check_dropout("rms_norm_add", x, p, rng)
+    _no_tangents("rms_norm_add", x, residual, weight)
     args = (x, residual, weight, float(eps), bool(offset), float(p), rng)
     if _eager(x, residual, weight, rng):
         if _wants_grad(x, residual, weight):
             return _AddFunction.apply(*args)
         return _add_fwd_run(*args, want_rstd=False)[:2]
     return torch.ops.rmsnorm_gb300.add_fwd(*args)[:2]
+
+
+def _share_rows(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether rows of two tensors of one shape (contiguous, or 2-D with spaced rows) share
+    memory; the halves of wider rows do not."""
+    def rows(t):
+        N = t.shape[-1]
+        pitch = t.stride(0) if t.dim() == 2 and t.shape[0] > 1 else N
+        return t.data_ptr(), pitch * t.element_size(), N * t.element_size(), t.numel() // N
+    (p, pitch, width, M), (q, pitch_b, _, _) = rows(a), rows(b)
+    if p >= q + (M - 1) * pitch_b + width or q >= p + (M - 1) * pitch + width:
+        return False
+    # interleaved: of one pitch, the columns of one in the gaps of the other
+    return not (pitch == pitch_b and width <= (q - p) % pitch <= pitch - width)
 
 
 def _add_in_place(x, residual, weight, eps, offset):
@@ -239,7 +265,8 @@ def rms_norm_add_(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor,
     for t in (x, residual):
         if not t.is_contiguous() and _row_view(t)[0] is not t:
             raise ValueError("rms_norm_add_ needs contiguous tensors, or 2-D ones with unit column stride")
-    if x.data_ptr() == residual.data_ptr() and x.numel():
+    _no_tangents("rms_norm_add_", x, residual, weight)
+    if x.numel() and _share_rows(x, residual):
         raise ValueError("rms_norm_add_: x and residual must not share memory")
     # always the op, which marks both as changed for whoever saved them for a backward
     torch.ops.rmsnorm_gb300.add_fwd_(x, residual, weight, float(eps), bool(offset))
@@ -303,6 +330,7 @@ def rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, off
     _check_rows("rms_norm_quant", x, residual, weight)
     if group not in (0, 32, 64, 128):
         raise ValueError("rms_norm_quant: group must be 0 (the row), 32, 64 or 128")
+    _no_tangents("rms_norm_quant", x, residual, weight)
     args = (x.detach(), None if residual is None else residual.detach(), weight.detach(), float(eps), bool(offset),
             int(group), bool(pow2))
     codes, scales, h = _quant_run(*args) if _eager(x, residual, weight) else torch.ops.rmsnorm_gb300.quant_fwd(*args)
@@ -500,6 +528,9 @@ def rms_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optional
         raise ValueError("rms_norm_rope: positions must be int64 with q's leading shape, on its device")
     if inv_freq.dim() != 1 or inv_freq.dtype != torch.float64 or inv_freq.device != q.device:
         raise ValueError("rms_norm_rope: inv_freq must be a 1-D float64 tensor on q's device")
+    if inv_freq.requires_grad and torch.is_grad_enabled():
+        raise ValueError("rms_norm_rope is not differentiable by inv_freq")
+    _no_tangents("rms_norm_rope", q, k, q_weight, k_weight, inv_freq)
     args = (q, k, q_weight, k_weight, positions, inv_freq, bool(interleaved), float(mscale), float(eps), bool(offset))
     if not _eager(q, k, q_weight, k_weight, positions, inv_freq):
         qo, ko = torch.ops.rmsnorm_gb300.rope_fwd(*args)
@@ -522,15 +553,17 @@ class RMSNormRope(torch.nn.Module):
         init = torch.zeros if offset else torch.ones
         self.q_weight = torch.nn.Parameter(init(head_dim, device=device, dtype=dtype))
         self.k_weight = torch.nn.Parameter(init(head_dim, device=device, dtype=dtype))
-        inv_freq, self.mscale = rope_frequencies(head_dim if rotary_dim is None else rotary_dim,
-                                                 device=self.q_weight.device, **frequencies)
+        self.frequencies = dict(frequencies, rotary_dim=head_dim if rotary_dim is None else rotary_dim)
+        inv_freq, self.mscale = rope_frequencies(device=self.q_weight.device, **self.frequencies)
         self.register_buffer("inv_freq", inv_freq, persistent=False)
 
     def _apply(self, fn, *args, **kwargs):
-        # a change of the module's dtype leaves the frequencies in 64 bits
+        # a change of the module's dtype leaves the frequencies in 64 bits, a move from
+        # the meta device computes them
         inv_freq = self.inv_freq
         super()._apply(fn, *args, **kwargs)
-        self.inv_freq = inv_freq.to(self.q_weight.device)
+        device = self.q_weight.device
+        self.inv_freq = rope_frequencies(device=device, **self.frequencies)[0] if inv_freq.is_meta else inv_freq.to(device)
         return self
 
     def forward(self, q: torch.Tensor, k: torch.Tensor,

@@ -273,3 +273,83 @@ def test_rope_module_keeps_its_frequencies_in_64_bits():
         fused.RMSNormRope(16, 8, base=500.0, device="cpu").to(torch.bfloat16)
     assert m.inv_freq.dtype == torch.float64 and m.q_weight.dtype == torch.bfloat16
     assert m.inv_freq.cpu().tolist() == fused.rope_frequencies(8, 500.0, device="cpu")[0].tolist()
+
+
+# --------------------------------------------------------------------------- #
+# calls that would overwrite themselves, lose a derivative or a trace
+# --------------------------------------------------------------------------- #
+def test_outputs_at_one_address_are_refused():
+    assert add_fwd(rstd=0x5000) == ARG
+    assert add_bwd(dgamma=0x6000) == ARG
+    assert add_bwd(dgamma=0x7000) == ARG
+    assert add_bwd(workspace=0x7000) == ARG
+    assert quant(h=0x5000) == ARG
+    assert quant(scales=0x5000) == ARG
+    assert quant(scales=0x4000) == ARG
+    # two sets at one address
+    assert rope(sets=2) == ARG
+    assert rope(bwd=True, sets=2) == ARG
+    sets = (B.RopeHeadsBwd * 2)(*[B.RopeHeadsBwd(0x1000, 128, 64, 0x2000, 128, 64, 0x3000, y, 128, 64, 0x5000, 2)
+                                  for y in (0x4000, 0x8000)])
+    assert B.rmsnorm_rope_bwd(sets, 0x6000, 4, 64, 64, 0x7000, 0, 1.0, 1e-6, 2, 0, 0x9000, 1 << 24) == ARG
+
+
+def test_output_rows_that_overlap_are_refused():
+    # two heads of a token and two tokens of a head at one place
+    assert rope(y_token=64, y_head=64) == SHAPE
+    assert rope(y_token=64, y_head=128, T=2, heads=3, positions=None) == NULL
+    assert rope(y_token=64, y_head=255, positions=None) == SHAPE
+    assert rope(y_token=64, y_head=256, positions=None) == NULL  # heads outside tokens: accepted so far
+    assert rope(bwd=True, dx_token=64, dx_head=64) == SHAPE
+    # inputs may
+    assert rope(x_token=64, x_head=64, positions=None) == NULL
+
+
+def test_in_place_addition_refuses_shared_rows():
+    buf = torch.zeros(8, 40)
+    w = torch.ones(16)
+    for a, b in ((buf[:, :16], buf[:, 8:24]), (buf[:4, :16], buf[2:6, :16]), (buf[:, :16], buf[:, :16]),
+                 (buf[:4, 16:32], buf[1:5, 8:24]), (buf.view(-1)[:64].view(4, 16), buf.view(-1)[48:112].view(4, 16))):
+        assert fused._share_rows(a, b) and fused._share_rows(b, a)
+        with pytest.raises(ValueError):
+            fused.rms_norm_add_(a, b, w)
+    for a, b in ((buf[:, :16], buf[:, 16:32]), (buf[:, 24:40], buf[:, 8:24]), (buf[:4, :16], buf[4:, :16]),
+                 (buf.view(-1)[:64].view(4, 16), buf.view(-1)[64:128].view(4, 16)), (buf[:1, :16], buf[:1, 16:32])):
+        assert not fused._share_rows(a, b) and not fused._share_rows(b, a)
+
+
+def test_forward_mode_and_frequencies_gradients_are_refused():
+    x, w = torch.zeros(4, 8), torch.ones(8)
+    h, pos, freq = torch.zeros(4, 2, 8), torch.zeros(4, dtype=torch.int64), torch.ones(4, dtype=torch.float64)
+    with torch.autograd.forward_ad.dual_level():
+        d = torch.autograd.forward_ad.make_dual(x, torch.ones(4, 8))
+        dh = torch.autograd.forward_ad.make_dual(h, torch.ones(4, 2, 8))
+        for call in (lambda: fused.rms_norm_add(d, x, w), lambda: fused.rms_norm_add_(x, d, w),
+                     lambda: fused.rms_norm_quant(d, w), lambda: fused.rms_norm_rope(dh, None, w, None, pos, freq)):
+            with pytest.raises(RuntimeError, match="forward-mode"):
+                call()
+    with pytest.raises(ValueError):
+        fused.rms_norm_rope(h, None, w, None, pos, freq.requires_grad_())
+
+
+def test_modes_and_transforms_take_the_custom_ops():
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    class Mode(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            return func(*args, **(kwargs or {}))
+    x = torch.zeros(3)
+    assert fused._eager(x, None, torch.nn.Parameter(x))
+    with Mode():
+        assert not fused._eager(x)
+    seen = []
+    torch.func.vmap(lambda t: seen.append(fused._eager(t)) or t)(x)
+    torch.func.grad(lambda t: seen.append(fused._eager(t)) or t.sum())(x)
+    assert seen == [False, False]
+
+
+def test_rope_module_from_the_meta_device():
+    m = fused.RMSNormRope(16, 8, base=500.0, device="meta")
+    assert m.inv_freq.is_meta
+    m = m.to_empty(device="cpu")
+    assert m.inv_freq.tolist() == fused.rope_frequencies(8, 500.0, device="cpu")[0].tolist()

@@ -290,3 +290,38 @@ def test_a_compiled_graph_has_no_breaks():
     out = torch.compile(f, backend="eager", fullgraph=True)(x, res)
     want = f(x, res)
     assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+def test_a_captured_training_step_draws_and_differentiates_anew():
+    N, p = 1032, 0.25
+    w, rng = leaf(weight(N, "bfloat16", False)), fused.dropout_state(3)
+    x, res, dy = (randn(1100, N, dtype="bfloat16", seed=s).cuda() for s in (95, 96, 97))
+    x.requires_grad_()
+    q, wq = leaf(randn(64, 3, 64, dtype="bfloat16", seed=98)), leaf(weight(64, "bfloat16", False))
+    pos, inv = torch.arange(64, device="cuda"), freqs(64).cuda()
+
+    def step():
+        y, h = fused.rms_norm_add(x, res, w, EPS, False, p, rng)
+        a, _ = fused.rms_norm_rope(q, None, wq, None, pos, inv)
+        out = (y, h, a) + torch.autograd.grad((y, a), (x, w, q, wq), (dy, a.detach()))
+        rng[1] += 1
+        return [t.detach() for t in out]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in (11, 12):
+        for offset in (5, 1 << 40):
+            with torch.no_grad():
+                x.copy_(randn(1100, N, dtype="bfloat16", seed=seed))
+            rng.copy_(torch.tensor([seed, offset]))
+            graph.replay()
+            replayed = [t.clone() for t in got]
+            assert rng.tolist() == [seed, offset + 1]
+            rng.copy_(torch.tensor([seed, offset]))
+            for a, b in zip(replayed, step()):
+                assert torch.equal(a, b)
