@@ -105,11 +105,14 @@ struct RopeArgs {
     int64_t units;
 };
 
+// How a head row is taken: entry by entry, or in 16-byte octets with neighbours paired,
+// whole octets of the halves paired, or the partners through shared memory.
+enum RopeRows { kRopeEntries = 0, kRopeNeighbours, kRopeHalves, kRopeSwap };
+
 struct RopePlan {
     int dtype = 0;
-    bool aligned = false;      // 16-byte octets; else element by element
-    bool interleaved = false;
-    int lanes = 0;             // per head row, where aligned
+    RopeRows rows = kRopeEntries;
+    int lanes = 0;             // per head row, of octets
     int pairs = 0;             // per lane, elsewhere
     int threads = 0;
     int64_t blocks = 0;

@@ -20,9 +20,10 @@ static_assert(kRopeMaxSets == RMSNORM_ROPE_MAX_SETS, "sets of a rope call");
 // 16.9 us without it, 1024 x 4096 15.7 with it).
 constexpr int64_t kRingLeastRows = 1024;
 
-// The rotation's backward: heads for which a group computes a token's cosines and sines
-// once (rope.cu), and blocks per SM (what its registers leave).
-constexpr int kRopeBwdRun = 8;
+// The rotation: most heads for which a group computes a token's cosines and sines once
+// (rope.cu), but for the forward of whole octets, and the backward's blocks per SM (what
+// its registers leave).
+constexpr int kRopeRun = 8;
 constexpr int kRopeBwdBlocks = 3;
 
 std::mutex g_fused_mu;
@@ -310,12 +311,11 @@ rmsnorm_status rope_plan(RopeArgs& a, int dtype, int interleaved, bool wide, boo
     const int sms = current_sms(dev);
     if (!sms) return RMSNORM_ERR_CUDA;
     p.dtype = dtype;
-    p.interleaved = interleaved != 0;
-    p.aligned = wide && a.D % 8 == 0 && (interleaved || a.R % 16 == 0);
+    if (wide && a.D % 8 == 0) p.rows = interleaved ? kRopeNeighbours : a.R % 16 == 0 ? kRopeHalves : kRopeSwap;
     p.threads = kFusedGroupThreads;
     int group = 32;  // lanes that share an item
-    if (p.aligned) {
-        const int64_t units = interleaved ? ceil_div(a.D, 16) : a.R / 16 + ceil_div(a.D - a.R, 16);
+    if (p.rows != kRopeEntries) {
+        const int64_t units = p.rows == kRopeHalves ? a.R / 16 + ceil_div(a.D - a.R, 16) : ceil_div(a.D, 16);
         for (p.lanes = 4; p.lanes < units;) p.lanes *= 2;
         group = p.lanes;
     } else {
@@ -323,8 +323,8 @@ rmsnorm_status rope_plan(RopeArgs& a, int dtype, int interleaved, bool wide, boo
     }
     const int64_t full = static_cast<int64_t>(sms) * 2048 / group;  // groups that fill the GPU
     p.smem = bwd ? static_cast<size_t>(p.threads / group) * a.D * 4 : 0;
-    if (p.aligned) {
-        const int batch = bwd ? kRopeBwdRun : rope_fwd_batch(dtype);
+    if (p.rows != kRopeEntries) {
+        const int batch = bwd || p.rows == kRopeSwap ? kRopeRun : rope_fwd_batch(dtype);
         a.chunk = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(batch, a.T * a.heads / full)));
         a.chunks0 = static_cast<int>(ceil_div(a.set[0].heads, a.chunk));
         a.nchunk = a.chunks0 + static_cast<int>(a.nsets > 1 ? ceil_div(a.set[1].heads, a.chunk) : 0);

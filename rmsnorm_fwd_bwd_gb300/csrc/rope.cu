@@ -21,8 +21,9 @@
 // TB/s; 138 us with the sines by sincospif and all heads of a token by one group, 125 us
 // with two heads in flight a lane instead of four), fp32 16384 x 40 x 128 97 us (6.9
 // TB/s); backward 16384 x 20 x 256 bf16 94 us (5.35 TB/s, bound by latency at 12 warps an
-// SM: its sums and weight hold the registers). 64 tokens: 2.2 us a call in a graph. Head
-// rows that do not split into octets go entry by entry, at 20-50% of the copy's rate.
+// SM: its sums and weight hold the registers). 64 tokens: 2.2 us a call in a graph. Halves
+// that do not meet octet by octet swap partners through shared memory (rope_fwd_swap); head
+// rows off 16 bytes or of no whole octets go entry by entry, at 13-40% of the copy's rate.
 #include "fused.h"
 #include "launch.h"
 #include "octet.cuh"
@@ -500,6 +501,281 @@ __global__ void __maxnreg__((DT == kF32 ? 168 : 144)) rope_bwd_octets(const Rope
     griddep_launch_dependents();
 }
 
+// Halves whose octets do not meet octets (R / 2 no multiple of 8), D whole octets: a lane
+// owns octets li and li + L as they stand and gets the entries' partners through shared
+// memory. A warp's entry e of octet h * L + li lies at [e][h][lane], so that a lane's
+// writes, and the reads at a fixed distance in the row, touch every bank once. Entries from
+// R on read a zero. Bound by instructions and, backward, by latency at 12 warps an SM.
+// Against entry by entry: bf16 32768 x 40 x 128 with 24 rotated 113 us and 231, its
+// backward at 16384 x 20 x 128 66 and 166; 256 with 250 rotated 69 and 273, 113 and 593;
+// 512 x 40 x 128 8.3 and 6.6, of which the turns and the places are most.
+constexpr int kSwapFloats = 8 * 2 * 32 + 8;  // of a warp, and the zero
+
+template <int L> struct Swap {
+    float* buf;    // this warp's two buffers: heads alternate, with one warp barrier each
+    int from[16];  // where the entries' partners lie
+    __device__ __forceinline__ Swap(float* all, const RopeArgs& a, int li) {
+        const int lane = threadIdx.x & 31;
+        buf = all + (threadIdx.x >> 5) * 2 * kSwapFloats;
+        if (lane < 2) buf[lane * kSwapFloats + kSwapFloats - 8] = 0.f;
+        const int half = a.R / 2;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const int col = column(k, li);
+            const int to = col < half ? col + half : col - half;
+            const int o = to >> 3;
+            from[k] = col < a.R ? (to & 7) * 64 + (o / L) * 32 + lane / L * L + o % L : kSwapFloats - 8;
+        }
+        __syncwarp();
+    }
+    // The column of a lane's entry k.
+    __device__ __forceinline__ static int column(int k, int li) { return 8 * ((k >> 3) * L + li) + (k & 7); }
+    // The partners of a lane's entries; `which`: not the buffer of the call before.
+    __device__ __forceinline__ void partners(int which, const uint64_t (&f)[8], uint64_t (&p)[8]) const {
+        float* b = buf + which * kSwapFloats;
+        float* mine = b + (threadIdx.x & 31);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f2_unpack(f[k], mine[(2 * k % 8) * 64 + k / 4 * 32], mine[(2 * k % 8 + 1) * 64 + k / 4 * 32]);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) p[k] = f2_pack(b[from[2 * k]], b[from[2 * k + 1]]);
+    }
+    // An entry is itself * c + its partner * s (back: turned back). Each angle is computed
+    // once: a lane has those of pairs 8 li to 8 li + 7, which are its octet's in the first
+    // half, and the second half gets them as it gets partners.
+    __device__ __forceinline__ void turns(const Turns& turns, const RopeArgs& a, int li, int64_t pos, bool back, uint64_t (&c)[8],
+                                          uint64_t (&s)[8]) const {
+        uint64_t c4[4], s4[4];
+        turns.of_lane(a, li, pos, c4, s4);
+        float cs[8], sn[8];
+        float* mine = buf + (threadIdx.x & 31);
+        __syncwarp();  // the last head's partners have been read
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            f2_unpack(c4[k], cs[2 * k], cs[2 * k + 1]);
+            f2_unpack(s4[k], sn[2 * k], sn[2 * k + 1]);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            mine[k * 64] = cs[k];
+            mine[k * 64 + kSwapFloats] = sn[k];
+        }
+        __syncwarp();
+        float ck[16], sk[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const int col = column(k, li);
+            ck[k] = col < a.R ? buf[from[k]] : 1.f;
+            sk[k] = buf[from[k] + kSwapFloats];  // 0 from R on
+            if (k < 8 && col < a.R / 2) {
+                ck[k] = cs[k];
+                sk[k] = -sn[k];
+            }
+            if (back) sk[k] = -sk[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            c[k] = f2_pack(ck[2 * k], ck[2 * k + 1]);
+            s[k] = f2_pack(sk[2 * k], sk[2 * k + 1]);
+        }
+        __syncwarp();
+    }
+};
+
+template <int DT>
+__device__ __forceinline__ void to_entries(const uint32_t (&w)[2][Oct<DT>::kWords], uint64_t (&f)[8]) {
+    octet_pairs<DT>(w[0], *reinterpret_cast<uint64_t(*)[4]>(&f[0]));
+    octet_pairs<DT>(w[1], *reinterpret_cast<uint64_t(*)[4]>(&f[4]));
+}
+template <int DT>
+__device__ __forceinline__ void store_entries(char* row, int a, int b, const uint64_t (&f)[8]) {
+    constexpr int EB = Elem<DT>::kBytes, B = Oct<DT>::kBytes;
+    uint32_t w[Oct<DT>::kWords];
+    pairs_octet<DT>(*reinterpret_cast<const uint64_t(*)[4]>(&f[0]), w);
+    octet_store<EB, Oct<DT>::kWords, true>(row + a * B, w, a >= 0 ? B : 0, false, false);
+    pairs_octet<DT>(*reinterpret_cast<const uint64_t(*)[4]>(&f[4]), w);
+    octet_store<EB, Oct<DT>::kWords, true>(row + b * B, w, b >= 0 ? B : 0, false, false);
+}
+template <int DT>
+__device__ __forceinline__ void entry_gains(const RopeSet& set, float one, int oa, int ob, uint64_t (&g)[8]) {
+    uint32_t w[2][Oct<DT>::kWords];
+    load16<DT>(static_cast<const char*>(set.gamma), oa, ob, set.gamma != nullptr, w);
+    to_entries<DT>(w, g);
+    const float add = set.gamma ? one : 1.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) g[k] = f2_add(g[k], f2_pack(add, add));
+}
+
+// As rope_fwd_octets, but with a run of heads as in rope_bwd_octets: a lane has twice the
+// cosines and sines to get.
+template <int DT, int L>
+__global__ void __maxnreg__(128) rope_fwd_swap(const RopeArgs a) {
+    constexpr int W = Oct<DT>::kWords;
+    constexpr int EB = Elem<DT>::kBytes;
+    constexpr int BATCH = rope_fwd_batch(DT);
+    __shared__ Turns turns;
+    __shared__ float swaps[kFusedGroupThreads / 32 * 2 * kSwapFloats];
+    const int li = threadIdx.x % L;
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * (blockDim.x / L) + threadIdx.x / L;
+    griddep_wait();
+    const bool live = item < a.T * a.nchunk;
+    int chunk;
+    const int64_t token = split_item(live ? item : 0, a.nchunk, chunk);
+    const int which = chunk >= a.chunks0 ? 1 : 0;
+    if (which) chunk -= a.chunks0;
+    const RopeSet& set = a.set[which];
+    const int from = chunk * a.chunk;
+    const int n = live ? min(a.chunk, set.heads - from) : 0;
+    const int oa = li < a.D / 8 ? li : -1, ob = li + L < a.D / 8 ? li + L : -1;
+    const char* xb = static_cast<const char*>(set.x) + (token * set.x_token + from * set.x_head) * EB;
+    char* yb = static_cast<char*>(set.y) + (token * set.y_token + from * set.y_head) * EB;
+    const int64_t x_step = set.x_head * EB, y_step = set.y_head * EB;
+    uint32_t xw[BATCH][2][W];
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) {
+        load16<DT>(xb, oa, ob, j < n, xw[j]);
+        xb += x_step;
+    }
+    uint64_t c[8], s[8];
+    const int64_t pos = a.pos[token];
+    const Swap<L> swap(swaps, a, li);
+    turns.fill(a, L);
+    __syncthreads();
+    swap.turns(turns, a, li, pos, false, c, s);
+    {
+        uint64_t g[8], gp[8];
+        entry_gains<DT>(set, a.one, oa, ob, g);
+        swap.partners(1, g, gp);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            c[k] = f2_mul(c[k], g[k]);
+            s[k] = f2_mul(s[k], gp[k]);
+        }
+    }
+    const float inv_d = 1.0f / static_cast<float>(a.D);
+    for (int h = 0; h < a.chunk; h += BATCH) {
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            if (h + j >= a.chunk) break;
+            uint64_t x[8], p[8];
+            to_entries<DT>(xw[j], x);
+            load16<DT>(xb, oa, ob, h + j + BATCH < n, xw[j]);
+            xb += x_step;
+            swap.partners(j & 1, x, p);
+            uint64_t ss = f2_mul(x[0], x[0]);
+#pragma unroll
+            for (int k = 1; k < 8; ++k) ss = f2_fma(x[k], x[k], ss);
+            float r = row_rsqrt(row_sum<L>(f2_sum(ss), nullptr), inv_d, a.eps);
+            if (!set.gamma) r = 1.f;
+            const uint64_t r2 = f2_pack(r, r);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = f2_mul(f2_fma(x[k], c[k], f2_mul(p[k], s[k])), r2);
+            if (h + j < n) store_entries<DT>(yb, oa, ob, x);
+            yb += y_step;
+        }
+    }
+    griddep_launch_dependents();
+}
+
+// As rope_bwd_octets.
+template <int DT, int L>
+__global__ void __maxnreg__(168) rope_bwd_swap(const RopeArgs a) {
+    constexpr int W = Oct<DT>::kWords;
+    constexpr int EB = Elem<DT>::kBytes;
+    extern __shared__ float sums[];  // [groups of the block][D]
+    __shared__ Turns turns;
+    __shared__ float swaps[kFusedGroupThreads / 32 * 2 * kSwapFloats];
+    const int li = threadIdx.x % L;
+    const int groups = blockDim.x / L;
+    const int group = threadIdx.x / L;
+    griddep_wait();
+    const int oa = li < a.D / 8 ? li : -1, ob = li + L < a.D / 8 ? li + L : -1;
+    const Swap<L> swap(swaps, a, li);
+    turns.fill(a, L);
+    __syncthreads();
+    const float inv_d = 1.0f / static_cast<float>(a.D);
+#pragma unroll 1
+    for (int i = 0; i < a.nsets; ++i) {
+        const RopeSet& set = a.set[i];
+        const bool norm = set.gamma != nullptr;
+        uint64_t g[8], acc[8];
+        entry_gains<DT>(set, a.one, oa, ob, g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] = f2_pack(0.f, 0.f);
+        const int run = min(a.chunk, set.heads);
+        const int nchunk = (set.heads + run - 1) / run;
+        const int64_t items = a.T * nchunk;
+        const int64_t d_step = set.dy_head * EB, x_step = set.x_head * EB, y_step = set.y_head * EB;
+        for (int64_t base = static_cast<int64_t>(blockIdx.x) * groups; base < items;
+             base += static_cast<int64_t>(gridDim.x) * groups) {
+            const int64_t item = base + group;
+            const bool live = item < items;
+            int chunk;
+            const int64_t token = split_item(live ? item : 0, nchunk, chunk);
+            const int from = chunk * run;
+            const int n = live ? min(run, set.heads - from) : 0;
+            const int64_t pos = a.pos[token];
+            const char* db = static_cast<const char*>(set.dy) + (token * set.dy_token + from * set.dy_head) * EB;
+            const char* xb = static_cast<const char*>(set.x) + (token * set.x_token + from * set.x_head) * EB;
+            char* yb = static_cast<char*>(set.y) + (token * set.y_token + from * set.y_head) * EB;
+            uint32_t dw[2][W], xw[2][W];
+            load16<DT>(db, oa, ob, n > 0, dw);
+            load16<DT>(xb, oa, ob, norm && n > 0, xw);
+            uint64_t c[8], s[8];
+            swap.turns(turns, a, li, pos, true, c, s);
+            // run is the same everywhere: the whole warp goes round as often
+#pragma unroll 2
+            for (int h = 0; h < run; ++h) {
+                uint64_t v[8], x[8], p[8];
+                to_entries<DT>(dw, v);
+                to_entries<DT>(xw, x);
+                db += d_step;
+                xb += x_step;
+                load16<DT>(db, oa, ob, h + 1 < n, dw);
+                load16<DT>(xb, oa, ob, norm && h + 1 < n, xw);
+                swap.partners(h & 1, v, p);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = f2_fma(v[k], c[k], f2_mul(p[k], s[k]));
+                if (norm) {
+                    uint64_t ss = f2_pack(0.f, 0.f), ux = f2_pack(0.f, 0.f);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        ss = f2_fma(x[k], x[k], ss);
+                        ux = f2_fma(f2_mul(v[k], g[k]), x[k], ux);
+                    }
+                    const float r = row_rsqrt(row_sum<L>(f2_sum(ss), nullptr), inv_d, a.eps);
+                    const float m = row_sum<L>(f2_sum(ux), nullptr) * inv_d * r;
+                    const float e = -(r * m);
+                    const uint64_t r2 = f2_pack(r, r), e2 = f2_pack(e, e);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        x[k] = f2_mul(x[k], r2);
+                        acc[k] = f2_fma(v[k], x[k], acc[k]);
+                        v[k] = f2_fma(x[k], e2, f2_mul(f2_mul(v[k], g[k]), r2));
+                    }
+                }
+                if (h < n) store_entries<DT>(yb, oa, ob, v);
+                yb += y_step;
+            }
+        }
+        if (!norm) continue;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int o = k < 4 ? oa : ob;
+            if (o >= 0) f2_unpack(acc[k], sums[group * a.D + 8 * o + 2 * (k & 3)], sums[group * a.D + 8 * o + 2 * (k & 3) + 1]);
+        }
+        __syncthreads();
+        float* out = a.ws + (i * a.units + blockIdx.x) * a.ldws;
+        for (int col = threadIdx.x; col < a.D; col += blockDim.x) {
+            float t = sums[col];
+            for (int k = 1; k < groups; ++k) t += sums[k * a.D + col];
+            out[col] = t;
+        }
+    }
+    griddep_launch_dependents();
+}
+
 // Any D, R and alignment: a warp takes a chunk of a token's heads, a lane the pairs
 // li, li + 32, ... (PK of them at most), loaded and stored entry by entry. The
 // entries from R on are paired as neighbours and not turned.
@@ -656,11 +932,14 @@ __global__ void __launch_bounds__(kFusedGroupThreads) rope_pairs(const RopeArgs 
 // ---------------------------------------------------------------------------
 // dispatch
 // ---------------------------------------------------------------------------
-template <int DT, bool INTER, bool BWD>
+template <int DT, RopeRows ROWS, bool BWD>
 static const void* rope_octets_for(int lanes) {
+    constexpr bool INTER = ROWS == kRopeNeighbours;
 #define RMSNORM_ROPE(L)                                                                              \
     if (lanes == L) {                                                                                \
-        if constexpr (BWD) return reinterpret_cast<const void*>(&rope_bwd_octets<DT, INTER, L>);     \
+        if constexpr (ROWS == kRopeSwap && BWD) return reinterpret_cast<const void*>(&rope_bwd_swap<DT, L>); \
+        else if constexpr (ROWS == kRopeSwap) return reinterpret_cast<const void*>(&rope_fwd_swap<DT, L>); \
+        else if constexpr (BWD) return reinterpret_cast<const void*>(&rope_bwd_octets<DT, INTER, L>); \
         else return reinterpret_cast<const void*>(&rope_fwd_octets<DT, INTER, L>);                   \
     }
     RMSNORM_ROPE(4)
@@ -672,8 +951,12 @@ static const void* rope_octets_for(int lanes) {
 }
 template <int DT, bool BWD>
 static const void* rope_kernel_for(const RopePlan& p) {
-    if (p.aligned)
-        return p.interleaved ? rope_octets_for<DT, true, BWD>(p.lanes) : rope_octets_for<DT, false, BWD>(p.lanes);
+    switch (p.rows) {
+    case kRopeNeighbours: return rope_octets_for<DT, kRopeNeighbours, BWD>(p.lanes);
+    case kRopeHalves: return rope_octets_for<DT, kRopeHalves, BWD>(p.lanes);
+    case kRopeSwap: return rope_octets_for<DT, kRopeSwap, BWD>(p.lanes);
+    default: break;
+    }
     return p.pairs <= 2 ? reinterpret_cast<const void*>(&rope_pairs<DT, 2, BWD>)
                         : reinterpret_cast<const void*>(&rope_pairs<DT, 8, BWD>);
 }

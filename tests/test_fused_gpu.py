@@ -718,6 +718,43 @@ def test_rope_bwd_layouts_and_weights(how, dtype):
             check_rope_bwd(dys, xs, ws, pos, R, dtype, inter, dxs, dws, 1.25, True)
 
 
+# rows of whole octets whose halves do not meet octet by octet (partners through shared
+# memory), with runs of several heads and without, and whole-octet halves with runs
+SWAP_SHAPES = [(3, 2, 1, 8, 6), (3, 2, 1, 8, 2), (6, 3, 2, 24, 18), (5, 5, 1, 64, 62), (5, 3, 2, 72, 72), (4, 3, 1, 120, 8),
+               (4, 9, 2, 128, 126), (4, 3, 1, 136, 134), (3, 2, 2, 256, 250), (3, 3, 1, 264, 2), (2, 2, 1, 512, 510),
+               (21000, 9, 2, 64, 12), (7000, 7, 6, 128, 40), (2300, 21, 1, 200, 104), (7000, 7, 6, 128, 64)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,Hq,Hk,D,R", SWAP_SHAPES)
+def test_rope_of_halves_off_the_octets(T, Hq, Hk, D, R, dtype):
+    xs = [randn(T, Hq, D, dtype=dtype, seed=100), randn(T, Hk, D, dtype=dtype, seed=101)]
+    dys = [randn(T, Hq, D, dtype=dtype, seed=102), randn(T, Hk, D, dtype=dtype, seed=103)]
+    pos = torch.arange(T) * 3 + 1
+    for how, ws, offset in (("dense", [weight(D, dtype, False), weight(D, dtype, False, 8)], False),
+                            ("wide", [None, weight(D, dtype, True)], True)):
+        check_rope(xs, ws, pos, R, dtype, False, run_rope(xs, ws, pos, R, dtype, False, 1.25, offset, how), 1.25, offset)
+        dxs, dws = run_rope_bwd(dys, xs, ws, pos, R, dtype, False, 1.25, offset, how)
+        check_rope_bwd(dys, xs, ws, pos, R, dtype, False, dxs, dws, 1.25, offset)
+
+
+@pytest.mark.parametrize("T,H", [(11, 5), (6000, 9)])
+def test_rope_of_halves_off_the_octets_in_place(T, H):
+    for dtype in DTYPES:
+        D, R = 128, 40
+        x, dy, w = randn(T, H, D, dtype=dtype, seed=104), randn(T, H, D, dtype=dtype, seed=105), weight(D, dtype, False)
+        pos = torch.arange(T)
+        want = run_rope([x], [w], pos, R, dtype, False)[0]
+        want_d, want_w = run_rope_bwd([dy], [x], [w], pos, R, dtype, False)
+        xt, dt, wt, pt, ft = x.cuda(), dy.cuda(), w.cuda(), pos.cuda(), freqs(R).cuda()
+        dw = torch.empty_like(wt)
+        ws = torch.empty(B.rmsnorm_rope_bwd_workspace_size(T, H, D, dtype), dtype=torch.uint8, device="cuda")
+        assert B.rmsnorm_rope_bwd(B.rope_heads_bwd([(dt, xt, wt, dt, dw)]), pt, T, D, R, ft, 0, 1.0, EPS, dtype, 0, ws,
+                                  ws.numel()) == 0
+        assert B.rmsnorm_rope_fwd(B.rope_heads([(xt, wt, xt)]), pt, T, D, R, ft, 0, 1.0, EPS, dtype, 0) == 0
+        assert torch.equal(dt.cpu(), want_d[0]) and torch.equal(dw.cpu(), want_w[0]) and torch.equal(xt.cpu(), want)
+
+
 def test_rope_bwd_is_deterministic():
     T, H, D = 3000, 3, 128
     dys, xs = [randn(T, H, D, dtype="bfloat16", seed=78)], [randn(T, H, D, dtype="bfloat16", seed=79)]
