@@ -321,7 +321,11 @@ rmsnorm_status rope_plan(RopeArgs& a, int dtype, int interleaved, bool wide, boo
     } else {
         p.pairs = static_cast<int>(ceil_div(a.R / 2 + ceil_div(a.D - a.R, 2), 32));
     }
-    const int64_t full = static_cast<int64_t>(sms) * 2048 / group;  // groups that fill the GPU
+    // groups that fill the GPU: 1024 threads an SM, of which the registers leave 640 in the
+    // forward and 384 in the backward (bf16 1024 x 40 x 128: forward 5.9 us, 8.8 by 2048
+    // threads; backward 14.5, 19.4 by 2048, 15.9 by 640), or 512 where a token's turns take
+    // longer (1536 x 40 x 128, 24 rotated: 9.7 us, 20.1 by 2048)
+    const int64_t full = static_cast<int64_t>(sms) * (p.rows == kRopeSwap ? 512 : 1024) / group;
     p.smem = bwd ? static_cast<size_t>(p.threads / group) * a.D * 4 : 0;
     if (p.rows != kRopeEntries) {
         const int batch = bwd || p.rows == kRopeSwap ? kRopeRun : rope_fwd_batch(dtype);

@@ -508,7 +508,7 @@ __global__ void __maxnreg__((DT == kF32 ? 168 : 144)) rope_bwd_octets(const Rope
 // R on read a zero. Bound by instructions and, backward, by latency at 12 warps an SM.
 // Against entry by entry: bf16 32768 x 40 x 128 with 24 rotated 113 us and 231, its
 // backward at 16384 x 20 x 128 66 and 166; 256 with 250 rotated 69 and 273, 113 and 593;
-// 512 x 40 x 128 8.3 and 6.6, of which the turns and the places are most.
+// 512 x 40 x 128 6.0 and 6.6.
 constexpr int kSwapFloats = 8 * 2 * 32 + 8;  // of a warp, and the zero
 
 template <int L> struct Swap {
