@@ -112,7 +112,7 @@ enum RopeRows { kRopeEntries = 0, kRopeNeighbours, kRopeHalves, kRopeSwap };
 struct RopePlan {
     int dtype = 0;
     RopeRows rows = kRopeEntries;
-    int lanes = 0;             // per head row, of octets
+    int lanes = 0;             // per head row
     int pairs = 0;             // per lane, elsewhere
     int threads = 0;
     int64_t blocks = 0;

@@ -313,14 +313,16 @@ rmsnorm_status rope_plan(RopeArgs& a, int dtype, int interleaved, bool wide, boo
     p.dtype = dtype;
     if (wide && a.D % 8 == 0) p.rows = interleaved ? kRopeNeighbours : a.R % 16 == 0 ? kRopeHalves : kRopeSwap;
     p.threads = kFusedGroupThreads;
-    int group = 32;  // lanes that share an item
     if (p.rows != kRopeEntries) {
         const int64_t units = p.rows == kRopeHalves ? a.R / 16 + ceil_div(a.D - a.R, 16) : ceil_div(a.D, 16);
         for (p.lanes = 4; p.lanes < units;) p.lanes *= 2;
-        group = p.lanes;
     } else {
-        p.pairs = static_cast<int>(ceil_div(a.R / 2 + ceil_div(a.D - a.R, 2), 32));
+        // up to four pairs a lane (eight of 32 lanes) and few lanes, whose sums take fewer steps
+        const int64_t pairs = a.R / 2 + ceil_div(a.D - a.R, 2);
+        for (p.lanes = 8; p.lanes < 32 && 4 * p.lanes < pairs;) p.lanes *= 2;
+        p.pairs = static_cast<int>(ceil_div(pairs, p.lanes));
     }
+    const int group = p.lanes;  // lanes that share an item
     // groups that fill the GPU: 1024 threads an SM, of which the registers leave 640 in the
     // forward and 384 in the backward (bf16 1024 x 40 x 128: forward 5.9 us, 8.8 by 2048
     // threads; backward 14.5, 19.4 by 2048, 15.9 by 640), or 512 where a token's turns take

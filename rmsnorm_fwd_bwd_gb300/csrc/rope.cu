@@ -23,7 +23,7 @@
 // TB/s); backward 16384 x 20 x 256 bf16 94 us (5.35 TB/s, bound by latency at 12 warps an
 // SM: its sums and weight hold the registers). 64 tokens: 2.2 us a call in a graph. Halves
 // that do not meet octet by octet swap partners through shared memory (rope_fwd_swap); head
-// rows off 16 bytes or of no whole octets go entry by entry, at 13-40% of the copy's rate.
+// rows off 16 bytes or of no whole octets go entry by entry, at 19-60% of the copy's rate.
 #include "fused.h"
 #include "launch.h"
 #include "octet.cuh"
@@ -507,7 +507,7 @@ __global__ void __maxnreg__((DT == kF32 ? 168 : 144)) rope_bwd_octets(const Rope
 // writes, and the reads at a fixed distance in the row, touch every bank once. Entries from
 // R on read a zero. Bound by instructions and, backward, by latency at 12 warps an SM.
 // Against entry by entry: bf16 32768 x 40 x 128 with 24 rotated 113 us and 231, its
-// backward at 16384 x 20 x 128 66 and 166; 256 with 250 rotated 69 and 273, 113 and 593;
+// backward at 16384 x 20 x 128 66 and 166; 256 with 250 rotated 69 and 143, 113 and 275;
 // 512 x 40 x 128 6.0 and 6.6.
 constexpr int kSwapFloats = 8 * 2 * 32 + 8;  // of a warp, and the zero
 
@@ -776,15 +776,17 @@ __global__ void __maxnreg__(168) rope_bwd_swap(const RopeArgs a) {
     griddep_launch_dependents();
 }
 
-// Any D, R and alignment: a warp takes a chunk of a token's heads, a lane the pairs
-// li, li + 32, ... (PK of them at most), loaded and stored entry by entry. The
-// entries from R on are paired as neighbours and not turned.
-template <int PK>
+// Any D, R and alignment: a group of L lanes takes a chunk of a token's heads, a lane the
+// pairs li, li + L, ... (PK of them at most), loaded and stored entry by entry. The
+// entries from R on are paired as neighbours and not turned. Bound by the loads' latency
+// and instructions. bf16 32768 x 40 x 90 212 us with four pairs a lane (two of 32 lanes 233,
+// eight 283), its backward at 16384 x 20 x 90 136 (158, 249), 16384 x 20 x 250 143 and 274.
+template <int L, int PK>
 __device__ __forceinline__ void lane_pairs(int li, const RopeArgs& a, bool inter, int (&ca)[PK], int (&cb)[PK]) {
     const int half = a.R / 2;
 #pragma unroll
     for (int k = 0; k < PK; ++k) {
-        const int i = li + 32 * k;
+        const int i = li + L * k;
         if (i < half) {
             ca[k] = inter ? 2 * i : i;
             cb[k] = inter ? 2 * i + 1 : i + half;
@@ -797,16 +799,25 @@ __device__ __forceinline__ void lane_pairs(int li, const RopeArgs& a, bool inter
     }
 }
 
-template <int DT, int PK, bool BWD>
+// A sum over a group's lanes, which groups of a warp come to apart where their chunks end.
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+    const uint32_t lanes = (L == 32 ? 0xffffffffu : (1u << (L & 31)) - 1u) << ((threadIdx.x & 31) / L * L);
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(lanes, v, o);
+    return v;
+}
+
+template <int DT, int L, int PK, bool BWD>
 __global__ void __launch_bounds__(kFusedGroupThreads) rope_pairs(const RopeArgs a) {
     constexpr int EB = Elem<DT>::kBytes;
-    extern __shared__ float sums[];  // backward: [warps of the block][D]
-    const int li = threadIdx.x & 31;
-    const int warp = threadIdx.x >> 5;
-    const int warps = blockDim.x >> 5;
+    extern __shared__ float sums[];  // backward: [groups of the block][D]
+    const int li = threadIdx.x % L;
+    const int group = threadIdx.x / L;
+    const int groups = blockDim.x / L;
     griddep_wait();
     int ca[PK], cb[PK];
-    lane_pairs<PK>(li, a, a.interleaved != 0, ca, cb);
+    lane_pairs<L, PK>(li, a, a.interleaved != 0, ca, cb);
     float acc[BWD ? kRopeMaxSets : 1][2 * PK];
 #pragma unroll
     for (int i = 0; i < (BWD ? kRopeMaxSets : 1); ++i)
@@ -814,25 +825,29 @@ __global__ void __launch_bounds__(kFusedGroupThreads) rope_pairs(const RopeArgs 
         for (int k = 0; k < 2 * PK; ++k) acc[i][k] = 0.f;
     const float inv_d = 1.0f / static_cast<float>(a.D);
     const int64_t items = a.T * a.nchunk;
-    for (int64_t item = static_cast<int64_t>(blockIdx.x) * warps + warp; item < items;
-         item += static_cast<int64_t>(gridDim.x) * warps) {
-        const int64_t token = item / a.nchunk;
-        const int lo = static_cast<int>(item % a.nchunk) * a.chunk;
+    for (int64_t item = static_cast<int64_t>(blockIdx.x) * groups + group; item < items;
+         item += static_cast<int64_t>(gridDim.x) * groups) {
+        int lo;
+        const int64_t token = split_item(item, a.nchunk, lo);
+        lo *= a.chunk;
         const int hi = min(lo + a.chunk, a.heads);
         const int64_t pos = a.pos[token];
         float c[PK], s[PK];
 #pragma unroll
-        for (int k = 0; k < PK; ++k) {
-            c[k] = 1.f;
-            s[k] = 0.f;
-            if (li + 32 * k < a.R / 2) {
-                const int32_t phase = phase_at(turns_per_position(a.inv_freq[li + 32 * k]), pos);
+        for (int k = 0; k < PK; k += 2) {
+            const int i0 = li + L * k, i1 = i0 + L, half = a.R / 2;
+            c[k] = c[k + 1] = 1.f;
+            s[k] = s[k + 1] = 0.f;
+            if (i0 < half) {
                 uint64_t c2, s2;
-                turn_pair(phase, phase, a.mscale, a.mscale, c2, s2);
-                float other;
-                f2_unpack(c2, c[k], other);
-                f2_unpack(s2, s[k], other);
-                if (BWD) s[k] = -s[k];
+                turn_pair(phase_at(turns_per_position(a.inv_freq[i0]), pos),
+                          i1 < half ? phase_at(turns_per_position(a.inv_freq[i1]), pos) : 0, a.mscale, a.mscale, c2, s2);
+                f2_unpack(c2, c[k], c[k + 1]);
+                f2_unpack(s2, s[k], s[k + 1]);
+            }
+            if (BWD) {
+                s[k] = -s[k];
+                s[k + 1] = -s[k + 1];
             }
         }
         int at = 0;
@@ -864,7 +879,7 @@ __global__ void __launch_bounds__(kFusedGroupThreads) rope_pairs(const RopeArgs 
                             if (gb) g[j] = entry<DT>(gb, col) + a.one;
                         }
                     }
-                    if (BWD && li + 32 * k < a.R / 2) {
+                    if (BWD && li + L * k < a.R / 2) {
                         const float p = v[2 * k], z = v[2 * k + 1];
                         v[2 * k] = p * c[k] - z * s[k];
                         v[2 * k + 1] = z * c[k] + p * s[k];
@@ -878,8 +893,8 @@ __global__ void __launch_bounds__(kFusedGroupThreads) rope_pairs(const RopeArgs 
                 }
                 float r = 1.f, m = 0.f;
                 if (gb) {
-                    r = row_rsqrt(warp_allsum(ss), inv_d, a.eps);
-                    if (BWD) m = warp_allsum(q) * inv_d * r;
+                    r = row_rsqrt(group_sum<L>(ss), inv_d, a.eps);
+                    if (BWD) m = group_sum<L>(q) * inv_d * r;
                 }
 #pragma unroll
                 for (int k = 0; k < PK; ++k) {
@@ -896,7 +911,7 @@ __global__ void __launch_bounds__(kFusedGroupThreads) rope_pairs(const RopeArgs 
                         }
                     } else {
                         const float z0 = (x[2 * k] * r) * g[2 * k], z1 = (x[2 * k + 1] * r) * g[2 * k + 1];
-                        const bool rotated = li + 32 * k < a.R / 2;
+                        const bool rotated = li + L * k < a.R / 2;
                         o0 = rotated ? z0 * c[k] - z1 * s[k] : z0;
                         o1 = rotated ? z1 * c[k] + z0 * s[k] : z1;
                     }
@@ -914,14 +929,14 @@ __global__ void __launch_bounds__(kFusedGroupThreads) rope_pairs(const RopeArgs 
             __syncthreads();
 #pragma unroll
             for (int k = 0; k < PK; ++k) {
-                if (ca[k] >= 0) sums[warp * a.D + ca[k]] = acc[i][2 * k];
-                if (cb[k] >= 0) sums[warp * a.D + cb[k]] = acc[i][2 * k + 1];
+                if (ca[k] >= 0) sums[group * a.D + ca[k]] = acc[i][2 * k];
+                if (cb[k] >= 0) sums[group * a.D + cb[k]] = acc[i][2 * k + 1];
             }
             __syncthreads();
             float* out = a.ws + (i * a.units + blockIdx.x) * a.ldws;
             for (int col = threadIdx.x; col < a.D; col += blockDim.x) {
                 float t = sums[col];
-                for (int k = 1; k < warps; ++k) t += sums[k * a.D + col];
+                for (int k = 1; k < groups; ++k) t += sums[k * a.D + col];
                 out[col] = t;
             }
         }
@@ -957,8 +972,13 @@ static const void* rope_kernel_for(const RopePlan& p) {
     case kRopeSwap: return rope_octets_for<DT, kRopeSwap, BWD>(p.lanes);
     default: break;
     }
-    return p.pairs <= 2 ? reinterpret_cast<const void*>(&rope_pairs<DT, 2, BWD>)
-                        : reinterpret_cast<const void*>(&rope_pairs<DT, 8, BWD>);
+    switch (p.lanes) {
+    case 8: return reinterpret_cast<const void*>(&rope_pairs<DT, 8, 4, BWD>);
+    case 16: return reinterpret_cast<const void*>(&rope_pairs<DT, 16, 4, BWD>);
+    default: break;
+    }
+    return p.pairs <= 4 ? reinterpret_cast<const void*>(&rope_pairs<DT, 32, 4, BWD>)
+                        : reinterpret_cast<const void*>(&rope_pairs<DT, 32, 8, BWD>);
 }
 
 const void* rope_kernel(const RopePlan& p, bool bwd) {
