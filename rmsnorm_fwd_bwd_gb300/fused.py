@@ -350,9 +350,10 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[s
     * ``"linear"``: every frequency divided by factor (positions are interpolated);
     * ``"ntk"``: the base raised so that the slowest pair is slowed by factor and the
       fastest not at all;
-    * ``"yarn"``: pairs that make more than ``fast_turns`` turns within
-      ``original_length`` positions keep their frequency, those below ``slow_turns``
-      are divided by factor, those between are blended by their index, and mscale =
+    * ``"yarn"`` (Peng, Quesnelle, Fan and Shippole, 2023): pairs that make more than
+      ``fast_turns`` turns within ``original_length`` positions keep their frequency, those
+      below ``slow_turns`` are divided by factor, those between are blended by their
+      index (which may reach its end behind the last pair), and mscale =
       0.1 ln(factor) + 1.
     """
     if rotary_dim < 2 or rotary_dim % 2:
@@ -375,7 +376,7 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[s
         def pair_of(turns):  # the pair, as a real number, that makes so many turns in original_length
             return rotary_dim * math.log(original_length / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
         low = max(math.floor(pair_of(fast_turns)), 0)
-        high = min(math.ceil(pair_of(slow_turns)), half - 1)
+        high = min(math.ceil(pair_of(slow_turns)), rotary_dim - 1)  # the published limit
         span = max(high - low, 0.001)
         slow = [min(max((i - low) / span, 0.0), 1.0) for i in range(half)]
         freq = [f * (1.0 - s) + f / factor * s for f, s in zip(freq, slow)]

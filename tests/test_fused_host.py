@@ -230,6 +230,26 @@ def test_rope_frequencies_refusals(args, kw):
         fused.rope_frequencies(*args, device="cpu", **kw)
 
 
+@pytest.mark.parametrize("R,base,length,factor", [(128, 1e4, 131072, 4.0), (128, 1e4, 65536, 4.0), (64, 1e4, 131072, 4.0),
+                                                  (64, 1e4, 1 << 20, 32.0), (128, 1e4, 4096, 4.0), (128, 1e6, 32768, 4.0),
+                                                  (2, 1e4, 4096, 2.0), (8, 10.0, 1 << 20, 4.0), (8, 300.0, 1 << 14, 4.0)])
+def test_yarn_frequencies_where_the_band_ends_behind_the_last_pair(R, base, length, factor):
+    # the published ramp over the pairs' index i, written with the turns that a pair makes: i is
+    # pair(n) for n turns where length * base^(-2 i / R) = 2 pi n
+    y, _ = fused.rope_frequencies(R, base, "yarn", factor, length, device="cpu")
+    i = np.arange(R // 2)
+    f = base ** (-2.0 * i / R)
+
+    def pair(n):
+        return R / 2 * np.log(length / (2 * np.pi * n)) / np.log(base)
+    low, high = max(np.floor(pair(32.0)), 0), min(np.ceil(pair(1.0)), R - 1)
+    slow = np.clip((i - low) / max(high - low, 0.001), 0, 1)
+    assert y.tolist() == pytest.approx((f * (1 - slow) + f / factor * slow).tolist(), rel=1e-12)
+    if pair(1.0) > R // 2:
+        # every pair makes more than a turn: none is slowed by the whole factor
+        assert length * f[-1] / (2 * np.pi) > 1.0 and (f / y.numpy()).max() < factor
+
+
 # --------------------------------------------------------------------------- #
 # the torch front end's checks (before any call)
 # --------------------------------------------------------------------------- #
