@@ -372,6 +372,8 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[s
     elif scaling == "yarn":
         if original_length < 1 or not base > 1.0:
             raise ValueError("yarn needs original_length and a base above 1")
+        if not 0.0 < slow_turns <= fast_turns < math.inf:
+            raise ValueError("yarn needs 0 < slow_turns <= fast_turns")
 
         def pair_of(turns):  # the pair, as a real number, that makes so many turns in original_length
             return rotary_dim * math.log(original_length / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))

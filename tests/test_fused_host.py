@@ -250,6 +250,13 @@ def test_yarn_frequencies_where_the_band_ends_behind_the_last_pair(R, base, leng
         assert length * f[-1] / (2 * np.pi) > 1.0 and (f / y.numpy()).max() < factor
 
 
+@pytest.mark.parametrize("fast,slow", [(32.0, 0.0), (0.0, 0.0), (32.0, -1.0), (1.0, 2.0), (float("inf"), 1.0),
+                                       (float("nan"), 1.0), (32.0, float("nan"))])
+def test_yarn_refuses_turns_that_give_no_band(fast, slow):
+    with pytest.raises(ValueError, match="turns"):
+        fused.rope_frequencies(64, 1e4, "yarn", 4.0, 4096, fast, slow, device="cpu")
+
+
 # --------------------------------------------------------------------------- #
 # the torch front end's checks (before any call)
 # --------------------------------------------------------------------------- #
