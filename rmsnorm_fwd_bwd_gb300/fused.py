@@ -464,23 +464,25 @@ def _(dq, dk, q, k, q_weight, k_weight, positions, inv_freq, interleaved, mscale
             q.new_empty((D,) if q_weight is not None else (0,)), q.new_empty((D,) if k_weight is not None else (0,)))
 
 
+def _rope_save(ctx, q, k, q_weight, k_weight, positions, inv_freq, *how):
+    # heads without a weight are turned back without their values
+    ctx.save_for_backward(None if q_weight is None else q, None if k_weight is None else k, q_weight, k_weight, positions,
+                          inv_freq)
+    ctx.has_k, ctx.how = k is not None, how
+
+
 def _rope_setup(ctx, inputs, output):
-    q, k, q_weight, k_weight, positions, inv_freq, interleaved, mscale, eps, offset = inputs
-    ctx.set_materialize_grads(False)
-    ctx.save_for_backward(q, k, q_weight, k_weight, positions, inv_freq)
-    ctx.how = (interleaved, mscale, eps, offset)
+    _rope_save(ctx, *inputs)
 
 
 def _rope_grads(ctx, dq, dk, run):
     q, k, q_weight, k_weight, positions, inv_freq = ctx.saved_tensors
-    if dq is None:
-        dq = torch.zeros_like(q)
-    if k is None:
+    if not ctx.has_k:
         dk = None
-    elif dk is None:
-        dk = torch.zeros_like(k)
-    gq, gk, gqw, gkw = run(dq, dk, q, k, q_weight, k_weight, positions, inv_freq, *ctx.how)
-    return (gq, gk if k is not None else None, gqw if q_weight is not None else None,
+    # without a weight the cotangents stand in: of the heads only the shape is needed
+    gq, gk, gqw, gkw = run(dq, dk, dq if q is None else q, dk if k is None else k, q_weight, k_weight, positions, inv_freq,
+                           *ctx.how)
+    return (gq, gk if ctx.has_k else None, gqw if q_weight is not None else None,
             gkw if k_weight is not None else None, None, None, None, None, None, None)
 
 
@@ -493,11 +495,9 @@ _rope_fwd.register_autograd(_rope_backward, setup_context=_rope_setup)
 
 class _RopeFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, q_weight, k_weight, positions, inv_freq, *how):
-        ctx.set_materialize_grads(False)
-        ctx.save_for_backward(q, k, q_weight, k_weight, positions, inv_freq)
-        ctx.how = how
-        return _rope_fwd_run(q, k, q_weight, k_weight, positions, inv_freq, *how)
+    def forward(ctx, *args):
+        _rope_save(ctx, *args)
+        return _rope_fwd_run(*args)
 
     @staticmethod
     def backward(ctx, dq, dk):

@@ -325,3 +325,29 @@ def test_a_captured_training_step_draws_and_differentiates_anew():
             rng.copy_(torch.tensor([seed, offset]))
             for a, b in zip(replayed, step()):
                 assert torch.equal(a, b)
+
+
+def test_a_rotation_without_weights_keeps_no_heads():
+    T, H, D, R = 9, 4, 64, 32
+    pos, inv = torch.arange(T, device="cuda") * 5, freqs(R).cuda()
+    w = weight(D, "float32", False)
+    dq, dk = randn(T, H, D, dtype="float32", seed=30), randn(T, 2, D, dtype="float32", seed=31)
+    for wq, wk in ((None, None), (w, None), (None, w)):
+        x = [randn(T, H, D, dtype="float32", seed=32), randn(T, 2, D, dtype="float32", seed=33)]
+        for through in (fused.rms_norm_rope, lambda *a: torch.ops.rmsnorm_gb300.rope_fwd(*a, False, 1.0, EPS, False)):
+            q, k = (leaf(t) for t in x)
+            wt = [None if v is None else leaf(v) for v in (wq, wk)]
+            held = []
+            with torch.autograd.graph.saved_tensors_hooks(lambda t: held.append(t.shape) or t, lambda t: t):
+                qo, ko = through(q * 1.0, k * 1.0, *wt, pos, inv)
+            assert (q.shape in held, k.shape in held) == (wq is not None, wk is not None)
+            torch.autograd.backward([qo, ko], [dq.cuda(), dk.cuda()])
+            check_rope_bwd([dq, dk], x, [wq, wk], pos.cpu(), R, "float32", False, [q.grad.cpu(), k.grad.cpu()],
+                           [None if v is None else v.grad.cpu() for v in wt])
+            # one output unused: no gradient there but zeros
+            q, k = (leaf(t) for t in x)
+            qo, _ = through(q, k, *wt, pos, inv)
+            qo.backward(dq.cuda())
+            assert torch.all(k.grad == 0)
+            if wq is None:
+                check_rope_bwd([dq], x[:1], [None], pos.cpu(), R, "float32", False, [q.grad.cpu()], [None])
