@@ -223,18 +223,30 @@ def rms_norm_add(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torc
     return torch.ops.rmsnorm_gb300.add_fwd(*args)[:2]
 
 
+def _row_bytes(t: torch.Tensor):
+    """(address, pitch, bytes of a row, rows) of a contiguous tensor, or a 2-D one with spaced rows."""
+    N = t.shape[-1]
+    pitch = t.stride(0) if t.dim() == 2 and t.shape[0] > 1 else N
+    return t.data_ptr(), pitch * t.element_size(), N * t.element_size(), t.numel() // N
+
+
 def _share_rows(a: torch.Tensor, b: torch.Tensor) -> bool:
     """Whether rows of two tensors of one shape (contiguous, or 2-D with spaced rows) share
     memory; the halves of wider rows do not."""
-    def rows(t):
-        N = t.shape[-1]
-        pitch = t.stride(0) if t.dim() == 2 and t.shape[0] > 1 else N
-        return t.data_ptr(), pitch * t.element_size(), N * t.element_size(), t.numel() // N
-    (p, pitch, width, M), (q, pitch_b, _, _) = rows(a), rows(b)
+    (p, pitch, width, M), (q, pitch_b, _, _) = _row_bytes(a), _row_bytes(b)
     if p >= q + (M - 1) * pitch_b + width or q >= p + (M - 1) * pitch + width:
         return False
     # interleaved: of one pitch, the columns of one in the gaps of the other
     return not (pitch == pitch_b and width <= (q - p) % pitch <= pitch - width)
+
+
+def _among_rows(w: torch.Tensor, t: torch.Tensor) -> bool:
+    """Whether a contiguous row ``w`` of t's width shares memory with one of t's rows."""
+    (q, _, width, _), (p, pitch, _, M) = _row_bytes(w), _row_bytes(t)
+    if q + width <= p or q >= p + (M - 1) * pitch + width:
+        return False
+    # in a gap between two rows, or not
+    return not width <= (q - p) % pitch <= pitch - width
 
 
 def _add_in_place(x, residual, weight, eps, offset):
@@ -268,6 +280,9 @@ def rms_norm_add_(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor,
     _no_tangents("rms_norm_add_", x, residual, weight)
     if x.numel() and _share_rows(x, residual):
         raise ValueError("rms_norm_add_: x and residual must not share memory")
+    # (a weight with a stride is laid out first)
+    if x.numel() and weight.is_contiguous() and (_among_rows(weight, x) or _among_rows(weight, residual)):
+        raise ValueError("rms_norm_add_: the weight must not share memory with x or residual")
     # always the op, which marks both as changed for whoever saved them for a backward
     torch.ops.rmsnorm_gb300.add_fwd_(x, residual, weight, float(eps), bool(offset))
     return x, residual

@@ -345,6 +345,22 @@ def test_in_place_addition_refuses_shared_rows():
         assert not fused._share_rows(a, b) and not fused._share_rows(b, a)
 
 
+def test_in_place_addition_refuses_a_weight_among_its_rows():
+    # the rows are overwritten while other blocks still read the weight
+    buf = torch.zeros(8, 40)
+    flat = buf.view(-1)
+    x, res = buf[:4, :16], buf[4:, 16:32]
+    for t in (x, res):
+        for w in (t[0], t[2], flat[t.storage_offset() + 5:][:16], flat[t.storage_offset() + 125:][:16]):
+            with pytest.raises(ValueError, match="weight"):
+                fused.rms_norm_add_(x, res, w)
+    with pytest.raises(ValueError, match="weight"):
+        fused.rms_norm_add_(flat[16:48].view(2, 16), flat[64:96].view(2, 16), flat[1:17])
+    # before, between and behind the rows: such a call goes on, to the library
+    for w in (flat[16:32], flat[120 + 16:120 + 32], flat[4 * 40:][:16], torch.ones(16)):
+        assert not any(fused._among_rows(w, t) for t in (x, res))
+
+
 def test_forward_mode_and_frequencies_gradients_are_refused():
     x, w = torch.zeros(4, 8), torch.ones(8)
     h, pos, freq = torch.zeros(4, 2, 8), torch.zeros(4, dtype=torch.int64), torch.ones(4, dtype=torch.float64)
