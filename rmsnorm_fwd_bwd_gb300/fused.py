@@ -250,6 +250,15 @@ def _among_rows(w: torch.Tensor, t: torch.Tensor) -> bool:
 
 
 def _add_in_place(x, residual, weight, eps, offset):
+    # (here, where tensors have their strides and addresses also in a traced or compiled program)
+    for t in (x, residual):
+        if not t.is_contiguous() and _row_view(t)[0] is not t:
+            raise ValueError("rms_norm_add_ needs contiguous tensors, or 2-D ones with unit column stride")
+    if x.numel() and _share_rows(x, residual):
+        raise ValueError("rms_norm_add_: x and residual must not share memory")
+    # (a weight with a stride is laid out first)
+    if x.numel() and weight.is_contiguous() and (_among_rows(weight, x) or _among_rows(weight, residual)):
+        raise ValueError("rms_norm_add_: the weight must not share memory with x or residual")
     with _on(x):
         M, N = _rows(x)
         ldx, ldr = (t.stride(0) if t.dim() == 2 and M > 1 else N for t in (x, residual))
@@ -274,15 +283,7 @@ def rms_norm_add_(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor,
     _check_rows("rms_norm_add_", x, residual, weight)
     if torch.is_grad_enabled() and any(t.requires_grad for t in (x, residual, weight)):
         raise ValueError("rms_norm_add_ is not differentiable: use rms_norm_add, or torch.no_grad()")
-    for t in (x, residual):
-        if not t.is_contiguous() and _row_view(t)[0] is not t:
-            raise ValueError("rms_norm_add_ needs contiguous tensors, or 2-D ones with unit column stride")
     _no_tangents("rms_norm_add_", x, residual, weight)
-    if x.numel() and _share_rows(x, residual):
-        raise ValueError("rms_norm_add_: x and residual must not share memory")
-    # (a weight with a stride is laid out first)
-    if x.numel() and weight.is_contiguous() and (_among_rows(weight, x) or _among_rows(weight, residual)):
-        raise ValueError("rms_norm_add_: the weight must not share memory with x or residual")
     # always the op, which marks both as changed for whoever saved them for a backward
     torch.ops.rmsnorm_gb300.add_fwd_(x, residual, weight, float(eps), bool(offset))
     return x, residual

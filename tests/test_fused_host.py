@@ -361,6 +361,21 @@ def test_in_place_addition_refuses_a_weight_among_its_rows():
         assert not any(fused._among_rows(w, t) for t in (x, res))
 
 
+def test_fake_tensors_take_every_call():
+    # what traces and compiles: tensors with shapes but no addresses
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    with FakeTensorMode():
+        x, res, w = (torch.empty(s, device="cuda") for s in ((4, 16), (4, 16), (16,)))
+        a, b = fused.rms_norm_add_(x, res, w)
+        assert a is x and b is res
+        assert [t.shape for t in fused.rms_norm_add(x, res, w)] == [x.shape, x.shape]
+        assert [t.shape for t in fused.rms_norm_quant(x, w, residual=res)] == [(4, 16), (4, 1), (4, 16)]
+        h, pos = torch.empty(4, 2, 8, device="cuda"), torch.empty(4, dtype=torch.int64, device="cuda")
+        q, k = fused.rms_norm_rope(h, h, None, None, pos, torch.empty(4, dtype=torch.float64, device="cuda"))
+        assert q.shape == k.shape == h.shape
+
+
 def test_forward_mode_and_frequencies_gradients_are_refused():
     x, w = torch.zeros(4, 8), torch.ones(8)
     h, pos, freq = torch.zeros(4, 2, 8), torch.zeros(4, dtype=torch.int64), torch.ones(4, dtype=torch.float64)

@@ -292,6 +292,20 @@ def test_a_compiled_graph_has_no_breaks():
     assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
 
 
+def test_the_in_place_addition_compiles_without_breaks():
+    w = weight(64, "float32", False).cuda()
+
+    def f(x, res):
+        y, h = fused.rms_norm_add_(x, res, w)
+        return y * 2, h + 1
+    (x, res), (xc, rc) = ([randn(6, 64, dtype="float32", seed=s).cuda() for s in (25, 26)] for _ in range(2))
+    want, out = f(x, res), torch.compile(f, backend="aot_eager", fullgraph=True)(xc, rc)
+    assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+    assert torch.equal(xc, x) and torch.equal(rc, res)
+    with pytest.raises(ValueError, match="memory"):     # the addresses are looked at when the op runs
+        torch.ops.rmsnorm_gb300.add_fwd_(x, x, w, EPS, False)
+
+
 def test_a_captured_training_step_draws_and_differentiates_anew():
     N, p = 1032, 0.25
     w, rng = leaf(weight(N, "bfloat16", False)), fused.dropout_state(3)
