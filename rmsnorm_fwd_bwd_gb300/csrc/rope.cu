@@ -320,6 +320,14 @@ __global__ void __maxnreg__(96) rope_fwd_octets(const RopeArgs a) {
             qc[k] = f2_mul(qc[k], c[k]);
         }
     }
+    // Rows with an infinity or a NaN are turned again, as their sum of squares tells; all rows are
+    // where a sine of 0 met such a gain behind the rotated entries (bf16, half of 128 rotated:
+    // 103.7 us without, 104.6 so, 104.9 with masked products).
+    uint64_t sines = f2_add(ps[0], qs[0]);
+#pragma unroll
+    for (int k = 1; k < 4; ++k) sines = f2_add(sines, f2_add(ps[k], qs[k]));
+    const float all = f2_sum(sines);
+    const float finite = all == all ? __int_as_float(0x7f800000) : 0.f;
     const float inv_d = 1.0f / static_cast<float>(a.D);
     // chunk is the same everywhere: the whole warp goes round as often (the sums see it)
 #pragma unroll
@@ -336,7 +344,7 @@ __global__ void __maxnreg__(96) rope_fwd_octets(const RopeArgs a) {
         const float r = set.gamma ? row_rsqrt(sum, inv_d, a.eps) : 1.f;
         const uint64_t r2 = f2_pack(r, r);
         turn_pairs(p, q, pc, qs, qc, ps);
-        if (rotated < 8 && j < n && !(sum < __int_as_float(0x7f800000)))
+        if (rotated < 8 && j < n && !(sum < finite))
             turn_again<DT, INTER>(xb + j * x_step, oa, ob, rotated, p, q, pc, qs, qc, ps);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {

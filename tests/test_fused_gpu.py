@@ -794,6 +794,28 @@ def test_rope_weight_gradient_of_infinite_cotangents(inter):
     assert torch.equal(got[rest], want[rest]) and not torch.isfinite(got[40])
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("D,R", [(64, 32), (64, 6), (128, 64), (128, 36), (50, 20), (128, 24), (256, 192)])
+def test_rope_infinite_weights_behind_the_rotated_entries_stay_where_they_are(D, R, inter, dtype):
+    x, dy = randn(5, 3, D, dtype=dtype, seed=93), randn(5, 3, D, dtype=dtype, seed=94)
+    w, pos = weight(D, dtype, False), torch.arange(5) * 9 + 1
+    bad = w.clone()
+    for col, v in ((R, float("inf")), (D - 1, float("nan")), ((R + D) // 2, float("-inf"))):
+        bad[col] = v
+    put = ~torch.isfinite(bad)
+    # both sets, one of them with the weight that is finite
+    want = run_rope([x, x], [w, w], pos, R, dtype, inter)
+    got = run_rope([x, x], [bad, w], pos, R, dtype, inter)
+    assert torch.equal(got[1], want[1]) and torch.equal(got[0][..., ~put], want[0][..., ~put])
+    assert torch.equal(got[0][..., put].isnan(), bad[put].isnan().expand(5, 3, -1))
+    inf = torch.isinf(bad)
+    assert torch.equal(got[0][..., inf], x[..., inf] * bad[inf])
+    # the weight's gradient does not depend on the weight
+    (_, want), (_, got) = (run_rope_bwd([dy], [x], [v], pos, R, dtype, inter) for v in (w, bad))
+    assert torch.equal(got[0], want[0])
+
+
 # --------------------------------------------------------------------------- #
 # streams, graphs, offsets beyond 32 bits
 # --------------------------------------------------------------------------- #
