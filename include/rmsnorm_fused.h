@@ -145,8 +145,10 @@ typedef struct {
  * alike, in one launch. positions: int64[T], any values; inv_freq:
  * float64[rotary_dim / 2], finite, in radians per position: a scaled context is a
  * matter of the frequencies (and mscale) given. Angles are reduced in 64-bit fixed
- * point: with frequencies below 4 an angle is off by less than 2^-31 of a turn at any
- * position up to 2^32 (and by some position * 2^-64 of a turn beyond). x * g is formed before r, as above. 1 <= D <= RMSNORM_ROPE_MAX_D,
+ * point: with frequencies below 4 by that an angle is off by less than 2^-31 of a turn at
+ * any position up to 2^32 (and by position * 2^-63 of a turn at others). What is left of a
+ * quarter turn is rounded to fp32, and its sine and cosine come out within 2^-21 of
+ * themselves. x * g is formed before r, as above. 1 <= D <= RMSNORM_ROPE_MAX_D,
  * rotary_dim even, 2 <= rotary_dim <= D; T may be 0; at most
  * RMSNORM_ROPE_MAX_HEADS heads in all sets.
  */

@@ -46,22 +46,37 @@ __device__ __forceinline__ uint64_t turns_per_position(double f) {
     return (b >> 63) ? 0ull - t : t;
 }
 
-// The turn's fraction at a position, in units of 2^-32 (a signed half turn either way).
-__device__ __forceinline__ int32_t phase_at(uint64_t per_position, int64_t pos) {
-    return static_cast<int32_t>((per_position * static_cast<uint64_t>(pos)) >> 32);
+// The turn's fraction at a position, in units of 2^-64 (a signed half turn either way).
+__device__ __forceinline__ int64_t phase_at(uint64_t per_position, int64_t pos) {
+    return static_cast<int64_t>(per_position * static_cast<uint64_t>(pos));
+}
+
+// What is left of a phase when the nearest quarter turn is taken off, as upper * 2^32 + lower,
+// each rounded to fp32: small angles, of slow pairs at near positions, have all its bits too
+// (the upper word alone is off by 1.5e-4 of an angle of 10^-5 radians; one conversion
+// from 64 bits cost the forward 2.6%, two from 32 nothing). q: the phase's upper
+// word, an eighth of a turn on.
+__device__ __forceinline__ void quarter_rest(int64_t p, uint32_t& q, float& upper, float& lower) {
+    const int32_t low = static_cast<int32_t>(p);  // below 0 it borrows from the upper word
+    q = static_cast<uint32_t>(static_cast<uint64_t>(p) >> 32) + 0x20000000u;
+    upper = static_cast<float>(static_cast<int32_t>(q & 0x3fffffffu) - 0x20000000 - (low >> 31));
+    lower = static_cast<float>(low);
 }
 
 // cos and sin, times m, of two angles given as phases. The nearest quarter turn is taken
 // off, and the rest, below pi / 4, goes through the Taylor series: sin to t^9 (the next
 // term is below 2^-28 there), cos to t^10 (below 2^-32), both angles in one packed
 // instruction. About half the instructions of two sincospif calls.
-__device__ __forceinline__ void turn_pair(int32_t p0, int32_t p1, float m0, float m1, uint64_t& c, uint64_t& s) {
-    const uint32_t q0 = static_cast<uint32_t>(p0) + 0x20000000u, q1 = static_cast<uint32_t>(p1) + 0x20000000u;
-    const float unit = 1.4629180792671596e-9f;  // 2 pi / 2^32
-    const float t0 = static_cast<float>(static_cast<int32_t>(q0 & 0x3fffffffu) - 0x20000000) * unit;
-    const float t1 = static_cast<float>(static_cast<int32_t>(q1 & 0x3fffffffu) - 0x20000000) * unit;
+__device__ __forceinline__ void turn_pair(int64_t p0, int64_t p1, float m0, float m1, uint64_t& c, uint64_t& s) {
+    uint32_t q0, q1;
     auto both = [](float v) { return f2_pack(v, v); };
-    const uint64_t t = f2_pack(t0, t1), z = f2_mul(t, t);
+    float u0, u1, l0, l1;
+    quarter_rest(p0, q0, u0, l0);
+    quarter_rest(p1, q1, u1, l1);
+    // in radians: 2 pi / 2^32 and 2 pi / 2^64
+    const uint64_t t = f2_fma(f2_pack(u0, u1), both(1.4629180792671596e-9f),
+                              f2_mul(f2_pack(l0, l1), both(3.4061215800865545e-19f)));
+    const uint64_t z = f2_mul(t, t);
     uint64_t p = f2_fma(z, both(1.f / 362880), both(-1.f / 5040));
     p = f2_fma(p, z, both(1.f / 120));
     p = f2_fma(p, z, both(-1.f / 6));

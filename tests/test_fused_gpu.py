@@ -650,6 +650,32 @@ def test_rope_far_and_odd_positions_and_frequencies(inter):
     assert (outs[0][0] - outs[0][2]).abs().max() <= 8 * ref.U * xs[0].abs().max() * 2
 
 
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("D,R,base", [(64, 64, 500000.0), (128, 64, 1e7), (128, 24, 1e6), (50, 20, 1e6), (256, 256, 1e10)])
+def test_rope_small_angles_to_the_last_bits(D, R, base, inter):
+    # a pair (0, 1) becomes (-sin, cos), the backward's (sin, cos): relative to a small sine, too, only
+    # roundings to fp32 count. The angle's words', the unit's and the sum's (3), the last step of
+    # the sine's series and the rest of it (2), mscale's (1) and the output's (1), and one for
+    # the terms left out: 8. Frequencies are off by 2^-63 turns, of at least 2^-37.
+    pos = torch.tensor([0, 1, 2, 3, 17, 1000, -1, -5])
+    freq = freqs(R, base)
+    x = torch.zeros(len(pos), 2, D)
+    second = torch.arange(1, R, 2) if inter else torch.arange(R // 2, R)
+    first = second - (1 if inter else R // 2)
+    x[..., second] = 1.0
+    t = (pos.double().unsqueeze(-1) * freq).unsqueeze(1).expand(-1, 2, -1)
+    near = t.abs() < 0.75
+    assert near.sum() > 4 * R // 2 and (t[near].abs() > 0).any() and freq.min() > 2.0 ** -34
+    q = x.cuda().requires_grad_()
+    out, _ = fused.rms_norm_rope(q, None, None, None, pos.cuda(), freq.cuda(), inter)
+    out.backward(x.cuda())
+    out, back = out.detach().cpu().double(), q.grad.cpu().double()
+    for got, sign in ((out, -1.0), (back, 1.0)):
+        s, c = got[..., first], got[..., second]
+        ref.assert_close(s[near], sign * torch.sin(t)[near], 8 * ref.U * torch.sin(t)[near].abs(), "sine")
+        ref.assert_close(c[near], torch.cos(t)[near], 8 * ref.U * torch.cos(t)[near], "cosine")
+
+
 @pytest.mark.parametrize("D,R", [(64, 64), (128, 32), (50, 20)])
 def test_rope_in_place(D, R):
     for dtype in DTYPES:
