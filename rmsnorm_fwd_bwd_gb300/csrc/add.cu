@@ -17,8 +17,8 @@
 // Measured on GB300, where a device copy moves 6.77 TB/s: 16384 x 4096 bf16 77 us (6.95
 // TB/s), 78.3 us with dropout (four octets a thread; two: 84.4); the same through a
 // TMA ring of persistent blocks, 83.6 us. 8192 x 4099 fp16, every row at another offset:
-// 52.7 us (5.1 TB/s, bound by instructions: the weight has to be shifted to each row; the
-// ring 71-107 us, several rows a block 60 us). 8 x 4096: 1.8 us a call in a graph.
+// 53.9 us (5.0 TB/s, bound by instructions: the weight has to be shifted to each row, and the
+// divisions and root of r cost 1.4 us; the ring 71-107 us, several rows a block 60 us). 8 x 4096: 1.8 us a call in a graph.
 #include "fused.h"
 #include "launch.h"
 #include "octet.cuh"
@@ -103,17 +103,23 @@ __global__ void __launch_bounds__(G > 0 ? kFusedGroupThreads : G < 0 ? kFusedWid
     }
     float s0, s1;
     f2_unpack(ss, s0, s1);
-    const float r = row_rsqrt(row_sum<G>(s0 + s1, part), a.inv_n, a.eps);
+    // as the library's other norms have it: y is theirs of h but for the order of the sum
+    const float r = 1.0f / sqrtf(row_sum<G>(s0 + s1, part) / static_cast<float>(a.N) + a.eps);
     if (live && t == 0 && a.rstd) a.rstd[row] = r;
-    const uint64_t r2 = f2_pack(r, r), one2 = f2_pack(a.one, a.one);
+    const uint64_t r2 = f2_pack(r, r), one2 = f2_pack(1.f, 1.f);
 #pragma unroll
     for (int v = 0; v < KB; ++v) {
         if (cut[v].live()) {
             uint64_t f[4], g[4];
             octet_pairs<DT>(xw[v], f);
             octet_pairs<DT>(gw[v], g);
+            if (a.one != 0.f) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = f2_mul(f2_mul(f[e], r2), f2_add(g[e], one2));
+                for (int e = 0; e < 4; ++e) f[e] = f2_mul(f2_mul(f2_add(g[e], one2), f[e]), r2);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[e] = f2_mul(f2_mul(f[e], r2), g[e]);
+            }
             pairs_octet<DT>(f, xw[v]);
         }
         octet_put<DT, AL>(yr + cut[v].col * EB, xw[v], cut[v].lo, cut[v].hi, on_word, G > 0 ? t == 0 : t % 32 == 0,

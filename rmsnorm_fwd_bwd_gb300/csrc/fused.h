@@ -41,7 +41,7 @@ struct AddArgs {
     int64_t M;
     int N;
     float eps;
-    float inv_n;                    // 1 / N
+    float inv_n;                    // quant: 1 / N
     float one;                      // 1 with the offset variant (g = 1 + gamma), else 0
     const unsigned long long* rng;  // dropout: {seed, offset} in device memory
     unsigned long long* rng_used;   // forward: a copy of them, may be null

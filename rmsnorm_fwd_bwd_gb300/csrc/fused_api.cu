@@ -402,7 +402,6 @@ extern "C" rmsnorm_status rmsnorm_add_fwd(const void* x, int64_t ldx, const void
     a.ldy = ldy;
     a.M = M;
     a.N = static_cast<int>(N);
-    a.inv_n = 1.0f / static_cast<float>(N);
     a.eps = eps;
     a.one = static_cast<float>(offset);
     const bool wide = wide_rows(N, s, {{x, ldx}, {residual, ldres}, {gamma, 0}, {h, ldh}, {y, ldy}});

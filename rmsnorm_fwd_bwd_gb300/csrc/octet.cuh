@@ -375,8 +375,9 @@ __device__ __forceinline__ float warp_allmax(float v) {
     return v;
 }
 
-// 1 / sqrt(sum / N + eps): rsqrtf is off by at most 2 units in the last place, and the
-// IEEE root and quotients would cost some forty instructions per thread and row.
+// 1 / sqrt(sum / N + eps) for head rows and for the scales of the 8-bit output (whose codes it
+// cancels from): rsqrtf is off by at most 2 units in the last place, and the IEEE root and
+// quotients would cost some forty instructions per thread and row.
 __device__ __forceinline__ float row_rsqrt(float sum, float inv_n, float eps) { return rsqrtf(fmaf(sum, inv_n, eps)); }
 
 template <int G>

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from rmsnorm_fwd_bwd_gb300 import fused
+from rmsnorm_fwd_bwd_gb300.autograd import rms_norm
 from tests import fused_ref as ref
 from tests.test_fused_gpu import (check_add_bwd, check_add_fwd, check_quant, check_rope, check_rope_bwd, freqs, randn,
                                   weight)
@@ -92,6 +93,22 @@ def test_rms_norm_add_in_place():
         assert a is x and b is res and torch.equal(x, y) and torch.equal(res, h)
     with pytest.raises(ValueError):
         fused.rms_norm_add_(x, x, w)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
+@pytest.mark.parametrize("offset", [False, True])
+@pytest.mark.parametrize("N", [64, 200, 1001, 4096, 4099, 5120, 16384])
+def test_rms_norm_add_is_the_norm_of_the_sum_bit_by_bit(N, offset, dtype):
+    # small whole numbers: sums of squares are exact in any order, so nothing else may differ
+    g = torch.Generator().manual_seed(N)
+    x, res = (torch.randint(-5, 6, (40, N), generator=g).to(ref.TYPES[dtype]).cuda() for _ in range(2))
+    w = weight(N, dtype, offset).cuda()
+    y, h = fused.rms_norm_add(x, res, w, EPS, offset)
+    assert torch.equal(h, x + res)
+    assert torch.equal(y, rms_norm(h, w, EPS, offset))
+    # r, which the backward gets, too
+    r = torch.ops.rmsnorm_gb300.fwd(h, w, EPS, offset)[1]
+    assert torch.equal(torch.ops.rmsnorm_gb300.add_fwd(x, res, w, EPS, offset, 0.0, None)[2], r)
 
 
 @pytest.mark.parametrize("group,pow2", [(0, False), (128, True)])
