@@ -139,7 +139,9 @@ static const void* add_fwd_for(int lanes, int octets) {
     RMSNORM_ADD_FWD(8, 2)
     RMSNORM_ADD_FWD(32, 1)
     RMSNORM_ADD_FWD(32, 2)
-    RMSNORM_ADD_FWD(32, 4)
+    if constexpr (MODE != kRowsOnePhase) {  // blocks take such rows from 65 octets on
+        RMSNORM_ADD_FWD(32, 4)
+    }
     RMSNORM_ADD_FWD(0, 2)
     if constexpr (MODE == kRowsAligned) {
         RMSNORM_ADD_FWD(0, 4)

@@ -430,7 +430,9 @@ static const void* bwd_rows_for(int lanes, int octets) {
     RMSNORM_ADD_BWD(8, 2)
     RMSNORM_ADD_BWD(32, 1)
     RMSNORM_ADD_BWD(32, 2)
-    RMSNORM_ADD_BWD(32, 4)
+    if constexpr (MODE != kRowsOnePhase) {  // blocks take such rows from 65 octets on
+        RMSNORM_ADD_BWD(32, 4)
+    }
     RMSNORM_ADD_BWD(0, 2)
     RMSNORM_ADD_BWD(0, 4)
     if constexpr (MODE != kRowsAligned) {

@@ -137,7 +137,9 @@ static const void* quant_rows_for(int lanes, int octets) {
     if (lanes == G && octets == KB) return reinterpret_cast<const void*>(&quant_rows<DT, MODE, G, KB>);
     RMSNORM_QUANT_ROWS(32, 1)
     RMSNORM_QUANT_ROWS(32, 2)
-    RMSNORM_QUANT_ROWS(32, 4)
+    if constexpr (MODE != kRowsOnePhase) {  // blocks take such rows from 65 octets on
+        RMSNORM_QUANT_ROWS(32, 4)
+    }
     RMSNORM_QUANT_ROWS(0, 2)
     if constexpr (MODE == kRowsAligned) {
         RMSNORM_QUANT_ROWS(0, 4)

@@ -1,6 +1,9 @@
 """The operators of include/rmsnorm_fused.h without a GPU: refusals (all before the
 library touches CUDA), the formulas of the 64-bit oracle, Philox, the rotation's
 frequencies, and the checks of the torch front end."""
+import os
+import re
+
 import numpy as np
 import pytest
 import torch
@@ -129,6 +132,16 @@ def test_workspace_sizes_of_invalid_arguments():
     assert B.rmsnorm_rope_bwd_workspace_size(4, 0, 64, 0) == 0
     assert B.rmsnorm_rope_bwd_workspace_size(4, 1, 513, 0) == 0
     assert B.rmsnorm_rope_bwd_workspace_size(4, 1, 64, 5) == 0
+
+
+def test_no_kernels_that_no_call_reaches():
+    # rows of one offset are given to 32 lanes up to 64 octets: two octets a lane, never four
+    root = os.path.join(os.path.dirname(build_mod.__file__), "_build")
+    for name, kernels in (("add", "add_fwd_rows"), ("add_bwd", "add_bwd_rows"), ("quant", "quant_rows")):
+        with open(os.path.join(root, name + ".ptxas.txt")) as f:
+            seen = set(re.findall(kernels + r"ILi(\d)ELi(\d)ELi(n?\d+)ELi(\d)E", f.read()))
+        assert len(seen) >= 30, name                    # (dtype, mode, lanes, octets)
+        assert not [s for s in seen if s[1:] == ("2", "32", "4")], name
 
 
 # --------------------------------------------------------------------------- #
