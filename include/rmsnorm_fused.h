@@ -17,7 +17,9 @@
  * In place: every row is read before it is written, so an output may be an input
  * of the same shape, dtype, pointer and pitch (h on residual, y on x, dresidual on
  * dy or dh, rotated heads on the heads). No other overlap is allowed; two outputs at
- * one address whose values differ are refused, and so are an output's rows that overlap.
+ * one address whose values differ are refused, and so are an output's rows that overlap
+ * and an output that starts where an input of another pitch, the weight (of several rows) or
+ * another set's heads do.
  */
 #ifndef RMSNORM_FUSED_H
 #define RMSNORM_FUSED_H

@@ -159,6 +159,14 @@ bool distinct(std::initializer_list<const void*> outputs) {
     return true;
 }
 
+// Whether the output's rows (NULL: not written) are those of each input at its address: of
+// one pitch (the weight has pitch 0: all rows read it).
+bool same_rows(int64_t M, const Operand& out, std::initializer_list<Operand> inputs) {
+    for (const Operand& in : inputs)
+        if (out.p && out.p == in.p && M > 1 && out.ld != in.ld) return false;
+    return true;
+}
+
 RowMode row_mode(bool wide, bool one) { return wide ? kRowsAligned : one ? kRowsOnePhase : kRowsAny; }
 
 // Every row of every operand on a 16-byte boundary (8 for 1-byte elements), and
@@ -289,6 +297,20 @@ bool output_strides_ok(int64_t token, int64_t head, int64_t heads, int64_t T, in
            (T <= 1 || heads <= 1 || token >= (heads - 1) * head + D || head >= (T - 1) * token + D);
 }
 
+// Whether a set's output, where it lies on an input of a set, is that set's heads, of the same
+// strides.
+bool same_heads(const RopeArgs& a, int64_t T, int nsets) {
+    for (int i = 0; i < nsets; ++i)
+        for (int j = 0; j < nsets; ++j) {
+            const RopeSet &o = a.set[i], &s = a.set[j];
+            if ((o.y == s.gamma && !(i == j && T <= 1 && s.heads <= 1)) ||
+                (o.y == s.x && !(i == j && (T <= 1 || o.y_token == s.x_token) && (s.heads <= 1 || o.y_head == s.x_head))) ||
+                (o.y == s.dy && !(i == j && (T <= 1 || o.y_token == s.dy_token) && (s.heads <= 1 || o.y_head == s.dy_head))))
+                return false;
+        }
+    return true;
+}
+
 rmsnorm_status check_rope(int nsets, int64_t T, int64_t D, int64_t R, int interleaved, float mscale, float eps,
                           rmsnorm_dtype dtype, int offset) {
     const rmsnorm_status st = check_common(T, D, dtype, offset);
@@ -384,7 +406,9 @@ extern "C" rmsnorm_status rmsnorm_add_fwd(const void* x, int64_t ldx, const void
     if (!check_dropout(dropout_p, rng, a, st)) return st;
     if (M == 0) return RMSNORM_OK;
     if (!x || !gamma || !y) return RMSNORM_ERR_NULL;
-    if (!distinct({h, y, rstd})) return RMSNORM_ERR_ARG;
+    if (!distinct({h, y, rstd}) || !same_rows(M, {h, ldh}, {{x, ldx}, {residual, ldres}, {gamma, 0}}) ||
+        !same_rows(M, {y, ldy}, {{x, ldx}, {residual, ldres}, {gamma, 0}}))
+        return RMSNORM_ERR_ARG;
     if (!aligned(x, s) || !aligned(residual, s) || !aligned(gamma, s) || !aligned(h, s) || !aligned(y, s) ||
         !aligned(rstd, 4))
         return RMSNORM_ERR_ALIGN;
@@ -453,8 +477,11 @@ extern "C" rmsnorm_status rmsnorm_add_bwd(const void* dy, int64_t lddy, const vo
         !aligned(dresidual, s) || !aligned(rstd, 4) || !aligned(workspace, 16))
         return RMSNORM_ERR_ALIGN;
     if ((st = check_rng(a)) != RMSNORM_OK) return st;
+    // without dropout dx and dresidual are equal, and may be one
     if (!distinct({dx, dgamma, workspace}) || !distinct({dresidual, dgamma, workspace}) ||
-        (a.threshold && !distinct({dx, dresidual})))
+        (a.threshold && !distinct({dx, dresidual})) ||
+        !same_rows(M, {dx, lddx}, {{dy, lddy}, {dh, lddh}, {h, ldh}, {gamma, 0}}) ||
+        !same_rows(M, {dresidual, lddres}, {{dy, lddy}, {dh, lddh}, {h, ldh}, {gamma, 0}, {dx, lddx}}))
         return RMSNORM_ERR_ARG;
     AddPlan p;
     const bool wide = wide_rows(N, s, {{dy, lddy}, {dh, lddh}, {h, ldh}, {gamma, 0}, {dx, lddx}, {dresidual, lddres}});
@@ -504,7 +531,10 @@ extern "C" rmsnorm_status rmsnorm_quant_fwd(const void* x, int64_t ldx, const vo
         return RMSNORM_ERR_SHAPE;
     if (M == 0) return RMSNORM_OK;
     if (!x || !gamma || !codes || !scales) return RMSNORM_ERR_NULL;
-    if (!distinct({h, codes, scales})) return RMSNORM_ERR_ARG;
+    // codes and scales are of other types than the inputs
+    if (!distinct({h, codes, scales}) || !distinct({x, codes, scales}) || !distinct({residual, codes, scales}) ||
+        !distinct({gamma, codes, scales}) || !same_rows(M, {h, ldh}, {{x, ldx}, {residual, ldres}, {gamma, 0}}))
+        return RMSNORM_ERR_ARG;
     if (!aligned(x, s) || !aligned(residual, s) || !aligned(gamma, s) || !aligned(h, s) || !aligned(scales, 4))
         return RMSNORM_ERR_ALIGN;
     AddArgs a = {};
@@ -571,7 +601,7 @@ extern "C" rmsnorm_status rmsnorm_rope_fwd(const rmsnorm_rope_heads* sets, int n
     }
     if (heads > RMSNORM_ROPE_MAX_HEADS) return RMSNORM_ERR_SHAPE;
     if (T == 0) return RMSNORM_OK;
-    if (!distinct({a.set[0].y, a.set[1].y})) return RMSNORM_ERR_ARG;
+    if (!distinct({a.set[0].y, a.set[1].y}) || !same_heads(a, T, nsets)) return RMSNORM_ERR_ARG;
     if (!positions || !inv_freq) return RMSNORM_ERR_NULL;
     if (!aligned(positions, 8) || !aligned(inv_freq, 8)) return RMSNORM_ERR_ALIGN;
     a.nsets = nsets;
@@ -641,7 +671,7 @@ extern "C" rmsnorm_status rmsnorm_rope_bwd(const rmsnorm_rope_heads_bwd* sets, i
     }
     if (heads > RMSNORM_ROPE_MAX_HEADS) return RMSNORM_ERR_SHAPE;
     if (nsets == 2 && sets[0].gamma && sets[1].gamma && sets[0].dgamma == sets[1].dgamma) return RMSNORM_ERR_ARG;
-    if (T > 0 && !distinct({a.set[0].y, a.set[1].y})) return RMSNORM_ERR_ARG;
+    if (T > 0 && (!distinct({a.set[0].y, a.set[1].y}) || !same_heads(a, T, nsets))) return RMSNORM_ERR_ARG;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     a.nsets = nsets;
     a.heads = static_cast<int>(heads);

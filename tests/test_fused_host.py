@@ -345,6 +345,40 @@ def test_output_rows_that_overlap_are_refused():
     assert rope(x_token=64, x_head=64, positions=None) == NULL
 
 
+def test_outputs_on_inputs_of_other_rows_are_refused():
+    # an output may lie on an input where its rows are the same; rows of another pitch, the weight,
+    # or another set's heads would be overwritten before they are read. (NULL: accepted so far;
+    # what follows is refused for another reason.)
+    for kw in (dict(h=0x1000), dict(h=0x2000), dict(y=0x1000), dict(y=0x2000)):
+        for ld in ("ldh", "ldy", "ldx", "ldres"):
+            hit = {"h": ("ldh",), "y": ("ldy",)}[next(iter(kw))] + ({0x1000: ("ldx",), 0x2000: ("ldres",)}[next(iter(kw.values()))])
+            assert add_fwd(**kw, **{ld: 16}, dropout_p=0.5) == (ARG if ld in hit else NULL), (kw, ld)
+        assert add_fwd(**kw, ldh=16, ldy=16, ldx=16, ldres=16, dropout_p=0.5) == NULL
+        assert add_fwd(**kw, M=1, ldh=16, ldy=24, dropout_p=0.5) == NULL
+    assert add_fwd(h=0x3000, dropout_p=0.5) == ARG and add_fwd(y=0x3000, dropout_p=0.5) == ARG
+    for out, ld in (("dx", "lddx"), ("dresidual", "lddres")):
+        for at in (0x1000, 0x2000, 0x3000):
+            assert add_bwd(**{out: at, ld: 16}) == ARG
+        assert add_bwd(**{out: 0x4000}) == ARG
+    assert add_bwd(dx=0x7000, lddx=16) == ARG
+    assert quant(h=0x1000, ldh=72) == ARG and quant(h=0x2000, ldres=72) == ARG and quant(h=0x3000) == ARG
+    for at in (0x1000, 0x2000, 0x3000):
+        assert quant(codes=at) == ARG and quant(scales=at) == ARG
+    assert rope(y=0x1000, positions=None) == NULL
+    assert rope(y=0x1000, y_token=256) == ARG and rope(y=0x1000, x_head=72) == ARG and rope(y=0x2000) == ARG
+    assert rope(y=0x1000, y_token=256, T=1, positions=None) == NULL
+    assert rope(bwd=True, dx=0x1000, dx_token=256) == ARG and rope(bwd=True, dx=0x2000, x_head=72) == ARG
+    assert rope(bwd=True, dx=0x3000) == ARG and rope(bwd=True, dx=0x1000, positions=None) == NULL
+    # one set's output on the other's heads
+    for y0, y1 in ((0x2000, 0x1000), (0x1000, 0x3000), (0x2000, 0x8000)):
+        sets = (B.RopeHeads * 2)(B.RopeHeads(0x1000, 128, 64, 0x3000, y0, 128, 64, 2),
+                                 B.RopeHeads(0x2000, 128, 64, 0x3800, y1, 128, 64, 2))
+        assert B.rmsnorm_rope_fwd(sets, 0x6000, 4, 64, 64, 0x7000, 0, 1.0, 1e-6, 2, 0) == ARG
+    sets = (B.RopeHeads * 2)(B.RopeHeads(0x1000, 128, 64, 0x3000, 0x1000, 128, 64, 2),
+                             B.RopeHeads(0x2000, 128, 64, 0x3000, 0x2000, 128, 64, 2))
+    assert B.rmsnorm_rope_fwd(sets, None, 4, 64, 64, 0x7000, 0, 1.0, 1e-6, 2, 0) == NULL
+
+
 def test_in_place_addition_refuses_shared_rows():
     buf = torch.zeros(8, 40)
     w = torch.ones(16)
