@@ -90,6 +90,7 @@ rmsnorm_status rmsnorm_add_bwd(const void* dy, int64_t lddy, const void* dh, int
  *     scale = max(amax(|y|) / 448, 2^-126)      pow2: rounded up to a power of two
  *     code  = y / scale, rounded to nearest-even
  *
+ * (fp32's y / scale: one that lies half way between two codes may become either of them.)
  * codes: uint8[M rows, pitch ldcodes]; scales: float32[M rows, pitch ldscales],
  * one per row or ceil(N / group). residual and h may be NULL, each on its own. A
  * group with a NaN gets a NaN scale; one with an infinity an infinite scale and

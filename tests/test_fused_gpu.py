@@ -530,6 +530,25 @@ def test_quant_of_the_smallest_products(group):
     assert codes[0, 3].float().item() == 448.0 and codes[0, 0].float().item() == 0.0
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N,group", [(64, 8192, 128), (300, 4096, 0), (70, 4099, 64), (500, 520, 32), (40, 16384, 0)])
+def test_quant_codes_are_the_nearest_but_at_the_borders(M, N, group, dtype):
+    # y / scale comes out within 2 (Y_REL + 2 u) + 3 u < 70 u < 2^-17 of itself: a code may differ from the exactly rounded one
+    # only where the exact quotient is that near to a border between two codes (products of
+    # bf16 numbers lie exactly on one now and then), and is its neighbour there
+    x, res, w = randn(M, N, dtype=dtype, seed=57), randn(M, N, dtype=dtype, seed=58), weight(N, dtype, False)
+    codes, scales, h = run_quant(x, res, w, dtype, group, False)
+    y, _ = ref.norm(h, w, EPS)
+    g = group or N
+    amax = torch.nn.functional.pad(y.abs(), (0, -N % g)).view(M, -1, g).amax(-1)
+    q = y / (amax / 448.0).repeat_interleave(g, dim=1)[:, :N]
+    got = codes.double()
+    near, far = (q * (1 + s * 2.0 ** -17) for s in (-1, 1))
+    low, high = (t.clamp(-448, 448).float().to(torch.float8_e4m3fn).double() for t in (near, far))
+    assert torch.all((got == low) | (got == high))
+    assert (low != high).double().mean() < 2e-3             # the others: exactly the nearest
+
+
 def test_quant_rounds_to_even_and_uses_the_whole_range():
     # y is exactly x here up to r: rows scaled so that the codes before rounding are known
     N = 4096
