@@ -14,10 +14,11 @@
 // Angles: position * inv_freq loses the angle in fp32 (at position 10^6 by 0.06
 // radians) and fp64 is slow on this GPU, but only the fraction of a turn matters.
 // Each inv_freq becomes a 64-bit fixed-point number of turns per position; its
-// product with the integer position, modulo 2^64, is the fraction exactly reduced.
+// product with the integer position, modulo 2^64, is the fraction exactly reduced, and
+// all its bits go into what is left of a quarter turn, which is rounded to fp32 once.
 //
 // Bound by HBM: the heads in and out (backward: dy and x in, dx out). Measured on GB300 (a
-// device copy moves 6.77 TB/s): forward 32768 tokens x 40 heads x 128 bf16 103 us (6.5
+// device copy moves 6.77 TB/s): forward 32768 tokens x 40 heads x 128 bf16 104 us (6.4
 // TB/s; 138 us with the sines by sincospif and all heads of a token by one group, 125 us
 // with two heads in flight a lane instead of four), fp32 16384 x 40 x 128 97 us (6.9
 // TB/s); backward 16384 x 20 x 256 bf16 94 us (5.35 TB/s, bound by latency at 12 warps an

@@ -99,7 +99,8 @@ def _pitched(t: Optional[torch.Tensor]):
 def dropout_state(seed: int, offset: int = 0, device="cuda") -> torch.Tensor:
     """{seed, offset} for the dropout of ``rms_norm_add``. The numbers depend on these
     and on the element's row and column alone: give every layer a seed of its own
-    and raise the offset every step (``state[1] += 1``, also inside a graph)."""
+    and raise the offset every step (``state[1] += 1``, also inside a graph). Where the
+    backward runs forwards again (activation checkpointing), raise it after the backward."""
     def signed(v):
         v &= (1 << 64) - 1
         return v - (1 << 64) if v >> 63 else v
