@@ -18,7 +18,8 @@
 // TB/s), 78.3 us with dropout (four octets a thread; two: 84.4); the same through a
 // TMA ring of persistent blocks, 83.6 us. 8192 x 4099 fp16, every row at another offset:
 // 53.9 us (5.0 TB/s, bound by instructions: the weight has to be shifted to each row, and the
-// divisions and root of r cost 1.4 us; the ring 71-107 us, several rows a block 60 us). 8 x 4096: 1.8 us a call in a graph.
+// divisions and root of r cost 1.4 us; the ring 71-107 us, several rows a block 60 us). 8 x
+// 4096: 1.8 us a call in a graph.
 #include "fused.h"
 #include "launch.h"
 #include "octet.cuh"
