@@ -1,0 +1,68 @@
+/*
+ * rmsnorm_serving.h -- C ABI of the operators between an RMSNorm and an attention in
+ * serving:
+ *
+ *   rmsnorm_quant_weight   a weight as e4m3 codes with a scale per block of 128 x 128
+ *   rmsnorm_quant_matmul   the product of rmsnorm_quant_fwd's codes with such a weight
+ *   rmsnorm_rope_append    head norm and rotation of queries and keys, with keys and values
+ *                          written to the rows of a paged cache
+ *
+ * Conventions are those of rmsnorm.h: device pointers on the current device, the caller owns
+ * every buffer and the stream, no allocation, no workspace, all checks on the host before any
+ * launch, status codes. None of them has a gradient. Rows are ld* elements apart (ld* >= the
+ * row; the gaps are neither read nor written), and any element-aligned pointer and pitch
+ * works; the fast paths want rows on 16-byte boundaries.
+ */
+#ifndef RMSNORM_SERVING_H
+#define RMSNORM_SERVING_H
+
+#include "rmsnorm_fused.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define RMSNORM_MATMUL_MAX 1048576 /* most rows and columns of a weight */
+#define RMSNORM_MATMUL_BLOCK 128
+
+/*
+ * The weight w[N, K] (dtype) as e4m3 codes (uint8[N rows, pitch ldcodes]; 1 sign, 4 exponent, 3
+ * fraction bits, largest 448) with a float32 scale per block of 128 x 128, the last ones
+ * of a row and column short (scales[ceil(N / 128) rows, pitch ldscales >= ceil(K / 128)]):
+ *
+ *     scale = max(amax(|w|) / 448, 2^-126)      pow2: rounded up to a power of two
+ *     code  = w / scale, rounded to nearest-even
+ *
+ * with both quotients rounded exactly. A block with a NaN gets a NaN scale, one with an
+ * infinity an infinite scale and codes of 0 and NaN. N may be 0. The outputs must not overlap
+ * the weight or each other.
+ */
+rmsnorm_status rmsnorm_quant_weight(const void* w, int64_t ldw, void* codes, int64_t ldcodes, float* scales,
+                                    int64_t ldscales, int64_t N, int64_t K, rmsnorm_dtype dtype, int pow2,
+                                    rmsnorm_stream_t stream);
+
+/*
+ * The product of 8-bit rows with an 8-bit weight:
+ *
+ *     y[m, n] = sum over k of (a[m, k] a_scales[m, k / group]) (b[n, k] b_scales[n / 128, k / 128]) + bias[n]
+ *
+ * a: e4m3 codes of M rows of K with scales per 128 columns (group 128: a_scales[M rows, pitch
+ * ldas >= ceil(K / 128)]) or per row (group 0: ldas >= 1), as rmsnorm_quant_fwd writes them; b:
+ * [N, K] with scales per block, as rmsnorm_quant_weight writes them. y[M, N] is fp32, fp16
+ * or bf16 (dtype), and bias[N], which may be NULL, of the same type. The products within a block
+ * of 128 columns are summed by the tensor cores in fp32, the blocks, times the product of
+ * their two scales, in fp32; one rounding to y's type. A pair of scales whose product passes
+ * fp32's range counts as infinite, or as 0 below it. A result depends on the
+ * operands and on M, N and K (which choose the order of the sums), not on the run. 1 <= N, K <=
+ * RMSNORM_MATMUL_MAX; M may be 0. y must not overlap an operand.
+ */
+rmsnorm_status rmsnorm_quant_matmul(const void* a, int64_t lda, const float* a_scales, int64_t ldas, const void* b,
+                                    int64_t ldb, const float* b_scales, int64_t ldbs, const void* bias, void* y,
+                                    int64_t ldy, int64_t M, int64_t N, int64_t K, rmsnorm_dtype dtype, int group,
+                                    rmsnorm_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* RMSNORM_SERVING_H */

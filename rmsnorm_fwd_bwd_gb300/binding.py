@@ -1,6 +1,6 @@
 """Python front end of ``librmsnorm.so`` (the C ABI in ``include/rmsnorm.h``,
-``include/layernorm.h``, ``include/rmsnorm_double_backward.h`` and
-``include/rmsnorm_fused.h``).
+``include/layernorm.h``, ``include/rmsnorm_double_backward.h``,
+``include/rmsnorm_fused.h`` and ``include/rmsnorm_serving.h``).
 
 The functions named like the C entry points take the same arguments in the same
 order and only marshal them: a pointer argument may be a torch tensor (its
@@ -92,6 +92,8 @@ def _load():
             "rmsnorm_rope_fwd": (I, [P, I, P, I64, I64, I64, P, I, F, F, I, I, P]),
             "rmsnorm_rope_bwd_workspace_size": (SZ, [I64, I64, I64, I]),
             "rmsnorm_rope_bwd": (I, [P, I, P, I64, I64, I64, P, I, F, F, I, I, P, SZ, P]),
+            "rmsnorm_quant_weight": (I, [P, I64, P, I64, P, I64, I64, I64, I, I, P]),
+            "rmsnorm_quant_matmul": (I, [P, I64, P, I64, P, I64, P, I64, P, P, I64, I64, I64, I64, I, I, P]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(lib, name)
@@ -312,6 +314,18 @@ def rmsnorm_rope_bwd(sets, positions, T, D, rotary_dim, inv_freq, interleaved, m
                                     int(T), int(D), int(rotary_dim), _addr(inv_freq), int(interleaved), float(mscale),
                                     float(eps), _dtype_code(dtype), int(offset), _addr(workspace),
                                     int(workspace_bytes), _stream(stream))
+
+
+def rmsnorm_quant_weight(w, ldw, codes, ldcodes, scales, ldscales, N, K, dtype, pow2=False, stream=None) -> int:
+    return _load().rmsnorm_quant_weight(_addr(w), int(ldw), _addr(codes), int(ldcodes), _addr(scales), int(ldscales),
+                                        int(N), int(K), _dtype_code(dtype), int(pow2), _stream(stream))
+
+
+def rmsnorm_quant_matmul(a, lda, a_scales, ldas, b, ldb, b_scales, ldbs, bias, y, ldy, M, N, K, dtype, group=128,
+                         stream=None) -> int:
+    return _load().rmsnorm_quant_matmul(_addr(a), int(lda), _addr(a_scales), int(ldas), _addr(b), int(ldb),
+                                        _addr(b_scales), int(ldbs), _addr(bias), _addr(y), int(ldy), int(M), int(N),
+                                        int(K), _dtype_code(dtype), int(group), _stream(stream))
 
 
 def rmsnorm_status_string(status: int) -> str:

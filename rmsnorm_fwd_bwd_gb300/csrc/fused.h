@@ -125,4 +125,11 @@ constexpr int rope_fwd_batch(int dtype) { return dtype == 0 ? 2 : 4; }
 
 const void* rope_kernel(const RopePlan& p, bool bwd);
 
+// SMs of the current device, whose number goes to dev; 0 on failure.
+int current_sms(int& dev);
+// Allow the kernel the device's whole shared memory.
+bool allow_shared_memory(const void* k, int dev);
+// Blocks of `threads` that an SM holds; 0 on failure. Sets the attribute above where needed.
+int resident_blocks(const void* k, int dev, int threads, size_t smem);
+
 }  // namespace rmsnorm

@@ -30,6 +30,8 @@ std::mutex g_fused_mu;
 std::map<int, int> g_fused_sms;                                   // SMs by device
 std::map<std::pair<const void*, std::pair<int, int>>, int> g_fused_fit;  // resident blocks per SM by (kernel, (device, threads))
 
+}  // namespace
+
 // SMs of the current device; 0 on failure.
 int current_sms(int& dev) {
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
@@ -69,6 +71,8 @@ int resident_blocks(const void* k, int dev, int threads, size_t smem) {
         return 0;
     }
 }
+
+namespace {
 
 cudaError_t launch(const void* k, int64_t blocks, int threads, size_t smem, void** params, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};

@@ -1,4 +1,4 @@
-// quant.cuh -- e4m3 codes and their scales, of quant.cu.
+// quant.cuh -- e4m3 codes and their scales, of quant.cu, weight.cu and append.cu.
 #pragma once
 
 #include "fused.h"
@@ -36,6 +36,13 @@ __device__ __forceinline__ float octet_amax(const uint64_t (&z)[4], int lo, int 
     return m;
 }
 
+// A positive normal number up to the next power of two: a carry out of the fraction raises
+// the exponent (infinity and NaN stay).
+__device__ __forceinline__ float power_of_two_above(float s) {
+    const uint32_t b = __float_as_uint(s);
+    return b < 0x7f800000u ? __uint_as_float((b + 0x007fffffu) & 0x7f800000u) : s;
+}
+
 // The scale of a group whose largest |z| is amax, with y = z * r; and the factors by which
 // z becomes codes, in this order: 1 and r / scale, the r of y and of the scale having
 // cancelled, or, at the least scale and for the smallest z, where that may overflow, r
@@ -44,12 +51,7 @@ __device__ __forceinline__ float quant_scale(float amax, float r, int pow2, floa
     float s = amax * r * (1.0f / 448.0f);
     const bool apart = s < 1.17549435e-38f || amax < 7.8886091e-31f;  // 2^-126 and 2^-100
     if (s < 1.17549435e-38f) s = 1.17549435e-38f;                   // a NaN stays
-    if (pow2) {
-        // up to the next power of two: a carry out of the fraction raises the exponent
-        // (infinity and NaN stay)
-        const uint32_t b = __float_as_uint(s);
-        if (b < 0x7f800000u) s = __uint_as_float((b + 0x007fffffu) & 0x7f800000u);
-    }
+    if (pow2) s = power_of_two_above(s);
     // the scale is a normal number and its inverse too: off by at most 1 unit in the last place
     float inv;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));

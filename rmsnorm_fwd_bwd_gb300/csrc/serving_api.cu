@@ -1,0 +1,211 @@
+// serving_api.cu -- the entry points of include/rmsnorm_serving.h: argument checks, launch
+// shapes and launches of the kernels in matmul.cu, weight.cu and append.cu.
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/rmsnorm_serving.h"
+#include "checks.h"
+#include "fused.h"
+#include "launch.h"
+#include "serving.h"
+
+namespace rmsnorm {
+namespace {
+
+constexpr int64_t kMatmulMost = RMSNORM_MATMUL_MAX;
+constexpr int64_t kBlock = RMSNORM_MATMUL_BLOCK;
+// Most blocks that share K: the portable size of a cluster.
+constexpr int64_t kMostSplit = 8;
+
+cudaError_t launch(const void* k, int64_t blocks, int threads, size_t smem, int cluster, void** params, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelExC(&cfg, k, params);
+}
+
+// Launch, and once more after the kernel's attributes are set again, which a device reset
+// since the first call discards.
+rmsnorm_status run(const void* k, int64_t blocks, int threads, size_t smem, int cluster, void** params, rmsnorm_stream_t stream) {
+    if (!k) return RMSNORM_ERR_UNSUPPORTED;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return RMSNORM_ERR_CUDA;
+    if (smem > 48 * 1024 && resident_blocks(k, dev, threads, smem) < 1) {
+        (void)cudaGetLastError();
+        return RMSNORM_ERR_CUDA;
+    }
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (launch(k, blocks, threads, smem, cluster, params, s) == cudaSuccess) return RMSNORM_OK;
+    (void)cudaGetLastError();
+    if (smem > 48 * 1024 && allow_shared_memory(k, dev) && launch(k, blocks, threads, smem, cluster, params, s) == cudaSuccess)
+        return RMSNORM_OK;
+    (void)cudaGetLastError();
+    return RMSNORM_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------------------
+// tensor maps
+// ---------------------------------------------------------------------------
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// Rows that TMA takes: on 16-byte boundaries (one row alone has no pitch).
+bool tma_rows(const void* p, int64_t ld, int64_t rows) { return aligned(p, 16) && (rows <= 1 || ld % 16 == 0); }
+
+// Boxes of `box` rows of 128 codes of a matrix [rows, K], swizzled by 128 bytes; what lies
+// outside of it reads as zero.
+bool tile_map(CUtensorMap& map, const void* p, int64_t ld, int64_t rows, int64_t K, int box) {
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(rows > 1 ? ld : round_up(K, 16))};
+    const cuuint32_t boxes[2] = {static_cast<cuuint32_t>(kBlock), static_cast<cuuint32_t>(box)};
+    const cuuint32_t steps[2] = {1, 1};
+    return encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, boxes, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How a product is cut. Few rows of a: b's rows in the accumulators' lanes, and K over as many
+// blocks as fill the GPU.
+void matmul_plan(int64_t M, int64_t N, int64_t K, bool tma, int dtype, int sms, MatmulPlan& p) {
+    p.dtype = dtype;
+    p.tma = tma;
+    const int64_t kblocks = ceil_div(K, kBlock);
+    p.wide = M > 128;
+    if (p.wide) {
+        p.n = tma ? 256 : 128;
+        p.blocks = std::min<int64_t>(ceil_div(M, 128) * ceil_div(N, p.n), sms);
+    } else {
+        for (p.n = 16; p.n < M;) p.n *= 2;
+        const int64_t tiles = ceil_div(M, p.n) * ceil_div(N, 128);
+        p.split = static_cast<int>(std::max<int64_t>(1, std::min({sms / tiles, kMostSplit, kblocks})));
+        p.blocks = tiles * p.split;
+    }
+    matmul_shape(p);
+}
+
+// Whether [p, p + bytes) and [q, q + more) share memory.
+bool overlap(const void* p, int64_t bytes, const void* q, int64_t more) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return p && q && bytes > 0 && more > 0 && a < b + static_cast<uintptr_t>(more) && b < a + static_cast<uintptr_t>(bytes);
+}
+
+int64_t span(int64_t rows, int64_t ld, int64_t width, int64_t bytes) { return rows > 0 ? ((rows - 1) * ld + width) * bytes : 0; }
+
+bool dtype_ok(rmsnorm_dtype dt) { return dt == RMSNORM_F32 || dt == RMSNORM_F16 || dt == RMSNORM_BF16; }
+
+}  // namespace
+}  // namespace rmsnorm
+
+using namespace rmsnorm;
+
+extern "C" rmsnorm_status rmsnorm_quant_weight(const void* w, int64_t ldw, void* codes, int64_t ldcodes, float* scales,
+                                               int64_t ldscales, int64_t N, int64_t K, rmsnorm_dtype dtype, int pow2,
+                                               rmsnorm_stream_t stream) {
+    if (!dtype_ok(dtype)) return RMSNORM_ERR_DTYPE;
+    if (pow2 != 0 && pow2 != 1) return RMSNORM_ERR_ARG;
+    const size_t s = elem_bytes(dtype);
+    if (N < 0 || N > kMatmulMost || K < 1 || K > kMatmulMost) return RMSNORM_ERR_SHAPE;
+    const int64_t kblocks = ceil_div(K, kBlock), nblocks = ceil_div(N, kBlock);
+    if (!pitch_ok(ldw, K, N, s) || !pitch_ok(ldcodes, K, N, 1) || !pitch_ok(ldscales, kblocks, nblocks, 4))
+        return RMSNORM_ERR_SHAPE;
+    if (N == 0) return RMSNORM_OK;
+    if (!w || !codes || !scales) return RMSNORM_ERR_NULL;
+    if (!aligned(w, s) || !aligned(scales, 4)) return RMSNORM_ERR_ALIGN;
+    const int64_t wb = span(N, ldw, K, s), cb = span(N, ldcodes, K, 1), sb = span(nblocks, ldscales, kblocks, 4);
+    if (overlap(w, wb, codes, cb) || overlap(w, wb, scales, sb) || overlap(codes, cb, scales, sb)) return RMSNORM_ERR_ARG;
+    WeightArgs a = {};
+    a.w = w;
+    a.codes = codes;
+    a.scales = scales;
+    a.ldw = ldw;
+    a.ldcodes = ldcodes;
+    a.ldscales = ldscales;
+    a.N = static_cast<int>(N);
+    a.K = static_cast<int>(K);
+    a.kblocks = static_cast<int>(kblocks);
+    a.pow2 = pow2;
+    const bool wide = K % 8 == 0 && aligned(w, 16) && ldw * static_cast<int64_t>(s) % 16 == 0 && aligned(codes, 8) && ldcodes % 8 == 0;
+    void* params[] = {&a};
+    return run(weight_kernel(dtype, wide), nblocks * kblocks, weight_threads(), 0, 1, params, stream);
+}
+
+extern "C" rmsnorm_status rmsnorm_quant_matmul(const void* a, int64_t lda, const float* a_scales, int64_t ldas, const void* b,
+                                               int64_t ldb, const float* b_scales, int64_t ldbs, const void* bias, void* y,
+                                               int64_t ldy, int64_t M, int64_t N, int64_t K, rmsnorm_dtype dtype, int group,
+                                               rmsnorm_stream_t stream) {
+    if (!dtype_ok(dtype)) return RMSNORM_ERR_DTYPE;
+    if (group != 0 && group != kBlock) return RMSNORM_ERR_ARG;
+    if (M < 0 || M > RMSNORM_MAX_M || N < 1 || N > kMatmulMost || K < 1 || K > kMatmulMost) return RMSNORM_ERR_SHAPE;
+    const size_t s = elem_bytes(dtype);
+    const int64_t kblocks = ceil_div(K, kBlock), nblocks = ceil_div(N, kBlock), per_row = group ? kblocks : 1;
+    if (!pitch_ok(lda, K, M, 1) || !pitch_ok(ldas, per_row, M, 4) || !pitch_ok(ldb, K, N, 1) || !pitch_ok(ldbs, kblocks, nblocks, 4) ||
+        !pitch_ok(ldy, N, M, s))
+        return RMSNORM_ERR_SHAPE;
+    if (M == 0) return RMSNORM_OK;
+    if (!a || !a_scales || !b || !b_scales || !y) return RMSNORM_ERR_NULL;
+    if (!aligned(a_scales, 4) || !aligned(b_scales, 4) || !aligned(bias, s) || !aligned(y, s)) return RMSNORM_ERR_ALIGN;
+    const int64_t yb = span(M, ldy, N, s);
+    if (overlap(y, yb, a, span(M, lda, K, 1)) || overlap(y, yb, a_scales, span(M, ldas, per_row, 4)) ||
+        overlap(y, yb, b, span(N, ldb, K, 1)) || overlap(y, yb, b_scales, span(nblocks, ldbs, kblocks, 4)) ||
+        overlap(y, yb, bias, N * s))
+        return RMSNORM_ERR_ARG;
+    int dev = 0;
+    const int sms = current_sms(dev);
+    if (!sms) {
+        (void)cudaGetLastError();
+        return RMSNORM_ERR_CUDA;
+    }
+    MatmulPlan p;
+    matmul_plan(M, N, K, tma_rows(a, lda, M) && tma_rows(b, ldb, N), dtype, sms, p);
+    MatmulArgs t = {};
+    t.a = static_cast<const uint8_t*>(a);
+    t.sa = a_scales;
+    t.b = static_cast<const uint8_t*>(b);
+    t.sb = b_scales;
+    t.bias = bias;
+    t.y = y;
+    t.lda = lda;
+    t.ldsa = ldas;
+    t.ldb = ldb;
+    t.ldsb = ldbs;
+    t.ldy = ldy;
+    t.M = M;
+    t.N = static_cast<int>(N);
+    t.K = static_cast<int>(K);
+    t.kblocks = static_cast<int>(kblocks);
+    t.per_row = group == 0;
+    t.m_tiles = static_cast<int>(ceil_div(M, p.wide ? 128 : p.n));
+    t.n_tiles = static_cast<int>(ceil_div(N, p.wide ? p.n : 128));
+    t.wide_y = aligned(y, 16) && ldy * static_cast<int64_t>(s) % 16 == 0;
+    t.err = device_error_word();
+    if (!t.err) return RMSNORM_ERR_CUDA;
+    CUtensorMap amap = {}, bmap = {};
+    if (p.tma && (!tile_map(amap, a, lda, M, K, p.wide ? 128 : p.n) || !tile_map(bmap, b, ldb, N, K, p.wide ? p.n : 128)))
+        return RMSNORM_ERR_CUDA;
+    void* params[] = {&t, &amap, &bmap};
+    return run(matmul_kernel(p), p.blocks, p.threads, p.smem, p.split, params, stream);
+}
