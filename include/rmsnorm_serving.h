@@ -61,6 +61,46 @@ rmsnorm_status rmsnorm_quant_matmul(const void* a, int64_t lda, const float* a_s
                                     int64_t ldy, int64_t M, int64_t N, int64_t K, rmsnorm_dtype dtype, int group,
                                     rmsnorm_stream_t stream);
 
+/*
+ * Heads of one kind for a paged cache, a model's keys or its values: entry d of head j of
+ * token t is at x[t * x_token + j * x_head + d] (strides in elements, as in
+ * rmsnorm_rope_heads), gamma[D] the weight of the keys' norm or NULL (always NULL of
+ * values). Entry d of head j of row i of page p of the cache is at rows[p * page + i * row + j *
+ * head + d], in any order of the three strides that keeps the rows apart. scales NULL: rows
+ * are of the call's dtype. Else they are e4m3 codes (uint8), with the head row's float32 scale
+ * at scales[p * scale_page + i * scale_row + j * scale_head]: scale = max(max|z| / 448, 2^-126),
+ * code = z / scale as in rmsnorm_quant_fwd, non-finite entries too.
+ */
+typedef struct {
+    const void* x;
+    int64_t x_token, x_head;
+    const void* gamma;
+    void* rows;
+    int64_t page, row, head;
+    float* scales;
+    int64_t scale_page, scale_row, scale_head;
+    int64_t heads;
+} rmsnorm_cache_heads;
+
+/*
+ * One step of serving before an attention: queries and keys are normalised and rotated as by
+ * rmsnorm_rope_fwd (same arguments), queries go to q's y, and keys and values (as they are) go
+ * to slot slots[t] of their caches: row slots[t] % page_size of page slots[t] / page_size,
+ * of `pages` pages. A negative slot (a padded token) stores nothing; its query is
+ * rotated all the same. A slot behind the last stores nothing and sets bit 2 of the device
+ * error word (rmsnorm_device_error). Slots of one call that are not negative must be
+ * distinct: of rows that share one, what remains is unspecified. Rows that no slot names
+ * are not touched. slots: int64[T]. q may be NULL (a prompt's keys alone), and v may be
+ * (keys that serve as values). The caches may be interleaved parts of one tensor of
+ * the same strides; they must not overlap the heads, the weights or each other otherwise. Values
+ * are copied bit by bit where their cache has no scales.
+ */
+rmsnorm_status rmsnorm_rope_append(const rmsnorm_rope_heads* q, const rmsnorm_cache_heads* k,
+                                   const rmsnorm_cache_heads* v, const int64_t* slots, int64_t pages,
+                                   int64_t page_size, const int64_t* positions, int64_t T, int64_t D,
+                                   int64_t rotary_dim, const double* inv_freq, int interleaved, float mscale, float eps,
+                                   rmsnorm_dtype dtype, int offset, rmsnorm_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -92,6 +92,7 @@ def _load():
             "rmsnorm_rope_fwd": (I, [P, I, P, I64, I64, I64, P, I, F, F, I, I, P]),
             "rmsnorm_rope_bwd_workspace_size": (SZ, [I64, I64, I64, I]),
             "rmsnorm_rope_bwd": (I, [P, I, P, I64, I64, I64, P, I, F, F, I, I, P, SZ, P]),
+            "rmsnorm_rope_append": (I, [P, P, P, P, I64, I64, P, I64, I64, I64, P, I, F, F, I, I, P]),
             "rmsnorm_quant_weight": (I, [P, I64, P, I64, P, I64, I64, I64, I, I, P]),
             "rmsnorm_quant_matmul": (I, [P, I64, P, I64, P, I64, P, I64, P, P, I64, I64, I64, I64, I, I, P]),
         }
@@ -326,6 +327,37 @@ def rmsnorm_quant_matmul(a, lda, a_scales, ldas, b, ldb, b_scales, ldbs, bias, y
     return _load().rmsnorm_quant_matmul(_addr(a), int(lda), _addr(a_scales), int(ldas), _addr(b), int(ldb),
                                         _addr(b_scales), int(ldbs), _addr(bias), _addr(y), int(ldy), int(M), int(N),
                                         int(K), _dtype_code(dtype), int(group), _stream(stream))
+
+
+class CacheHeads(ctypes.Structure):
+    """rmsnorm_cache_heads: keys or values and their paged cache (see include/rmsnorm_serving.h)."""
+    _fields_ = [("x", ctypes.c_void_p), ("x_token", ctypes.c_int64), ("x_head", ctypes.c_int64),
+                ("gamma", ctypes.c_void_p),
+                ("rows", ctypes.c_void_p), ("page", ctypes.c_int64), ("row", ctypes.c_int64), ("head", ctypes.c_int64),
+                ("scales", ctypes.c_void_p), ("scale_page", ctypes.c_int64), ("scale_row", ctypes.c_int64),
+                ("scale_head", ctypes.c_int64), ("heads", ctypes.c_int64)]
+
+
+def cache_heads(x, gamma, rows, scales=None):
+    """The ``k`` or ``v`` of rmsnorm_rope_append: x [tokens, heads, D], gamma [D] or None, the
+    cache's rows [pages, page_size, heads, D] with unit stride in D (a transposed view where
+    heads lie outside of rows) and, of an e4m3 cache, scales [pages, page_size, heads]. It
+    holds the tensors' addresses, as rope_heads does."""
+    if rows.dim() != 4 or (rows.shape[3] > 1 and rows.stride(3) != 1):
+        raise ValueError("a cache is [pages, page_size, heads, D] with unit stride in D")
+    if scales is not None and scales.dim() != 3:
+        raise ValueError("scales are [pages, page_size, heads]")
+    return (CacheHeads * 1)(CacheHeads(*_head_strides(x), _addr(gamma), rows.data_ptr(), *rows.stride()[:3], _addr(scales),
+                                       *(scales.stride() if scales is not None else (0, 0, 0)), x.shape[1]))
+
+
+def rmsnorm_rope_append(q, k, v, slots, pages, page_size, positions, T, D, rotary_dim, inv_freq, interleaved, mscale, eps,
+                        dtype, offset, stream=None) -> int:
+    """q: what rope_heads returns for one set, or None; k, v: what cache_heads returns (v or None)."""
+    return _load().rmsnorm_rope_append(*(None if h is None else ctypes.addressof(h) for h in (q, k, v)), _addr(slots),
+                                       int(pages), int(page_size), _addr(positions), int(T), int(D), int(rotary_dim),
+                                       _addr(inv_freq), int(interleaved), float(mscale), float(eps), _dtype_code(dtype),
+                                       int(offset), _stream(stream))
 
 
 def rmsnorm_status_string(status: int) -> str:

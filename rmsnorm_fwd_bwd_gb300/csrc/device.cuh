@@ -16,6 +16,8 @@ constexpr uint32_t kDevErrWaitTimeout = 1u;
 // Bit 1 (debug builds, -DRMSNORM_DEBUG): a row kernel was about to read bytes
 // outside the tensor it reads; the read was skipped.
 constexpr uint32_t kDevErrOutOfBounds = 2u;
+// Bit 2: a token's slot lies behind the last of its cache; nothing was stored for it.
+constexpr uint32_t kDevErrSlot = 4u;
 #ifdef RMSNORM_DEBUG
 constexpr bool kDebugReads = true;
 #else

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/rmsnorm.h"
+
 namespace rmsnorm {
 
 // Most rope sets (query heads, key heads) of one call.
@@ -123,7 +125,21 @@ struct RopePlan {
 // flight together (128 bytes a lane).
 constexpr int rope_fwd_batch(int dtype) { return dtype == 0 ? 2 : 4; }
 
+// Most heads for which a group computes a token's cosines and sines once, but for the forward
+// of whole octets.
+constexpr int kRopeRun = 8;
+
 const void* rope_kernel(const RopePlan& p, bool bwd);
+// How head rows are taken, and the lanes (and pairs of each) that take one; wide: they start on
+// 16-byte boundaries.
+void rope_lanes(int64_t D, int64_t R, int interleaved, bool wide, RopePlan& p);
+
+// Checks that the entry points of heads share. Strides of [T, heads, D] heads; of an output,
+// whose rows must not overlap (tokens outside heads, or heads outside tokens); the numbers.
+bool strides_ok(int64_t token, int64_t head, int64_t heads, int64_t T, int64_t D);
+bool output_strides_ok(int64_t token, int64_t head, int64_t heads, int64_t T, int64_t D);
+rmsnorm_status check_rope(int nsets, int64_t T, int64_t D, int64_t R, int interleaved, float mscale, float eps,
+                          rmsnorm_dtype dtype, int offset);
 
 // SMs of the current device, whose number goes to dev; 0 on failure.
 int current_sms(int& dev);

@@ -20,10 +20,7 @@ static_assert(kRopeMaxSets == RMSNORM_ROPE_MAX_SETS, "sets of a rope call");
 // 16.9 us without it, 1024 x 4096 15.7 with it).
 constexpr int64_t kRingLeastRows = 1024;
 
-// The rotation: most heads for which a group computes a token's cosines and sines once
-// (rope.cu), but for the forward of whole octets, and the backward's blocks per SM (what
-// its registers leave).
-constexpr int kRopeRun = 8;
+// The rotation's backward's blocks per SM (what its registers leave).
 constexpr int kRopeBwdBlocks = 3;
 
 std::mutex g_fused_mu;
@@ -286,6 +283,8 @@ rmsnorm_status run(const void* k, const AddPlan& p, AddArgs& a, rmsnorm_stream_t
     return RMSNORM_ERR_CUDA;
 }
 
+}  // namespace
+
 // ---------------------------------------------------------------------------
 // rope
 // ---------------------------------------------------------------------------
@@ -301,6 +300,33 @@ bool output_strides_ok(int64_t token, int64_t head, int64_t heads, int64_t T, in
            (T <= 1 || heads <= 1 || token >= (heads - 1) * head + D || head >= (T - 1) * token + D);
 }
 
+rmsnorm_status check_rope(int nsets, int64_t T, int64_t D, int64_t R, int interleaved, float mscale, float eps,
+                          rmsnorm_dtype dtype, int offset) {
+    const rmsnorm_status st = check_common(T, D, dtype, offset);
+    if (st != RMSNORM_OK) return st;
+    if (D > RMSNORM_ROPE_MAX_D || R < 2 || R > D || R % 2 != 0) return RMSNORM_ERR_SHAPE;
+    if (!std::isfinite(eps) || !(eps > 0.0f)) return RMSNORM_ERR_EPS;
+    if (nsets < 1 || nsets > RMSNORM_ROPE_MAX_SETS || (interleaved != 0 && interleaved != 1) || !std::isfinite(mscale))
+        return RMSNORM_ERR_ARG;
+    return RMSNORM_OK;
+}
+
+void rope_lanes(int64_t D, int64_t R, int interleaved, bool wide, RopePlan& p) {
+    if (wide && D % 8 == 0) p.rows = interleaved ? kRopeNeighbours : R % 16 == 0 ? kRopeHalves : kRopeSwap;
+    p.threads = kFusedGroupThreads;
+    if (p.rows != kRopeEntries) {
+        const int64_t units = p.rows == kRopeHalves ? R / 16 + ceil_div(D - R, 16) : ceil_div(D, 16);
+        for (p.lanes = 4; p.lanes < units;) p.lanes *= 2;
+    } else {
+        // up to four pairs a lane (eight of 32 lanes) and few lanes, whose sums take fewer steps
+        const int64_t pairs = R / 2 + ceil_div(D - R, 2);
+        for (p.lanes = 8; p.lanes < 32 && 4 * p.lanes < pairs;) p.lanes *= 2;
+        p.pairs = static_cast<int>(ceil_div(pairs, p.lanes));
+    }
+}
+
+namespace {
+
 // Whether a set's output, where it lies on an input of a set, is that set's heads, of the same
 // strides.
 bool same_heads(const RopeArgs& a, int64_t T, int nsets) {
@@ -313,17 +339,6 @@ bool same_heads(const RopeArgs& a, int64_t T, int nsets) {
                 return false;
         }
     return true;
-}
-
-rmsnorm_status check_rope(int nsets, int64_t T, int64_t D, int64_t R, int interleaved, float mscale, float eps,
-                          rmsnorm_dtype dtype, int offset) {
-    const rmsnorm_status st = check_common(T, D, dtype, offset);
-    if (st != RMSNORM_OK) return st;
-    if (D > RMSNORM_ROPE_MAX_D || R < 2 || R > D || R % 2 != 0) return RMSNORM_ERR_SHAPE;
-    if (!std::isfinite(eps) || !(eps > 0.0f)) return RMSNORM_ERR_EPS;
-    if (nsets < 1 || nsets > RMSNORM_ROPE_MAX_SETS || (interleaved != 0 && interleaved != 1) || !std::isfinite(mscale))
-        return RMSNORM_ERR_ARG;
-    return RMSNORM_OK;
 }
 
 bool rope_wide(const RopeSet& s, size_t e) {
@@ -340,17 +355,7 @@ rmsnorm_status rope_plan(RopeArgs& a, int dtype, int interleaved, bool wide, boo
     const int sms = current_sms(dev);
     if (!sms) return RMSNORM_ERR_CUDA;
     p.dtype = dtype;
-    if (wide && a.D % 8 == 0) p.rows = interleaved ? kRopeNeighbours : a.R % 16 == 0 ? kRopeHalves : kRopeSwap;
-    p.threads = kFusedGroupThreads;
-    if (p.rows != kRopeEntries) {
-        const int64_t units = p.rows == kRopeHalves ? a.R / 16 + ceil_div(a.D - a.R, 16) : ceil_div(a.D, 16);
-        for (p.lanes = 4; p.lanes < units;) p.lanes *= 2;
-    } else {
-        // up to four pairs a lane (eight of 32 lanes) and few lanes, whose sums take fewer steps
-        const int64_t pairs = a.R / 2 + ceil_div(a.D - a.R, 2);
-        for (p.lanes = 8; p.lanes < 32 && 4 * p.lanes < pairs;) p.lanes *= 2;
-        p.pairs = static_cast<int>(ceil_div(pairs, p.lanes));
-    }
+    rope_lanes(a.D, a.R, interleaved, wide, p);
     const int group = p.lanes;  // lanes that share an item
     // groups that fill the GPU: 1024 threads an SM, of which the registers leave 640 in the
     // forward and 384 in the backward (bf16 1024 x 40 x 128: forward 5.9 us, 8.8 by 2048

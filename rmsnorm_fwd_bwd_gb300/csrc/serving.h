@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "fused.h"
+
 namespace rmsnorm {
 
 // The 8-bit product y = (a sa) (b sb)^T + bias.
@@ -52,6 +54,27 @@ struct WeightArgs {
 
 const void* weight_kernel(int dtype, bool aligned);
 int weight_threads();
+
+// Heads of one kind of an append: queries (y: their output, y_token a token's stride), keys or
+// values (y: the cache's rows, y_token the stride between a page's rows).
+struct AppendSet : RopeSet {
+    int64_t y_page;
+    float* scales;  // of e4m3 rows; null: rows in the heads' type
+    int64_t scale_page, scale_row, scale_head;
+};
+
+// The rotation's members are RopeArgs' (its sets are not used); a kind that is missing has no
+// heads.
+struct AppendArgs : RopeArgs {
+    AppendSet sets[3];
+    int first[3];              // chunk of a token with which a kind starts
+    const int64_t* slots;
+    int64_t pages;
+    int page_size;
+    uint32_t* err;
+};
+
+const void* append_kernel(const RopePlan& p, bool codes);
 
 const void* matmul_kernel(const MatmulPlan& p);
 // Threads and shared memory of a plan whose other members are set.

@@ -115,6 +115,36 @@ bool overlap(const void* p, int64_t bytes, const void* q, int64_t more) {
 
 int64_t span(int64_t rows, int64_t ld, int64_t width, int64_t bytes) { return rows > 0 ? ((rows - 1) * ld + width) * bytes : 0; }
 
+// Dimensions of a tensor by count and stride, outside of `inner` elements: whether no two of
+// its elements meet (each stride steps over all that lies inside of it), and the elements
+// from its first to behind its last.
+struct Dim {
+    int64_t count, stride;
+};
+bool nested(std::initializer_list<Dim> dims, int64_t inner, int64_t& extent) {
+    Dim d[4];
+    int n = 0;
+    for (const Dim& x : dims)
+        if (x.count > 1) d[n++] = x;
+    std::sort(d, d + n, [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
+    extent = inner;
+    for (int i = 0; i < n; ++i) {
+        if (d[i].stride < extent || d[i].stride > (int64_t(1) << 46) / d[i].count) return false;
+        extent += (d[i].count - 1) * d[i].stride;
+    }
+    return extent <= int64_t(1) << 46;
+}
+
+// Whether two caches of one kind of rows keep out of each other: apart, or, of the same
+// strides, interleaved as the halves of one tensor.
+bool caches_apart(const void* p, const void* q, int64_t span_p, int64_t span_q, int64_t bytes, bool same, const Dim& page,
+                  const Dim& row, const Dim& head, int64_t inner) {
+    if (!overlap(p, span_p, q, span_q)) return true;
+    const int64_t apart = reinterpret_cast<intptr_t>(q) - reinterpret_cast<intptr_t>(p);
+    int64_t all;
+    return same && apart % bytes == 0 && nested({page, row, head, {2, std::abs(apart / bytes)}}, inner, all);
+}
+
 bool dtype_ok(rmsnorm_dtype dt) { return dt == RMSNORM_F32 || dt == RMSNORM_F16 || dt == RMSNORM_BF16; }
 
 }  // namespace
@@ -208,4 +238,153 @@ extern "C" rmsnorm_status rmsnorm_quant_matmul(const void* a, int64_t lda, const
         return RMSNORM_ERR_CUDA;
     void* params[] = {&t, &amap, &bmap};
     return run(matmul_kernel(p), p.blocks, p.threads, p.smem, p.split, params, stream);
+}
+
+extern "C" rmsnorm_status rmsnorm_rope_append(const rmsnorm_rope_heads* q, const rmsnorm_cache_heads* k,
+                                              const rmsnorm_cache_heads* v, const int64_t* slots, int64_t pages,
+                                              int64_t page_size, const int64_t* positions, int64_t T, int64_t D,
+                                              int64_t rotary_dim, const double* inv_freq, int interleaved, float mscale,
+                                              float eps, rmsnorm_dtype dtype, int offset, rmsnorm_stream_t stream) {
+    rmsnorm_status st = check_rope(1, T, D, rotary_dim, interleaved, mscale, eps, dtype, offset);
+    if (st != RMSNORM_OK) return st;
+    if (!k) return RMSNORM_ERR_NULL;
+    if (pages < 1 || page_size < 1 || page_size > INT32_MAX || pages > (int64_t(1) << 46) / page_size) return RMSNORM_ERR_SHAPE;
+    const int64_t s = elem_bytes(dtype);
+    AppendArgs a = {};
+    bool wide = true, codes = false;
+    int64_t heads = 0, bytes[3] = {0, 0, 0}, extent[3] = {0, 0, 0}, scale_extent[3] = {0, 0, 0};
+    if (q) {
+        if (q->heads < 1 || q->heads > RMSNORM_ROPE_MAX_HEADS || !strides_ok(q->x_token, q->x_head, q->heads, T, D) ||
+            !output_strides_ok(q->y_token, q->y_head, q->heads, T, D))
+            return RMSNORM_ERR_SHAPE;
+        AppendSet& t = a.sets[0];
+        t.x = q->x;
+        t.gamma = q->gamma;
+        t.y = q->y;
+        t.x_token = q->x_token;
+        t.x_head = q->x_head;
+        t.y_token = q->y_token;
+        t.y_head = q->y_head;
+        t.heads = static_cast<int>(q->heads);
+        bytes[0] = s;
+        extent[0] = T > 0 ? (T - 1) * q->y_token + (q->heads - 1) * q->y_head + D : 0;
+        heads += q->heads;
+    }
+    for (int i = 1; i < 3; ++i) {
+        const rmsnorm_cache_heads* c = i == 1 ? k : v;
+        if (!c) continue;
+        if (c->heads < 1 || c->heads > RMSNORM_ROPE_MAX_HEADS || !strides_ok(c->x_token, c->x_head, c->heads, T, D) ||
+            !nested({{pages, c->page}, {page_size, c->row}, {c->heads, c->head}}, D, extent[i]) ||
+            (c->scales &&
+             !nested({{pages, c->scale_page}, {page_size, c->scale_row}, {c->heads, c->scale_head}}, 1, scale_extent[i])))
+            return RMSNORM_ERR_SHAPE;
+        if (i == 2 && c->gamma) return RMSNORM_ERR_ARG;  // values are not normalised
+        AppendSet& t = a.sets[i];
+        t.x = c->x;
+        t.gamma = c->gamma;
+        t.y = c->rows;
+        t.x_token = c->x_token;
+        t.x_head = c->x_head;
+        t.y_page = c->page;
+        t.y_token = c->row;
+        t.y_head = c->head;
+        t.scales = c->scales;
+        t.scale_page = c->scale_page;
+        t.scale_row = c->scale_row;
+        t.scale_head = c->scale_head;
+        t.heads = static_cast<int>(c->heads);
+        bytes[i] = c->scales ? 1 : s;
+        codes = codes || c->scales;
+        heads += c->heads;
+    }
+    if (heads > RMSNORM_ROPE_MAX_HEADS) return RMSNORM_ERR_SHAPE;
+    if (T == 0) return RMSNORM_OK;
+    const int64_t words = 16 / s;
+    for (int i = 0; i < 3; ++i) {
+        const AppendSet& t = a.sets[i];
+        if (!t.heads) continue;
+        if (!t.x || !t.y) return RMSNORM_ERR_NULL;
+        if (!aligned(t.x, s) || !aligned(t.gamma, s) || !aligned(t.y, bytes[i]) || !aligned(t.scales, 4)) return RMSNORM_ERR_ALIGN;
+        const int64_t w = t.scales ? 8 : words;
+        wide = wide && aligned(t.x, 16) && aligned(t.gamma, 16) && t.x_token % words == 0 && t.x_head % words == 0 &&
+               aligned(t.y, t.scales ? 8 : 16) && t.y_page % w == 0 && t.y_token % w == 0 && t.y_head % w == 0;
+    }
+    if (!slots || !positions || !inv_freq) return RMSNORM_ERR_NULL;
+    if (!aligned(slots, 8) || !aligned(positions, 8) || !aligned(inv_freq, 8)) return RMSNORM_ERR_ALIGN;
+    // what is written against what is read and written: the queries' output may be the queries
+    for (int i = 0; i < 3; ++i) {
+        const AppendSet& o = a.sets[i];
+        if (!o.heads) continue;
+        for (int j = 0; j < 3; ++j) {
+            const AppendSet& t = a.sets[j];
+            if (!t.heads) continue;
+            const int64_t read = ((T - 1) * t.x_token + (t.heads - 1) * t.x_head + D) * s;
+            // the queries' output may be the queries, or lie between other heads of their rows
+            if (i > 0 ? overlap(o.y, extent[i] * bytes[i], t.x, read)
+                      : o.y == t.x && !(j == 0 && (T <= 1 || o.y_token == t.x_token) && (t.heads <= 1 || o.y_head == t.x_head)))
+                return RMSNORM_ERR_ARG;
+            if (overlap(o.y, extent[i] * bytes[i], t.gamma, D * s) || overlap(o.scales, scale_extent[i] * 4, t.x, read) ||
+                overlap(o.scales, scale_extent[i] * 4, t.gamma, D * s) ||
+                overlap(o.scales, scale_extent[i] * 4, t.y, extent[j] * bytes[j]))
+                return RMSNORM_ERR_ARG;
+        }
+        if (i > 0 && overlap(o.y, extent[i] * bytes[i], a.sets[0].y, extent[0] * bytes[0])) return RMSNORM_ERR_ARG;
+        for (const void* p : {static_cast<const void*>(slots), static_cast<const void*>(positions)})
+            if (overlap(o.y, extent[i] * bytes[i], p, T * 8) || overlap(o.scales, scale_extent[i] * 4, p, T * 8)) return RMSNORM_ERR_ARG;
+        if (overlap(o.y, extent[i] * bytes[i], inv_freq, rotary_dim * 4) ||
+            overlap(o.scales, scale_extent[i] * 4, inv_freq, rotary_dim * 4))
+            return RMSNORM_ERR_ARG;
+    }
+    if (v) {
+        const AppendSet &x = a.sets[1], &y = a.sets[2];
+        const int most = std::max(x.heads, y.heads);
+        const bool same = bytes[1] == bytes[2] && x.y_page == y.y_page && x.y_token == y.y_token && x.y_head == y.y_head;
+        if (!caches_apart(x.y, y.y, extent[1] * bytes[1], extent[2] * bytes[2], bytes[1], same, {pages, x.y_page},
+                          {page_size, x.y_token}, {most, x.y_head}, D))
+            return RMSNORM_ERR_ARG;
+        const bool same_scales = x.scale_page == y.scale_page && x.scale_row == y.scale_row && x.scale_head == y.scale_head;
+        if (x.scales && y.scales &&
+            !caches_apart(x.scales, y.scales, scale_extent[1] * 4, scale_extent[2] * 4, 4, same_scales, {pages, x.scale_page},
+                          {page_size, x.scale_row}, {most, x.scale_head}, 1))
+            return RMSNORM_ERR_ARG;
+    }
+    int dev = 0;
+    const int sms = current_sms(dev);
+    if (!sms) {
+        (void)cudaGetLastError();
+        return RMSNORM_ERR_CUDA;
+    }
+    a.heads = static_cast<int>(heads);
+    a.pos = positions;
+    a.inv_freq = inv_freq;
+    a.T = T;
+    a.D = static_cast<int>(D);
+    a.R = static_cast<int>(rotary_dim);
+    a.interleaved = interleaved;
+    a.mscale = mscale;
+    a.eps = eps;
+    a.one = static_cast<float>(offset);
+    a.slots = slots;
+    a.pages = pages;
+    a.page_size = static_cast<int>(page_size);
+    a.err = device_error_word();
+    if (!a.err) return RMSNORM_ERR_CUDA;
+    RopePlan p;
+    p.dtype = dtype;
+    rope_lanes(D, rotary_dim, interleaved, wide, p);
+    // heads to a group as in the rotation alone (rope_plan): all of a batch where the tokens
+    // fill the GPU, fewer where they do not
+    const int64_t full = static_cast<int64_t>(sms) * (p.rows == kRopeSwap ? 512 : 1024) / p.lanes;
+    const int64_t most = p.rows == kRopeEntries ? heads : p.rows == kRopeSwap ? kRopeRun : rope_fwd_batch(dtype);
+    a.chunk = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, T * heads / full)));
+    a.nchunk = 0;
+    for (int i = 0; i < 3; ++i) {
+        a.first[i] = a.nchunk;
+        a.nchunk += static_cast<int>(ceil_div(a.sets[i].heads, a.chunk));
+    }
+    p.blocks = ceil_div(T * a.nchunk, p.threads / p.lanes);
+    if (p.rows == kRopeEntries) p.blocks = std::min<int64_t>(p.blocks, static_cast<int64_t>(sms) * 64);
+    if (p.blocks > INT32_MAX) return RMSNORM_ERR_SHAPE;
+    void* params[] = {&a};
+    return run(append_kernel(p, codes), p.blocks, p.threads, 0, 1, params, stream);
 }

@@ -178,3 +178,232 @@ def test_weight_special_values():
     assert torch.isinf(s[1, 0]) and torch.isnan(v[130, 10]) and (v[131:256, :128] == 0).all()
     assert s[2, 2] == 2.0 ** -126
     assert torch.isfinite(v[128:, 128:]).all() and torch.isfinite(s[1:, 1:]).all()
+
+
+# --------------------------------------------------------------------------- #
+# keys and values into a paged cache
+# --------------------------------------------------------------------------- #
+EPS = 1e-6
+
+
+class Cache:
+    """A paged cache [pages, size, heads, D] of one type in one of the orders that caches have, filled with
+    a byte that tells what was written; ``t`` and ``s`` are the rows and their scales (or None)."""
+
+    def __init__(self, pages, size, heads, D, dtype, bits8, order, seed=0):
+        dt = F8 if bits8 else ref.TYPES[dtype]
+        e = torch.empty(0, dtype=dt).element_size()
+        gap = {"spaced": 3}.get(order, 0)
+        width = D + gap
+        if order in ("rows", "spaced"):
+            strides = (size * heads * width, heads * width, width)
+        elif order == "heads first":
+            strides = (heads * size * width, width, size * width)
+        elif order == "keys and values":                    # [pages, 2, size, heads, D]
+            strides = (2 * size * heads * width, heads * width, width)
+        self.buf = torch.full((pages * strides[0] * e + 64 * e,), 0x55, dtype=torch.uint8, device="cuda")
+        typed = self.buf.view(dt)
+        self.start = gap
+        self.t = typed.as_strided((pages, size, heads, D), (*strides, 1), self.start)
+        self.typed, self.strides, self.shape = typed, strides, (pages, size, heads, D)
+        self.sbuf = torch.full((pages, size, heads + gap), 7.0, device="cuda") if bits8 else None
+        self.s = self.sbuf[..., :heads] if bits8 else None
+
+    def other(self):
+        """The values' half of a cache of keys and values."""
+        c = object.__new__(Cache)
+        c.__dict__ = dict(self.__dict__)
+        _, size, heads, D = self.shape
+        c.start = size * heads * (self.strides[2])
+        c.t = self.typed.as_strided(self.shape, (*self.strides, 1), c.start)
+        if self.sbuf is not None:
+            c.sbuf = torch.full_like(self.sbuf, 7.0)
+            c.s = c.sbuf[..., :heads]
+        return c
+
+    def rows(self, slots):
+        size = self.shape[1]
+        return self.t[slots // size, slots % size], None if self.s is None else self.s[slots // size, slots % size]
+
+    def untouched_but(self, slots, *more):
+        """Every byte that is not a row of the given slots (of this cache and others in its buffer) is as it was."""
+        mark = torch.zeros(self.typed.shape, dtype=torch.bool, device="cuda")
+        for c in (self, *more):
+            view = mark.as_strided(c.shape, (*c.strides, 1), c.start)
+            view[slots // c.shape[1], slots % c.shape[1]] = True
+        raw = self.buf.view(-1, self.typed.element_size())
+        assert (raw[~mark] == 0x55).all(), "written outside the slots"
+        for c in (self, *more):
+            if c.sbuf is not None:
+                m = torch.zeros(c.sbuf.shape, dtype=torch.bool, device="cuda")
+                m[slots // c.shape[1], slots % c.shape[1], :c.shape[2]] = True
+                assert (c.sbuf[~m] == 7.0).all()
+
+
+def randn(*shape, dtype, seed, scale=1.0):
+    return (torch.randn(*shape, generator=torch.Generator().manual_seed(seed)) * scale).to(ref.TYPES[dtype])
+
+
+def freqs(R, base=10000.0):
+    return torch.tensor([base ** (-2.0 * i / R) for i in range(R // 2)], dtype=torch.float64)
+
+
+def spaced_heads(x, how):
+    """x [T, H, D] on the GPU, as it lies in one of the layouts that a model has."""
+    T, H, D = x.shape
+    lead, tok, head = {"dense": (0, H * D, D), "fused": (2 * D, (H + 5) * D, D), "odd": (3, H * (D + 5) + 1, D + 5)}[how]
+    buf = torch.full((lead + T * tok + D + 64,), 3.0).to(x.dtype).cuda()
+    t = buf.as_strided((T, H, D), (tok, head, 1), lead)
+    t.copy_(x)
+    return t
+
+
+def check_rows(got, scales, x, w, pos, R, inter, mscale, offset, dtype):
+    """Rows of a cache against z: rotated keys, or the values as they are (w: "values")."""
+    if isinstance(w, str):
+        if scales is None:
+            assert torch.equal(got.view(torch.uint8), x.cuda().view(torch.uint8))
+            return
+        z, err = x.double(), torch.zeros(x.shape, dtype=torch.float64)
+    else:
+        z, err = ref.rope_fwd(x, w, pos, freqs(R), inter, mscale, EPS, offset)
+    if scales is None:
+        ref.assert_close(got, z, err + ref.rounding(z.abs() + err, ref.TYPES[dtype]), "rows")
+        return
+    s = scales.double().cpu().unsqueeze(-1)
+    amax = z.abs().amax(-1, keepdim=True)
+    # the largest |z| is off by at most the largest error, the product with r / 448 by 3 u
+    ref.assert_close(s, (amax / 448.0).clamp_min(2.0 ** -126), (err.amax(-1, keepdim=True) + 3 * U * amax) / 448.0, "scales")
+    # the factors r / scale: 1 / scale off by a unit in the last place (2 u) and the products by u each
+    off = err + 5 * U * z.abs()
+    ref.assert_close(got.double().cpu() * s, z, off + torch.maximum((z.abs() + off) * 2.0 ** -4, s * 2.0 ** -10), "codes")
+
+
+def run_append(T, Hq, Hk, D, R, dtype, size=16, bits8=(False, False), inter=False, offset=False, mscale=1.0, order="rows",
+               how="dense", pos=None, slots=None, weights=True, with_q=True, with_v=True, seed=80, in_place=False):
+    q, k, v = (randn(T, h, D, dtype=dtype, seed=seed + i, scale=1.5) for i, h in enumerate((Hq, Hk, Hk)))
+    wq, wk = (randn(D, dtype=dtype, seed=seed + 3 + i, scale=0.2) + (0 if offset else 1) for i in range(2)) if weights else (None, None)
+    pages = -(-T // size) + 3
+    if slots is None:
+        slots = torch.randperm(pages * size, generator=torch.Generator().manual_seed(seed + 9))[:T]
+    if pos is None:
+        pos = torch.arange(T) * 37 + 5
+    kc = Cache(pages, size, Hk, D, dtype, bits8[0], order)
+    vc = kc.other() if order == "keys and values" else Cache(pages, size, Hk, D, dtype, bits8[1], order)
+    qg, kg, vg = (spaced_heads(t, how) for t in (q, k, v))
+    out = qg if in_place else torch.full((T, Hq, D), 5.0).to(qg.dtype).cuda()
+    wg = [None if w is None else w.cuda() for w in (wq, wk)]
+    sg, pg, fg = slots.cuda(), pos.cuda(), freqs(R).cuda()
+    st = B.rmsnorm_rope_append(B.rope_heads([(qg, wg[0], out)]) if with_q else None, B.cache_heads(kg, wg[1], kc.t, kc.s),
+                               B.cache_heads(vg, None, vc.t, vc.s) if with_v else None, sg, pages, size, pg, T, D, R, fg,
+                               int(inter), mscale, EPS, dtype, int(offset))
+    assert st == 0, B.rmsnorm_status_string(st)
+    stored = (slots >= 0) & (slots < pages * size)
+    at = slots[stored].cuda()
+    if order == "keys and values":
+        kc.untouched_but(at, vc)
+    else:
+        kc.untouched_but(at)
+        vc.untouched_but(at if with_v else at[:0])
+    check_rows(*kc.rows(at), k[stored], wk, pos[stored], R, inter, mscale, offset, dtype)
+    if with_v:
+        check_rows(*vc.rows(at), v[stored], "values", None, R, inter, mscale, offset, dtype)
+    if with_q:
+        want, err = ref.rope_fwd(q, wq, pos, freqs(R), inter, mscale, EPS, offset)
+        ref.assert_close(out, want, err + ref.rounding(want.abs() + err, ref.TYPES[dtype]), "queries")
+    return kc, vc, out
+
+
+HEADS = [(1, 1, 1, 2, 2), (5, 3, 1, 8, 8), (3, 2, 2, 16, 16), (7, 4, 2, 64, 64), (6, 5, 1, 64, 32), (4, 8, 2, 80, 80),
+         (4, 3, 3, 96, 48), (9, 7, 1, 128, 128), (3, 32, 8, 128, 128), (5, 2, 1, 128, 24), (3, 4, 4, 192, 128),
+         (4, 3, 1, 256, 256), (2, 3, 1, 512, 512), (5, 2, 1, 33, 32), (3, 2, 1, 77, 6), (2, 2, 1, 511, 510), (2, 5, 3, 90, 90),
+         (700, 5, 2, 64, 64), (3, 70, 9, 40, 16), (900, 12, 4, 80, 40), (300, 9, 3, 90, 44)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("bits8", [False, True])
+@pytest.mark.parametrize("T,Hq,Hk,D,R", HEADS)
+def test_append_shapes(T, Hq, Hk, D, R, bits8, inter, dtype):
+    run_append(T, Hq, Hk, D, R, dtype, bits8=(bits8, bits8), inter=inter)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("order", ["heads first", "spaced", "keys and values"])
+@pytest.mark.parametrize("how", ["fused", "odd"])
+@pytest.mark.parametrize("bits8", [(False, False), (True, True), (True, False), (False, True)])
+def test_append_layouts(bits8, how, order, dtype):
+    if order == "keys and values" and bits8[0] != bits8[1]:
+        pytest.skip("one tensor has one type")
+    for T, Hq, Hk, D, R in ((6, 3, 2, 64, 32), (50, 4, 1, 128, 128), (40, 3, 3, 36, 20), (40, 4, 2, 72, 40)):
+        for size in (1, 7, 64):
+            run_append(T, Hq, Hk, D, R, dtype, size=size, bits8=bits8, offset=True, mscale=1.25, order=order, how=how)
+
+
+@pytest.mark.parametrize("bits8", [False, True])
+def test_append_without_weights_queries_or_values(bits8):
+    for D, R in ((64, 64), (64, 24), (50, 30)):
+        run_append(9, 4, 2, D, R, "bfloat16", bits8=(bits8, bits8), weights=False)
+        run_append(9, 4, 2, D, R, "bfloat16", bits8=(bits8, bits8), with_q=False)
+        run_append(9, 4, 2, D, R, "float16", bits8=(bits8, bits8), with_v=False)
+        run_append(9, 4, 2, D, R, "float32", bits8=(bits8, bits8), with_q=False, with_v=False)
+        run_append(9, 4, 2, D, R, "bfloat16", bits8=(bits8, bits8), in_place=True, how="fused")
+
+
+@pytest.mark.parametrize("bits8", [False, True])
+def test_append_padded_tokens_and_slots_behind_the_last(bits8):
+    for D, R in ((64, 64), (64, 24), (50, 30)):
+        slots = torch.randperm(96)[:60]
+        slots[::3] = -1
+        slots[7] = -(1 << 40)
+        run_append(60, 4, 2, D, R, "bfloat16", bits8=(bits8, bits8), slots=slots)
+        assert B.rmsnorm_device_error(clear=True) == 0
+        slots[5] = 7 * 16                                   # the first behind seven pages of 16
+        slots[8] = 1 << 62
+        run_append(60, 4, 2, D, R, "bfloat16", bits8=(bits8, bits8), slots=slots)
+        assert B.rmsnorm_device_error(clear=True) == 4
+
+
+def test_append_to_a_cache_of_more_than_2_to_the_32_entries():
+    # 8 GiB and more of codes: offsets past 32 bits, of which a few rows are read
+    pages, size, H, D = 70000, 64, 8, 128
+    kc = torch.empty(pages, size, H, D, dtype=F8, device="cuda")
+    ks = torch.empty(pages, size, H, device="cuda")
+    T = 5
+    k, w = randn(T, H, D, dtype="bfloat16", seed=1), randn(D, dtype="bfloat16", seed=2) + 1
+    slots = torch.tensor([0, pages * size - 1, (1 << 22) + 1, 3, pages * size // 2])
+    pos = torch.arange(T)
+    kg, wg, sg, pg, fg = k.cuda(), w.cuda(), slots.cuda(), pos.cuda(), freqs(D).cuda()
+    heads = B.cache_heads(kg, wg, kc, ks)
+    assert B.rmsnorm_rope_append(None, heads, None, sg, pages, size, pg, T, D, D, fg, 0, 1.0, EPS, "bfloat16", 0) == 0
+    check_rows(kc[sg // size, sg % size], ks[sg // size, sg % size], k, w, pos, D, False, 1.0, False, "bfloat16")
+
+
+def test_append_of_infinities_and_nan_keeps_them_in_their_rows():
+    T, H, D, R = 6, 2, 64, 32
+    for bits8 in (False, True):
+        for inter in (False, True):
+            k, v = randn(T, H, D, dtype="float32", seed=5), randn(T, H, D, dtype="float32", seed=6)
+            k[1, 0, 50] = float("inf")                      # behind the rotated entries
+            k[2, 1, 3] = float("nan")
+            v[1, 1, 7] = float("-inf")
+            v[3, 0, 9] = float("nan")
+            v[4, 0] = 0.0
+            v[4, 0, 5] = -0.0
+            kc, vc = (Cache(1, 16, H, D, "float32", bits8, "rows") for _ in range(2))
+            kg, vg, sg, pg, fg = k.cuda(), v.cuda(), torch.arange(T).cuda(), torch.arange(T).cuda(), freqs(R).cuda()
+            args = (B.cache_heads(kg, None, kc.t, kc.s), B.cache_heads(vg, None, vc.t, vc.s))
+            assert B.rmsnorm_rope_append(None, *args, sg, 1, 16, pg, T, D, R, fg, int(inter), 1.0, EPS, "float32", 0) == 0
+            got_k, got_v = (c.t[0, :T].double().cpu() for c in (kc, vc))
+            clean = torch.ones(T, H, dtype=torch.bool)
+            clean[1, 0] = clean[2, 1] = False
+            z, _ = ref.rope_fwd(k, None, torch.arange(T), freqs(R), inter, 1.0, EPS)
+            if bits8:
+                assert torch.isinf(kc.s[0, 1, 0]) and torch.isnan(kc.s[0, 2, 1]) and torch.isinf(vc.s[0, 1, 1])
+                assert torch.isnan(got_k[1, 0, 50]) and (got_k[1, 0, :50] == 0).all()
+                assert torch.isnan(vc.s[0, 3, 0]) and vc.s[0, 4, 0] == 2.0 ** -126 and (got_v[4, 0] == 0).all()
+            else:
+                # the infinity stays where it is
+                assert torch.equal(torch.isfinite(got_k[1, 0]), torch.isfinite(k[1, 0]))
+                assert torch.equal(vc.t[0, :T].cpu().view(torch.int32), v.view(torch.int32))
+            assert torch.isfinite(got_k[clean]).all()

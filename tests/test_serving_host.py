@@ -51,3 +51,61 @@ def matmul(**kw):
 ])
 def test_quant_matmul_refusals(want, kw):
     assert matmul(**kw) == want
+
+
+def append(q=True, v=True, **kw):
+    qs = dict(x=0x1000000, x_token=256, x_head=64, gamma=0x1100000, y=0x1200000, y_token=256, y_head=64, heads=4)
+    ks = dict(x=0x2000000, x_token=128, x_head=64, gamma=0x2100000, rows=0x3000000, page=2048, row=128, head=64, scales=None,
+              scale_page=0, scale_row=0, scale_head=0, heads=2)
+    vs = dict(ks, x=0x4000000, gamma=None, rows=0x5000000)
+    a = dict(slots=0x6000000, pages=10, page_size=16, positions=0x6100000, T=4, D=64, rotary_dim=64, inv_freq=0x6200000,
+             interleaved=0, mscale=1.0, eps=1e-6, dtype=2, offset=0, stream=0)
+    for name, value in kw.items():
+        kind, _, field = name.partition("_")
+        (qs if kind == "q" else ks if kind == "k" else vs if kind == "v" else a)[field if kind in "qkv" else name] = value
+    keep = [(B.RopeHeads * 1)(B.RopeHeads(**qs)), (B.CacheHeads * 1)(B.CacheHeads(**ks)), (B.CacheHeads * 1)(B.CacheHeads(**vs))]
+    return B.rmsnorm_rope_append(keep[0] if q else None, keep[1], keep[2] if v else None, **a)
+
+
+SCALES = dict(k_scales=0x7000000, k_scale_page=32, k_scale_row=2, k_scale_head=1)
+
+
+@pytest.mark.parametrize("want,kw", [
+    (DTYPE, dict(dtype=4)), (ARG, dict(offset=2)), (SHAPE, dict(D=513)), (SHAPE, dict(rotary_dim=0)), (SHAPE, dict(rotary_dim=3)),
+    (SHAPE, dict(rotary_dim=66)), (EPS, dict(eps=0.0)), (ARG, dict(interleaved=2)), (ARG, dict(mscale=float("inf"))),
+    (SHAPE, dict(T=-1)), (SHAPE, dict(pages=0)), (SHAPE, dict(page_size=0)), (SHAPE, dict(page_size=1 << 31)),
+    (SHAPE, dict(pages=1 << 45)), (SHAPE, dict(q_heads=0)), (SHAPE, dict(k_heads=0)), (SHAPE, dict(v_heads=65537)),
+    (SHAPE, dict(q_x_token=63)), (SHAPE, dict(q_y_head=63)), (SHAPE, dict(k_x_head=-64)), (SHAPE, dict(k_row=127)),
+    (SHAPE, dict(k_head=63)), (SHAPE, dict(k_page=2047)), (SHAPE, dict(v_page=0)), (SHAPE, dict(v_row=-128)),
+    (SHAPE, dict(k_page=1 << 60)), (SHAPE, dict(SCALES, k_scale_row=1)), (SHAPE, dict(SCALES, k_scale_page=31)),
+    (ARG, dict(v_gamma=0x7000000)), (OK, dict(T=0, q_x=None, k_x=None, k_rows=None, slots=None, positions=None)),
+    (NULL, dict(q_x=None)), (NULL, dict(q_y=None)), (NULL, dict(k_x=None)), (NULL, dict(k_rows=None)), (NULL, dict(v_x=None)),
+    (NULL, dict(slots=None)), (NULL, dict(positions=None)), (NULL, dict(inv_freq=None)), (ALIGN, dict(q_x=0x1000001)),
+    (ALIGN, dict(k_rows=0x3000001)), (ALIGN, dict(SCALES, k_scales=0x7000002)), (ALIGN, dict(slots=0x6000004)),
+    (ALIGN, dict(positions=0x6100004)), (ALIGN, dict(k_gamma=0x2100001)),
+    (ARG, dict(k_rows=0x2000000)), (ARG, dict(k_rows=0x4000000 + 1022)), (ARG, dict(v_rows=0x3000000)),
+    (ARG, dict(v_rows=0x3000000 + 64)), (ARG, dict(v_rows=0x3000000 + 2 * 2048 * 10 - 2)), (ARG, dict(k_rows=0x1200000)),
+    (ARG, dict(k_rows=0x1100000)), (ARG, dict(k_rows=0x6000000)), (ARG, dict(SCALES, k_scales=0x3000000)),
+    (ARG, dict(SCALES, k_scales=0x2000000)), (ARG, dict(q_y=0x2000000)), (ARG, dict(q_y=0x1000000, q_y_token=512)),
+    (ARG, dict(q_y=0x1100000)), (ARG, dict(SCALES, v_scales=0x7000000, v_scale_page=32, v_scale_row=2, v_scale_head=1)),
+    # the halves of one tensor must have its strides, and rows of the other must fit between
+    (ARG, dict(v_rows=0x3000000 + 2 * 2048)), (ARG, dict(k_page=4096, v_page=2048, v_rows=0x3000000 + 2 * 2048)),
+    (ARG, dict(k_page=4096, v_page=4096, v_rows=0x3000000 + 2 * 2048 - 2)),
+])
+def test_append_refusals(want, kw):
+    assert append(**kw) == want
+
+
+def test_append_wants_keys():
+    assert B.rmsnorm_rope_append(None, None, None, 0x1000, 1, 1, 0x2000, 1, 64, 64, 0x3000, 0, 1.0, 1e-6, 2, 0, 0) == NULL
+
+
+def test_cache_heads_checks_its_tensors():
+    import torch
+    x, rows = torch.empty(2, 2, 8), torch.empty(3, 4, 2, 8)
+    with pytest.raises(ValueError):
+        B.cache_heads(x, None, rows[0])
+    with pytest.raises(ValueError):
+        B.cache_heads(x, None, rows.transpose(2, 3))
+    with pytest.raises(ValueError):
+        B.cache_heads(x, None, rows, torch.empty(3, 4))
