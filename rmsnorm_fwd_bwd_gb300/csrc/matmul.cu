@@ -8,13 +8,13 @@
 // fp32; the sum over blocks is taken in fp32 registers, by one multiply-add per element and
 // block (two of them in one packed instruction).
 //
-// Two kernels. matmul_wide: a tile of 128 rows of a (a thread's row of the accumulator) and
-// 128 or 256 of b, persistent blocks. matmul_thin, for few rows of a: the operands change places, a
-// tile is 128 rows of b and 16 to 128 of a, and the blocks of a cluster share K. In both one
-// thread keeps a ring of tiles full by TMA, one issues the matrix instructions into one of
-// several accumulators in tensor memory, and warps of four add finished ones up meanwhile.
-// Rows off 16 bytes, which TMA does not take, are loaded by four warps in words
-// that are shifted together.
+// Three kernels. matmul_pair: pairs of blocks on tiles of 256 x 256, a thread to a row of the
+// accumulator. matmul_wide: single blocks on tiles of 128 x 128. matmul_thin, for few rows
+// of a: the operands change places, a tile is 128 rows of b and 16 to 128 of a, and the blocks of a
+// cluster share K. In all of them one thread keeps a ring of tiles full by TMA, one issues
+// the matrix instructions into one of several accumulators in tensor memory, and warps of four
+// add finished ones up meanwhile. Rows off 16 bytes, which TMA does not take, are loaded
+// by three warps in words that are shifted together.
 #include "octet.cuh"
 #include "serving.h"
 #include "tcgen05.cuh"
@@ -24,10 +24,10 @@ namespace {
 
 constexpr int kTileBytes = 128 * kTileK;  // 128 rows
 
-constexpr int wide_stages(int n) { return n == 256 ? 4 : 6; }
+constexpr int kWideStages = 6, kPairStages = 6;
 constexpr int thin_stages(int n) { return n <= 32 ? 9 : n == 64 ? 8 : 6; }
 // Accumulators in tensor memory that are under way.
-constexpr int wide_buffers(int n) { return 512 / n; }
+constexpr int kWideBuffers = 4, kPairBuffers = 2;
 constexpr int kThinBuffers = 4;
 constexpr int thin_columns(int n) { return kThinBuffers * n; }
 
@@ -123,27 +123,48 @@ template <int STAGES, int BUFFERS> struct Bars {
     }
 };
 
-// The thread that issues matrix instructions: `blocks` blocks of K through the ring (X rows
-// by Y rows, X's tile first in a stage) into the accumulators in turn.
-template <int STAGES, int BUFFERS, int Y>
+// The warp that issues matrix instructions: `blocks` blocks of K through the ring (X rows by Y
+// rows, X's tile first in a stage of BYTES) into the accumulators in turn. PAIR: for both blocks
+// of a cluster, X of 256 rows. The loop is the whole warp's, see elect_lane (16384 x 8192 x 8192
+// 1110 us with a loop of one thread).
+template <int STAGES, int BUFFERS, int Y, bool PAIR>
 __device__ __forceinline__ void issue(Bars<STAGES, BUFFERS>& bars, uint32_t tiles, uint32_t tmem, int64_t blocks, uint32_t* err) {
-    constexpr uint32_t kStage = kTileBytes + Y * kTileK;
-    constexpr uint32_t idesc = e4m3_idesc(128, Y);
+    constexpr uint32_t kStage = PAIR ? 2 * kTileBytes : kTileBytes + Y * kTileK;
+    constexpr uint32_t idesc = e4m3_idesc(PAIR ? 256 : 128, Y);
+    const uint64_t x0 = tile_desc(tiles), y0 = tile_desc(tiles + kTileBytes);
+    const uint32_t full = smem_u32(bars.full), empty = smem_u32(bars.empty), done = smem_u32(bars.done),
+                   taken = smem_u32(bars.taken);
     Ring<STAGES> s;
     Ring<BUFFERS> b;
     for (int64_t i = 0; i < blocks; ++i) {
-        if (!mbar_wait_bounded(smem_u32(&bars.taken[b.at]), b.phase ^ 1u, err) ||
-            !mbar_wait_bounded(smem_u32(&bars.full[s.at]), s.phase, err)) {
-            mma_commit(smem_u32(&bars.drain));
+        const bool ok = mbar_wait_bounded(taken + 8 * b.at, b.phase ^ 1u, err) && mbar_wait_bounded(full + 8 * s.at, s.phase, err);
+        if (!__all_sync(0xffffffffu, ok)) {
+            if (elect_lane()) {
+                const uint32_t drain = smem_u32(&bars.drain);
+                if (PAIR) mma_commit_pair(drain);
+                else mma_commit(drain);
+            }
             mbar_wait_bounded(smem_u32(&bars.drain), 0, err);
             return;
         }
         tmem_fence_after();
-        const uint64_t x = tile_desc(tiles + s.at * kStage), y = tile_desc(tiles + s.at * kStage + kTileBytes);
+        if (elect_lane()) {
+            const uint64_t x = x0 + s.at * (kStage >> 4), y = y0 + s.at * (kStage >> 4);
+            const uint32_t d = tmem + b.at * Y;
 #pragma unroll
-        for (int k = 0; k < kTileK / 32; ++k) mma_e4m3(tmem + b.at * Y, x + 2 * k, y + 2 * k, idesc, k > 0);
-        mma_commit(smem_u32(&bars.empty[s.at]));
-        mma_commit(smem_u32(&bars.done[b.at]));
+            for (int k = 0; k < kTileK / 32; ++k) {
+                if (PAIR) mma_e4m3_pair(d, x + 2 * k, y + 2 * k, idesc, k > 0);
+                else mma_e4m3(d, x + 2 * k, y + 2 * k, idesc, k > 0);
+            }
+            if (PAIR) {
+                mma_commit_pair(empty + 8 * s.at);
+                mma_commit_pair(done + 8 * b.at);
+            } else {
+                mma_commit(empty + 8 * s.at);
+                mma_commit(done + 8 * b.at);
+            }
+        }
+        __syncwarp();
         s.next();
         b.next();
     }
@@ -156,29 +177,33 @@ __device__ __forceinline__ void drain_tiles(Bars<STAGES, BUFFERS>& bars, int64_t
         mbar_wait_bounded(smem_u32(&bars.full[i % STAGES]), static_cast<uint32_t>(i / STAGES & 1), err);
 }
 
-// A finished accumulator's columns [0, C) of this thread's row, times f (two columns' factors
-// to a word, or one factor for all), added to acc.
-template <int C, class Factor>
-__device__ __forceinline__ void add_up(uint32_t tmem, uint64_t (&acc)[C / 2], uint32_t taken, Factor&& factor) {
+// A finished accumulator's columns [0, C) of this thread's row, each times its factor, added to
+// acc; `arrive` gives it back as soon as it is in registers. Single multiply-adds: packed pairs
+// want their operands in pairs of registers, where the loads do not put them, and cost as many
+// moves (16384 x 8192 x 8192 1375 us with them, 1100 without).
+template <int C, class Arrive, class Factor>
+__device__ __forceinline__ void add_up(uint32_t tmem, float (&acc)[C], Arrive&& arrive, Factor&& factor) {
     constexpr int W = C < 32 ? 16 : 32;
+    uint32_t t[2][W];
+    tmem_load(tmem, t[0]);
 #pragma unroll
     for (int c = 0; c < C; c += W) {
-        uint32_t t[W];
-        tmem_load(tmem + c, t);
-        tmem_wait_loads();
-        if (c + W == C) {
+        uint32_t(&now)[W] = t[(c / W) & 1];
+        tmem_wait_loads(now);
+        if (c + W < C) {
+            tmem_load(tmem + c + W, t[(c / W + 1) & 1]);
+        } else {
             tmem_fence_before();
             __syncwarp();
-            if ((threadIdx.x & 31) == 0) mbar_arrive(taken);
+            if ((threadIdx.x & 31) == 0) arrive();
         }
 #pragma unroll
-        for (int i = 0; i < W; i += 2)
-            acc[(c + i) / 2] = f2_fma(f2_pack(__uint_as_float(t[i]), __uint_as_float(t[i + 1])), factor(c + i), acc[(c + i) / 2]);
+        for (int i = 0; i < W; ++i) acc[c + i] = fmaf(__uint_as_float(now[i]), factor(c + i), acc[c + i]);
     }
 }
 
-// The tile of a persistent block's turn `t`: bands of up to 16 tiles of a, and within a band
-// b's tiles one after the other, so that the blocks of a wave share both in the L2.
+// The tile of turn `t`: bands of up to 16 tiles of a, and within a band b's tiles one after the
+// other, so that the blocks that run at a time share both in the L2.
 __device__ __forceinline__ void tile_at(const MatmulArgs& a, int64_t t, int& m, int& n) {
     constexpr int kBand = 16;
     const int64_t per_band = static_cast<int64_t>(kBand) * a.n_tiles;
@@ -189,130 +214,203 @@ __device__ __forceinline__ void tile_at(const MatmulArgs& a, int64_t t, int& m, 
     m = band * kBand + rest - n * rows;
 }
 
-// Threads: the warps that add up, the issuer's, the loaders', and for two groups of adders a
-// group's rest, since registers are handed over by groups of four warps.
-constexpr int wide_threads(int n, bool tma) { return n == 256 ? 384 : n + 32 + (tma ? 32 : kLoaders); }
-constexpr int thin_threads(bool tma) { return 160 + (tma ? 32 : kLoaders); }
+// A warp that adds up 128 columns of an accumulator (from its column `shift` on) for the tiles
+// from `first` on, every `step`th, and stores them. A tile has `rows` rows, of which this
+// block has those from `row_shift` on.
+template <int DT, int BN, int BUFFERS, class Done, class Taken>
+__device__ __forceinline__ void add_tiles(const MatmulArgs& a, uint32_t tmem, int shift, int64_t first, int64_t step, int rows,
+                                          int row_shift, Done&& done, Taken&& taken) {
+    constexpr int EB = Elem<DT>::kBytes, V = Elem<DT>::kVec;
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
+    const uint32_t mine = tmem + (static_cast<uint32_t>(quarter) << 21) + shift;
+    const int64_t all = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
+    Ring<BUFFERS> b;
+    bool ok = true;
+    for (int64_t t = first; t < all; t += step) {
+        __syncwarp();
+        if (!ok) break;  // in all lanes
+        int m, n;
+        tile_at(a, t, m, n);
+        const int64_t row = static_cast<int64_t>(m) * rows + row_shift + quarter * 32 + lane;
+        const int col = n * BN + shift;
+        const bool live = row < a.M && col < a.N;
+        const float* sa = a.sa + (live ? row * a.ldsa : 0);
+        const float* sb = a.sb + (live ? (col >> 7) * a.ldsb : 0);
+        float acc[128];
+#pragma unroll
+        for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+        float fa = live ? sa[0] : 0.f, fb = live ? sb[0] : 0.f;
+        for (int kb = 0; kb < a.kblocks; ++kb) {
+            const float f = fa * fb;
+            if (live && kb + 1 < a.kblocks) {
+                if (!a.per_row) fa = sa[kb + 1];
+                fb = sb[kb + 1];
+            }
+            ok = mbar_wait_bounded(done(b.at), b.phase, a.err);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            tmem_fence_after();
+            add_up<128>(mine + b.at * BN, acc, [&] { taken(b.at); }, [&](int) { return f; });
+            b.next();
+        }
+        __syncwarp();
+        if (!ok || !live) continue;
+        char* out = static_cast<char*>(a.y) + (row * a.ldy + col) * EB;
+#pragma unroll
+        for (int c = 0; c < 128; c += V) {
+            float v[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = acc[c + i];
+            if (a.bias) {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (col + c + i < a.N) v[i] += Elem<DT>::ld(a.bias, col + c + i);
+            }
+            if (a.wide_y && col + c + V <= a.N) {
+                *reinterpret_cast<uint4*>(out + c * EB) = Elem<DT>::pack(v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (col + c + i < a.N) Elem<DT>::st(out, c + i, v[i]);
+            }
+        }
+    }
+}
 
-template <int DT, int BN, bool TMA>
-__global__ void __launch_bounds__(wide_threads(BN, TMA), 1)
+constexpr int wide_threads(bool tma) { return 160 + (tma ? 32 : kLoaders); }
+constexpr int thin_threads(bool tma) { return 160 + (tma ? 32 : kLoaders); }
+constexpr int kPairThreads = 384;
+
+template <int DT, bool TMA>
+__global__ void __launch_bounds__(wide_threads(TMA), 1)
     matmul_wide(const MatmulArgs a, const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap) {
-    constexpr int STAGES = wide_stages(BN), BUFFERS = wide_buffers(BN);
-    constexpr uint32_t kStage = kTileBytes + BN * kTileK;
+    constexpr int STAGES = kWideStages, BUFFERS = kWideBuffers;
+    constexpr uint32_t kStage = 2 * kTileBytes;
     extern __shared__ char dynamic[];
     __shared__ Bars<STAGES, BUFFERS> bars;
     const uint32_t tiles = (smem_u32(dynamic) + 1023u) & ~1023u;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kIssuer = BN / 32, kProducer = kIssuer + 1;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform to the compiler
+    constexpr int kIssuer = 4, kProducer = 5;
     if (warp == kIssuer) tmem_alloc(smem_u32(&bars.tmem), 512);
-    if (threadIdx.x == 0) bars.init(TMA ? 1 : kLoaders, BN / 32);
+    if (threadIdx.x == 0) bars.init(TMA ? 1 : kLoaders, 4);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = bars.tmem;
     griddep_wait();
     const int64_t all = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
-    // of two groups of adders the 384 threads have 168 registers at first: the 8 warps that add
-    // up take 232, the other 4 keep 40
-    if (warp >= kIssuer) {
-        if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        if (warp >= kProducer) {
-            if (TMA ? warp == kProducer && lane == 0 : true) {
-                Ring<STAGES> s;
-                int64_t issued = 0;
-                bool ok = true;
-                for (int64_t t = blockIdx.x; ok && t < all; t += gridDim.x) {
-                    int m, n;
-                    tile_at(a, t, m, n);
-                    for (int kb = 0; kb < a.kblocks; ++kb) {
-                        if (!(ok = mbar_wait_bounded(smem_u32(&bars.empty[s.at]), s.phase ^ 1u, a.err))) break;
-                        const uint32_t dst = tiles + s.at * kStage, full = smem_u32(&bars.full[s.at]);
-                        if constexpr (TMA) {
-                            mbar_arrive_expect_tx(full, kStage);
-                            tile_g2s(dst, &amap, kb * kTileK, m * 128, full);
-                            tile_g2s(dst + kTileBytes, &bmap, kb * kTileK, n * BN, full);
-                        } else {
-                            const int thread = threadIdx.x - kProducer * 32;
-                            load_tile<128>(dst, a.a, a.lda, static_cast<int64_t>(m) * 128, a.M, kb * kTileK, a.K, thread);
-                            load_tile<BN>(dst + kTileBytes, a.b, a.ldb, static_cast<int64_t>(n) * BN, a.N, kb * kTileK, a.K, thread);
-                            fence_proxy_async_smem();
-                            mbar_arrive(full);
-                        }
-                        ++issued;
-                        s.next();
-                    }
-                }
-                if (TMA && !ok) drain_tiles(bars, issued, a.err);
-            }
-            __syncwarp();
-        } else if (warp == kIssuer) {
-            if (lane == 0) {
-                const int64_t mine = all > blockIdx.x ? (all - blockIdx.x - 1) / gridDim.x + 1 : 0;
-                issue<STAGES, BUFFERS, BN>(bars, tiles, tmem, mine * a.kblocks, a.err);
-            }
-            __syncwarp();
-        }
-    } else {
-        if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-        const int half = warp >> 2;  // of the tile's columns, 128 each
-        const uint32_t mine = tmem + (static_cast<uint32_t>(warp & 3) << 21) + half * 128;
-        Ring<BUFFERS> b;
+    if (warp >= kProducer) {
+        Ring<STAGES> s;
+        int64_t issued = 0;
         bool ok = true;
-        for (int64_t t = blockIdx.x; t < all; t += gridDim.x) {
-            __syncwarp();
-            if (!ok) break;  // in all lanes
+        for (int64_t t = blockIdx.x; ok && t < all; t += gridDim.x) {
             int m, n;
             tile_at(a, t, m, n);
-            const int64_t row = static_cast<int64_t>(m) * 128 + (warp & 3) * 32 + lane;
-            const int col = n * BN + half * 128;
-            const bool live = row < a.M && col < a.N;
-            const float* sa = a.sa + (live ? row * a.ldsa : 0);
-            const float* sb = a.sb + (live ? (col >> 7) * a.ldsb : 0);
-            uint64_t acc[64];
-#pragma unroll
-            for (int i = 0; i < 64; ++i) acc[i] = 0ull;
-            float fa = live ? sa[0] : 0.f, fb = live ? sb[0] : 0.f;
             for (int kb = 0; kb < a.kblocks; ++kb) {
-                const float f = fa * fb;
-                if (live && kb + 1 < a.kblocks) {
-                    if (!a.per_row) fa = sa[kb + 1];
-                    fb = sb[kb + 1];
-                }
-                ok = mbar_wait_bounded(smem_u32(&bars.done[b.at]), b.phase, a.err);
+                ok = mbar_wait_bounded(smem_u32(bars.empty) + 8 * s.at, s.phase ^ 1u, a.err);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                tmem_fence_after();
-                const uint64_t f2 = f2_pack(f, f);
-                add_up<128>(mine + b.at * BN, acc, smem_u32(&bars.taken[b.at]), [&](int) { return f2; });
-                b.next();
-            }
-            __syncwarp();
-            if (!ok || !live) continue;
-            constexpr int EB = Elem<DT>::kBytes, V = Elem<DT>::kVec;
-            char* out = static_cast<char*>(a.y) + (row * a.ldy + col) * EB;
-#pragma unroll
-            for (int c = 0; c < 128; c += V) {
-                float v[V];
-#pragma unroll
-                for (int i = 0; i < V; i += 2) f2_unpack(acc[(c + i) / 2], v[i], v[i + 1]);
-                if (a.bias) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        if (col + c + i < a.N) v[i] += Elem<DT>::ld(a.bias, col + c + i);
-                }
-                if (a.wide_y && col + c + V <= a.N) {
-                    *reinterpret_cast<uint4*>(out + c * EB) = Elem<DT>::pack(v);
+                const uint32_t dst = tiles + s.at * kStage, full = smem_u32(bars.full) + 8 * s.at;
+                if constexpr (TMA) {
+                    if (elect_lane()) {
+                        mbar_arrive_expect_tx(full, kStage);
+                        tile_g2s(dst, &amap, kb * kTileK, m * 128, full);
+                        tile_g2s(dst + kTileBytes, &bmap, kb * kTileK, n * 128, full);
+                    }
+                    __syncwarp();
                 } else {
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        if (col + c + i < a.N) Elem<DT>::st(out, c + i, v[i]);
+                    const int thread = threadIdx.x - kProducer * 32;
+                    load_tile<128>(dst, a.a, a.lda, static_cast<int64_t>(m) * 128, a.M, kb * kTileK, a.K, thread);
+                    load_tile<128>(dst + kTileBytes, a.b, a.ldb, static_cast<int64_t>(n) * 128, a.N, kb * kTileK, a.K, thread);
+                    fence_proxy_async_smem();
+                    mbar_arrive(full);
                 }
+                ++issued;
+                s.next();
             }
         }
+        if (TMA && !ok) drain_tiles(bars, issued, a.err);
+    } else if (warp == kIssuer) {
+        const int64_t mine = all > blockIdx.x ? (all - blockIdx.x - 1) / gridDim.x + 1 : 0;
+        issue<STAGES, BUFFERS, 128, false>(bars, tiles, tmem, mine * a.kblocks, a.err);
+    } else {
+        add_tiles<DT, 128, BUFFERS>(a, tmem, 0, blockIdx.x, gridDim.x, 128, 0, [&](int i) { return smem_u32(&bars.done[i]); },
+                                    [&](int i) { mbar_arrive(smem_u32(&bars.taken[i])); });
     }
     griddep_launch_dependents();
     tmem_fence_before();
     __syncthreads();
     if (warp == kIssuer) tmem_free(tmem, 512);
+}
+
+// Pairs of blocks (clusters of two): a tile of 256 rows of a by 256 of b, for which each block
+// loads 128 rows of both; the tensor cores of both work on one instruction, from one thread
+// of the first block, and read the other block's half of b from its shared memory. Two
+// thirds of the L2's traffic of blocks on their own.
+template <int DT>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    matmul_pair(const MatmulArgs a, const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap) {
+    constexpr int STAGES = kPairStages, BUFFERS = kPairBuffers;
+    constexpr uint32_t kStage = 2 * kTileBytes;
+    extern __shared__ char dynamic[];
+    __shared__ Bars<STAGES, BUFFERS> bars;
+    const uint32_t tiles = (smem_u32(dynamic) + 1023u) & ~1023u;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform to the compiler
+    const int rank = static_cast<int>(cluster_rank());
+    constexpr int kIssuer = 8, kProducer = 9;
+    if (warp == kIssuer) tmem_alloc_pair(smem_u32(&bars.tmem), 512);
+    // an accumulator is taken when the 8 warps of both blocks have it
+    if (threadIdx.x == 0) bars.init(1, 16);
+    __syncwarp();
+    tmem_fence_before();
+    cluster_sync();
+    tmem_fence_after();
+    const uint32_t tmem = bars.tmem;
+    griddep_wait();
+    const int64_t all = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
+    const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    // the 384 threads have 168 registers at first: the 8 warps that add up take 232, the others
+    // keep 40
+    if (warp >= kIssuer) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == kProducer) {
+            Ring<STAGES> s;
+            int64_t issued = 0;
+            bool ok = true;
+            // the first block's barriers count both blocks' tiles
+            const uint32_t both = dsmem_map(smem_u32(bars.full), 0);
+            for (int64_t t = first; ok && t < all; t += step) {
+                int m, n;
+                tile_at(a, t, m, n);
+                for (int kb = 0; kb < a.kblocks; ++kb) {
+                    ok = mbar_wait_bounded(smem_u32(bars.empty) + 8 * s.at, s.phase ^ 1u, a.err);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    if (elect_lane()) {
+                        const uint32_t dst = tiles + s.at * kStage;
+                        if (rank == 0) mbar_arrive_expect_tx(smem_u32(bars.full) + 8 * s.at, 2 * kStage);
+                        tile_g2s_pair(dst, &amap, kb * kTileK, m * 256 + rank * 128, both + 8 * s.at);
+                        tile_g2s_pair(dst + kTileBytes, &bmap, kb * kTileK, n * 256 + rank * 128, both + 8 * s.at);
+                    }
+                    __syncwarp();
+                    ++issued;
+                    s.next();
+                }
+            }
+            if (!ok && rank == 0) drain_tiles(bars, issued, a.err);
+        } else if (warp == kIssuer && rank == 0) {
+            const int64_t mine = all > first ? (all - first - 1) / step + 1 : 0;
+            issue<STAGES, BUFFERS, 256, true>(bars, tiles, tmem, mine * a.kblocks, a.err);
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        add_tiles<DT, 256, BUFFERS>(a, tmem, (warp >> 2) * 128, first, step, 256, rank * 128,
+                                    [&](int i) { return smem_u32(&bars.done[i]); },
+                                    [&](int i) { mbar_arrive_cluster(dsmem_map(smem_u32(&bars.taken[i]), 0)); });
+    }
+    griddep_launch_dependents();
+    tmem_fence_before();
+    __syncwarp();
+    cluster_sync();  // no block leaves before the other's instructions and arrivals
+    if (warp == kIssuer) tmem_free_pair(tmem, 512);
 }
 
 // Few rows of a: 128 rows of b are the accumulator's lanes, NT rows of a its columns. The
@@ -328,7 +426,7 @@ __global__ void __launch_bounds__(thin_threads(TMA), 1)
     __shared__ alignas(16) float factors[2][NT];
     const uint32_t base = smem_u32(dynamic), tiles = (base + 1023u) & ~1023u;
     float* sums = reinterpret_cast<float*>(dynamic + (tiles - base));  // [NT][128], where the tiles were
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform to the compiler
     constexpr int kIssuer = 4, kProducer = 5;
     if (warp == kIssuer) tmem_alloc(smem_u32(&bars.tmem), thin_columns(NT));
     if (threadIdx.x == 0) bars.init(TMA ? 1 : kLoaders, 4);
@@ -348,31 +446,33 @@ __global__ void __launch_bounds__(thin_threads(TMA), 1)
     const int rows = static_cast<int>(min(static_cast<int64_t>(NT), a.M - t0));
     bool ok = true;
     if (warp >= kProducer) {
-        if (!TMA || lane == 0) {
-            Ring<STAGES> s;
-            int64_t issued = 0;
-            for (int kb = from; kb < to; ++kb) {
-                if (!(ok = mbar_wait_bounded(smem_u32(&bars.empty[s.at]), s.phase ^ 1u, a.err))) break;
-                const uint32_t dst = tiles + s.at * kStage, full = smem_u32(&bars.full[s.at]);
-                if constexpr (TMA) {
+        Ring<STAGES> s;
+        int64_t issued = 0;
+        for (int kb = from; kb < to; ++kb) {
+            ok = mbar_wait_bounded(smem_u32(bars.empty) + 8 * s.at, s.phase ^ 1u, a.err);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            const uint32_t dst = tiles + s.at * kStage, full = smem_u32(bars.full) + 8 * s.at;
+            if constexpr (TMA) {
+                if (elect_lane()) {
                     mbar_arrive_expect_tx(full, kStage);
                     tile_g2s(dst, &bmap, kb * kTileK, n * 128, full);
                     tile_g2s(dst + kTileBytes, &amap, kb * kTileK, m * NT, full);
-                } else {
-                    const int thread = threadIdx.x - kProducer * 32;
-                    load_tile<128>(dst, a.b, a.ldb, static_cast<int64_t>(n) * 128, a.N, kb * kTileK, a.K, thread);
-                    load_tile<NT>(dst + kTileBytes, a.a, a.lda, t0, a.M, kb * kTileK, a.K, thread);
-                    fence_proxy_async_smem();
-                    mbar_arrive(full);
                 }
-                ++issued;
-                s.next();
+                __syncwarp();
+            } else {
+                const int thread = threadIdx.x - kProducer * 32;
+                load_tile<128>(dst, a.b, a.ldb, static_cast<int64_t>(n) * 128, a.N, kb * kTileK, a.K, thread);
+                load_tile<NT>(dst + kTileBytes, a.a, a.lda, t0, a.M, kb * kTileK, a.K, thread);
+                fence_proxy_async_smem();
+                mbar_arrive(full);
             }
-            if (TMA && !ok) drain_tiles(bars, issued, a.err);
+            ++issued;
+            s.next();
         }
+        if (TMA && !ok) drain_tiles(bars, issued, a.err);
         __syncwarp();
     } else if (warp == kIssuer) {
-        if (lane == 0) issue<STAGES, BUFFERS, NT>(bars, tiles, tmem, to - from, a.err);
+        issue<STAGES, BUFFERS, NT, false>(bars, tiles, tmem, to - from, a.err);
         __syncwarp();
     } else {
         const uint32_t mine = tmem + (static_cast<uint32_t>(warp) << 21);
@@ -381,9 +481,9 @@ __global__ void __launch_bounds__(thin_threads(TMA), 1)
         const float* sa = a.sa + (has ? (t0 + threadIdx.x) * a.ldsa : 0);
         const float* sb = a.sb + n * a.ldsb;
         float fa = has ? sa[a.per_row ? 0 : from] : 0.f, fb = sb[from];
-        uint64_t acc[NT / 2];
+        float acc[NT];
 #pragma unroll
-        for (int i = 0; i < NT / 2; ++i) acc[i] = 0ull;
+        for (int i = 0; i < NT; ++i) acc[i] = 0.f;
         Ring<BUFFERS> b;
         for (int kb = from; kb < to; ++kb) {
             float* f = factors[kb & 1];
@@ -398,8 +498,7 @@ __global__ void __launch_bounds__(thin_threads(TMA), 1)
             // (a wait that gave up: the others go on meeting at the barrier)
             if (ok) {
                 tmem_fence_after();
-                add_up<NT>(mine + b.at * NT, acc, smem_u32(&bars.taken[b.at]),
-                           [&](int c) { return *reinterpret_cast<const uint64_t*>(f + c); });
+                add_up<NT>(mine + b.at * NT, acc, [&] { mbar_arrive(smem_u32(&bars.taken[b.at])); }, [&](int c) { return f[c]; });
             }
             b.next();
         }
@@ -407,17 +506,12 @@ __global__ void __launch_bounds__(thin_threads(TMA), 1)
         if (split == 1) {
             if (ok && col < a.N) {
 #pragma unroll
-                for (int j = 0; j < NT; j += 2) {
-                    float v0, v1;
-                    f2_unpack(acc[j / 2], v0, v1);
-                    if (j < rows) Elem<DT>::st(static_cast<char*>(a.y) + ((t0 + j) * a.ldy + col) * EB, 0, v0 + bias);
-                    if (j + 1 < rows) Elem<DT>::st(static_cast<char*>(a.y) + ((t0 + j + 1) * a.ldy + col) * EB, 0, v1 + bias);
-                }
+                for (int j = 0; j < NT; ++j)
+                    if (j < rows) Elem<DT>::st(static_cast<char*>(a.y) + ((t0 + j) * a.ldy + col) * EB, 0, acc[j] + bias);
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < NT; j += 2)
-                f2_unpack(acc[j / 2], sums[j * 128 + threadIdx.x], sums[(j + 1) * 128 + threadIdx.x]);
+            for (int j = 0; j < NT; ++j) sums[j * 128 + threadIdx.x] = acc[j];
         }
     }
     griddep_launch_dependents();
@@ -442,11 +536,8 @@ __global__ void __launch_bounds__(thin_threads(TMA), 1)
 }
 
 template <int DT, bool TMA> const void* kernel_for(const MatmulPlan& p) {
-    if (p.wide) {
-        if constexpr (TMA)
-            if (p.n == 256) return reinterpret_cast<const void*>(&matmul_wide<DT, 256, TMA>);
-        return p.n == 128 ? reinterpret_cast<const void*>(&matmul_wide<DT, 128, TMA>) : nullptr;
-    }
+    if (p.how == kMatmulPair) return TMA ? reinterpret_cast<const void*>(&matmul_pair<DT>) : nullptr;
+    if (p.how == kMatmulWide) return reinterpret_cast<const void*>(&matmul_wide<DT, TMA>);
     switch (p.n) {
     case 16: return reinterpret_cast<const void*>(&matmul_thin<DT, 16, TMA>);
     case 32: return reinterpret_cast<const void*>(&matmul_thin<DT, 32, TMA>);
@@ -468,9 +559,10 @@ const void* matmul_kernel(const MatmulPlan& p) {
 }
 
 void matmul_shape(MatmulPlan& p) {
-    const int stages = p.wide ? wide_stages(p.n) : thin_stages(p.n);
-    p.threads = p.wide ? wide_threads(p.n, p.tma) : thin_threads(p.tma);
-    p.smem = 1024 + static_cast<size_t>(stages) * (kTileBytes + p.n * kTileK);
+    const bool thin = p.how == kMatmulThin;
+    const int stages = thin ? thin_stages(p.n) : p.how == kMatmulWide ? kWideStages : kPairStages;
+    p.threads = thin ? thin_threads(p.tma) : p.how == kMatmulWide ? wide_threads(p.tma) : kPairThreads;
+    p.smem = 1024 + static_cast<size_t>(stages) * (kTileBytes + (thin ? p.n * kTileK : kTileBytes));
 }
 
 }  // namespace rmsnorm

@@ -29,14 +29,16 @@ struct MatmulArgs {
     uint32_t* err;     // device error word
 };
 
-// A launch shape. wide: tiles of 128 rows of a by 128 or 256 of b (`n`), persistent blocks;
-// else tiles of 128 rows of b by `n` rows of a, K split over clusters of `split` blocks.
+// Tiles of a product: 256 rows of a by 256 of b, of a pair of blocks; 128 by 128; or 128 rows of
+// b by `n` rows of a, with K split over the blocks of a cluster.
+enum MatmulTiles { kMatmulPair = 0, kMatmulWide, kMatmulThin };
+
 struct MatmulPlan {
     int dtype = 0;
-    bool wide = false;
+    MatmulTiles how = kMatmulPair;
     bool tma = false;  // tiles by TMA, which wants a's and b's rows on 16-byte boundaries
-    int n = 0;
-    int split = 1;
+    int n = 0;         // thin: rows of a
+    int cluster = 1;   // blocks
     int threads = 0;
     int64_t blocks = 0;
     size_t smem = 0;

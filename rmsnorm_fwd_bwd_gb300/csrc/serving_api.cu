@@ -93,19 +93,25 @@ bool tile_map(CUtensorMap& map, const void* p, int64_t ld, int64_t rows, int64_t
 void matmul_plan(int64_t M, int64_t N, int64_t K, bool tma, int dtype, int sms, MatmulPlan& p) {
     p.dtype = dtype;
     p.tma = tma;
-    const int64_t kblocks = ceil_div(K, kBlock);
-    p.wide = M > 128;
-    if (p.wide) {
-        p.n = tma ? 256 : 128;
-        p.blocks = std::min<int64_t>(ceil_div(M, 128) * ceil_div(N, p.n), sms);
-    } else {
+    p.how = M <= 128 ? kMatmulThin : tma ? kMatmulPair : kMatmulWide;
+    if (p.how == kMatmulThin) {
         for (p.n = 16; p.n < M;) p.n *= 2;
         const int64_t tiles = ceil_div(M, p.n) * ceil_div(N, 128);
-        p.split = static_cast<int>(std::max<int64_t>(1, std::min({sms / tiles, kMostSplit, kblocks})));
-        p.blocks = tiles * p.split;
+        p.cluster = static_cast<int>(std::max<int64_t>(1, std::min({sms / tiles, kMostSplit, ceil_div(K, kBlock)})));
+        p.blocks = tiles * p.cluster;
+    } else if (p.how == kMatmulWide) {
+        p.blocks = std::min<int64_t>(ceil_div(M, 128) * ceil_div(N, 128), sms);
+    } else {
+        p.cluster = 2;
+        p.blocks = 2 * std::min<int64_t>(ceil_div(M, 256) * ceil_div(N, 256), sms / 2);
     }
     matmul_shape(p);
 }
+
+// Rows of a tile of a and of b, and of the boxes that are loaded.
+int tile_rows_a(const MatmulPlan& p) { return p.how == kMatmulThin ? p.n : p.how == kMatmulPair ? 256 : 128; }
+int tile_rows_b(const MatmulPlan& p) { return p.how == kMatmulPair ? 256 : 128; }
+int box_rows_a(const MatmulPlan& p) { return p.how == kMatmulThin ? p.n : 128; }
 
 // Whether [p, p + bytes) and [q, q + more) share memory.
 bool overlap(const void* p, int64_t bytes, const void* q, int64_t more) {
@@ -228,16 +234,16 @@ extern "C" rmsnorm_status rmsnorm_quant_matmul(const void* a, int64_t lda, const
     t.K = static_cast<int>(K);
     t.kblocks = static_cast<int>(kblocks);
     t.per_row = group == 0;
-    t.m_tiles = static_cast<int>(ceil_div(M, p.wide ? 128 : p.n));
-    t.n_tiles = static_cast<int>(ceil_div(N, p.wide ? p.n : 128));
+    t.m_tiles = static_cast<int>(ceil_div(M, tile_rows_a(p)));
+    t.n_tiles = static_cast<int>(ceil_div(N, tile_rows_b(p)));
     t.wide_y = aligned(y, 16) && ldy * static_cast<int64_t>(s) % 16 == 0;
     t.err = device_error_word();
     if (!t.err) return RMSNORM_ERR_CUDA;
     CUtensorMap amap = {}, bmap = {};
-    if (p.tma && (!tile_map(amap, a, lda, M, K, p.wide ? 128 : p.n) || !tile_map(bmap, b, ldb, N, K, p.wide ? p.n : 128)))
+    if (p.tma && (!tile_map(amap, a, lda, M, K, box_rows_a(p)) || !tile_map(bmap, b, ldb, N, K, 128)))
         return RMSNORM_ERR_CUDA;
     void* params[] = {&t, &amap, &bmap};
-    return run(matmul_kernel(p), p.blocks, p.threads, p.smem, p.split, params, stream);
+    return run(matmul_kernel(p), p.blocks, p.threads, p.smem, p.cluster, params, stream);
 }
 
 extern "C" rmsnorm_status rmsnorm_rope_append(const rmsnorm_rope_heads* q, const rmsnorm_cache_heads* k,
