@@ -22,10 +22,13 @@
 namespace rmsnorm {
 namespace {
 
+constexpr int kMostSplit = kMatmulMostSplit;
 constexpr int kTileBytes = 128 * kTileK;  // 128 rows
 
 constexpr int kWideStages = 6, kPairStages = 6;
-constexpr int thin_stages(int n) { return n <= 32 ? 9 : n == 64 ? 8 : 6; }
+// Two blocks to an SM, but for 128 rows of a, which leave room for one.
+constexpr int thin_blocks(int n) { return n < 128 ? 2 : 1; }
+constexpr int thin_stages(int n) { return n < 32 ? 5 : n < 128 ? 4 : 6; }
 // Accumulators in tensor memory that are under way.
 constexpr int kWideBuffers = 4, kPairBuffers = 2;
 constexpr int kThinBuffers = 4;
@@ -177,7 +180,8 @@ __device__ __forceinline__ void drain_tiles(Bars<STAGES, BUFFERS>& bars, int64_t
         mbar_wait_bounded(smem_u32(&bars.full[i % STAGES]), static_cast<uint32_t>(i / STAGES & 1), err);
 }
 
-// A finished accumulator's columns [0, C) of this thread's row, each times its factor, added to
+// A finished accumulator's columns [0, C) of this thread's row, each times its factor (given for
+// four columns), added to
 // acc; `arrive` gives it back as soon as it is in registers. Single multiply-adds: packed pairs
 // want their operands in pairs of registers, where the loads do not put them, and cost as many
 // moves (16384 x 8192 x 8192 1375 us with them, 1100 without).
@@ -198,7 +202,13 @@ __device__ __forceinline__ void add_up(uint32_t tmem, float (&acc)[C], Arrive&& 
             if ((threadIdx.x & 31) == 0) arrive();
         }
 #pragma unroll
-        for (int i = 0; i < W; ++i) acc[c + i] = fmaf(__uint_as_float(now[i]), factor(c + i), acc[c + i]);
+        for (int i = 0; i < W; i += 4) {
+            const float4 f = factor(c + i);
+            acc[c + i] = fmaf(__uint_as_float(now[i]), f.x, acc[c + i]);
+            acc[c + i + 1] = fmaf(__uint_as_float(now[i + 1]), f.y, acc[c + i + 1]);
+            acc[c + i + 2] = fmaf(__uint_as_float(now[i + 2]), f.z, acc[c + i + 2]);
+            acc[c + i + 3] = fmaf(__uint_as_float(now[i + 3]), f.w, acc[c + i + 3]);
+        }
     }
 }
 
@@ -249,7 +259,7 @@ __device__ __forceinline__ void add_tiles(const MatmulArgs& a, uint32_t tmem, in
             ok = mbar_wait_bounded(done(b.at), b.phase, a.err);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tmem_fence_after();
-            add_up<128>(mine + b.at * BN, acc, [&] { taken(b.at); }, [&](int) { return f; });
+            add_up<128>(mine + b.at * BN, acc, [&] { taken(b.at); }, [&](int) { return make_float4(f, f, f, f); });
             b.next();
         }
         __syncwarp();
@@ -416,25 +426,33 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // Few rows of a: 128 rows of b are the accumulator's lanes, NT rows of a its columns. The
 // blocks of a cluster take a part of K each; their sums meet in shared memory and are
 // added in the blocks' order, so that the result does not depend on who was first.
+// Blocks of K whose factors lie in shared memory at a time.
+constexpr int kFactorBlocks = 16;
+
 template <int DT, int NT, bool TMA>
-__global__ void __launch_bounds__(thin_threads(TMA), 1)
+__global__ void __launch_bounds__(thin_threads(TMA), thin_blocks(NT))
     matmul_thin(const MatmulArgs a, const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap) {
     constexpr int STAGES = thin_stages(NT), BUFFERS = kThinBuffers;
     constexpr uint32_t kStage = kTileBytes + NT * kTileK;
     extern __shared__ char dynamic[];
     __shared__ Bars<STAGES, BUFFERS> bars;
-    __shared__ alignas(16) float factors[2][NT];
+    __shared__ alignas(16) float factors[2][kFactorBlocks][NT + 4];
     const uint32_t base = smem_u32(dynamic), tiles = (base + 1023u) & ~1023u;
     float* sums = reinterpret_cast<float*>(dynamic + (tiles - base));  // [NT][128], where the tiles were
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform to the compiler
     constexpr int kIssuer = 4, kProducer = 5;
     if (warp == kIssuer) tmem_alloc(smem_u32(&bars.tmem), thin_columns(NT));
     if (threadIdx.x == 0) bars.init(TMA ? 1 : kLoaders, 4);
+    if (TMA && threadIdx.x == kProducer * 32) {
+        prefetch_map(&amap);
+        prefetch_map(&bmap);
+    }
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = bars.tmem;
     griddep_wait();
+    griddep_launch_dependents();
     const int split = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
     const int tile = static_cast<int>(blockIdx.x) / split;
     const int m = tile / a.n_tiles, n = tile - m * a.n_tiles;
@@ -476,31 +494,49 @@ __global__ void __launch_bounds__(thin_threads(TMA), 1)
         __syncwarp();
     } else {
         const uint32_t mine = tmem + (static_cast<uint32_t>(warp) << 21);
-        // thread j has the scales of row j
-        const bool has = static_cast<int>(threadIdx.x) < rows;
-        const float* sa = a.sa + (has ? (t0 + threadIdx.x) * a.ldsa : 0);
-        const float* sb = a.sb + n * a.ldsb;
-        float fa = has ? sa[a.per_row ? 0 : from] : 0.f, fb = sb[from];
+        // factors of kFactorBlocks blocks at a time: a thread loads those of block `fb` of a chunk for
+        // the rows fr, fr + 8, ..., a chunk ahead
+        constexpr int E = kFactorBlocks * NT / 128;
+        const int fb = threadIdx.x % kFactorBlocks, fr = threadIdx.x / kFactorBlocks;
+        const float* sa = a.sa + (a.per_row ? 0 : fb);
+        const float* sb = a.sb + n * a.ldsb + fb;
+        float fv[E], fs;
+        const auto fetch = [&](int kb) {
+            const bool in = kb + fb < to;
+            fs = in ? sb[kb] : 0.f;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const int row = fr + 8 * i;
+                fv[i] = in && row < rows ? sa[(t0 + row) * a.ldsa + (a.per_row ? 0 : kb)] : 0.f;
+            }
+        };
+        const auto keep = [&](int which) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) factors[which][fb][fr + 8 * i] = fv[i] * fs;
+            named_barrier_sync(1, 128);
+        };
         float acc[NT];
 #pragma unroll
         for (int i = 0; i < NT; ++i) acc[i] = 0.f;
         Ring<BUFFERS> b;
-        for (int kb = from; kb < to; ++kb) {
-            float* f = factors[kb & 1];
-            if (static_cast<int>(threadIdx.x) < NT) f[threadIdx.x] = fa * fb;
-            if (kb + 1 < to) {
-                if (has && !a.per_row) fa = sa[kb + 1];
-                fb = sb[kb + 1];
-            }
-            named_barrier_sync(1, 128);
-            ok = mbar_wait_bounded(smem_u32(&bars.done[b.at]), b.phase, a.err) && ok;
-            ok = __all_sync(0xffffffffu, ok);
-            // (a wait that gave up: the others go on meeting at the barrier)
-            if (ok) {
+        fetch(from);
+        keep(0);
+        int which = 0;
+        for (int k0 = from; k0 < to; k0 += kFactorBlocks, which ^= 1) {
+            const bool more = k0 + kFactorBlocks < to;
+            if (more) fetch(k0 + kFactorBlocks);
+            const int n_blocks = min(kFactorBlocks, to - k0);
+            for (int i = 0; i < n_blocks; ++i) {
+                ok = mbar_wait_bounded(smem_u32(bars.done) + 8 * b.at, b.phase, a.err) && ok;
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 tmem_fence_after();
-                add_up<NT>(mine + b.at * NT, acc, [&] { mbar_arrive(smem_u32(&bars.taken[b.at])); }, [&](int c) { return f[c]; });
+                const float* f = factors[which][i];
+                add_up<NT>(mine + b.at * NT, acc, [&] { mbar_arrive(smem_u32(bars.taken) + 8 * b.at); },
+                           [&](int c) { return *reinterpret_cast<const float4*>(f + c); });
+                b.next();
             }
-            b.next();
+            // (where a wait gave up the others go on meeting at the barrier)
+            if (more) keep(which ^ 1);
         }
         const float bias = a.bias && col < a.N ? Elem<DT>::ld(a.bias, col) : 0.f;
         if (split == 1) {
@@ -514,7 +550,6 @@ __global__ void __launch_bounds__(thin_threads(TMA), 1)
             for (int j = 0; j < NT; ++j) sums[j * 128 + threadIdx.x] = acc[j];
         }
     }
-    griddep_launch_dependents();
     __syncwarp();
     if (split > 1) {
         cluster_sync();
@@ -522,8 +557,11 @@ __global__ void __launch_bounds__(thin_threads(TMA), 1)
             const float bias = a.bias ? Elem<DT>::ld(a.bias, col) : 0.f;
             const uint32_t at = smem_u32(sums) + threadIdx.x * 4;
             for (int j = rank; j < rows; j += split) {
-                float v = 0.f;
-                for (int r = 0; r < split; ++r) v += dsmem_ld_f32(dsmem_map(at + j * 512, r));
+                float part[kMostSplit], v = 0.f;
+#pragma unroll
+                for (int r = 0; r < kMostSplit; ++r) part[r] = r < split ? dsmem_ld_f32(dsmem_map(at + j * 512, r)) : 0.f;
+#pragma unroll
+                for (int r = 0; r < kMostSplit; ++r) v += part[r];
                 Elem<DT>::st(static_cast<char*>(a.y) + ((t0 + j) * a.ldy + col) * EB, 0, v + bias);
             }
         }

@@ -29,6 +29,9 @@ struct MatmulArgs {
     uint32_t* err;     // device error word
 };
 
+// Most blocks that share K: the portable size of a cluster.
+constexpr int kMatmulMostSplit = 8;
+
 // Tiles of a product: 256 rows of a by 256 of b, of a pair of blocks; 128 by 128; or 128 rows of
 // b by `n` rows of a, with K split over the blocks of a cluster.
 enum MatmulTiles { kMatmulPair = 0, kMatmulWide, kMatmulThin };

@@ -2,6 +2,9 @@
 // shapes and launches of the kernels in matmul.cu, weight.cu and append.cu.
 #include <algorithm>
 #include <cmath>
+#include <map>
+#include <mutex>
+#include <utility>
 
 #include "../../include/rmsnorm_serving.h"
 #include "checks.h"
@@ -14,22 +17,27 @@ namespace {
 
 constexpr int64_t kMatmulMost = RMSNORM_MATMUL_MAX;
 constexpr int64_t kBlock = RMSNORM_MATMUL_BLOCK;
-// Most blocks that share K: the portable size of a cluster.
-constexpr int64_t kMostSplit = 8;
 
-cudaError_t launch(const void* k, int64_t blocks, int threads, size_t smem, int cluster, void** params, cudaStream_t s) {
+cudaLaunchConfig_t launch_config(int64_t blocks, int threads, size_t smem, int cluster, cudaStream_t s,
+                                 cudaLaunchAttribute* attr) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
     cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+cudaError_t launch(const void* k, int64_t blocks, int threads, size_t smem, int cluster, void** params, cudaStream_t s) {
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = launch_config(blocks, threads, smem, cluster, s, attr);
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelExC(&cfg, k, params);
 }
 
@@ -88,16 +96,47 @@ bool tile_map(CUtensorMap& map, const void* p, int64_t ld, int64_t rows, int64_t
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How a product is cut. Few rows of a: b's rows in the accumulators' lanes, and K over as many
-// blocks as fill the GPU.
-void matmul_plan(int64_t M, int64_t N, int64_t K, bool tma, int dtype, int sms, MatmulPlan& p) {
+std::mutex g_serving_mu;
+std::map<std::pair<const void*, std::pair<int, int>>, int> g_clusters;  // by (kernel, (device, blocks of a cluster))
+
+// Clusters of the plan's blocks that the device holds at a time; 0 on failure. Fewer than its
+// SMs would hold where their groups are no multiple of a cluster: 48 clusters of 6 blocks,
+// two to an SM, do not fit 152 SMs.
+int active_clusters(const MatmulPlan& p, int dev) {
+    const void* k = matmul_kernel(p);
+    if (!k || resident_blocks(k, dev, p.threads, p.smem) < 1) return 0;
+    try {
+        std::lock_guard<std::mutex> lock(g_serving_mu);
+        int& n = g_clusters[{k, {dev, p.cluster}}];
+        if (n == 0) {
+            cudaLaunchAttribute attr[1];
+            const cudaLaunchConfig_t cfg = launch_config(p.cluster, p.threads, p.smem, p.cluster, nullptr, attr);
+            if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess) n = 0;
+        }
+        return n;
+    } catch (...) {
+        return 0;
+    }
+}
+
+// How a product is cut; false on failure. Few rows of a: b's rows in the accumulators' lanes, and
+// K over as many blocks as the GPU holds at a time.
+bool matmul_plan(int64_t M, int64_t N, int64_t K, bool tma, int dtype, int dev, int sms, MatmulPlan& p) {
     p.dtype = dtype;
     p.tma = tma;
     p.how = M <= 128 ? kMatmulThin : tma ? kMatmulPair : kMatmulWide;
+    if (p.how == kMatmulThin)
+        for (p.n = 16; p.n < M && p.n < 128;) p.n *= 2;
+    matmul_shape(p);
     if (p.how == kMatmulThin) {
-        for (p.n = 16; p.n < M;) p.n *= 2;
         const int64_t tiles = ceil_div(M, p.n) * ceil_div(N, 128);
-        p.cluster = static_cast<int>(std::max<int64_t>(1, std::min({sms / tiles, kMostSplit, ceil_div(K, kBlock)})));
+        p.cluster = static_cast<int>(std::min<int64_t>(kMatmulMostSplit, ceil_div(K, kBlock)));
+        while (p.cluster > 1) {
+            const int fit = active_clusters(p, dev);
+            if (fit < 1) return false;
+            if (tiles <= fit) break;
+            --p.cluster;
+        }
         p.blocks = tiles * p.cluster;
     } else if (p.how == kMatmulWide) {
         p.blocks = std::min<int64_t>(ceil_div(M, 128) * ceil_div(N, 128), sms);
@@ -105,7 +144,7 @@ void matmul_plan(int64_t M, int64_t N, int64_t K, bool tma, int dtype, int sms, 
         p.cluster = 2;
         p.blocks = 2 * std::min<int64_t>(ceil_div(M, 256) * ceil_div(N, 256), sms / 2);
     }
-    matmul_shape(p);
+    return true;
 }
 
 // Rows of a tile of a and of b, and of the boxes that are loaded.
@@ -216,7 +255,10 @@ extern "C" rmsnorm_status rmsnorm_quant_matmul(const void* a, int64_t lda, const
         return RMSNORM_ERR_CUDA;
     }
     MatmulPlan p;
-    matmul_plan(M, N, K, tma_rows(a, lda, M) && tma_rows(b, ldb, N), dtype, sms, p);
+    if (!matmul_plan(M, N, K, tma_rows(a, lda, M) && tma_rows(b, ldb, N), dtype, dev, sms, p)) {
+        (void)cudaGetLastError();
+        return RMSNORM_ERR_CUDA;
+    }
     MatmulArgs t = {};
     t.a = static_cast<const uint8_t*>(a);
     t.sa = a_scales;

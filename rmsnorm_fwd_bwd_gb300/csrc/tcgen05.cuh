@@ -85,6 +85,19 @@ __device__ __forceinline__ void tile_g2s_pair(uint32_t dst, const CUtensorMap* m
         "l"(map), "r"(x), "r"(y), "r"(cluster_bar)
         : "memory");
 }
+// Whether a phase of an mbarrier is complete, without waiting for it.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
 // An arrival on a barrier of another block of the cluster (or this one) that hands no memory
 // over but tensor memory whose loads are done, and so is relaxed: a release to the cluster waits for
 // all the thread's memory operations (16384 x 8192 x 8192 2038 us with it, 1110 without).
