@@ -10,7 +10,7 @@
 //
 // Three kernels. matmul_pair: pairs of blocks on tiles of 256 x 256, a thread to a row of the
 // accumulator. matmul_wide: single blocks on tiles of 128 x 128. matmul_thin, for few rows
-// of a: the operands change places, a tile is 128 rows of b and 16 to 128 of a, and the blocks of a
+// of a: the operands change places, a tile is 128 rows of b and 16 to 64 of a, and the blocks of a
 // cluster share K. In all of them one thread keeps a ring of tiles full by TMA, one issues
 // the matrix instructions into one of several accumulators in tensor memory, and warps of four
 // add finished ones up meanwhile. Rows off 16 bytes, which TMA does not take, are loaded
@@ -25,74 +25,35 @@ namespace {
 constexpr int kMostSplit = kMatmulMostSplit;
 constexpr int kTileBytes = 128 * kTileK;  // 128 rows
 
-constexpr int kWideStages = 6, kPairStages = 6;
-// Two blocks to an SM, but for 128 rows of a, which leave room for one.
-constexpr int thin_blocks(int n) { return n < 128 ? 2 : 1; }
-constexpr int thin_stages(int n) { return n < 32 ? 5 : n < 128 ? 4 : 6; }
+constexpr int kPairStages = 6;
+// Two blocks to an SM, where rows need no raw place.
+constexpr int thin_blocks(bool tma) { return tma ? 2 : 1; }
+constexpr int thin_stages(int n, bool tma) { return tma && n < 32 ? 5 : 4; }
 // Accumulators in tensor memory that are under way.
 constexpr int kWideBuffers = 4, kPairBuffers = 2;
 constexpr int kThinBuffers = 4;
 constexpr int thin_columns(int n) { return kThinBuffers * n; }
 
-// 16 codes of a row from column k on, any alignment; those from `left` on are zero. Only
-// 16-byte words that hold a code of the row are read.
-__device__ __forceinline__ uint4 codes16(const uint8_t* p, int64_t left) {
-    uint32_t s[9];
-    const uint32_t sh = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15);
-    const uint4* q = reinterpret_cast<const uint4*>(p - sh);
-    uint4 v = make_uint4(0u, 0u, 0u, 0u), u = v;
-    if (left > 0) v = q[0];
-    if (static_cast<int64_t>(sh) + (left < 16 ? left : 16) > 16) u = q[1];
-    s[0] = v.x; s[1] = v.y; s[2] = v.z; s[3] = v.w;
-    s[4] = u.x; s[5] = u.y; s[6] = u.z; s[7] = u.w;
-    s[8] = 0u;
+// 32 bytes, of which the 16 from byte `sh` on come back.
+__device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, uint32_t sh) {
+    uint32_t s[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     if (sh & 8u) {
 #pragma unroll
         for (int i = 0; i < 6; ++i) s[i] = s[i + 2];
     }
     if (sh & 4u) {
 #pragma unroll
-        for (int i = 0; i < 6; ++i) s[i] = s[i + 1];
+        for (int i = 0; i < 5; ++i) s[i] = s[i + 1];
     }
     const uint32_t bits = 8u * (sh & 3u);
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        w[i] = __funnelshift_r(s[i], s[i + 1], bits);
-        const int64_t n = left - 4 * i;  // codes of this word
-        if (n < 4) w[i] = n <= 0 ? 0u : w[i] & ((1u << (8 * static_cast<int>(n))) - 1u);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    return make_uint4(__funnelshift_r(s[0], s[1], bits), __funnelshift_r(s[1], s[2], bits), __funnelshift_r(s[2], s[3], bits),
+                      __funnelshift_r(s[3], s[4], bits));
 }
 
-// The threads that load tiles of rows off 16 bytes: with those that add up and the one that
-// issues they are eight warps, which leaves each all the registers that a thread can have.
-constexpr int kLoaders = 96;
-
-// ROWS rows of a tile from row r0 and column k0 on, into swizzled shared memory, by kLoaders
-// threads: rows and columns outside of the matrix are zero.
-template <int ROWS>
-__device__ __forceinline__ void load_tile(uint32_t dst, const uint8_t* base, int64_t ld, int64_t r0, int64_t rows, int k0,
-                                          int K, int thread) {
-    constexpr int BATCH = 4;
-#pragma unroll 1
-    for (int first = thread; first < ROWS * 8; first += kLoaders * BATCH) {
-        uint4 v[BATCH];
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-            const int at = first + kLoaders * i, row = at >> 3, k = k0 + (at & 7) * 16;
-            const bool in = at < ROWS * 8 && r0 + row < rows;
-            v[i] = codes16(base + (in ? (r0 + row) * ld : 0) + (in ? k : 0), in ? static_cast<int64_t>(K) - k : 0);
-        }
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-            const int at = first + kLoaders * i, row = at >> 3, c = at & 7;
-            if (at < ROWS * 8)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + row * kTileK + ((c ^ (row & 7)) << 4)),
-                             "r"(v[i].x), "r"(v[i].y), "r"(v[i].z), "r"(v[i].w)
-                             : "memory");
-        }
-    }
+// The first n of 16 codes, the others 0.
+__device__ __forceinline__ uint4 first_codes(uint4 v, int n) {
+    const auto part = [&](uint32_t w, int at) { return n >= at + 4 ? w : n <= at ? 0u : w & ((1u << (8 * (n - at))) - 1u); };
+    return make_uint4(part(v.x, 0), part(v.y, 4), part(v.z, 8), part(v.w, 12));
 }
 
 // Position in a ring of N places: index and phase.
@@ -173,6 +134,129 @@ __device__ __forceinline__ void issue(Bars<STAGES, BUFFERS>& bars, uint32_t tile
     }
 }
 
+// Rows off 16 bytes. A row of a block of K lies in 9 words of 16 bytes at most. kLoaders threads
+// copy these as they are into one of three places (cp.async, two blocks ahead; words without
+// a code of the row are not read and become zeros), and then move each row's 16-byte pieces, shifted
+// from two words, to their swizzled places in the tile. Of single loads, 16 bytes with the
+// shift in between, a row's latency showed (1001 x 5120 x 4099 574 us).
+constexpr int kLoaders = 256;
+constexpr int kRawWords = kTileK / 16 + 1, kRawAhead = 2;
+constexpr int kRawRow = 16 * kRawWords;
+
+struct RawSide {
+    const uint8_t* base;
+    int64_t ld, row0, rows;
+};
+
+// A thread's part of the words of ROWS rows: where they lie in the first block of K, and
+// from how many codes of a block on they hold one.
+template <int ROWS> struct RawWords {
+    static constexpr int kAll = ROWS * kRawWords, kMine = (kAll + kLoaders - 1) / kLoaders;
+    const uint8_t* src[kMine];
+    int from[kMine];
+    const uint8_t* any;  // a word that may be named where none is read
+    __device__ __forceinline__ void rows(const RawSide& x, int thread) {
+        any = x.base - (reinterpret_cast<uintptr_t>(x.base) & 15);
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int at = i * kLoaders + thread, row = at / kRawWords, word = at - row * kRawWords;
+            const bool in = at < kAll && x.row0 + row < x.rows;
+            const uint8_t* p = x.base + (in ? (x.row0 + row) * x.ld : 0);
+            const int sh = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+            src[i] = p - sh + 16 * word;
+            from[i] = in ? 16 * word - sh : kTileK;
+        }
+    }
+    // Block kb, of which `left` codes are the rows'.
+    __device__ __forceinline__ void copy(uint32_t raw, int kb, int left, int thread) const {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            if (kAll % kLoaders != 0 && i * kLoaders + thread >= kAll) break;
+            const bool some = from[i] < left;
+            const uint8_t* p = some ? src[i] + static_cast<int64_t>(kb) * kTileK : any;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(raw + (i * kLoaders + thread) * 16), "l"(p),
+                         "r"(some ? 16 : 0)
+                         : "memory");
+        }
+    }
+};
+
+// The rows from `raw` into the tile. A thread has every 32nd row, and these, as tiles, start at one
+// offset from a 16-byte boundary, `sh`.
+template <int ROWS>
+__device__ __forceinline__ void shift_rows(uint32_t tile, const char* raw, uint32_t sh, int left, int thread) {
+    const int row = thread >> 3, c = thread & 7;
+    tile += row * kTileK + ((c ^ (row & 7)) << 4);
+    raw += row * kRawRow + c * 16;
+#pragma unroll
+    for (int i = 0; i < ROWS; i += 32) {
+        if (ROWS % 32 != 0 && row >= ROWS) break;
+        const uint4* p = reinterpret_cast<const uint4*>(raw + i * kRawRow);
+        uint4 v = shifted(p[0], p[1], sh);
+        if (left < kTileK) v = first_codes(v, left - 16 * c);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile + i * kTileK), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                     : "memory");
+    }
+}
+
+// The tiles of X rows and of Y by kLoaders threads. at.next(kb): the next block of K and whether
+// there is one; at.rows(x, y): its tile's rows on both sides, which change where kb is `from`.
+template <int STAGES, int BUFFERS, int X, int Y, class At>
+__device__ __forceinline__ void load_tiles(Bars<STAGES, BUFFERS>& bars, uint32_t tiles, char* raw, const MatmulArgs& a, int from,
+                                           int thread, uint32_t shx, uint32_t shy, At at) {
+    constexpr uint32_t kStage = (X + Y) * kTileK;
+    constexpr int kRaw = (X + Y) * kRawRow;
+    At ahead = at;
+    RawWords<X> wx;
+    RawWords<Y> wy;
+    int slot = 0, to = 0;
+    const auto copy = [&] {
+        int kb;
+        if (ahead.next(kb)) {
+            if (kb == from) {
+                RawSide x, y;
+                ahead.rows(x, y);
+                wx.rows(x, thread);
+                wy.rows(y, thread);
+            }
+            const uint32_t dst = smem_u32(raw) + to * kRaw;
+            const int left = min(a.K - kb * kTileK, kTileK);
+            wx.copy(dst, kb, left, thread);
+            wy.copy(dst + X * kRawRow, kb, left, thread);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        to = to == kRawAhead ? 0 : to + 1;
+    };
+    for (int i = 0; i < kRawAhead; ++i) copy();
+    Ring<STAGES> s;
+    bool ok = true;
+    int kb;
+    while (at.next(kb)) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRawAhead - 1) : "memory");
+        named_barrier_sync(2, kLoaders);  // everyone's words are there, and the block before is shifted
+        copy();
+        // (where a wait gives up the thread goes on to the barriers, but waits no more)
+        ok = ok && mbar_wait_bounded(smem_u32(bars.empty) + 8 * s.at, s.phase ^ 1u, a.err);
+        if (__all_sync(0xffffffffu, ok)) {
+            const uint32_t dst = tiles + s.at * kStage;
+            const int left = a.K - kb * kTileK;
+            shift_rows<X>(dst, raw + slot * kRaw, shx, left, thread);
+            shift_rows<Y>(dst + X * kTileK, raw + slot * kRaw + X * kRawRow, shy, left, thread);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if ((thread & 31) == 0) mbar_arrive(smem_u32(bars.full) + 8 * s.at);
+        }
+        slot = slot == kRawAhead ? 0 : slot + 1;
+        s.next();
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// The offset from a 16-byte boundary of row `thread / 8` of a matrix, and of every 16th after it.
+__device__ __forceinline__ uint32_t raw_shift(const uint8_t* base, int64_t ld, int thread) {
+    return (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(base)) + static_cast<uint32_t>(thread >> 3) * static_cast<uint32_t>(ld)) & 15u;
+}
+
 // After a wait that gave up: the tiles that are still on their way, `issued` in all.
 template <int STAGES, int BUFFERS>
 __device__ __forceinline__ void drain_tiles(Bars<STAGES, BUFFERS>& bars, int64_t issued, uint32_t* err) {
@@ -224,131 +308,283 @@ __device__ __forceinline__ void tile_at(const MatmulArgs& a, int64_t t, int& m, 
     m = band * kBand + rest - n * rows;
 }
 
-// A warp that adds up 128 columns of an accumulator (from its column `shift` on) for the tiles
-// from `first` on, every `step`th, and stores them. A tile has `rows` rows, of which this
-// block has those from `row_shift` on.
-template <int DT, int BN, int BUFFERS, class Done, class Taken>
-__device__ __forceinline__ void add_tiles(const MatmulArgs& a, uint32_t tmem, int shift, int64_t first, int64_t step, int rows,
-                                          int row_shift, Done&& done, Taken&& taken) {
-    constexpr int EB = Elem<DT>::kBytes, V = Elem<DT>::kVec;
-    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
-    const uint32_t mine = tmem + (static_cast<uint32_t>(quarter) << 21) + shift;
-    const int64_t all = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
-    Ring<BUFFERS> b;
-    bool ok = true;
-    for (int64_t t = first; t < all; t += step) {
-        __syncwarp();
-        if (!ok) break;  // in all lanes
-        int m, n;
-        tile_at(a, t, m, n);
-        const int64_t row = static_cast<int64_t>(m) * rows + row_shift + quarter * 32 + lane;
-        const int col = n * BN + shift;
-        const bool live = row < a.M && col < a.N;
-        const float* sa = a.sa + (live ? row * a.ldsa : 0);
-        const float* sb = a.sb + (live ? (col >> 7) * a.ldsb : 0);
-        float acc[128];
-#pragma unroll
-        for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-        float fa = live ? sa[0] : 0.f, fb = live ? sb[0] : 0.f;
-        for (int kb = 0; kb < a.kblocks; ++kb) {
-            const float f = fa * fb;
-            if (live && kb + 1 < a.kblocks) {
-                if (!a.per_row) fa = sa[kb + 1];
-                fb = sb[kb + 1];
-            }
-            ok = mbar_wait_bounded(done(b.at), b.phase, a.err);
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            tmem_fence_after();
-            add_up<128>(mine + b.at * BN, acc, [&] { taken(b.at); }, [&](int) { return make_float4(f, f, f, f); });
-            b.next();
+// A row's scale times its columns' block's, of the blocks of K one after the other from `from`
+// to `to`, loaded a block ahead.
+struct Scales {
+    const float *sa, *sb;
+    float fa, fb;
+    bool live, per_row;
+    __device__ __forceinline__ Scales(const MatmulArgs& a, int64_t row, int col, int from)
+        : live(row < a.M && col < a.N), per_row(a.per_row != 0) {
+        sa = a.sa + (live ? row * a.ldsa + (per_row ? 0 : from) : 0);
+        sb = a.sb + (live ? (col >> 7) * a.ldsb + from : 0);
+        fa = live ? *sa : 0.f;
+        fb = live ? *sb : 0.f;
+    }
+    __device__ __forceinline__ float next(bool more) {
+        const float f = fa * fb;
+        if (live && more) {
+            if (!per_row) fa = *++sa;
+            fb = *++sb;
         }
-        __syncwarp();
-        if (!ok || !live) continue;
-        char* out = static_cast<char*>(a.y) + (row * a.ldy + col) * EB;
+        return f;
+    }
+};
+
+// The blocks of K from `from` to `to` of this thread's row and 128 columns (at `mine` in tensor
+// memory) added up; false where a wait gave up (in all lanes).
+template <int BN, int BUFFERS, class Done, class Taken>
+__device__ __forceinline__ bool add_blocks(const MatmulArgs& a, uint32_t mine, int64_t row, int col, int from, int to,
+                                           Ring<BUFFERS>& b, float (&acc)[128], Done&& done, Taken&& taken) {
+    Scales scales(a, row, col, from);
 #pragma unroll
-        for (int c = 0; c < 128; c += V) {
-            float v[V];
+    for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+    for (int kb = from; kb < to; ++kb) {
+        const float f = scales.next(kb + 1 < to);
+        const bool ok = mbar_wait_bounded(done(b.at), b.phase, a.err);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        tmem_fence_after();
+        add_up<128>(mine + b.at * BN, acc, [&] { taken(b.at); }, [&](int) { return make_float4(f, f, f, f); });
+        b.next();
+    }
+    return true;
+}
+
+// A row's 128 sums, with the bias, to y.
+template <int DT>
+__device__ __forceinline__ void store_row(const MatmulArgs& a, int64_t row, int col, const float (&acc)[128]) {
+    constexpr int EB = Elem<DT>::kBytes, V = Elem<DT>::kVec;
+    char* out = static_cast<char*>(a.y) + (row * a.ldy + col) * EB;
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = acc[c + i];
-            if (a.bias) {
+    for (int c = 0; c < 128; c += V) {
+        float v[V];
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (col + c + i < a.N) v[i] += Elem<DT>::ld(a.bias, col + c + i);
+        for (int i = 0; i < V; ++i) v[i] = acc[c + i];
+        if (a.bias) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (col + c + i < a.N) v[i] += Elem<DT>::ld(a.bias, col + c + i);
+        }
+        if (a.wide_y && col + c + V <= a.N) {
+            *reinterpret_cast<uint4*>(out + c * EB) = Elem<DT>::pack(v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (col + c + i < a.N) Elem<DT>::st(out, c + i, v[i]);
+        }
+    }
+}
+
+// The blocks of K of a cluster's block.
+struct Share {
+    int from, to;
+    __device__ __forceinline__ Share(const MatmulArgs& a, int rank, int split)
+        : from(static_cast<int>(static_cast<int64_t>(a.kblocks) * rank / split)),
+          to(static_cast<int>(static_cast<int64_t>(a.kblocks) * (rank + 1) / split)) {}
+};
+
+// The cluster's sums [rows][PITCH], at one place in its blocks' shared memory, added in the blocks'
+// order and stored, four warps of a block to every split-th four rows: row r is row0 + r of y,
+// its 128 columns are those from col0 on, four to a lane. Two rows at a time, so that their
+// loads, of up to 8 blocks, are under way together.
+template <int DT, int PITCH>
+__device__ __forceinline__ void store_cluster(const MatmulArgs& a, uint32_t sums, int64_t row0, int rows, int col0, int rank,
+                                              int split, int warp) {
+    constexpr int EB = Elem<DT>::kBytes;
+    const int lane = threadIdx.x & 31, col = col0 + 4 * lane;
+    float bias[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bias[i] = a.bias && col + i < a.N ? Elem<DT>::ld(a.bias, col + i) : 0.f;
+    const int step = 4 * split;
+    for (int first = rank * 4 + warp; first < rows; first += 2 * step) {
+        float4 part[2][kMostSplit];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t at = sums + ((first + i * step) * PITCH + 4 * lane) * 4;
+#pragma unroll
+            for (int k = 0; k < kMostSplit; ++k) {
+                part[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k < split && first + i * step < rows) part[i][k] = dsmem_ld_f4(dsmem_map(at, k));
             }
-            if (a.wide_y && col + c + V <= a.N) {
-                *reinterpret_cast<uint4*>(out + c * EB) = Elem<DT>::pack(v);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (first + i * step >= rows) break;
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < kMostSplit; ++k) {
+                v[0] += part[i][k].x;
+                v[1] += part[i][k].y;
+                v[2] += part[i][k].z;
+                v[3] += part[i][k].w;
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[c] += bias[c];
+            char* out = static_cast<char*>(a.y) + ((row0 + first + i * step) * a.ldy + col) * EB;
+            if (a.wide_y && col + 4 <= a.N) {
+                if constexpr (EB == 4) *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
+                else *reinterpret_cast<uint2*>(out) = make_uint2(Elem<DT>::pack2(v[0], v[1]), Elem<DT>::pack2(v[2], v[3]));
             } else {
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (col + c + i < a.N) Elem<DT>::st(out, c + i, v[i]);
+                for (int c = 0; c < 4; ++c)
+                    if (col + c < a.N) Elem<DT>::st(out, c, v[c]);
             }
         }
     }
 }
 
-constexpr int wide_threads(bool tma) { return 160 + (tma ? 32 : kLoaders); }
-constexpr int thin_threads(bool tma) { return 160 + (tma ? 32 : kLoaders); }
+// Threads: the warps that add up, the issuer's, and the one that loads by TMA; or, where loaders
+// shift rows, groups of four warps throughout, since registers are handed over by these: 512
+// threads have 128 registers at first, of which those that add up take 232, the issuer's
+// group keeps 40 and the loaders 120.
+constexpr int tile_threads(bool tma) { return tma ? 192 : 256 + kLoaders; }
 constexpr int kPairThreads = 384;
+// Stages of the tiles, and behind them the raw rows of the loaders.
+constexpr int wide_stages(bool tma) { return tma ? 6 : 3; }
+constexpr size_t raw_bytes(int rows, bool tma) { return tma ? 0 : static_cast<size_t>(kRawAhead + 1) * rows * kRawRow; }
 
+constexpr int kWidePitch = 132;  // of a row of sums: 16-byte pieces of 8 rows touch every bank once
+
+// The blocks of K of a persistent block's tiles, for load_tiles.
+struct WideBlocks {
+    const MatmulArgs& a;
+    int64_t turn, step, all;
+    Share share;
+    int kb;
+    __device__ __forceinline__ bool next(int& now) {
+        if (kb == share.to) {
+            kb = share.from;
+            turn += step;
+        }
+        now = kb++;
+        return turn < all;
+    }
+    __device__ __forceinline__ void rows(RawSide& x, RawSide& y) const {
+        int m, n;
+        tile_at(a, turn, m, n);
+        x = {a.a, a.lda, static_cast<int64_t>(m) * 128, a.M};
+        y = {a.b, a.ldb, static_cast<int64_t>(n) * 128, a.N};
+    }
+};
+// Those of one tile.
+struct ThinBlocks {
+    RawSide x, y;
+    int kb, to;
+    __device__ __forceinline__ bool next(int& now) {
+        now = kb++;
+        return now < to;
+    }
+    __device__ __forceinline__ void rows(RawSide& xs, RawSide& ys) const {
+        xs = x;
+        ys = y;
+    }
+};
+
+// One block to a tile, persistent; or, where tiles are few, the blocks of a cluster to a tile, a
+// part of K each.
 template <int DT, bool TMA>
-__global__ void __launch_bounds__(wide_threads(TMA), 1)
+__global__ void __launch_bounds__(tile_threads(TMA), 1)
     matmul_wide(const MatmulArgs a, const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap) {
-    constexpr int STAGES = kWideStages, BUFFERS = kWideBuffers;
+    constexpr int STAGES = wide_stages(TMA), BUFFERS = kWideBuffers;
     constexpr uint32_t kStage = 2 * kTileBytes;
     extern __shared__ char dynamic[];
     __shared__ Bars<STAGES, BUFFERS> bars;
-    const uint32_t tiles = (smem_u32(dynamic) + 1023u) & ~1023u;
+    const uint32_t base = smem_u32(dynamic), tiles = (base + 1023u) & ~1023u;
+    char* const first_tile = dynamic + (tiles - base);
+    float* const sums = reinterpret_cast<float*>(first_tile);  // [128][kWidePitch], where the tiles were
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform to the compiler
-    constexpr int kIssuer = 4, kProducer = 5;
-    if (warp == kIssuer) tmem_alloc(smem_u32(&bars.tmem), 512);
-    if (threadIdx.x == 0) bars.init(TMA ? 1 : kLoaders, 4);
+    if (warp == 4) tmem_alloc(smem_u32(&bars.tmem), 512);
+    if (threadIdx.x == 0) bars.init(TMA ? 1 : kLoaders / 32, 4);
+    if (TMA && threadIdx.x == 160) {
+        prefetch_map(&amap);
+        prefetch_map(&bmap);
+    }
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = bars.tmem;
     griddep_wait();
+    const int split = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
     const int64_t all = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
-    if (warp >= kProducer) {
-        Ring<STAGES> s;
-        int64_t issued = 0;
-        bool ok = true;
-        for (int64_t t = blockIdx.x; ok && t < all; t += gridDim.x) {
-            int m, n;
-            tile_at(a, t, m, n);
-            for (int kb = 0; kb < a.kblocks; ++kb) {
-                ok = mbar_wait_bounded(smem_u32(bars.empty) + 8 * s.at, s.phase ^ 1u, a.err);
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                const uint32_t dst = tiles + s.at * kStage, full = smem_u32(bars.full) + 8 * s.at;
-                if constexpr (TMA) {
+    const int64_t first = blockIdx.x / split, step = gridDim.x / split;
+    const Share share(a, rank, split);
+    if (warp >= 4) {
+        if constexpr (!TMA) {
+            if (warp < 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+            else asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+        }
+        if (warp == 4) {
+            const int64_t mine = all > first ? (all - first - 1) / step + 1 : 0;
+            issue<STAGES, BUFFERS, 128, false>(bars, tiles, tmem, mine * (share.to - share.from), a.err);
+        } else if (TMA) {
+            Ring<STAGES> s;
+            int64_t issued = 0;
+            bool ok = true;
+            for (int64_t turn = first; ok && turn < all; turn += step) {
+                int m, n;
+                tile_at(a, turn, m, n);
+                for (int kb = share.from; kb < share.to; ++kb) {
+                    ok = mbar_wait_bounded(smem_u32(bars.empty) + 8 * s.at, s.phase ^ 1u, a.err);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     if (elect_lane()) {
+                        const uint32_t dst = tiles + s.at * kStage, full = smem_u32(bars.full) + 8 * s.at;
                         mbar_arrive_expect_tx(full, kStage);
                         tile_g2s(dst, &amap, kb * kTileK, m * 128, full);
                         tile_g2s(dst + kTileBytes, &bmap, kb * kTileK, n * 128, full);
                     }
                     __syncwarp();
-                } else {
-                    const int thread = threadIdx.x - kProducer * 32;
-                    load_tile<128>(dst, a.a, a.lda, static_cast<int64_t>(m) * 128, a.M, kb * kTileK, a.K, thread);
-                    load_tile<128>(dst + kTileBytes, a.b, a.ldb, static_cast<int64_t>(n) * 128, a.N, kb * kTileK, a.K, thread);
-                    fence_proxy_async_smem();
-                    mbar_arrive(full);
+                    ++issued;
+                    s.next();
                 }
-                ++issued;
-                s.next();
             }
+            if (!ok) drain_tiles(bars, issued, a.err);
+        } else if (warp >= 8) {
+            const int thread = threadIdx.x - 256;
+            load_tiles<STAGES, BUFFERS, 128, 128>(bars, tiles, first_tile + STAGES * kStage, a, share.from, thread,
+                                                  raw_shift(a.a, a.lda, thread), raw_shift(a.b, a.ldb, thread),
+                                                  WideBlocks{a, first, step, all, share, share.from});
         }
-        if (TMA && !ok) drain_tiles(bars, issued, a.err);
-    } else if (warp == kIssuer) {
-        const int64_t mine = all > blockIdx.x ? (all - blockIdx.x - 1) / gridDim.x + 1 : 0;
-        issue<STAGES, BUFFERS, 128, false>(bars, tiles, tmem, mine * a.kblocks, a.err);
+        __syncwarp();
+        if (split > 1) {
+            cluster_sync();
+            cluster_sync();
+        }
     } else {
-        add_tiles<DT, 128, BUFFERS>(a, tmem, 0, blockIdx.x, gridDim.x, 128, 0, [&](int i) { return smem_u32(&bars.done[i]); },
-                                    [&](int i) { mbar_arrive(smem_u32(&bars.taken[i])); });
+        if constexpr (!TMA) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        const uint32_t mine = tmem + (static_cast<uint32_t>(warp) << 21);
+        Ring<BUFFERS> b;
+        bool ok = true;
+        int m = 0, n = 0;
+        for (int64_t turn = first; ok && turn < all; turn += step) {
+            tile_at(a, turn, m, n);
+            const int64_t row = static_cast<int64_t>(m) * 128 + threadIdx.x;
+            float acc[128];
+            ok = add_blocks<128, BUFFERS>(a, mine, row, n * 128, share.from, share.to, b, acc,
+                                          [&](int i) { return smem_u32(bars.done) + 8 * i; },
+                                          [&](int i) { mbar_arrive(smem_u32(bars.taken) + 8 * i); });
+            if (split > 1) {
+#pragma unroll
+                for (int i = 0; i < 128; i += 4)
+                    *reinterpret_cast<float4*>(sums + threadIdx.x * kWidePitch + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+            } else if (ok && row < a.M) {
+                store_row<DT>(a, row, n * 128, acc);
+            }
+            __syncwarp();
+        }
+        if (split > 1) {
+            cluster_sync();
+            const int64_t row0 = static_cast<int64_t>(m) * 128;
+            if (ok)
+                store_cluster<DT, kWidePitch>(a, smem_u32(sums), row0, static_cast<int>(min(int64_t(128), a.M - row0)), n * 128, rank,
+                                              split, warp);
+            __syncwarp();
+            cluster_sync();
+        }
     }
     griddep_launch_dependents();
     tmem_fence_before();
     __syncthreads();
-    if (warp == kIssuer) tmem_free(tmem, 512);
+    if (warp == 4) tmem_free(tmem, 512);
 }
 
 // Pairs of blocks (clusters of two): a tile of 256 rows of a by 256 of b, for which each block
@@ -412,9 +648,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-        add_tiles<DT, 256, BUFFERS>(a, tmem, (warp >> 2) * 128, first, step, 256, rank * 128,
-                                    [&](int i) { return smem_u32(&bars.done[i]); },
-                                    [&](int i) { mbar_arrive_cluster(dsmem_map(smem_u32(&bars.taken[i]), 0)); });
+        const int half = warp >> 2;  // of the tile's columns
+        const uint32_t mine = tmem + (static_cast<uint32_t>(warp & 3) << 21) + half * 128;
+        Ring<BUFFERS> b;
+        bool ok = true;
+        for (int64_t turn = first; ok && turn < all; turn += step) {
+            int m, n;
+            tile_at(a, turn, m, n);
+            const int64_t row = static_cast<int64_t>(m) * 256 + rank * 128 + (threadIdx.x & 127);
+            const int col = n * 256 + half * 128;
+            float acc[128];
+            ok = add_blocks<256, BUFFERS>(a, mine, row, col, 0, a.kblocks, b, acc, [&](int i) { return smem_u32(bars.done) + 8 * i; },
+                                          [&](int i) { mbar_arrive_cluster(dsmem_map(smem_u32(bars.taken) + 8 * i, 0)); });
+            if (ok && row < a.M && col < a.N) store_row<DT>(a, row, col, acc);
+            __syncwarp();
+        }
     }
     griddep_launch_dependents();
     tmem_fence_before();
@@ -430,20 +678,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 constexpr int kFactorBlocks = 16;
 
 template <int DT, int NT, bool TMA>
-__global__ void __launch_bounds__(thin_threads(TMA), thin_blocks(NT))
+__global__ void __launch_bounds__(tile_threads(TMA), thin_blocks(TMA))
     matmul_thin(const MatmulArgs a, const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap) {
-    constexpr int STAGES = thin_stages(NT), BUFFERS = kThinBuffers;
+    constexpr int STAGES = thin_stages(NT, TMA), BUFFERS = kThinBuffers;
     constexpr uint32_t kStage = kTileBytes + NT * kTileK;
     extern __shared__ char dynamic[];
     __shared__ Bars<STAGES, BUFFERS> bars;
     __shared__ alignas(16) float factors[2][kFactorBlocks][NT + 4];
     const uint32_t base = smem_u32(dynamic), tiles = (base + 1023u) & ~1023u;
-    float* sums = reinterpret_cast<float*>(dynamic + (tiles - base));  // [NT][128], where the tiles were
+    char* const first_tile = dynamic + (tiles - base);
+    float* const sums = reinterpret_cast<float*>(first_tile);  // [NT][128], where the tiles were
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform to the compiler
-    constexpr int kIssuer = 4, kProducer = 5;
+    constexpr int kIssuer = 4;
     if (warp == kIssuer) tmem_alloc(smem_u32(&bars.tmem), thin_columns(NT));
-    if (threadIdx.x == 0) bars.init(TMA ? 1 : kLoaders, 4);
-    if (TMA && threadIdx.x == kProducer * 32) {
+    if (threadIdx.x == 0) bars.init(TMA ? 1 : kLoaders / 32, 4);
+    if (TMA && threadIdx.x == 160) {
         prefetch_map(&amap);
         prefetch_map(&bmap);
     }
@@ -457,42 +706,49 @@ __global__ void __launch_bounds__(thin_threads(TMA), thin_blocks(NT))
     const int tile = static_cast<int>(blockIdx.x) / split;
     const int m = tile / a.n_tiles, n = tile - m * a.n_tiles;
     const int64_t t0 = static_cast<int64_t>(m) * NT;
-    const int from = static_cast<int>(static_cast<int64_t>(a.kblocks) * rank / split);
-    const int to = static_cast<int>(static_cast<int64_t>(a.kblocks) * (rank + 1) / split);
+    const Share share(a, rank, split);
+    const int from = share.from, to = share.to;
     constexpr int EB = Elem<DT>::kBytes;
     const int col = n * 128 + threadIdx.x;  // of y, for the threads that add up
     const int rows = static_cast<int>(min(static_cast<int64_t>(NT), a.M - t0));
     bool ok = true;
-    if (warp >= kProducer) {
-        Ring<STAGES> s;
-        int64_t issued = 0;
-        for (int kb = from; kb < to; ++kb) {
-            ok = mbar_wait_bounded(smem_u32(bars.empty) + 8 * s.at, s.phase ^ 1u, a.err);
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            const uint32_t dst = tiles + s.at * kStage, full = smem_u32(bars.full) + 8 * s.at;
-            if constexpr (TMA) {
+    if (warp >= 4) {
+        if constexpr (!TMA) {
+            if (warp < 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+            else asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+        }
+        if (warp == kIssuer) {
+            issue<STAGES, BUFFERS, NT, false>(bars, tiles, tmem, to - from, a.err);
+        } else if (TMA) {
+            Ring<STAGES> s;
+            int64_t issued = 0;
+            for (int kb = from; kb < to; ++kb) {
+                ok = mbar_wait_bounded(smem_u32(bars.empty) + 8 * s.at, s.phase ^ 1u, a.err);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 if (elect_lane()) {
+                    const uint32_t dst = tiles + s.at * kStage, full = smem_u32(bars.full) + 8 * s.at;
                     mbar_arrive_expect_tx(full, kStage);
                     tile_g2s(dst, &bmap, kb * kTileK, n * 128, full);
                     tile_g2s(dst + kTileBytes, &amap, kb * kTileK, m * NT, full);
                 }
                 __syncwarp();
-            } else {
-                const int thread = threadIdx.x - kProducer * 32;
-                load_tile<128>(dst, a.b, a.ldb, static_cast<int64_t>(n) * 128, a.N, kb * kTileK, a.K, thread);
-                load_tile<NT>(dst + kTileBytes, a.a, a.lda, t0, a.M, kb * kTileK, a.K, thread);
-                fence_proxy_async_smem();
-                mbar_arrive(full);
+                ++issued;
+                s.next();
             }
-            ++issued;
-            s.next();
+            if (!ok) drain_tiles(bars, issued, a.err);
+        } else if (warp >= 8) {
+            const int thread = threadIdx.x - 256;
+            load_tiles<STAGES, BUFFERS, 128, NT>(bars, tiles, first_tile + STAGES * kStage, a, from, thread,
+                                                 raw_shift(a.b, a.ldb, thread), raw_shift(a.a, a.lda, thread),
+                                                 ThinBlocks{{a.b, a.ldb, static_cast<int64_t>(n) * 128, a.N}, {a.a, a.lda, t0, a.M}, from, to});
         }
-        if (TMA && !ok) drain_tiles(bars, issued, a.err);
         __syncwarp();
-    } else if (warp == kIssuer) {
-        issue<STAGES, BUFFERS, NT, false>(bars, tiles, tmem, to - from, a.err);
-        __syncwarp();
+        if (split > 1) {
+            cluster_sync();
+            cluster_sync();
+        }
     } else {
+        if constexpr (!TMA) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         const uint32_t mine = tmem + (static_cast<uint32_t>(warp) << 21);
         // factors of kFactorBlocks blocks at a time: a thread loads those of block `fb` of a chunk for
         // the rows fr, fr + 8, ..., a chunk ahead
@@ -527,7 +783,7 @@ __global__ void __launch_bounds__(thin_threads(TMA), thin_blocks(NT))
             if (more) fetch(k0 + kFactorBlocks);
             const int n_blocks = min(kFactorBlocks, to - k0);
             for (int i = 0; i < n_blocks; ++i) {
-                ok = mbar_wait_bounded(smem_u32(bars.done) + 8 * b.at, b.phase, a.err) && ok;
+                ok = ok && mbar_wait_bounded(smem_u32(bars.done) + 8 * b.at, b.phase, a.err);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 tmem_fence_after();
                 const float* f = factors[which][i];
@@ -538,8 +794,8 @@ __global__ void __launch_bounds__(thin_threads(TMA), thin_blocks(NT))
             // (where a wait gave up the others go on meeting at the barrier)
             if (more) keep(which ^ 1);
         }
-        const float bias = a.bias && col < a.N ? Elem<DT>::ld(a.bias, col) : 0.f;
         if (split == 1) {
+            const float bias = a.bias && col < a.N ? Elem<DT>::ld(a.bias, col) : 0.f;
             if (ok && col < a.N) {
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
@@ -548,25 +804,12 @@ __global__ void __launch_bounds__(thin_threads(TMA), thin_blocks(NT))
         } else {
 #pragma unroll
             for (int j = 0; j < NT; ++j) sums[j * 128 + threadIdx.x] = acc[j];
+            __syncwarp();
+            cluster_sync();
+            if (ok) store_cluster<DT, 128>(a, smem_u32(sums), t0, rows, n * 128, rank, split, warp);
+            __syncwarp();
+            cluster_sync();
         }
-    }
-    __syncwarp();
-    if (split > 1) {
-        cluster_sync();
-        if (warp < 4 && ok && col < a.N) {
-            const float bias = a.bias ? Elem<DT>::ld(a.bias, col) : 0.f;
-            const uint32_t at = smem_u32(sums) + threadIdx.x * 4;
-            for (int j = rank; j < rows; j += split) {
-                float part[kMostSplit], v = 0.f;
-#pragma unroll
-                for (int r = 0; r < kMostSplit; ++r) part[r] = r < split ? dsmem_ld_f32(dsmem_map(at + j * 512, r)) : 0.f;
-#pragma unroll
-                for (int r = 0; r < kMostSplit; ++r) v += part[r];
-                Elem<DT>::st(static_cast<char*>(a.y) + ((t0 + j) * a.ldy + col) * EB, 0, v + bias);
-            }
-        }
-        __syncwarp();
-        cluster_sync();
     }
     tmem_fence_before();
     __syncthreads();
@@ -580,7 +823,6 @@ template <int DT, bool TMA> const void* kernel_for(const MatmulPlan& p) {
     case 16: return reinterpret_cast<const void*>(&matmul_thin<DT, 16, TMA>);
     case 32: return reinterpret_cast<const void*>(&matmul_thin<DT, 32, TMA>);
     case 64: return reinterpret_cast<const void*>(&matmul_thin<DT, 64, TMA>);
-    case 128: return reinterpret_cast<const void*>(&matmul_thin<DT, 128, TMA>);
     default: return nullptr;
     }
 }
@@ -598,9 +840,10 @@ const void* matmul_kernel(const MatmulPlan& p) {
 
 void matmul_shape(MatmulPlan& p) {
     const bool thin = p.how == kMatmulThin;
-    const int stages = thin ? thin_stages(p.n) : p.how == kMatmulWide ? kWideStages : kPairStages;
-    p.threads = thin ? thin_threads(p.tma) : p.how == kMatmulWide ? wide_threads(p.tma) : kPairThreads;
-    p.smem = 1024 + static_cast<size_t>(stages) * (kTileBytes + (thin ? p.n * kTileK : kTileBytes));
+    const int rows = 128 + (thin ? p.n : 128);
+    const int stages = thin ? thin_stages(p.n, p.tma) : p.how == kMatmulWide ? wide_stages(p.tma) : kPairStages;
+    p.threads = p.how == kMatmulPair ? kPairThreads : tile_threads(p.tma);
+    p.smem = 1024 + static_cast<size_t>(stages) * rows * kTileK + raw_bytes(rows, p.tma);
 }
 
 }  // namespace rmsnorm

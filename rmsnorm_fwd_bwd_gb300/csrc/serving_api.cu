@@ -119,31 +119,37 @@ int active_clusters(const MatmulPlan& p, int dev) {
     }
 }
 
-// How a product is cut; false on failure. Few rows of a: b's rows in the accumulators' lanes, and
-// K over as many blocks as the GPU holds at a time.
+// How a product is cut; false on failure. Few rows of a: b's rows in the accumulators' lanes.
+// More: 128 x 128 by single blocks or 256 x 256 by pairs, whichever takes less, a turn of
+// the pairs taking as long as 1.85 of the others' (N = K = 4096: 512 rows 12.9 us and 19.5,
+// 1024 rows 23.3 and 20.3). Where tiles leave half of the SMs without one, K is
+// shared by as many blocks as the GPU holds at a time.
 bool matmul_plan(int64_t M, int64_t N, int64_t K, bool tma, int dtype, int dev, int sms, MatmulPlan& p) {
     p.dtype = dtype;
     p.tma = tma;
-    p.how = M <= 128 ? kMatmulThin : tma ? kMatmulPair : kMatmulWide;
-    if (p.how == kMatmulThin)
-        for (p.n = 16; p.n < M && p.n < 128;) p.n *= 2;
-    matmul_shape(p);
-    if (p.how == kMatmulThin) {
-        const int64_t tiles = ceil_div(M, p.n) * ceil_div(N, 128);
-        p.cluster = static_cast<int>(std::min<int64_t>(kMatmulMostSplit, ceil_div(K, kBlock)));
-        while (p.cluster > 1) {
-            const int fit = active_clusters(p, dev);
-            if (fit < 1) return false;
-            if (tiles <= fit) break;
-            --p.cluster;
-        }
-        p.blocks = tiles * p.cluster;
-    } else if (p.how == kMatmulWide) {
-        p.blocks = std::min<int64_t>(ceil_div(M, 128) * ceil_div(N, 128), sms);
+    const int64_t wide = ceil_div(M, 128) * ceil_div(N, 128), pairs = ceil_div(M, 256) * ceil_div(N, 256);
+    if (M <= 64) {
+        p.how = kMatmulThin;
+        for (p.n = 16; p.n < M;) p.n *= 2;
     } else {
-        p.cluster = 2;
-        p.blocks = 2 * std::min<int64_t>(ceil_div(M, 256) * ceil_div(N, 256), sms / 2);
+        p.how = !tma || 100 * ceil_div(wide, sms) <= 185 * ceil_div(pairs, sms / 2) ? kMatmulWide : kMatmulPair;
     }
+    matmul_shape(p);
+    if (p.how == kMatmulPair) {
+        p.cluster = 2;
+        p.blocks = 2 * std::min<int64_t>(pairs, sms / 2);
+        return true;
+    }
+    const int64_t tiles = p.how == kMatmulThin ? ceil_div(M, p.n) * ceil_div(N, 128) : wide;
+    // (four blocks of K at least to each in tiles of 128 x 128, whose sums take longer to meet)
+    p.cluster = static_cast<int>(std::min<int64_t>(kMatmulMostSplit, p.how == kMatmulThin ? ceil_div(K, kBlock) : std::max<int64_t>(1, K / (4 * kBlock))));
+    while (p.cluster > 1) {
+        const int fit = active_clusters(p, dev);
+        if (fit < 1) return false;
+        if (tiles <= fit) break;
+        --p.cluster;
+    }
+    p.blocks = p.cluster > 1 || p.how == kMatmulThin ? tiles * p.cluster : std::min<int64_t>(tiles, sms);
     return true;
 }
 

@@ -85,17 +85,11 @@ __device__ __forceinline__ void tile_g2s_pair(uint32_t dst, const CUtensorMap* m
         "l"(map), "r"(x), "r"(y), "r"(cluster_bar)
         : "memory");
 }
-// Whether a phase of an mbarrier is complete, without waiting for it.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return done != 0;
+// 16 bytes of another block's shared memory.
+__device__ __forceinline__ float4 dsmem_ld_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
 }
 
 // An arrival on a barrier of another block of the cluster (or this one) that hands no memory
