@@ -19,50 +19,58 @@
 namespace rmsnorm {
 namespace {
 
-// The heads that a group of lanes takes, and where they go.
+// The heads that a group of lanes takes, and where they go. A block's groups take heads of one
+// kind (queries, keys or values, in this order of the blocks): what that kind does without is
+// skipped by the whole block, and its description is read from the arguments at a known place.
 struct Work {
-    const AppendSet* set;
+    AppendSet set;
+    int kind;
     int64_t token;
-    int from, n;      // heads; none where the token has no slot
-    bool rotate;      // not the values
-    char* out;        // row of head `from`
-    int64_t step;     // bytes between heads
-    float* scales;    // of head `from`, or null
+    int from, n;       // heads from `from` on, of which there are n
+    int stored;        // heads that are stored: n, or none where the token has no slot
+    char* out;         // row of head `from`
+    int64_t step;      // bytes between heads
+    float* scales;     // of head `from`, or null
+    __device__ __forceinline__ bool rotate() const { return kind < 2; }
 };
 
-// One thread in a group reports a slot behind the cache's last.
-template <int DT>
-__device__ __forceinline__ Work work_of(const AppendArgs& a, int64_t item, bool reports) {
-    constexpr int EB = Elem<DT>::kBytes;
+__device__ __forceinline__ Work work_of(const AppendArgs& a, int lanes) {
     Work w;
-    const bool live = item < a.T * a.nchunk;
+    w.kind = blockIdx.x >= static_cast<unsigned>(a.first[2]) ? 2 : blockIdx.x >= static_cast<unsigned>(a.first[1]) ? 1 : 0;
+    w.set = w.kind == 0 ? a.sets[0] : w.kind == 1 ? a.sets[1] : a.sets[2];
+    const int first = w.kind == 0 ? 0 : w.kind == 1 ? a.first[1] : a.first[2];
+    const int64_t item = static_cast<int64_t>(blockIdx.x - first) * (blockDim.x / lanes) + threadIdx.x / lanes;
+    const int nchunk = (w.set.heads + a.chunk - 1) / a.chunk;
+    const bool live = item < a.T * nchunk;
     int chunk;
-    w.token = split_item(live ? item : 0, a.nchunk, chunk);
-    const int kind = chunk >= a.first[2] ? 2 : chunk >= a.first[1] ? 1 : 0;
-    const AppendSet& s = a.sets[kind];
-    w.set = &s;
-    w.rotate = kind < 2;
-    w.from = (chunk - a.first[kind]) * a.chunk;
-    w.n = live ? min(a.chunk, s.heads - w.from) : 0;
+    w.token = split_item(live ? item : 0, nchunk, chunk);
+    w.from = chunk * a.chunk;
+    w.n = live ? min(a.chunk, w.set.heads - w.from) : 0;
+    return w;
+}
+
+// Where they go. Apart from work_of, so that the slot is read while the heads are under way. One
+// thread of a group reports a slot behind the cache's last.
+template <int DT> __device__ __forceinline__ void place(const AppendArgs& a, Work& w, bool reports) {
+    const AppendSet& s = w.set;
     w.scales = nullptr;
+    w.stored = w.n;
     int64_t page = 0, row = w.token;
-    if (kind > 0 && w.n > 0) {
+    if (w.kind > 0) {
         const int64_t slot = a.slots[w.token];
-        if (slot < 0 || slot >= a.pages * a.page_size) {
-            w.n = 0;
-            row = 0;
-            if (slot >= 0 && reports) atomicOr(a.err, kDevErrSlot);
-        } else {
-            int at;
-            page = split_item(slot, a.page_size, at);
-            row = at;
+        const bool in = slot >= 0 && slot < a.pages * a.page_size;
+        int at;
+        page = split_item(in ? slot : 0, a.page_size, at);
+        row = at;
+        if (!in) {
+            if (slot >= 0 && reports && w.n > 0) atomicOr(a.err, kDevErrSlot);
+            w.stored = 0;
         }
         if (s.scales) w.scales = s.scales + page * s.scale_page + row * s.scale_row + w.from * s.scale_head;
     }
-    const int bytes = s.scales ? 1 : EB;
+    const int bytes = s.scales ? 1 : Elem<DT>::kBytes;
     w.out = static_cast<char*>(s.y) + (page * s.y_page + row * s.y_token + w.from * s.y_head) * bytes;
     w.step = s.y_head * bytes;
-    return w;
 }
 
 // The largest of a group's values, a NaN before any number.
@@ -109,8 +117,8 @@ __global__ void __maxnreg__(96) append_octets(const __grid_constant__ AppendArgs
     __shared__ Turns turns;
     const int li = threadIdx.x % L;
     griddep_wait();
-    const Work w = work_of<DT>(a, static_cast<int64_t>(blockIdx.x) * (blockDim.x / L) + threadIdx.x / L, li == 0);
-    const AppendSet& set = *w.set;
+    Work w = work_of(a, L);
+    const AppendSet& set = w.set;
     int oa, ob;
     lane_octets<INTER>(li, a.D, a.R, oa, ob);
     const int rotated = rotated_pairs(a, li);
@@ -119,9 +127,28 @@ __global__ void __maxnreg__(96) append_octets(const __grid_constant__ AppendArgs
     uint32_t xw[BATCH][2][W];
 #pragma unroll
     for (int j = 0; j < BATCH; ++j) load16<DT>(xb + j * x_step, oa, ob, j < w.n, xw[j]);
+    if (!w.rotate()) {  // values
+        place<DT>(a, w, li == 0);
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            if (j >= a.chunk) break;
+            if (CODES && set.scales) {
+                uint64_t za[4], zb[4];
+                octet_pairs<DT>(xw[j][0], za);
+                octet_pairs<DT>(xw[j][1], zb);
+                const float amax = group_amax<L>(max_magnitude(octet_amax<true>(za, 0, 8), octet_amax<true>(zb, 0, 8)));
+                if (j < w.stored) store_codes(w.out + j * w.step, w.scales + j * set.scale_head, oa, ob, za, zb, amax, 1.f, li == 0);
+            } else if (j < w.stored) {
+                store_words<DT>(w.out + j * w.step, oa, ob, xw[j]);
+            }
+        }
+        griddep_launch_dependents();
+        return;
+    }
     uint64_t pc[4], ps[4], qc[4], qs[4];
     load_gains<DT, INTER>(set, a.one, oa, ob, pc, qc);
     const int64_t pos = a.pos[w.token];
+    place<DT>(a, w, li == 0);
     turns.fill(a, L);
     __syncthreads();
     {
@@ -155,57 +182,37 @@ __global__ void __maxnreg__(96) append_octets(const __grid_constant__ AppendArgs
         for (int k = 0; k < 4; ++k) ss = f2_fma(q[k], q[k], ss);
         const float sum = row_sum<L>(f2_sum(ss), nullptr);
         const float r = set.gamma ? row_rsqrt(sum, inv_d, a.eps) : 1.f;
-        if (w.rotate) {
-            turn_pairs(p, q, pc, qs, qc, ps);
-            if (rotated < 8 && j < w.n && !(sum < finite))
-                turn_again<DT, INTER>(xb + j * x_step, oa, ob, rotated, p, q, pc, qs, qc, ps);
-        }
+        turn_pairs(p, q, pc, qs, qc, ps);
+        if (rotated < 8 && j < w.n && !(sum < finite))
+            turn_again<DT, INTER>(xb + j * x_step, oa, ob, rotated, p, q, pc, qs, qc, ps);
         char* row = w.out + j * w.step;
-        if constexpr (CODES) {
-            float amax = 0.f;
+        if (CODES && set.scales) {
+            // the octets' entries in order again
+            uint64_t za[4], zb[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                float u, v;
-                f2_unpack(p[k], u, v);
-                amax = max_magnitude(max_magnitude(amax, u), v);
-                f2_unpack(q[k], u, v);
-                amax = max_magnitude(max_magnitude(amax, u), v);
-            }
-            amax = group_amax<L>(amax);
-            if (set.scales) {
-                // the octets' entries in order again
-                uint64_t za[4], zb[4];
                 if constexpr (INTER) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float p0, p1, q0, q1;
-                        f2_unpack(p[k], p0, p1);
-                        f2_unpack(q[k], q0, q1);
-                        (k < 2 ? za : zb)[2 * (k & 1)] = f2_pack(p0, q0);
-                        (k < 2 ? za : zb)[2 * (k & 1) + 1] = f2_pack(p1, q1);
-                    }
+                    float p0, p1, q0, q1;
+                    f2_unpack(p[k], p0, p1);
+                    f2_unpack(q[k], q0, q1);
+                    (k < 2 ? za : zb)[2 * (k & 1)] = f2_pack(p0, q0);
+                    (k < 2 ? za : zb)[2 * (k & 1) + 1] = f2_pack(p1, q1);
                 } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        za[k] = p[k];
-                        zb[k] = q[k];
-                    }
+                    za[k] = p[k];
+                    zb[k] = q[k];
                 }
-                if (j < w.n) store_codes(row, w.scales + j * set.scale_head, oa, ob, za, zb, amax, r, li == 0);
-                continue;
             }
-        }
-        if (!w.rotate) {
-            if (j < w.n) store_words<DT>(row, oa, ob, xw[j]);
-            continue;
-        }
-        const uint64_t r2 = f2_pack(r, r);
+            const float amax = group_amax<L>(max_magnitude(octet_amax<true>(za, 0, 8), octet_amax<true>(zb, 0, 8)));
+            if (j < w.stored) store_codes(row, w.scales + j * set.scale_head, oa, ob, za, zb, amax, r, li == 0);
+        } else {
+            const uint64_t r2 = f2_pack(r, r);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            p[k] = f2_mul(p[k], r2);
-            q[k] = f2_mul(q[k], r2);
+            for (int k = 0; k < 4; ++k) {
+                p[k] = f2_mul(p[k], r2);
+                q[k] = f2_mul(q[k], r2);
+            }
+            if (j < w.stored) store_pairs<DT, INTER>(row, oa, ob, p, q);
         }
-        if (j < w.n) store_pairs<DT, INTER>(row, oa, ob, p, q);
     }
     griddep_launch_dependents();
 }
@@ -220,8 +227,8 @@ __global__ void __maxnreg__(128) append_swap(const __grid_constant__ AppendArgs 
     __shared__ float swaps[kFusedGroupThreads / 32 * 2 * kSwapFloats];
     const int li = threadIdx.x % L;
     griddep_wait();
-    const Work w = work_of<DT>(a, static_cast<int64_t>(blockIdx.x) * (blockDim.x / L) + threadIdx.x / L, li == 0);
-    const AppendSet& set = *w.set;
+    Work w = work_of(a, L);
+    const AppendSet& set = w.set;
     const int oa = li < a.D / 8 ? li : -1, ob = li + L < a.D / 8 ? li + L : -1;
     const char* xb = static_cast<const char*>(set.x) + (w.token * set.x_token + w.from * set.x_head) * EB;
     const int64_t x_step = set.x_head * EB;
@@ -233,6 +240,7 @@ __global__ void __maxnreg__(128) append_swap(const __grid_constant__ AppendArgs 
     }
     uint64_t c[8], s[8];
     const int64_t pos = a.pos[w.token];
+    place<DT>(a, w, li == 0);
     const Swap<L> swap(swaps, a, li);
     turns.fill(a, L);
     __syncthreads();
@@ -270,11 +278,11 @@ __global__ void __maxnreg__(128) append_swap(const __grid_constant__ AppendArgs 
             for (int k = 1; k < 8; ++k) ss = f2_fma(x[k], x[k], ss);
             float r = row_rsqrt(row_sum<L>(f2_sum(ss), nullptr), inv_d, a.eps);
             if (!set.gamma) r = 1.f;
-            if (w.rotate) {
+            if (w.rotate()) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) x[k] = f2_fma(x[k], c[k], f2_mul(p[k], s[k]));
             }
-            const bool live = h + j < w.n;
+            const bool live = h + j < w.stored;
             const uint64_t(&xa)[4] = *reinterpret_cast<const uint64_t(*)[4]>(&x[0]);
             const uint64_t(&xo)[4] = *reinterpret_cast<const uint64_t(*)[4]>(&x[4]);
             if constexpr (CODES) {
@@ -282,7 +290,7 @@ __global__ void __maxnreg__(128) append_swap(const __grid_constant__ AppendArgs 
                 if (set.scales && live) store_codes(row, scale, oa, ob, xa, xo, amax, r, li == 0);
             }
             if (!set.scales && live) {
-                if (w.rotate) {
+                if (w.rotate()) {
                     const uint64_t r2 = f2_pack(r, r);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) x[k] = f2_mul(x[k], r2);
@@ -307,79 +315,75 @@ __global__ void __launch_bounds__(kFusedGroupThreads) append_pairs(const __grid_
     int ca[PK], cb[PK];
     lane_pairs<L, PK>(li, a, a.interleaved != 0, ca, cb);
     const float inv_d = 1.0f / static_cast<float>(a.D);
-    const int64_t items = a.T * a.nchunk;
-    const int64_t groups = blockDim.x / L;
-    // the whole warp goes round as often (the sums see it)
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * groups; base < items; base += gridDim.x * groups) {
-        const Work w = work_of<DT>(a, base + threadIdx.x / L, li == 0);
-        const AppendSet& set = *w.set;
-        const int64_t pos = a.pos[w.token];
-        float c[PK], s[PK];
+    Work w = work_of(a, L);
+    const AppendSet& set = w.set;
+    place<DT>(a, w, li == 0);
+    const int64_t pos = a.pos[w.token];
+    float c[PK], s[PK];
 #pragma unroll
-        for (int k = 0; k < PK; k += 2) {
-            const int i0 = li + L * k, i1 = i0 + L, half = a.R / 2;
-            c[k] = c[k + 1] = 1.f;
-            s[k] = s[k + 1] = 0.f;
-            if (i0 < half) {
-                uint64_t c2, s2;
-                turn_pair(phase_at(turns_per_position(a.inv_freq[i0]), pos),
-                          i1 < half ? phase_at(turns_per_position(a.inv_freq[i1]), pos) : 0, a.mscale, a.mscale, c2, s2);
-                f2_unpack(c2, c[k], c[k + 1]);
-                f2_unpack(s2, s[k], s[k + 1]);
+    for (int k = 0; k < PK; k += 2) {
+        const int i0 = li + L * k, i1 = i0 + L, half = a.R / 2;
+        c[k] = c[k + 1] = 1.f;
+        s[k] = s[k + 1] = 0.f;
+        if (i0 < half) {
+            uint64_t c2, s2;
+            turn_pair(phase_at(turns_per_position(a.inv_freq[i0]), pos),
+                      i1 < half ? phase_at(turns_per_position(a.inv_freq[i1]), pos) : 0, a.mscale, a.mscale, c2, s2);
+            f2_unpack(c2, c[k], c[k + 1]);
+            f2_unpack(s2, s[k], s[k + 1]);
+        }
+    }
+    const char* gb = static_cast<const char*>(set.gamma);
+    for (int h = 0; h < a.chunk; ++h) {
+        const bool live = h < w.n;
+        const char* xr = static_cast<const char*>(set.x) + (w.token * set.x_token + (w.from + h) * set.x_head) * EB;
+        float x[2 * PK];
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 2 * PK; ++j) {
+            const int col = j & 1 ? cb[j / 2] : ca[j / 2];
+            x[j] = live && col >= 0 ? entry<DT>(xr, col) : 0.f;
+            ss = fmaf(x[j], x[j], ss);
+        }
+        const float r = gb ? row_rsqrt(group_sum<L>(ss), inv_d, a.eps) : 1.f;
+        float amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < PK; ++k) {
+            if (w.rotate()) {
+                float z0 = x[2 * k], z1 = x[2 * k + 1];
+                if (gb) {
+                    // where the r is left out, as in the octets
+                    const float f = set.scales ? 1.f : r;
+                    z0 = (z0 * f) * (ca[k] >= 0 ? entry<DT>(gb, ca[k]) + a.one : 0.f);
+                    z1 = (z1 * f) * (cb[k] >= 0 ? entry<DT>(gb, cb[k]) + a.one : 0.f);
+                }
+                const bool rotated = li + L * k < a.R / 2;
+                x[2 * k] = rotated ? z0 * c[k] - z1 * s[k] : z0;
+                x[2 * k + 1] = rotated ? z1 * c[k] + z0 * s[k] : z1;
+            }
+            amax = max_magnitude(max_magnitude(amax, x[2 * k]), x[2 * k + 1]);
+        }
+        float f0 = 1.f, f1 = 1.f;
+        if constexpr (CODES) {
+            amax = group_amax<L>(amax);
+            if (set.scales) {
+                const float scale = quant_scale(amax, r, 0, f0, f1);
+                if (h < w.stored && li == 0) w.scales[h * set.scale_head] = scale;
             }
         }
-        const char* gb = static_cast<const char*>(set.gamma);
-        for (int h = 0; h < a.chunk; ++h) {
-            const bool live = h < w.n;
-            const char* xr = static_cast<const char*>(set.x) + (w.token * set.x_token + (w.from + h) * set.x_head) * EB;
-            float x[2 * PK];
-            float ss = 0.f;
+        char* row = w.out + h * w.step;
 #pragma unroll
-            for (int j = 0; j < 2 * PK; ++j) {
-                const int col = j & 1 ? cb[j / 2] : ca[j / 2];
-                x[j] = live && col >= 0 ? entry<DT>(xr, col) : 0.f;
-                ss = fmaf(x[j], x[j], ss);
-            }
-            const float r = gb ? row_rsqrt(group_sum<L>(ss), inv_d, a.eps) : 1.f;
-            float amax = 0.f;
-#pragma unroll
-            for (int k = 0; k < PK; ++k) {
-                if (w.rotate) {
-                    float z0 = x[2 * k], z1 = x[2 * k + 1];
-                    if (gb) {
-                        // where the r is left out, as in the octets
-                        const float f = set.scales ? 1.f : r;
-                        z0 = (z0 * f) * (ca[k] >= 0 ? entry<DT>(gb, ca[k]) + a.one : 0.f);
-                        z1 = (z1 * f) * (cb[k] >= 0 ? entry<DT>(gb, cb[k]) + a.one : 0.f);
-                    }
-                    const bool rotated = li + L * k < a.R / 2;
-                    x[2 * k] = rotated ? z0 * c[k] - z1 * s[k] : z0;
-                    x[2 * k + 1] = rotated ? z1 * c[k] + z0 * s[k] : z1;
-                }
-                amax = max_magnitude(max_magnitude(amax, x[2 * k]), x[2 * k + 1]);
-            }
-            float f0 = 1.f, f1 = 1.f;
-            if constexpr (CODES) {
-                amax = group_amax<L>(amax);
-                if (set.scales) {
-                    const float scale = quant_scale(amax, r, 0, f0, f1);
-                    if (live && li == 0) w.scales[h * set.scale_head] = scale;
-                }
-            }
-            char* row = w.out + h * w.step;
-#pragma unroll
-            for (int j = 0; j < 2 * PK; ++j) {
-                const int col = j & 1 ? cb[j / 2] : ca[j / 2];
-                if (!live || col < 0) continue;
-                if (CODES && set.scales) {
-                    row[col] = static_cast<char>(e4m3_pair(f2_pack(x[j] * f0, 0.f), f1));
-                } else if (w.rotate) {
-                    Elem<DT>::st(row, col, x[j]);
-                } else if constexpr (EB == 2) {  // values as they are, the payloads of NaNs too
-                    reinterpret_cast<uint16_t*>(row)[col] = reinterpret_cast<const uint16_t*>(xr)[col];
-                } else {
-                    reinterpret_cast<uint32_t*>(row)[col] = reinterpret_cast<const uint32_t*>(xr)[col];
-                }
+        for (int j = 0; j < 2 * PK; ++j) {
+            const int col = j & 1 ? cb[j / 2] : ca[j / 2];
+            if (h >= w.stored || col < 0) continue;
+            if (CODES && set.scales) {
+                row[col] = static_cast<char>(e4m3_pair(f2_pack(x[j] * f0, 0.f), f1));
+            } else if (w.rotate()) {
+                Elem<DT>::st(row, col, x[j]);
+            } else if constexpr (EB == 2) {  // values as they are, the payloads of NaNs too
+                reinterpret_cast<uint16_t*>(row)[col] = reinterpret_cast<const uint16_t*>(xr)[col];
+            } else {
+                reinterpret_cast<uint32_t*>(row)[col] = reinterpret_cast<const uint32_t*>(xr)[col];
             }
         }
     }

@@ -72,7 +72,7 @@ struct AppendSet : RopeSet {
 // heads.
 struct AppendArgs : RopeArgs {
     AppendSet sets[3];
-    int first[3];              // chunk of a token with which a kind starts
+    int first[3];              // block with which a kind starts
     const int64_t* slots;
     int64_t pages;
     int page_size;

@@ -431,13 +431,11 @@ extern "C" rmsnorm_status rmsnorm_rope_append(const rmsnorm_rope_heads* q, const
     const int64_t full = static_cast<int64_t>(sms) * (p.rows == kRopeSwap ? 512 : 1024) / p.lanes;
     const int64_t most = p.rows == kRopeEntries ? heads : p.rows == kRopeSwap ? kRopeRun : rope_fwd_batch(dtype);
     a.chunk = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, T * heads / full)));
-    a.nchunk = 0;
+    p.blocks = 0;
     for (int i = 0; i < 3; ++i) {
-        a.first[i] = a.nchunk;
-        a.nchunk += static_cast<int>(ceil_div(a.sets[i].heads, a.chunk));
+        a.first[i] = static_cast<int>(std::min<int64_t>(p.blocks, INT32_MAX));
+        p.blocks += ceil_div(T * ceil_div(a.sets[i].heads, a.chunk), p.threads / p.lanes);
     }
-    p.blocks = ceil_div(T * a.nchunk, p.threads / p.lanes);
-    if (p.rows == kRopeEntries) p.blocks = std::min<int64_t>(p.blocks, static_cast<int64_t>(sms) * 64);
     if (p.blocks > INT32_MAX) return RMSNORM_ERR_SHAPE;
     void* params[] = {&a};
     return run(append_kernel(p, codes), p.blocks, p.threads, 0, 1, params, stream);
