@@ -334,6 +334,12 @@ __global__ void __launch_bounds__(kFusedGroupThreads) append_pairs(const __grid_
         }
     }
     const char* gb = static_cast<const char*>(set.gamma);
+    float g[2 * PK];
+#pragma unroll
+    for (int j = 0; j < 2 * PK; ++j) {
+        const int col = j & 1 ? cb[j / 2] : ca[j / 2];
+        g[j] = gb && col >= 0 ? entry<DT>(gb, col) + a.one : 1.f;
+    }
     for (int h = 0; h < a.chunk; ++h) {
         const bool live = h < w.n;
         const char* xr = static_cast<const char*>(set.x) + (w.token * set.x_token + (w.from + h) * set.x_head) * EB;
@@ -352,10 +358,10 @@ __global__ void __launch_bounds__(kFusedGroupThreads) append_pairs(const __grid_
             if (w.rotate()) {
                 float z0 = x[2 * k], z1 = x[2 * k + 1];
                 if (gb) {
-                    // where the r is left out, as in the octets
+                    // of codes the r is left out, as in the octets
                     const float f = set.scales ? 1.f : r;
-                    z0 = (z0 * f) * (ca[k] >= 0 ? entry<DT>(gb, ca[k]) + a.one : 0.f);
-                    z1 = (z1 * f) * (cb[k] >= 0 ? entry<DT>(gb, cb[k]) + a.one : 0.f);
+                    z0 = (z0 * f) * g[2 * k];
+                    z1 = (z1 * f) * g[2 * k + 1];
                 }
                 const bool rotated = li + L * k < a.R / 2;
                 x[2 * k] = rotated ? z0 * c[k] - z1 * s[k] : z0;

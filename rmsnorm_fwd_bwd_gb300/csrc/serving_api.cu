@@ -426,10 +426,11 @@ extern "C" rmsnorm_status rmsnorm_rope_append(const rmsnorm_rope_heads* q, const
     RopePlan p;
     p.dtype = dtype;
     rope_lanes(D, rotary_dim, interleaved, wide, p);
-    // heads to a group as in the rotation alone (rope_plan): all of a batch where the tokens
-    // fill the GPU, fewer where they do not
+    // heads to a group as in the rotation alone (rope_plan): a batch where the tokens fill the GPU,
+    // fewer where they do not; and a run of heads where a group's turns take longer (bf16
+    // 8192 x 48 x 90 110 us with 8 heads, 116 with 4, 120 with 16)
     const int64_t full = static_cast<int64_t>(sms) * (p.rows == kRopeSwap ? 512 : 1024) / p.lanes;
-    const int64_t most = p.rows == kRopeEntries ? heads : p.rows == kRopeSwap ? kRopeRun : rope_fwd_batch(dtype);
+    const int64_t most = p.rows == kRopeEntries || p.rows == kRopeSwap ? kRopeRun : rope_fwd_batch(dtype);
     a.chunk = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, T * heads / full)));
     p.blocks = 0;
     for (int i = 0; i < 3; ++i) {
