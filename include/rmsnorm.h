@@ -188,7 +188,8 @@ const char* rmsnorm_status_string(rmsnorm_status status);
 /*
  * Device error word of the CURRENT device. Kernels that wait on an mbarrier
  * give up after a bounded number of polls, set bit 0 of this word and skip
- * their stores, so a hang becomes a reported error. Reading synchronizes the
+ * their stores, so a hang becomes a reported error. Bit 2: a token's slot lay behind
+ * the last of its paged cache (rmsnorm_serving.h). Reading synchronizes the
  * device. *flags receives the word; clear != 0 resets it to 0.
  */
 rmsnorm_status rmsnorm_device_error(uint32_t* flags, int clear);

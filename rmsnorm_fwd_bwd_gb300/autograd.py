@@ -53,7 +53,8 @@ class DeviceError(RuntimeError):
 def check_device_error(clear: bool = True) -> None:
     """Raise DeviceError if any kernel on the current device has set the device
     error word since it was last cleared (bit 0: a bounded wait gave up; bit 1,
-    debug builds: a read outside its tensor). Synchronizes the device."""
+    debug builds: a read outside its tensor; bit 2: a token's slot behind the last of
+    its paged cache). Synchronizes the device."""
     word = binding.rmsnorm_device_error(clear=clear)
     if word:
         raise DeviceError(f"RMSNorm kernels reported device error word {word:#x}")

@@ -590,3 +590,11 @@ class RMSNormRope(torch.nn.Module):
                 positions: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
         return rms_norm_rope(q, k, self.q_weight, self.k_weight, positions, self.inv_freq, self.interleaved,
                              self.mscale, self.eps, self.offset)
+
+    def append(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
+               cache) -> torch.Tensor:
+        """The queries; keys and values go to ``slots`` of a ``serving.PagedCache`` (``serving.rms_norm_rope_append``)."""
+        from . import serving
+        return serving.rms_norm_rope_append(q, k, v, self.q_weight, self.k_weight, positions, slots, self.inv_freq, cache.k,
+                                            cache.v, cache.k_scales, cache.v_scales, self.interleaved, self.mscale,
+                                            self.eps, self.offset)

@@ -407,3 +407,177 @@ def test_append_of_infinities_and_nan_keeps_them_in_their_rows():
                 assert torch.equal(torch.isfinite(got_k[1, 0]), torch.isfinite(k[1, 0]))
                 assert torch.equal(vc.t[0, :T].cpu().view(torch.int32), v.view(torch.int32))
             assert torch.isfinite(got_k[clean]).all()
+
+
+# --------------------------------------------------------------------------- #
+# more of the products: every way of cutting them, special values, use
+# --------------------------------------------------------------------------- #
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N,K,layout", [(1300, 2000, 384, "dense"),     # pairs of blocks
+                                          (5000, 4100, 256, "padded"),    # pairs, several tiles each
+                                          (2500, 1300, 301, "dense"),     # 128 x 128, several tiles, rows off 16 bytes
+                                          (150, 2600, 1024, "dense"),     # clusters that share K
+                                          (70, 900, 2050, "shifted"), (20, 300, 16384, "dense"), (64, 20000, 256, "dense"),
+                                          (40, 1, 700, "odd pitch"), (700, 1, 640, "dense"), (1, 5, 100000, "dense")])
+def test_matmul_of_every_cut(M, N, K, layout, dtype):
+    for group in (0, 128):
+        a, lda, b, ldb, sa, sb = product_inputs(M, N, K, group, 7, layout)
+        check_product(a, b, sa, sb, dtype, group, product(a, lda, b, ldb, sa, sb, dtype, group))
+
+
+@pytest.mark.parametrize("M", [3, 100, 1400])
+def test_matmul_output_of_any_alignment_and_scales_of_any_pitch(M):
+    N, K = 1999, 260
+    a, lda, b, ldb, sa, sb = product_inputs(M, N, K, 128, 21)
+    wide_a, wide_b = torch.full((M, 7), float("nan"), device="cuda"), torch.full((sb.shape[0], 9), float("nan"), device="cuda")
+    wide_a[:, 1:4], wide_b[:, 2:5] = sa, sb
+    for dtype in DTYPES:
+        for start, pitch in ((0, 2000), (1, 2001), (8, 2008)):
+            buf = torch.full((start + M * pitch + 64,), 7.0, dtype=ref.TYPES[dtype], device="cuda")
+            y = buf[start:start + M * pitch].view(M, pitch)
+            assert B.rmsnorm_quant_matmul(a, lda, wide_a[:, 1:], 7, b, ldb, wide_b[:, 2:], 9, None, y, pitch, M, N, K, dtype,
+                                          128) == 0
+            check_product(a, b, sa, sb, dtype, 128, y)
+            assert (buf[:start] == 7.0).all() and (buf[start + M * pitch:] == 7.0).all()
+
+
+@pytest.mark.parametrize("M,K", [(5, 300), (5, 304), (90, 300), (90, 304), (1500, 384)])
+def test_matmul_of_nan_and_infinite_scales_stays_in_their_rows_and_columns(M, K):
+    N = 1400
+    a, lda, b, ldb, sa, sb = product_inputs(M, N, K, 128, 31)
+    sa[1, 1] = float("nan")                                 # a row
+    sb[3, 0] = float("nan")                                 # 128 columns
+    a.view(torch.uint8)[2, 7] = 0x7F                        # a NaN among the codes
+    b.view(torch.uint8)[700, K - 1] = 0xFF
+    sa[4] = 0.0
+    y = product(a, lda, b, ldb, sa, sb, "float32", 128)[:, :N]
+    bad = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    bad[1] = bad[2] = True
+    bad[:, 384:512] = True
+    bad[:, 700] = True
+    assert torch.equal(torch.isnan(y), bad)
+    clean = ~bad
+    assert (y[4][clean[4]] == 0).all()
+    sb[3, 0], sa[1, 1] = 0.0, 0.0
+    a.view(torch.uint8)[2, 7], b.view(torch.uint8)[700, K - 1] = 0, 0
+    want, err = product_bound(a, b, sa, sb, 128)
+    assert ((y.double() - want).abs() <= err + want.abs() * U)[clean].all()
+
+
+def test_matmul_results_are_the_same_bits_every_time():
+    for M, N, K in ((8, 4096, 4096), (150, 2600, 1024), (90, 512, 1031), (1300, 2000, 640)):
+        a, lda, b, ldb, sa, sb = product_inputs(M, N, K, 128, 41)
+        first = product(a, lda, b, ldb, sa, sb, "float32", 128)
+        for _ in range(5):
+            assert torch.equal(product(a, lda, b, ldb, sa, sb, "float32", 128), first)
+
+
+def test_matmul_of_rows_past_32_bits():
+    # codes 3 GiB apart, and an output of more than 2^32 bytes
+    M, N, K, pitch = 40000, 300, 130, 80000
+    buf = torch.zeros(M * pitch, dtype=torch.uint8, device="cuda")
+    a = buf.view(F8).as_strided((M, K), (pitch, 1))
+    rows = torch.tensor([0, 1, 26843, 26844, 39999])
+    v, _ = codes(len(rows), K, 51)
+    buf.view(M, pitch)[rows.cuda(), :K] = v.contiguous().view(torch.uint8)
+    b, ldb = codes(N, K, 52)
+    sa, sb = torch.ones(M, 2, device="cuda"), torch.ones(3, 2, device="cuda")
+    y = torch.empty(M * 60000, dtype=torch.bfloat16, device="cuda")
+    assert B.rmsnorm_quant_matmul(a, pitch, sa, 2, b, ldb, sb, 2, None, y, 60000, M, N, K, "bfloat16", 128) == 0
+    got = y.view(M, 60000)[:, :N]
+    want, err = product_bound(v, b, sa[:5], sb, 128)
+    ref.assert_close(got[rows.cuda()], want, err + ref.rounding(want.abs() + err, torch.bfloat16), "y")
+    assert (got[2:26843] == 0).all()
+
+
+def everything(seed):
+    """One call of each operator on inputs of a seed, as functions of the buffers; returns (calls, buffers)."""
+    T, H, D = 33, 4, 64
+    a, lda, b, ldb, sa, sb = product_inputs(T, 3 * H * D, 512, 128, seed)
+    w = randn(300, 200, dtype="bfloat16", seed=seed).cuda()
+    st = {"a": a, "sa": sa, "w": w, "y": torch.zeros(T, 3 * H * D, dtype=torch.bfloat16, device="cuda"),
+          "wc": torch.zeros(300, 200, dtype=F8, device="cuda"), "ws": torch.zeros(3, 2, device="cuda"),
+          "q": torch.zeros(T, H, D, dtype=torch.bfloat16, device="cuda"), "pos": torch.arange(T, device="cuda"),
+          "slots": torch.arange(T, device="cuda") * 2 + 1, "kc": torch.zeros(5, 16, H, D, dtype=F8, device="cuda"),
+          "vc": torch.zeros(5, 16, H, D, dtype=F8, device="cuda"), "ks": torch.zeros(5, 16, H, device="cuda"),
+          "vs": torch.zeros(5, 16, H, device="cuda"), "f": freqs(D).cuda()}
+    q, k, v = st["y"].view(T, 3, H, D).unbind(1)
+    heads = (B.rope_heads([(q, None, st["q"])]), B.cache_heads(k, None, st["kc"], st["ks"]),
+             B.cache_heads(v, None, st["vc"], st["vs"]))
+
+    def calls(stream=None):
+        assert B.rmsnorm_quant_weight(w, 200, st["wc"], 200, st["ws"], 2, 300, 200, "bfloat16", False, stream) == 0
+        assert B.rmsnorm_quant_matmul(a, lda, sa, 4, b, ldb, sb, 4, None, st["y"], 3 * H * D, T, 3 * H * D, 512, "bfloat16",
+                                      128, stream) == 0
+        assert B.rmsnorm_rope_append(*heads, st["slots"], 5, 16, st["pos"], T, D, D, st["f"], 0, 1.0, EPS, "bfloat16", 0,
+                                     stream) == 0
+    return calls, st
+
+
+OUTS = ("wc", "ws", "y", "q", "kc", "vc", "ks", "vs")
+
+
+def same(st, want):
+    return all(torch.equal(st[n].view(torch.uint8), want[n].view(torch.uint8)) for n in OUTS)
+
+
+def test_captured_and_replayed_with_new_inputs():
+    calls, st = everything(1)
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        calls()
+    for seed in (2, 3):
+        eager, other = everything(seed)
+        eager()
+        st["a"].copy_(other["a"])
+        st["sa"].copy_(other["sa"])
+        st["w"].copy_(other["w"])
+        # the weights of both are of different seeds: the product's stays that of seed 1
+        for n in OUTS:
+            st[n].zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(st["wc"].view(torch.uint8), other["wc"].view(torch.uint8)) and torch.equal(st["ws"], other["ws"])
+        want, err = product_bound(st["a"], product_inputs(33, 768, 512, 128, 1)[2], st["sa"], product_inputs(33, 768, 512, 128, 1)[5], 128)
+        ref.assert_close(st["y"], want, err + ref.rounding(want.abs() + err, torch.bfloat16), "y")
+        q, k, v = st["y"].cpu().view(33, 3, 4, 64).unbind(1)
+        check_rows(st["kc"].view(80, 4, 64)[st["slots"]], st["ks"].view(80, 4)[st["slots"]], k, None, st["pos"].cpu(), 64, False, 1.0, False,
+                   "bfloat16")
+        check_rows(st["vc"].view(80, 4, 64)[st["slots"]], st["vs"].view(80, 4)[st["slots"]], v, "values", None, 64, False, 1.0, False,
+                   "bfloat16")
+
+
+def test_two_streams_at_once():
+    made = [everything(s) for s in (5, 6)]
+    for calls, _ in made:
+        calls()
+    torch.cuda.synchronize()
+    want = [{n: st[n].clone() for n in OUTS} for _, st in made]
+    streams = [torch.cuda.Stream() for _ in made]
+    for _ in range(20):
+        for (calls, st), s in zip(made, streams):
+            with torch.cuda.stream(s):
+                for n in OUTS:
+                    st[n].zero_()
+                calls()
+    torch.cuda.synchronize()
+    assert all(same(st, w) for (_, st), w in zip(made, want))
+
+
+def test_calls_that_follow_each_other_see_each_others_results():
+    # each kernel may start before the one before it has ended; the chain is the same as with waits
+    calls, st = everything(9)
+    calls()
+    torch.cuda.synchronize()
+    want = {n: st[n].clone() for n in OUTS}
+    for _ in range(50):
+        for n in OUTS:
+            st[n].zero_()
+        calls()
+    torch.cuda.synchronize()
+    assert same(st, want)

@@ -109,3 +109,84 @@ def test_cache_heads_checks_its_tensors():
         B.cache_heads(x, None, rows.transpose(2, 3))
     with pytest.raises(ValueError):
         B.cache_heads(x, None, rows, torch.empty(3, 4))
+
+
+# --------------------------------------------------------------------------- #
+# the torch front end's checks, before the library is called
+# --------------------------------------------------------------------------- #
+def test_quant_weight_front_checks():
+    import torch
+    from rmsnorm_fwd_bwd_gb300 import serving
+    for w in (torch.zeros(4), torch.zeros(2, 3, 4), torch.zeros(3, 0)):
+        with pytest.raises(ValueError):
+            serving.quant_weight(w)
+
+
+def test_quant_matmul_front_checks():
+    import torch
+    from rmsnorm_fwd_bwd_gb300 import serving
+    f8 = torch.float8_e4m3fn
+    good = dict(codes=torch.zeros(3, 200).to(f8), scales=torch.ones(3, 2), weight=torch.zeros(130, 200).to(f8),
+                weight_scales=torch.ones(2, 2), bias=torch.zeros(130, dtype=torch.bfloat16))
+    for bad in (dict(codes=torch.zeros(3, 200)), dict(weight=torch.zeros(130, 200)), dict(scales=torch.ones(3, 2).double()),
+                dict(weight_scales=torch.ones(2, 2).half()), dict(codes=torch.zeros(3, 199).to(f8)), dict(scales=torch.ones(3, 3)),
+                dict(scales=torch.ones(2, 2)), dict(scales=torch.ones(2)), dict(weight_scales=torch.ones(2, 1)),
+                dict(weight_scales=torch.ones(1, 2)), dict(bias=torch.zeros(130)), dict(bias=torch.zeros(129, dtype=torch.bfloat16)),
+                dict(weight=torch.zeros(200).to(f8)), dict(scales=torch.ones(3, 2, device="meta"))):
+        with pytest.raises(ValueError):
+            serving.quant_matmul(**dict(good, **bad))
+
+
+def test_rope_append_front_checks():
+    import torch
+    from rmsnorm_fwd_bwd_gb300 import serving
+    f8 = torch.float8_e4m3fn
+    pos = torch.arange(3)
+    good = dict(q=torch.zeros(3, 4, 8), k=torch.zeros(3, 2, 8), v=torch.zeros(3, 2, 8), q_weight=torch.ones(8),
+                k_weight=torch.ones(8), positions=pos, slots=pos, inv_freq=torch.ones(4, dtype=torch.float64),
+                k_cache=torch.zeros(2, 5, 2, 8), v_cache=torch.zeros(2, 5, 2, 8), k_scales=None, v_scales=None)
+    for bad in (dict(q=torch.zeros(2, 4, 8)), dict(q=torch.zeros(3, 4, 6)), dict(q=torch.zeros(3, 0, 8)), dict(q=torch.zeros(3, 4, 8).half()),
+                dict(v=torch.zeros(3, 2, 6)), dict(v=torch.zeros(3, 2, 8).half()), dict(q_weight=torch.ones(7)),
+                dict(k_weight=torch.ones(8).half()), dict(q=None), dict(v=None), dict(v_cache=None),
+                dict(positions=pos.int()), dict(positions=pos[:2]), dict(slots=pos.int()), dict(slots=pos[:2]),
+                dict(inv_freq=torch.ones(4)), dict(k_cache=torch.zeros(2, 5, 3, 8)), dict(k_cache=torch.zeros(2, 5, 2, 7)),
+                dict(k_cache=torch.zeros(10, 2, 8)), dict(k_cache=torch.zeros(2, 5, 8, 2).transpose(2, 3)),
+                dict(k_cache=torch.zeros(2, 5, 2, 8).half()), dict(k_cache=torch.zeros(0, 5, 2, 8)),
+                dict(k_scales=torch.ones(2, 5, 2)), dict(v_cache=torch.zeros(3, 5, 2, 8)),
+                dict(k_cache=torch.zeros(2, 5, 2, 8).to(f8)),
+                dict(k_cache=torch.zeros(2, 5, 2, 8).to(f8), k_scales=torch.ones(2, 5, 2).half()),
+                dict(k_cache=torch.zeros(2, 5, 2, 8).to(f8), k_scales=torch.ones(2, 5, 1)),
+                dict(k=torch.zeros(3, 2, 8, requires_grad=True)), dict(k_weight=torch.ones(8, requires_grad=True)),
+                dict(slots=torch.arange(3, device="meta"))):
+        with pytest.raises(ValueError):
+            serving.rms_norm_rope_append(**dict(good, **bad))
+
+
+def test_quant_linear_keeps_codes_and_scales_through_changes_of_type():
+    import torch
+    from rmsnorm_fwd_bwd_gb300 import serving
+    lin = serving.QuantLinear(200, 130, True, device="cpu")
+    lin.weight.view(torch.uint8).copy_(torch.arange(130 * 200).remainder(120).view(130, 200))
+    lin.weight_scales.copy_(torch.rand(2, 2))
+    before = lin.weight.clone().view(torch.uint8), lin.weight_scales.clone()
+    lin.half()
+    assert lin.out_dtype == torch.float16 and lin.bias.dtype == torch.float16
+    assert torch.equal(lin.weight.view(torch.uint8), before[0]) and torch.equal(lin.weight_scales, before[1])
+    assert set(lin.state_dict()) == {"weight", "weight_scales", "bias"}
+    with pytest.raises(ValueError):
+        serving.RMSNormQuantLinear(torch.ones(200), lin, group=64)
+
+
+def test_paged_cache_shapes():
+    import torch
+    from rmsnorm_fwd_bwd_gb300 import serving
+    for first in (False, True):
+        c = serving.PagedCache(3, 5, 2, 8, bits8=True, heads_first=first, device="cpu")
+        assert c.k.shape == c.v.shape == (3, 5, 2, 8) and c.k_scales.shape == c.v_scales.shape == (3, 5, 2)
+        assert c.k.stride() == ((80, 8, 40, 1) if first else (80, 16, 8, 1))
+        c.k.view(torch.uint8)[1, 2] = 0x38                  # 1.0
+        c.k_scales[1, 2] = 3.0
+        k, v = c.rows(torch.tensor([7, 0]))
+        assert (k[0] == 3.0).all() and (k[1] == 0.0).all() and (v == 0.0).all()
+    c = serving.PagedCache(3, 5, 2, 8, dtype=torch.float16, device="cpu")
+    assert c.k.dtype == torch.float16 and c.k_scales is None
