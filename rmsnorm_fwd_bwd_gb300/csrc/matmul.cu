@@ -331,14 +331,32 @@ struct Scales {
     }
 };
 
-// The blocks of K from `from` to `to` of this thread's row and 128 columns (at `mine` in tensor
-// memory) added up; false where a wait gave up (in all lanes).
-template <int BN, int BUFFERS, class Done, class Taken>
-__device__ __forceinline__ bool add_blocks(const MatmulArgs& a, uint32_t mine, int64_t row, int col, int from, int to,
-                                           Ring<BUFFERS>& b, float (&acc)[128], Done&& done, Taken&& taken) {
-    Scales scales(a, row, col, from);
+// 128 sums before the first block of K: the bias of their columns, or 0.
+template <int DT>
+__device__ __forceinline__ void start_sums(const MatmulArgs& a, int col, bool bias, float (&acc)[128]) {
+    constexpr int EB = Elem<DT>::kBytes, V = Elem<DT>::kVec;
 #pragma unroll
     for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+    if (!bias || !a.bias) return;
+    if (a.wide_bias && col + 128 <= a.N) {
+#pragma unroll
+        for (int c = 0; c < 128; c += V)
+            Elem<DT>::unpack(__ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(a.bias) + (col + c) * EB)),
+                             *reinterpret_cast<float(*)[V]>(&acc[c]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 128; ++i)
+            if (col + i < a.N) acc[i] = Elem<DT>::ld(a.bias, col + i);
+    }
+}
+
+// The blocks of K from `from` to `to` of this thread's row and 128 columns (at `mine` in tensor
+// memory) added up, with the bias or without; false where a wait gave up (in all lanes).
+template <int DT, int BN, int BUFFERS, class Done, class Taken>
+__device__ __forceinline__ bool add_blocks(const MatmulArgs& a, uint32_t mine, int64_t row, int col, int from, int to, bool bias,
+                                           Ring<BUFFERS>& b, float (&acc)[128], Done&& done, Taken&& taken) {
+    Scales scales(a, row, col, from);
+    start_sums<DT>(a, col, bias, acc);
     for (int kb = from; kb < to; ++kb) {
         const float f = scales.next(kb + 1 < to);
         const bool ok = mbar_wait_bounded(done(b.at), b.phase, a.err);
@@ -350,28 +368,55 @@ __device__ __forceinline__ bool add_blocks(const MatmulArgs& a, uint32_t mine, i
     return true;
 }
 
-// A row's 128 sums, with the bias, to y.
+// Places for 64 bytes of a warp's 32 rows, 80 apart: 16-byte pieces of 8 rows touch every bank once.
+constexpr int kPieceRow = 80;
+struct RowPieces {
+    alignas(16) char at[32 * kPieceRow];
+};
+
+// A warp's 32 rows (from row0 on, a thread's sums its own row's) of 128 columns (from col on) to y. They change places in shared memory, 64 bytes of each row at a time, so that four
+// lanes store a row's 64 bytes (a thread storing its own row's pieces touches 32 lines with every
+// store: 2048 x 4096 x 5120 into fp32 58 us), or 32 lanes single entries side by side
+// where y's rows are off 16 bytes.
 template <int DT>
-__device__ __forceinline__ void store_row(const MatmulArgs& a, int64_t row, int col, const float (&acc)[128]) {
-    constexpr int EB = Elem<DT>::kBytes, V = Elem<DT>::kVec;
-    char* out = static_cast<char*>(a.y) + (row * a.ldy + col) * EB;
+__device__ __forceinline__ void store_rows(const MatmulArgs& a, RowPieces& pieces, int64_t row0, int col, const float (&acc)[128]) {
+    constexpr int EB = Elem<DT>::kBytes, V = Elem<DT>::kVec, C = 64 / EB;
+    const int lane = threadIdx.x & 31;
+    char* const mine = pieces.at + lane * kPieceRow;
+    const int rows = static_cast<int>(min(int64_t(32), a.M - row0)), cols = min(128, a.N - col);
+    char* const out = static_cast<char*>(a.y) + (row0 * a.ldy + col) * EB;
 #pragma unroll
-    for (int c = 0; c < 128; c += V) {
-        float v[V];
+    for (int c = 0; c < 128; c += C) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = acc[c + i];
-        if (a.bias) {
+        for (int u = 0; u < 4; ++u) {
+            float v[V];
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (col + c + i < a.N) v[i] += Elem<DT>::ld(a.bias, col + c + i);
+            for (int i = 0; i < V; ++i) v[i] = acc[c + V * u + i];
+            *reinterpret_cast<uint4*>(mine + 16 * u) = Elem<DT>::pack(v);
         }
-        if (a.wide_y && col + c + V <= a.N) {
-            *reinterpret_cast<uint4*>(out + c * EB) = Elem<DT>::pack(v);
+        __syncwarp();
+        if (a.wide_y && c + C <= cols) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 8 * i + (lane >> 2);
+                if (r < rows)
+                    *reinterpret_cast<uint4*>(out + (r * a.ldy + c) * EB + (lane & 3) * 16) =
+                        *reinterpret_cast<const uint4*>(pieces.at + r * kPieceRow + (lane & 3) * 16);
+            }
         } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (col + c + i < a.N) Elem<DT>::st(out, c + i, v[i]);
+            constexpr int R = 32 / C;  // rows at a time
+            const int k = lane % C;
+            if (c + k < cols) {
+#pragma unroll 4
+                for (int r = lane / C; r < rows; r += R) {
+                    const char* from = pieces.at + r * kPieceRow + k * EB;
+                    char* to = out + (r * a.ldy + c + k) * EB;
+                    if constexpr (EB == 4) *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(from);
+                    else *reinterpret_cast<uint16_t*>(to) = *reinterpret_cast<const uint16_t*>(from);
+                }
+            }
         }
+        __syncwarp();
     }
 }
 
@@ -489,6 +534,7 @@ __global__ void __launch_bounds__(tile_threads(TMA), 1)
     constexpr uint32_t kStage = 2 * kTileBytes;
     extern __shared__ char dynamic[];
     __shared__ Bars<STAGES, BUFFERS> bars;
+    __shared__ RowPieces pieces[4];
     const uint32_t base = smem_u32(dynamic), tiles = (base + 1023u) & ~1023u;
     char* const first_tile = dynamic + (tiles - base);
     float* const sums = reinterpret_cast<float*>(first_tile);  // [128][kWidePitch], where the tiles were
@@ -559,15 +605,15 @@ __global__ void __launch_bounds__(tile_threads(TMA), 1)
             tile_at(a, turn, m, n);
             const int64_t row = static_cast<int64_t>(m) * 128 + threadIdx.x;
             float acc[128];
-            ok = add_blocks<128, BUFFERS>(a, mine, row, n * 128, share.from, share.to, b, acc,
+            ok = add_blocks<DT, 128, BUFFERS>(a, mine, row, n * 128, share.from, share.to, split == 1, b, acc,
                                           [&](int i) { return smem_u32(bars.done) + 8 * i; },
                                           [&](int i) { mbar_arrive(smem_u32(bars.taken) + 8 * i); });
             if (split > 1) {
 #pragma unroll
                 for (int i = 0; i < 128; i += 4)
                     *reinterpret_cast<float4*>(sums + threadIdx.x * kWidePitch + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
-            } else if (ok && row < a.M) {
-                store_row<DT>(a, row, n * 128, acc);
+            } else if (ok) {
+                store_rows<DT>(a, pieces[warp], row - (threadIdx.x & 31), n * 128, acc);
             }
             __syncwarp();
         }
@@ -598,6 +644,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     constexpr uint32_t kStage = 2 * kTileBytes;
     extern __shared__ char dynamic[];
     __shared__ Bars<STAGES, BUFFERS> bars;
+    __shared__ RowPieces pieces[8];
     const uint32_t tiles = (smem_u32(dynamic) + 1023u) & ~1023u;
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform to the compiler
     const int rank = static_cast<int>(cluster_rank());
@@ -658,9 +705,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const int64_t row = static_cast<int64_t>(m) * 256 + rank * 128 + (threadIdx.x & 127);
             const int col = n * 256 + half * 128;
             float acc[128];
-            ok = add_blocks<256, BUFFERS>(a, mine, row, col, 0, a.kblocks, b, acc, [&](int i) { return smem_u32(bars.done) + 8 * i; },
+            ok = add_blocks<DT, 256, BUFFERS>(a, mine, row, col, 0, a.kblocks, true, b, acc, [&](int i) { return smem_u32(bars.done) + 8 * i; },
                                           [&](int i) { mbar_arrive_cluster(dsmem_map(smem_u32(bars.taken) + 8 * i, 0)); });
-            if (ok && row < a.M && col < a.N) store_row<DT>(a, row, col, acc);
+            if (ok && col < a.N) store_rows<DT>(a, pieces[warp], row - (threadIdx.x & 31), col, acc);
             __syncwarp();
         }
     }

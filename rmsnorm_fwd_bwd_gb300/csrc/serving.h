@@ -26,6 +26,7 @@ struct MatmulArgs {
     int per_row;       // one scale per row of a
     int m_tiles, n_tiles;
     int wide_y;        // y's rows on 16-byte boundaries
+    int wide_bias;     // there is a bias, and it starts on one
     uint32_t* err;     // device error word
 };
 

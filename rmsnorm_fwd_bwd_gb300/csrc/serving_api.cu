@@ -285,6 +285,7 @@ extern "C" rmsnorm_status rmsnorm_quant_matmul(const void* a, int64_t lda, const
     t.m_tiles = static_cast<int>(ceil_div(M, tile_rows_a(p)));
     t.n_tiles = static_cast<int>(ceil_div(N, tile_rows_b(p)));
     t.wide_y = aligned(y, 16) && ldy * static_cast<int64_t>(s) % 16 == 0;
+    t.wide_bias = bias && aligned(bias, 16);
     t.err = device_error_word();
     if (!t.err) return RMSNORM_ERR_CUDA;
     CUtensorMap amap = {}, bmap = {};
