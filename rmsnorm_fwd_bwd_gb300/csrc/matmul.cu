@@ -134,13 +134,15 @@ __device__ __forceinline__ void issue(Bars<STAGES, BUFFERS>& bars, uint32_t tile
     }
 }
 
-// Rows off 16 bytes. A row of a block of K lies in 9 words of 16 bytes at most. kLoaders threads
-// copy these as they are into one of three places (cp.async, two blocks ahead; words without
-// a code of the row are not read and become zeros), and then move each row's 16-byte pieces, shifted
-// from two words, to their swizzled places in the tile. Of single loads, 16 bytes with the
-// shift in between, a row's latency showed (1001 x 5120 x 4099 574 us).
-constexpr int kLoaders = 256;
-constexpr int kRawWords = kTileK / 16 + 1, kRawAhead = 2;
+// Rows off 16 bytes. A row of a block of K lies in 9 words of 16 bytes at most. Each of kLoaders / 32
+// warps copies its rows' words as they are into one of three places (cp.async, three blocks ahead;
+// words without a code of the row are not read and become zeros), and then moves the rows' 16-byte
+// pieces, shifted from two words, to their swizzled places in the tile. No warp waits for
+// another's rows. Bound by shared memory (a tile is written and read twice before the matrix
+// instructions read it) and the loaders' instructions: 1001 x 5120 x 4099 107 us; 574 with single
+// loads and the shift in between, 126 with all loaders' rows behind one barrier.
+constexpr int kLoaders = 256, kLoaderWarps = kLoaders / 32;
+constexpr int kRawWords = kTileK / 16 + 1, kRawAhead = 3;
 constexpr int kRawRow = 16 * kRawWords;
 
 struct RawSide {
@@ -148,67 +150,70 @@ struct RawSide {
     int64_t ld, row0, rows;
 };
 
-// A thread's part of the words of ROWS rows: where they lie in the first block of K, and
-// from how many codes of a block on they hold one.
-template <int ROWS> struct RawWords {
-    static constexpr int kAll = ROWS * kRawWords, kMine = (kAll + kLoaders - 1) / kLoaders;
+// A lane's part of R rows of a warp (the first is row0 of the matrix): its words in the first block
+// of K, and from how many codes of a block on they hold one; and the pieces that it shifts.
+template <int R> struct RawRows {
+    static constexpr int kAll = R * kRawWords, kMine = (kAll + 31) / 32;
+    static constexpr int kPieces = R * 8, kShifts = (kPieces + 31) / 32;
     const uint8_t* src[kMine];
     int from[kMine];
-    const uint8_t* any;  // a word that may be named where none is read
-    __device__ __forceinline__ void rows(const RawSide& x, int thread) {
+    uint32_t sh[kShifts];  // a piece's row's offset from a 16-byte boundary
+    const uint8_t* any;    // a word that may be named where none is read
+    __device__ __forceinline__ void rows(const RawSide& x, int64_t row0, int lane) {
         any = x.base - (reinterpret_cast<uintptr_t>(x.base) & 15);
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
-            const int at = i * kLoaders + thread, row = at / kRawWords, word = at - row * kRawWords;
-            const bool in = at < kAll && x.row0 + row < x.rows;
-            const uint8_t* p = x.base + (in ? (x.row0 + row) * x.ld : 0);
-            const int sh = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
-            src[i] = p - sh + 16 * word;
-            from[i] = in ? 16 * word - sh : kTileK;
+            const int at = i * 32 + lane, row = at / kRawWords, word = at - row * kRawWords;
+            const bool in = at < kAll && row0 + row < x.rows;
+            const uint8_t* p = x.base + (in ? (row0 + row) * x.ld : 0);
+            const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+            src[i] = p - off + 16 * word;
+            from[i] = in ? 16 * word - off : kTileK;
         }
+        const uint32_t low = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(x.base)), ld = static_cast<uint32_t>(x.ld);
+#pragma unroll
+        for (int i = 0; i < kShifts; ++i) sh[i] = (low + static_cast<uint32_t>(row0 + ((i * 32 + lane) >> 3)) * ld) & 15u;
     }
     // Block kb, of which `left` codes are the rows'.
-    __device__ __forceinline__ void copy(uint32_t raw, int kb, int left, int thread) const {
+    __device__ __forceinline__ void copy(uint32_t raw, int kb, int left, int lane) const {
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
-            if (kAll % kLoaders != 0 && i * kLoaders + thread >= kAll) break;
+            if (kAll % 32 != 0 && i * 32 + lane >= kAll) break;
             const bool some = from[i] < left;
             const uint8_t* p = some ? src[i] + static_cast<int64_t>(kb) * kTileK : any;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(raw + (i * kLoaders + thread) * 16), "l"(p),
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(raw + (i * 32 + lane) * 16), "l"(p),
                          "r"(some ? 16 : 0)
+                         : "memory");
+        }
+    }
+    // The rows from `raw` into the tile, whose first row of theirs is `first`, a multiple of 8 or of R.
+    __device__ __forceinline__ void shift(uint32_t tile, const char* raw, int first, int left, int lane) const {
+#pragma unroll
+        for (int i = 0; i < kShifts; ++i) {
+            const int at = i * 32 + lane, row = at >> 3, c = at & 7;
+            if (kPieces % 32 != 0 && at >= kPieces) break;
+            const uint4* p = reinterpret_cast<const uint4*>(raw + row * kRawRow + c * 16);
+            uint4 v = shifted(p[0], p[1], sh[i]);
+            if (left < kTileK) v = first_codes(v, left - 16 * c);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile + (first + row) * kTileK + ((c ^ ((first + row) & 7)) << 4)),
+                         "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                          : "memory");
         }
     }
 };
 
-// The rows from `raw` into the tile. A thread has every 32nd row, and these, as tiles, start at one
-// offset from a 16-byte boundary, `sh`.
-template <int ROWS>
-__device__ __forceinline__ void shift_rows(uint32_t tile, const char* raw, uint32_t sh, int left, int thread) {
-    const int row = thread >> 3, c = thread & 7;
-    tile += row * kTileK + ((c ^ (row & 7)) << 4);
-    raw += row * kRawRow + c * 16;
-#pragma unroll
-    for (int i = 0; i < ROWS; i += 32) {
-        if (ROWS % 32 != 0 && row >= ROWS) break;
-        const uint4* p = reinterpret_cast<const uint4*>(raw + i * kRawRow);
-        uint4 v = shifted(p[0], p[1], sh);
-        if (left < kTileK) v = first_codes(v, left - 16 * c);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile + i * kTileK), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                     : "memory");
-    }
-}
-
-// The tiles of X rows and of Y by kLoaders threads. at.next(kb): the next block of K and whether
-// there is one; at.rows(x, y): its tile's rows on both sides, which change where kb is `from`.
+// The tiles of X rows and of Y by the loaders. at.next(kb): the next block of K and whether there is
+// one; at.rows(x, y): its tile's rows on both sides, which change where kb is `from`.
 template <int STAGES, int BUFFERS, int X, int Y, class At>
 __device__ __forceinline__ void load_tiles(Bars<STAGES, BUFFERS>& bars, uint32_t tiles, char* raw, const MatmulArgs& a, int from,
-                                           int thread, uint32_t shx, uint32_t shy, At at) {
+                                           int thread, At at) {
     constexpr uint32_t kStage = (X + Y) * kTileK;
-    constexpr int kRaw = (X + Y) * kRawRow;
+    constexpr int RX = X / kLoaderWarps, RY = Y / kLoaderWarps, kRaw = (X + Y) * kRawRow;
+    const int warp = thread >> 5, lane = thread & 31;
+    raw += warp * (RX + RY) * kRawRow;
     At ahead = at;
-    RawWords<X> wx;
-    RawWords<Y> wy;
+    RawRows<RX> wx;
+    RawRows<RY> wy;
     int slot = 0, to = 0;
     const auto copy = [&] {
         int kb;
@@ -216,45 +221,36 @@ __device__ __forceinline__ void load_tiles(Bars<STAGES, BUFFERS>& bars, uint32_t
             if (kb == from) {
                 RawSide x, y;
                 ahead.rows(x, y);
-                wx.rows(x, thread);
-                wy.rows(y, thread);
+                wx.rows(x, x.row0 + warp * RX, lane);
+                wy.rows(y, y.row0 + warp * RY, lane);
             }
             const uint32_t dst = smem_u32(raw) + to * kRaw;
             const int left = min(a.K - kb * kTileK, kTileK);
-            wx.copy(dst, kb, left, thread);
-            wy.copy(dst + X * kRawRow, kb, left, thread);
+            wx.copy(dst, kb, left, lane);
+            wy.copy(dst + RX * kRawRow, kb, left, lane);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        to = to == kRawAhead ? 0 : to + 1;
+        to = to == kRawAhead - 1 ? 0 : to + 1;
     };
     for (int i = 0; i < kRawAhead; ++i) copy();
     Ring<STAGES> s;
-    bool ok = true;
     int kb;
     while (at.next(kb)) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kRawAhead - 1) : "memory");
-        named_barrier_sync(2, kLoaders);  // everyone's words are there, and the block before is shifted
+        const bool ok = mbar_wait_bounded(smem_u32(bars.empty) + 8 * s.at, s.phase ^ 1u, a.err);
+        if (!__all_sync(0xffffffffu, ok)) break;  // (and the warp's words are there)
+        const uint32_t dst = tiles + s.at * kStage;
+        const int left = a.K - kb * kTileK;
+        wx.shift(dst, raw + slot * kRaw, warp * RX, left, lane);
+        wy.shift(dst + X * kTileK, raw + slot * kRaw + RX * kRawRow, warp * RY, left, lane);
+        fence_proxy_async_smem();
+        __syncwarp();  // (and the place is free again)
+        if (lane == 0) mbar_arrive(smem_u32(bars.full) + 8 * s.at);
         copy();
-        // (where a wait gives up the thread goes on to the barriers, but waits no more)
-        ok = ok && mbar_wait_bounded(smem_u32(bars.empty) + 8 * s.at, s.phase ^ 1u, a.err);
-        if (__all_sync(0xffffffffu, ok)) {
-            const uint32_t dst = tiles + s.at * kStage;
-            const int left = a.K - kb * kTileK;
-            shift_rows<X>(dst, raw + slot * kRaw, shx, left, thread);
-            shift_rows<Y>(dst + X * kTileK, raw + slot * kRaw + X * kRawRow, shy, left, thread);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if ((thread & 31) == 0) mbar_arrive(smem_u32(bars.full) + 8 * s.at);
-        }
-        slot = slot == kRawAhead ? 0 : slot + 1;
+        slot = slot == kRawAhead - 1 ? 0 : slot + 1;
         s.next();
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-}
-
-// The offset from a 16-byte boundary of row `thread / 8` of a matrix, and of every 16th after it.
-__device__ __forceinline__ uint32_t raw_shift(const uint8_t* base, int64_t ld, int thread) {
-    return (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(base)) + static_cast<uint32_t>(thread >> 3) * static_cast<uint32_t>(ld)) & 15u;
 }
 
 // After a wait that gave up: the tiles that are still on their way, `issued` in all.
@@ -486,7 +482,7 @@ constexpr int tile_threads(bool tma) { return tma ? 192 : 256 + kLoaders; }
 constexpr int kPairThreads = 384;
 // Stages of the tiles, and behind them the raw rows of the loaders.
 constexpr int wide_stages(bool tma) { return tma ? 6 : 3; }
-constexpr size_t raw_bytes(int rows, bool tma) { return tma ? 0 : static_cast<size_t>(kRawAhead + 1) * rows * kRawRow; }
+constexpr size_t raw_bytes(int rows, bool tma) { return tma ? 0 : static_cast<size_t>(kRawAhead) * rows * kRawRow; }
 
 constexpr int kWidePitch = 132;  // of a row of sums: 16-byte pieces of 8 rows touch every bank once
 
@@ -540,7 +536,7 @@ __global__ void __launch_bounds__(tile_threads(TMA), 1)
     float* const sums = reinterpret_cast<float*>(first_tile);  // [128][kWidePitch], where the tiles were
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform to the compiler
     if (warp == 4) tmem_alloc(smem_u32(&bars.tmem), 512);
-    if (threadIdx.x == 0) bars.init(TMA ? 1 : kLoaders / 32, 4);
+    if (threadIdx.x == 0) bars.init(TMA ? 1 : kLoaderWarps, 4);
     if (TMA && threadIdx.x == 160) {
         prefetch_map(&amap);
         prefetch_map(&bmap);
@@ -587,7 +583,6 @@ __global__ void __launch_bounds__(tile_threads(TMA), 1)
         } else if (warp >= 8) {
             const int thread = threadIdx.x - 256;
             load_tiles<STAGES, BUFFERS, 128, 128>(bars, tiles, first_tile + STAGES * kStage, a, share.from, thread,
-                                                  raw_shift(a.a, a.lda, thread), raw_shift(a.b, a.ldb, thread),
                                                   WideBlocks{a, first, step, all, share, share.from});
         }
         __syncwarp();
@@ -738,7 +733,7 @@ __global__ void __launch_bounds__(tile_threads(TMA), thin_blocks(TMA))
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform to the compiler
     constexpr int kIssuer = 4;
     if (warp == kIssuer) tmem_alloc(smem_u32(&bars.tmem), thin_columns(NT));
-    if (threadIdx.x == 0) bars.init(TMA ? 1 : kLoaders / 32, 4);
+    if (threadIdx.x == 0) bars.init(TMA ? 1 : kLoaderWarps, 4);
     if (TMA && threadIdx.x == 160) {
         prefetch_map(&amap);
         prefetch_map(&bmap);
@@ -786,7 +781,6 @@ __global__ void __launch_bounds__(tile_threads(TMA), thin_blocks(TMA))
         } else if (warp >= 8) {
             const int thread = threadIdx.x - 256;
             load_tiles<STAGES, BUFFERS, 128, NT>(bars, tiles, first_tile + STAGES * kStage, a, from, thread,
-                                                 raw_shift(a.b, a.ldb, thread), raw_shift(a.a, a.lda, thread),
                                                  ThinBlocks{{a.b, a.ldb, static_cast<int64_t>(n) * 128, a.N}, {a.a, a.lda, t0, a.M}, from, to});
         }
         __syncwarp();
