@@ -22,7 +22,6 @@
 namespace rmsnorm {
 namespace {
 
-constexpr int kMostSplit = kMatmulMostSplit;
 constexpr int kTileBytes = 128 * kTileK;  // 128 rows
 
 constexpr int kPairStages = 6;
@@ -426,49 +425,56 @@ struct Share {
 
 // The cluster's sums [rows][PITCH], at one place in its blocks' shared memory, added in the blocks'
 // order and stored, four warps of a block to every split-th four rows: row r is row0 + r of y,
-// its 128 columns are those from col0 on, four to a lane. Two rows at a time, so that their
-// loads, of up to 8 blocks, are under way together.
+// its 128 columns are those from col0 on, four to a lane. Four rows and four blocks at a time,
+// whose loads are under way together.
 template <int DT, int PITCH>
 __device__ __forceinline__ void store_cluster(const MatmulArgs& a, uint32_t sums, int64_t row0, int rows, int col0, int rank,
                                               int split, int warp) {
-    constexpr int EB = Elem<DT>::kBytes;
+    constexpr int EB = Elem<DT>::kBytes, B = 4;
     const int lane = threadIdx.x & 31, col = col0 + 4 * lane;
     float bias[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) bias[i] = a.bias && col + i < a.N ? Elem<DT>::ld(a.bias, col + i) : 0.f;
     const int step = 4 * split;
-    for (int first = rank * 4 + warp; first < rows; first += 2 * step) {
-        float4 part[2][kMostSplit];
+    for (int first = rank * 4 + warp; first < rows; first += B * step) {
+        float v[B][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t at = sums + ((first + i * step) * PITCH + 4 * lane) * 4;
+        for (int i = 0; i < B; ++i) v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
+#pragma unroll 1
+        for (int k0 = 0; k0 < split; k0 += 4) {
+            float4 part[B][4];
 #pragma unroll
-            for (int k = 0; k < kMostSplit; ++k) {
-                part[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (k < split && first + i * step < rows) part[i][k] = dsmem_ld_f4(dsmem_map(at, k));
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t from = dsmem_map(sums, min(k0 + k, split - 1));
+#pragma unroll
+                for (int i = 0; i < B; ++i) {
+                    part[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (k0 + k < split && first + i * step < rows) part[i][k] = dsmem_ld_f4(from + ((first + i * step) * PITCH + 4 * lane) * 4);
+                }
             }
+#pragma unroll
+            for (int i = 0; i < B; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[i][0] += part[i][k].x;
+                    v[i][1] += part[i][k].y;
+                    v[i][2] += part[i][k].z;
+                    v[i][3] += part[i][k].w;
+                }
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < B; ++i) {
             if (first + i * step >= rows) break;
-            float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int k = 0; k < kMostSplit; ++k) {
-                v[0] += part[i][k].x;
-                v[1] += part[i][k].y;
-                v[2] += part[i][k].z;
-                v[3] += part[i][k].w;
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) v[c] += bias[c];
+            for (int c = 0; c < 4; ++c) v[i][c] += bias[c];
             char* out = static_cast<char*>(a.y) + ((row0 + first + i * step) * a.ldy + col) * EB;
             if (a.wide_y && col + 4 <= a.N) {
-                if constexpr (EB == 4) *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
-                else *reinterpret_cast<uint2*>(out) = make_uint2(Elem<DT>::pack2(v[0], v[1]), Elem<DT>::pack2(v[2], v[3]));
+                if constexpr (EB == 4) *reinterpret_cast<float4*>(out) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+                else *reinterpret_cast<uint2*>(out) = make_uint2(Elem<DT>::pack2(v[i][0], v[i][1]), Elem<DT>::pack2(v[i][2], v[i][3]));
             } else {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    if (col + c < a.N) Elem<DT>::st(out, c, v[c]);
+                    if (col + c < a.N) Elem<DT>::st(out, c, v[i][c]);
             }
         }
     }
