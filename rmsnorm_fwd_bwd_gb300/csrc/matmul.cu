@@ -6,15 +6,24 @@
 //     y[m, n] = sum over blocks j of sa[m, j] * sb[n / 128, j] * (a_j b_j^T)[m, n].
 // The inner products of a block, 128 products of codes, are summed by the tensor cores in
 // fp32; the sum over blocks is taken in fp32 registers, by one multiply-add per element and
-// block (two of them in one packed instruction).
+// block.
 //
 // Three kernels. matmul_pair: pairs of blocks on tiles of 256 x 256, a thread to a row of the
 // accumulator. matmul_wide: single blocks on tiles of 128 x 128. matmul_thin, for few rows
-// of a: the operands change places, a tile is 128 rows of b and 16 to 64 of a, and the blocks of a
-// cluster share K. In all of them one thread keeps a ring of tiles full by TMA, one issues
-// the matrix instructions into one of several accumulators in tensor memory, and warps of four
-// add finished ones up meanwhile. Rows off 16 bytes, which TMA does not take, are loaded
-// by three warps in words that are shifted together.
+// of a: the operands change places, a tile is 128 rows of b and 16 to 64 of a. Where tiles are
+// few the blocks of a cluster share a tile's K. In all of them one warp keeps a ring of tiles full
+// by TMA, one issues the matrix instructions into one of several accumulators in tensor
+// memory, and warps of four add finished ones up meanwhile. Rows off 16 bytes, which TMA does not
+// take, are copied as they lie by eight warps, which shift them into the tiles.
+//
+// Measured on GB300 (device copy 6.79 TB/s; bf16 products of the library 1.94 PFLOP/s, 1.73 under
+// the power limit): 16384 x 8192 x 8192 into bf16 780-815 us (2.7 PFLOP/s at 1350 W, the power
+// limit; the tensor cores are busy for half of the time, and the sums, 128 multiply-adds a
+// thread and block, bound the rest), 2048 x 4096 x 5120 into fp32 with a bias 41 us (128 tiles
+// are two turns of 76 pairs), 512 x 4096 x 4096 12.5 us, 64 x 8192 x 8192 17.3 us and 8 x 6144 x
+// 4096 8 us (the weight's bytes in 11 and 3.4 us of it, at 6 to 7 TB/s; the rest is the start
+// of a ring, 1.2 us, and the meeting of a cluster's sums, 1.5 to 2.5), 1001 x 5120 x 4099, rows off 16
+// bytes, 107 us.
 #include "octet.cuh"
 #include "serving.h"
 #include "tcgen05.cuh"
@@ -481,11 +490,22 @@ __device__ __forceinline__ void store_cluster(const MatmulArgs& a, uint32_t sums
 }
 
 // Threads: the warps that add up, the issuer's, and the one that loads by TMA; or, where loaders
-// shift rows, groups of four warps throughout, since registers are handed over by these: 512
-// threads have 128 registers at first, of which those that add up take 232, the issuer's
-// group keeps 40 and the loaders 120.
+// shift rows, and in pairs, groups of four warps throughout, between which registers are handed over.
 constexpr int tile_threads(bool tma) { return tma ? 192 : 256 + kLoaders; }
 constexpr int kPairThreads = 384;
+// Registers of a thread that adds up, of the issuer's group and of a loader. A group that asks for
+// more than all have at launch would wait for ever.
+constexpr int kAddRegs = 232, kIssueRegs = 40, kLoadRegs = 120;
+constexpr int launch_regs(int threads) { return 65536 / threads / 8 * 8; }
+static_assert(kAddRegs + kIssueRegs + kLoaders / 128 * kLoadRegs <= tile_threads(false) / 128 * launch_regs(tile_threads(false)),
+              "registers of loaders' blocks");
+static_assert(2 * kAddRegs + kIssueRegs <= kPairThreads / 128 * launch_regs(kPairThreads), "registers of pairs");
+template <int REGS> __device__ __forceinline__ void take_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS> __device__ __forceinline__ void give_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
 // Stages of the tiles, and behind them the raw rows of the loaders.
 constexpr int wide_stages(bool tma) { return tma ? 6 : 3; }
 constexpr size_t raw_bytes(int rows, bool tma) { return tma ? 0 : static_cast<size_t>(kRawAhead) * rows * kRawRow; }
@@ -558,8 +578,8 @@ __global__ void __launch_bounds__(tile_threads(TMA), 1)
     const Share share(a, rank, split);
     if (warp >= 4) {
         if constexpr (!TMA) {
-            if (warp < 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-            else asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+            if (warp < 8) give_registers<kIssueRegs>();
+            else give_registers<kLoadRegs>();
         }
         if (warp == 4) {
             const int64_t mine = all > first ? (all - first - 1) / step + 1 : 0;
@@ -597,7 +617,7 @@ __global__ void __launch_bounds__(tile_threads(TMA), 1)
             cluster_sync();
         }
     } else {
-        if constexpr (!TMA) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        if constexpr (!TMA) take_registers<kAddRegs>();
         const uint32_t mine = tmem + (static_cast<uint32_t>(warp) << 21);
         Ring<BUFFERS> b;
         bool ok = true;
@@ -661,10 +681,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     griddep_wait();
     const int64_t all = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
     const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
-    // the 384 threads have 168 registers at first: the 8 warps that add up take 232, the others
-    // keep 40
     if (warp >= kIssuer) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        give_registers<kIssueRegs>();
         if (warp == kProducer) {
             Ring<STAGES> s;
             int64_t issued = 0;
@@ -695,7 +713,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         __syncwarp();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        take_registers<kAddRegs>();
         const int half = warp >> 2;  // of the tile's columns
         const uint32_t mine = tmem + (static_cast<uint32_t>(warp & 3) << 21) + half * 128;
         Ring<BUFFERS> b;
@@ -762,8 +780,8 @@ __global__ void __launch_bounds__(tile_threads(TMA), thin_blocks(TMA))
     bool ok = true;
     if (warp >= 4) {
         if constexpr (!TMA) {
-            if (warp < 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-            else asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+            if (warp < 8) give_registers<kIssueRegs>();
+            else give_registers<kLoadRegs>();
         }
         if (warp == kIssuer) {
             issue<STAGES, BUFFERS, NT, false>(bars, tiles, tmem, to - from, a.err);
@@ -795,7 +813,7 @@ __global__ void __launch_bounds__(tile_threads(TMA), thin_blocks(TMA))
             cluster_sync();
         }
     } else {
-        if constexpr (!TMA) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        if constexpr (!TMA) take_registers<kAddRegs>();
         const uint32_t mine = tmem + (static_cast<uint32_t>(warp) << 21);
         // factors of kFactorBlocks blocks at a time: a thread loads those of block `fb` of a chunk for
         // the rows fr, fr + 8, ..., a chunk ahead
