@@ -4,8 +4,8 @@
 // w / scale rounded to nearest-even, both quotients exactly rounded: the same codes wherever
 // a checkpoint is turned into them. A block of 512 threads holds one block of the weight in
 // registers (four octets a thread), so that the weight is read once. Bound by the blocks' phases,
-// loads, maximum, stores, three blocks to an SM: 8192 x 8192 bf16 43 us (4.6 TB/s; 51 us with
-// 256 threads, 47 with two blocks), 4099 x 5000 fp32 18.3 (5.6 TB/s).
+// loads, maximum, stores, three blocks to an SM: 8192 x 8192 bf16 40.6 us (5.0 TB/s; 46.6 with two
+// blocks, 54 with persistent ones that load ahead), 4099 x 5000 fp32 18.0 (5.7 TB/s).
 #include "octet.cuh"
 #include "quant.cuh"
 #include "serving.h"
@@ -17,24 +17,33 @@ constexpr int kThreads = 512;
 constexpr int kRows = kThreads / 16;                // of a block at a time: 16 threads hold a row
 constexpr int kOctets = 128 / kRows;                // per thread
 
-// Codes of w / s for an octet. w times the inverse of s is off by less than 2^-23 of the quotient: where
-// the codes of that a little smaller and a little larger are one, it is the quotient's; else, near the
-// border between two, the quotients are taken (about one octet in 10^4; with quotients
-// throughout 8192 x 8192 bf16 took 62.5 us).
+// The largest magnitude among a thread's words, as bits: those of numbers without their sign are in
+// the numbers' order, infinity above them and NaN above that. 16-bit types: two to a word.
+template <int DT> __device__ __forceinline__ uint32_t larger_bits(uint32_t m, uint32_t w) {
+    return DT == kF32 ? max(m, w & 0x7fffffffu) : __vmaxu2(m, w & 0x7fff7fffu);
+}
+template <int DT> __device__ __forceinline__ float bits_value(uint32_t m) {
+    if (DT == kF32) return __uint_as_float(m);
+    const uint32_t v = max(m >> 16, m & 0xffffu);
+    return DT == kF16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(v))) : __uint_as_float(v << 16);
+}
+
+// Codes of w / s for an octet. w times the inverse of s is off by less than 2^-22 of the quotient, the
+// inverse's rounding included: where the codes of w times a little less (`less`) and a little more
+// are one, it is the quotient's; else, near the border between two, the quotients are taken
+// (about one octet in 10^4; with quotients throughout 8192 x 8192 bf16 took 62.5 us).
 template <int DT>
-__device__ __forceinline__ void octet_quotients(const uint32_t (&w)[Oct<DT>::kWords], float s, float inv, uint32_t (&code)[2]) {
-    constexpr float kLess = 1.0f - 0x1p-22f, kMore = 1.0f + 0x1p-22f;
+__device__ __forceinline__ void octet_quotients(const uint32_t (&w)[Oct<DT>::kWords], float s, float less, float more,
+                                                uint32_t (&code)[2]) {
     uint64_t z[4];
     octet_pairs<DT>(w, z);
-    uint32_t more[2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) z[i] = f2_mul(z[i], f2_pack(inv, inv));
+    uint32_t other[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        code[i] = e4m3_pair(z[2 * i], kLess) | e4m3_pair(z[2 * i + 1], kLess) << 16;
-        more[i] = e4m3_pair(z[2 * i], kMore) | e4m3_pair(z[2 * i + 1], kMore) << 16;
+        code[i] = e4m3_pair(z[2 * i], less) | e4m3_pair(z[2 * i + 1], less) << 16;
+        other[i] = e4m3_pair(z[2 * i], more) | e4m3_pair(z[2 * i + 1], more) << 16;
     }
-    if (code[0] == more[0] && code[1] == more[1]) return;
+    if (code[0] == other[0] && code[1] == other[1]) return;
     float f[8];
     Oct<DT>::unpack(w, f);
 #pragma unroll
@@ -63,14 +72,12 @@ __global__ void __launch_bounds__(kThreads, 3) quant_weight_blocks(const WeightA
         for (int j = 0; j < W; ++j) v[i][j] = 0u;
         if (hi > 0) octet_load<DT, ALIGNED>(w + i * kRows * a.ldw * EB, 0, hi, v[i]);
     }
-    float amax = 0.f;
+    uint32_t m = 0u;
 #pragma unroll
-    for (int i = 0; i < kOctets; ++i) {
-        uint64_t z[4];
-        octet_pairs<DT>(v[i], z);
-        amax = max_magnitude(amax, octet_amax<true>(z, 0, 8));
-    }
-    amax = warp_allmax(amax);
+    for (int i = 0; i < kOctets; ++i)
+#pragma unroll
+        for (int j = 0; j < W; ++j) m = larger_bits<DT>(m, v[i][j]);
+    float amax = warp_allmax(bits_value<DT>(m));
     const int lane = threadIdx.x & 31;
     if (lane == 0) part[threadIdx.x >> 5] = amax;
     __syncthreads();
@@ -79,13 +86,14 @@ __global__ void __launch_bounds__(kThreads, 3) quant_weight_blocks(const WeightA
     if (s < 1.17549435e-38f) s = 1.17549435e-38f;  // 2^-126; a NaN stays
     if (a.pow2) s = power_of_two_above(s);
     if (threadIdx.x == 0) a.scales[static_cast<int64_t>(blockIdx.x / a.kblocks) * a.ldscales + kb] = s;
-    const float inv = 1.0f / s;
+    // (infinite scales: 0, for codes of 0 and NaN)
+    const float inv = 1.0f / s, less = inv * (1.0f - 0x1p-22f), more = inv * (1.0f + 0x1p-22f);
     const bool first = o == 0, last = o == 15 || col + 8 >= a.K;
     char* out = static_cast<char*>(a.codes) + row0 * a.ldcodes + col;
 #pragma unroll
     for (int i = 0; i < kOctets; ++i) {
         uint32_t code[2];
-        octet_quotients<DT>(v[i], s, inv, code);
+        octet_quotients<DT>(v[i], s, less, more, code);
         octet_store<1, 2, ALIGNED>(out + i * kRows * a.ldcodes, code, row0 + kRows * i < a.N ? width : 0, first, last);
     }
     griddep_launch_dependents();
