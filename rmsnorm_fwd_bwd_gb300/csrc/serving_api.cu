@@ -121,8 +121,8 @@ int active_clusters(const MatmulPlan& p, int dev) {
 
 // How a product is cut; false on failure. Few rows of a: b's rows in the accumulators' lanes.
 // More: 128 x 128 by single blocks or 256 x 256 by pairs, whichever takes less, a turn of
-// the pairs taking as long as 1.85 of the others' (N = K = 4096: 512 rows 12.9 us and 19.5,
-// 1024 rows 23.3 and 20.3). Where tiles leave half of the SMs without one, K is
+// the pairs taking as long as 1.55 of the others' (N = K = 4096: 512 rows 12.6 us and 17.1,
+// 1024 rows 22.4 and 18.2, 8192 rows 142 and 111). Where tiles leave half of the SMs without one, K is
 // shared by as many blocks as the GPU holds at a time.
 bool matmul_plan(int64_t M, int64_t N, int64_t K, bool tma, int dtype, int dev, int sms, MatmulPlan& p) {
     p.dtype = dtype;
@@ -132,7 +132,7 @@ bool matmul_plan(int64_t M, int64_t N, int64_t K, bool tma, int dtype, int dev, 
         p.how = kMatmulThin;
         for (p.n = 16; p.n < M;) p.n *= 2;
     } else {
-        p.how = !tma || 100 * ceil_div(wide, sms) <= 185 * ceil_div(pairs, sms / 2) ? kMatmulWide : kMatmulPair;
+        p.how = !tma || 100 * ceil_div(wide, sms) <= 155 * ceil_div(pairs, sms / 2) ? kMatmulWide : kMatmulPair;
     }
     matmul_shape(p);
     if (p.how == kMatmulPair) {
