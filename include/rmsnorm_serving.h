@@ -52,9 +52,9 @@ rmsnorm_status rmsnorm_quant_weight(const void* w, int64_t ldw, void* codes, int
  * or bf16 (dtype), and bias[N], which may be NULL, of the same type. The products within a block
  * of 128 columns are summed by the tensor cores in fp32, the blocks, times the product of
  * their two scales, in fp32; one rounding to y's type. A pair of scales whose product passes
- * fp32's range counts as infinite, or as 0 below it. A result depends on the
- * operands and on M, N and K (which choose the order of the sums), not on the run. 1 <= N, K <=
- * RMSNORM_MATMUL_MAX; M may be 0. y must not overlap an operand.
+ * fp32's range counts as infinite, or as 0 below it. A result depends on the operands, their
+ * alignment, M, N, K and the device (which choose the order of the sums), not on the run.
+ * 1 <= N, K <= RMSNORM_MATMUL_MAX; M may be 0. y must not overlap an operand.
  */
 rmsnorm_status rmsnorm_quant_matmul(const void* a, int64_t lda, const float* a_scales, int64_t ldas, const void* b,
                                     int64_t ldb, const float* b_scales, int64_t ldbs, const void* bias, void* y,

@@ -145,7 +145,8 @@ __global__ void __maxnreg__(96) append_octets(const __grid_constant__ AppendArgs
                 octet_pairs<DT>(xw[j][0], za);
                 octet_pairs<DT>(xw[j][1], zb);
                 const float amax = group_amax<L>(max_magnitude(octet_amax<true>(za, 0, 8), octet_amax<true>(zb, 0, 8)));
-                if (j < w.stored) store_codes(w.out + j * w.step, w.scales + j * set.scale_head, oa, ob, za, zb, amax, 1.f, li == 0);
+                float* scale = w.scales + j * set.scale_head;
+                if (j < w.stored) store_codes(w.out + j * w.step, scale, oa, ob, za, zb, amax, 1.f, li == 0);
             } else if (j < w.stored) {
                 store_words<DT>(w.out + j * w.step, oa, ob, xw[j]);
             }

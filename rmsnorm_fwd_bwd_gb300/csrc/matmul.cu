@@ -95,10 +95,10 @@ template <int STAGES, int BUFFERS> struct Bars {
     }
 };
 
-// The warp that issues matrix instructions: `blocks` blocks of K through the ring (X rows by Y
-// rows, X's tile first in a stage of BYTES) into the accumulators in turn. PAIR: for both blocks
-// of a cluster, X of 256 rows. The loop is the whole warp's, see elect_lane (16384 x 8192 x 8192
-// 1110 us with a loop of one thread).
+// The warp that issues matrix instructions: `blocks` blocks of K through the ring (a stage has a tile
+// of 128 rows and one of Y) into the accumulators in turn. PAIR: for both blocks of a cluster, 256
+// rows by 256. The loop is the whole warp's, see elect_lane (16384 x 8192 x 8192 1110 us with a
+// loop of one thread).
 template <int STAGES, int BUFFERS, int Y, bool PAIR>
 __device__ __forceinline__ void issue(Bars<STAGES, BUFFERS>& bars, uint32_t tiles, uint32_t tmem, int64_t blocks, uint32_t* err) {
     constexpr uint32_t kStage = PAIR ? 2 * kTileBytes : kTileBytes + Y * kTileK;
@@ -165,7 +165,8 @@ template <int R> struct RawRows {
     static constexpr int kPieces = R * 8, kShifts = (kPieces + 31) / 32;
     const uint8_t* src[kMine];
     int from[kMine];
-    uint32_t sh[kShifts];  // a piece's row's offset from a 16-byte boundary
+    uint32_t sh[kShifts];  // a piece's row's offset from a 16-byte boundary: tiles start 16 rows apart at
+                           // least, so that it is the same for each, also while the next one is copied
     const uint8_t* any;    // a word that may be named where none is read
     __device__ __forceinline__ void rows(const RawSide& x, int64_t row0, int lane) {
         any = x.base - (reinterpret_cast<uintptr_t>(x.base) & 15);
@@ -194,7 +195,7 @@ template <int R> struct RawRows {
                          : "memory");
         }
     }
-    // The rows from `raw` into the tile, whose first row of theirs is `first`, a multiple of 8 or of R.
+    // The rows from `raw` into the tile, the first of them its row `first`.
     __device__ __forceinline__ void shift(uint32_t tile, const char* raw, int first, int left, int lane) const {
 #pragma unroll
         for (int i = 0; i < kShifts; ++i) {
@@ -203,9 +204,8 @@ template <int R> struct RawRows {
             const uint4* p = reinterpret_cast<const uint4*>(raw + row * kRawRow + c * 16);
             uint4 v = shifted(p[0], p[1], sh[i]);
             if (left < kTileK) v = first_codes(v, left - 16 * c);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile + (first + row) * kTileK + ((c ^ ((first + row) & 7)) << 4)),
-                         "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                         : "memory");
+            const uint32_t to = tile + (first + row) * kTileK + ((c ^ ((first + row) & 7)) << 4);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
         }
     }
 };
@@ -246,7 +246,8 @@ __device__ __forceinline__ void load_tiles(Bars<STAGES, BUFFERS>& bars, uint32_t
     while (at.next(kb)) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kRawAhead - 1) : "memory");
         const bool ok = mbar_wait_bounded(smem_u32(bars.empty) + 8 * s.at, s.phase ^ 1u, a.err);
-        if (!__all_sync(0xffffffffu, ok)) break;  // (and the warp's words are there)
+        if (!__all_sync(0xffffffffu, ok)) break;
+        __syncwarp();  // the words that the other lanes waited for are there
         const uint32_t dst = tiles + s.at * kStage;
         const int left = a.K - kb * kTileK;
         wx.shift(dst, raw + slot * kRaw, warp * RX, left, lane);
@@ -269,8 +270,7 @@ __device__ __forceinline__ void drain_tiles(Bars<STAGES, BUFFERS>& bars, int64_t
 }
 
 // A finished accumulator's columns [0, C) of this thread's row, each times its factor (given for
-// four columns), added to
-// acc; `arrive` gives it back as soon as it is in registers. Single multiply-adds: packed pairs
+// four columns), added to acc; `arrive` gives it back as soon as it is in registers. Single multiply-adds: packed pairs
 // want their operands in pairs of registers, where the loads do not put them, and cost as many
 // moves (16384 x 8192 x 8192 1375 us with them, 1100 without).
 template <int C, class Arrive, class Factor>
@@ -378,8 +378,9 @@ struct RowPieces {
     alignas(16) char at[32 * kPieceRow];
 };
 
-// A warp's 32 rows (from row0 on, a thread's sums its own row's) of 128 columns (from col on) to y. They change places in shared memory, 64 bytes of each row at a time, so that four
-// lanes store a row's 64 bytes (a thread storing its own row's pieces touches 32 lines with every
+// A warp's 32 rows (from row0 on, a thread's sums its own row's) of 128 columns (from col on) to y.
+// They change places in shared memory, 64 bytes of each row at a time, so that four lanes store
+// a row's 64 bytes (a thread storing its own row's pieces touches 32 lines with every
 // store: 2048 x 4096 x 5120 into fp32 58 us), or 32 lanes single entries side by side
 // where y's rows are off 16 bytes.
 template <int DT>
@@ -458,7 +459,8 @@ __device__ __forceinline__ void store_cluster(const MatmulArgs& a, uint32_t sums
 #pragma unroll
                 for (int i = 0; i < B; ++i) {
                     part[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (k0 + k < split && first + i * step < rows) part[i][k] = dsmem_ld_f4(from + ((first + i * step) * PITCH + 4 * lane) * 4);
+                    if (k0 + k < split && first + i * step < rows)
+                        part[i][k] = dsmem_ld_f4(from + ((first + i * step) * PITCH + 4 * lane) * 4);
                 }
             }
 #pragma unroll
@@ -479,7 +481,9 @@ __device__ __forceinline__ void store_cluster(const MatmulArgs& a, uint32_t sums
             char* out = static_cast<char*>(a.y) + ((row0 + first + i * step) * a.ldy + col) * EB;
             if (a.wide_y && col + 4 <= a.N) {
                 if constexpr (EB == 4) *reinterpret_cast<float4*>(out) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
-                else *reinterpret_cast<uint2*>(out) = make_uint2(Elem<DT>::pack2(v[i][0], v[i][1]), Elem<DT>::pack2(v[i][2], v[i][3]));
+                else
+                    *reinterpret_cast<uint2*>(out) =
+                        make_uint2(Elem<DT>::pack2(v[i][0], v[i][1]), Elem<DT>::pack2(v[i][2], v[i][3]));
             } else {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
@@ -632,7 +636,8 @@ __global__ void __launch_bounds__(tile_threads(TMA), 1)
             if (split > 1) {
 #pragma unroll
                 for (int i = 0; i < 128; i += 4)
-                    *reinterpret_cast<float4*>(sums + threadIdx.x * kWidePitch + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+                    *reinterpret_cast<float4*>(sums + threadIdx.x * kWidePitch + i) =
+                        make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
             } else if (ok) {
                 store_rows<DT>(a, pieces[warp], row - (threadIdx.x & 31), n * 128, acc);
             }
@@ -641,9 +646,8 @@ __global__ void __launch_bounds__(tile_threads(TMA), 1)
         if (split > 1) {
             cluster_sync();
             const int64_t row0 = static_cast<int64_t>(m) * 128;
-            if (ok)
-                store_cluster<DT, kWidePitch>(a, smem_u32(sums), row0, static_cast<int>(min(int64_t(128), a.M - row0)), n * 128, rank,
-                                              split, warp);
+            const int rows = static_cast<int>(min(int64_t(128), a.M - row0));
+            if (ok) store_cluster<DT, kWidePitch>(a, smem_u32(sums), row0, rows, n * 128, rank, split, warp);
             __syncwarp();
             cluster_sync();
         }
@@ -724,8 +728,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const int64_t row = static_cast<int64_t>(m) * 256 + rank * 128 + (threadIdx.x & 127);
             const int col = n * 256 + half * 128;
             float acc[128];
-            ok = add_blocks<DT, 256, BUFFERS>(a, mine, row, col, 0, a.kblocks, true, b, acc, [&](int i) { return smem_u32(bars.done) + 8 * i; },
-                                          [&](int i) { mbar_arrive_cluster(dsmem_map(smem_u32(bars.taken) + 8 * i, 0)); });
+            ok = add_blocks<DT, 256, BUFFERS>(a, mine, row, col, 0, a.kblocks, true, b, acc,
+                                              [&](int i) { return smem_u32(bars.done) + 8 * i; },
+                                              [&](int i) { mbar_arrive_cluster(dsmem_map(smem_u32(bars.taken) + 8 * i, 0)); });
             if (ok && col < a.N) store_rows<DT>(a, pieces[warp], row - (threadIdx.x & 31), col, acc);
             __syncwarp();
         }
@@ -737,12 +742,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (warp == kIssuer) tmem_free_pair(tmem, 512);
 }
 
-// Few rows of a: 128 rows of b are the accumulator's lanes, NT rows of a its columns. The
-// blocks of a cluster take a part of K each; their sums meet in shared memory and are
-// added in the blocks' order, so that the result does not depend on who was first.
 // Blocks of K whose factors lie in shared memory at a time.
 constexpr int kFactorBlocks = 16;
 
+// Few rows of a: 128 rows of b are the accumulator's lanes, NT rows of a its columns. The
+// blocks of a cluster take a part of K each; their sums meet in shared memory and are
+// added in the blocks' order, so that the result does not depend on who was first.
 template <int DT, int NT, bool TMA>
 __global__ void __launch_bounds__(tile_threads(TMA), thin_blocks(TMA))
     matmul_thin(const MatmulArgs a, const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap) {
@@ -804,8 +809,9 @@ __global__ void __launch_bounds__(tile_threads(TMA), thin_blocks(TMA))
             if (!ok) drain_tiles(bars, issued, a.err);
         } else if (warp >= 8) {
             const int thread = threadIdx.x - 256;
+            const RawSide x = {a.b, a.ldb, static_cast<int64_t>(n) * 128, a.N}, y = {a.a, a.lda, t0, a.M};
             load_tiles<STAGES, BUFFERS, 128, NT>(bars, tiles, first_tile + STAGES * kStage, a, from, thread,
-                                                 ThinBlocks{{a.b, a.ldb, static_cast<int64_t>(n) * 128, a.N}, {a.a, a.lda, t0, a.M}, from, to});
+                                                 ThinBlocks{x, y, from, to});
         }
         __syncwarp();
         if (split > 1) {

@@ -142,7 +142,8 @@ bool matmul_plan(int64_t M, int64_t N, int64_t K, bool tma, int dtype, int dev, 
     }
     const int64_t tiles = p.how == kMatmulThin ? ceil_div(M, p.n) * ceil_div(N, 128) : wide;
     // (four blocks of K at least to each in tiles of 128 x 128, whose sums take longer to meet)
-    p.cluster = static_cast<int>(std::min<int64_t>(kMatmulMostSplit, p.how == kMatmulThin ? ceil_div(K, kBlock) : std::max<int64_t>(1, K / (4 * kBlock))));
+    const int64_t parts = p.how == kMatmulThin ? ceil_div(K, kBlock) : std::max<int64_t>(1, K / (4 * kBlock));
+    p.cluster = static_cast<int>(std::min<int64_t>(kMatmulMostSplit, parts));
     while (p.cluster > 1) {
         const int fit = active_clusters(p, dev);
         if (fit < 1) return false;
@@ -229,7 +230,8 @@ extern "C" rmsnorm_status rmsnorm_quant_weight(const void* w, int64_t ldw, void*
     a.K = static_cast<int>(K);
     a.kblocks = static_cast<int>(kblocks);
     a.pow2 = pow2;
-    const bool wide = K % 8 == 0 && aligned(w, 16) && ldw * static_cast<int64_t>(s) % 16 == 0 && aligned(codes, 8) && ldcodes % 8 == 0;
+    const bool wide = K % 8 == 0 && aligned(w, 16) && ldw * static_cast<int64_t>(s) % 16 == 0 && aligned(codes, 8) &&
+                      ldcodes % 8 == 0;
     void* params[] = {&a};
     return run(weight_kernel(dtype, wide), nblocks * kblocks, weight_threads(), 0, 1, params, stream);
 }
@@ -243,8 +245,8 @@ extern "C" rmsnorm_status rmsnorm_quant_matmul(const void* a, int64_t lda, const
     if (M < 0 || M > RMSNORM_MAX_M || N < 1 || N > kMatmulMost || K < 1 || K > kMatmulMost) return RMSNORM_ERR_SHAPE;
     const size_t s = elem_bytes(dtype);
     const int64_t kblocks = ceil_div(K, kBlock), nblocks = ceil_div(N, kBlock), per_row = group ? kblocks : 1;
-    if (!pitch_ok(lda, K, M, 1) || !pitch_ok(ldas, per_row, M, 4) || !pitch_ok(ldb, K, N, 1) || !pitch_ok(ldbs, kblocks, nblocks, 4) ||
-        !pitch_ok(ldy, N, M, s))
+    if (!pitch_ok(lda, K, M, 1) || !pitch_ok(ldas, per_row, M, 4) || !pitch_ok(ldb, K, N, 1) ||
+        !pitch_ok(ldbs, kblocks, nblocks, 4) || !pitch_ok(ldy, N, M, s))
         return RMSNORM_ERR_SHAPE;
     if (M == 0) return RMSNORM_OK;
     if (!a || !a_scales || !b || !b_scales || !y) return RMSNORM_ERR_NULL;
@@ -385,7 +387,8 @@ extern "C" rmsnorm_status rmsnorm_rope_append(const rmsnorm_rope_heads* q, const
         }
         if (i > 0 && overlap(o.y, extent[i] * bytes[i], a.sets[0].y, extent[0] * bytes[0])) return RMSNORM_ERR_ARG;
         for (const void* p : {static_cast<const void*>(slots), static_cast<const void*>(positions)})
-            if (overlap(o.y, extent[i] * bytes[i], p, T * 8) || overlap(o.scales, scale_extent[i] * 4, p, T * 8)) return RMSNORM_ERR_ARG;
+            if (overlap(o.y, extent[i] * bytes[i], p, T * 8) || overlap(o.scales, scale_extent[i] * 4, p, T * 8))
+                return RMSNORM_ERR_ARG;
         if (overlap(o.y, extent[i] * bytes[i], inv_freq, rotary_dim * 4) ||
             overlap(o.scales, scale_extent[i] * 4, inv_freq, rotary_dim * 4))
             return RMSNORM_ERR_ARG;
