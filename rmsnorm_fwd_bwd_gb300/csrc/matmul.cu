@@ -146,9 +146,11 @@ __device__ __forceinline__ void issue(Bars<STAGES, BUFFERS>& bars, uint32_t tile
 // warps copies its rows' words as they are into one of three places (cp.async, three blocks ahead;
 // words without a code of the row are not read and become zeros), and then moves the rows' 16-byte
 // pieces, shifted from two words, to their swizzled places in the tile. No warp waits for
-// another's rows. Bound by shared memory (a tile is written and read twice before the matrix
-// instructions read it) and the loaders' instructions: 1001 x 5120 x 4099 107 us; 574 with single
-// loads and the shift in between, 126 with all loaders' rows behind one barrier.
+// another's rows. Bound by the L1's pipeline: a row of 144 bytes touches two lines (without the copies
+// 83 us, without the shifts 68, without both 33), and a tile goes through shared memory three times.
+// 1001 x 5120 x 4099 107 us; 574 with single loads and the shift in between, 126 with all loaders'
+// rows behind one barrier, 129 with twice the loaders in two groups that take the blocks in turn, 207 with a
+// bulk copy of each row.
 constexpr int kLoaders = 256, kLoaderWarps = kLoaders / 32;
 constexpr int kRawWords = kTileK / 16 + 1, kRawAhead = 3;
 constexpr int kRawRow = 16 * kRawWords;
