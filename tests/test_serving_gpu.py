@@ -282,7 +282,9 @@ def check_rows(got, scales, x, w, pos, R, inter, mscale, offset, dtype):
 def run_append(T, Hq, Hk, D, R, dtype, size=16, bits8=(False, False), inter=False, offset=False, mscale=1.0, order="rows",
                how="dense", pos=None, slots=None, weights=True, with_q=True, with_v=True, seed=80, in_place=False):
     q, k, v = (randn(T, h, D, dtype=dtype, seed=seed + i, scale=1.5) for i, h in enumerate((Hq, Hk, Hk)))
-    wq, wk = (randn(D, dtype=dtype, seed=seed + 3 + i, scale=0.2) + (0 if offset else 1) for i in range(2)) if weights else (None, None)
+    wq = wk = None
+    if weights:
+        wq, wk = (randn(D, dtype=dtype, seed=seed + 3 + i, scale=0.2) + (0 if offset else 1) for i in range(2))
     pages = -(-T // size) + 3
     if slots is None:
         slots = torch.randperm(pages * size, generator=torch.Generator().manual_seed(seed + 9))[:T]
@@ -329,12 +331,10 @@ def test_append_shapes(T, Hq, Hk, D, R, bits8, inter, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
-@pytest.mark.parametrize("order", ["heads first", "spaced", "keys and values"])
 @pytest.mark.parametrize("how", ["fused", "odd"])
-@pytest.mark.parametrize("bits8", [(False, False), (True, True), (True, False), (False, True)])
-def test_append_layouts(bits8, how, order, dtype):
-    if order == "keys and values" and bits8[0] != bits8[1]:
-        pytest.skip("one tensor has one type")
+@pytest.mark.parametrize("order,bits8", [(o, (k, v)) for o in ("heads first", "spaced", "keys and values") for k in (False, True)
+                                         for v in (False, True) if o != "keys and values" or k == v])  # one tensor has one type
+def test_append_layouts(order, bits8, how, dtype):
     for T, Hq, Hk, D, R in ((6, 3, 2, 64, 32), (50, 4, 1, 128, 128), (40, 3, 3, 36, 20), (40, 4, 2, 72, 40)):
         for size in (1, 7, 64):
             run_append(T, Hq, Hk, D, R, dtype, size=size, bits8=bits8, offset=True, mscale=1.25, order=order, how=how)
@@ -543,13 +543,13 @@ def test_captured_and_replayed_with_new_inputs():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(st["wc"].view(torch.uint8), other["wc"].view(torch.uint8)) and torch.equal(st["ws"], other["ws"])
-        want, err = product_bound(st["a"], product_inputs(33, 768, 512, 128, 1)[2], st["sa"], product_inputs(33, 768, 512, 128, 1)[5], 128)
+        _, _, b, _, _, sb = product_inputs(33, 768, 512, 128, 1)
+        want, err = product_bound(st["a"], b, st["sa"], sb, 128)
         ref.assert_close(st["y"], want, err + ref.rounding(want.abs() + err, torch.bfloat16), "y")
         q, k, v = st["y"].cpu().view(33, 3, 4, 64).unbind(1)
-        check_rows(st["kc"].view(80, 4, 64)[st["slots"]], st["ks"].view(80, 4)[st["slots"]], k, None, st["pos"].cpu(), 64, False, 1.0, False,
-                   "bfloat16")
-        check_rows(st["vc"].view(80, 4, 64)[st["slots"]], st["vs"].view(80, 4)[st["slots"]], v, "values", None, 64, False, 1.0, False,
-                   "bfloat16")
+        for rows, scales, heads, w in (("kc", "ks", k, None), ("vc", "vs", v, "values")):
+            check_rows(st[rows].view(80, 4, 64)[st["slots"]], st[scales].view(80, 4)[st["slots"]], heads, w, st["pos"].cpu(), 64,
+                       False, 1.0, False, "bfloat16")
 
 
 def test_two_streams_at_once():
@@ -581,3 +581,57 @@ def test_calls_that_follow_each_other_see_each_others_results():
         calls()
     torch.cuda.synchronize()
     assert same(st, want)
+
+
+def test_append_of_more_values_than_keys():
+    # heads of two kinds need not be as many
+    T, Hk, Hv, D, size = 70, 2, 5, 64, 16
+    k, v = randn(T, Hk, D, dtype="bfloat16", seed=3), randn(T, Hv, D, dtype="bfloat16", seed=4)
+    pos, slots = torch.arange(T), torch.randperm(96, generator=torch.Generator().manual_seed(5))[:T]
+    for bits8 in (False, True):
+        kc, vc = Cache(6, size, Hk, D, "bfloat16", bits8, "rows"), Cache(6, size, Hv, D, "bfloat16", bits8, "heads first")
+        kg, vg, sg, pg, fg = k.cuda(), v.cuda(), slots.cuda(), pos.cuda(), freqs(D).cuda()
+        heads = B.cache_heads(kg, None, kc.t, kc.s), B.cache_heads(vg, None, vc.t, vc.s)
+        assert B.rmsnorm_rope_append(None, *heads, sg, 6, size, pg, T, D, D, fg, 0, 1.0, EPS, "bfloat16", 0) == 0
+        kc.untouched_but(sg)
+        vc.untouched_but(sg)
+        check_rows(*kc.rows(sg), k, None, pos, D, False, 1.0, False, "bfloat16")
+        check_rows(*vc.rows(sg), v, "values", None, D, False, 1.0, False, "bfloat16")
+
+
+@pytest.mark.parametrize("M,K", [(40, 512), (150, 515), (1300, 640)])
+def test_matmul_of_rows_with_themselves(M, K):
+    # one tensor on both sides, with scales of each kind
+    a, lda = codes(M, K, 61)
+    g = torch.Generator().manual_seed(62)
+    n, k = -(-M // 128), -(-K // 128)
+    sa, sb = torch.rand(M, k, generator=g).cuda() + 0.1, torch.rand(n, k, generator=g).cuda() + 0.1
+    check_product(a, a, sa, sb, "float32", 128, product(a, lda, a, lda, sa, sb, "float32", 128))
+
+
+def test_matmul_and_append_from_two_threads():
+    import threading
+    made = [everything(s) for s in (11, 12)]
+    for calls, _ in made:
+        calls()
+    torch.cuda.synchronize()
+    want = [{n: st[n].clone() for n in OUTS} for _, st in made]
+    failed = []
+
+    def work(calls, st):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(20):
+                    for n in OUTS:
+                        st[n].zero_()
+                    calls()
+            stream.synchronize()
+        except Exception as e:  # noqa: BLE001 -- reported by the assertion below
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=m) for m in made]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed and all(same(st, w) for (_, st), w in zip(made, want))

@@ -119,8 +119,8 @@ def test_ops_pass_opcheck_and_compile_traces_them():
     pos, inv = torch.arange(T).cuda(), freqs(64).cuda()
     caches = [serving.PagedCache(4, 10, 2, 64) for _ in range(2)]
     args = (q.cuda(), k.cuda(), v.cuda(), None, None, pos, pos, inv)
-    torch.library.opcheck(torch.ops.rmsnorm_gb300.rope_append, (*args, caches[0].k, caches[0].v, None, None, False, 1.0, EPS, False),
-                          test_utils=tests)
+    torch.library.opcheck(torch.ops.rmsnorm_gb300.rope_append,
+                          (*args, caches[0].k, caches[0].v, None, None, False, 1.0, EPS, False), test_utils=tests)
     one = torch.ops.rmsnorm_gb300.rope_append(*args, caches[0].k, caches[0].v, None, None, False, 1.0, EPS, False)
     two = serving.rms_norm_rope_append(*args, caches[1].k, caches[1].v)
     assert torch.equal(one, two) and torch.equal(caches[0].k, caches[1].k) and torch.equal(caches[0].v, caches[1].v)
@@ -173,7 +173,8 @@ def test_from_the_residual_stream_to_the_cache_and_an_attention(group, bits8):
     prompt = total - 3
     queries, hs, ys = ([t] for t in step(x[:prompt], res[:prompt], pos[:prompt].cuda(), slots[:prompt]))
     # one decoding step, captured, and replayed for the three tokens
-    bx, bres, bpos, bslot = x[:1].clone(), res[:1].clone(), torch.zeros(1, dtype=torch.int64, device="cuda"), -torch.ones(1, dtype=torch.int64, device="cuda")
+    bx, bres = x[:1].clone(), res[:1].clone()
+    bpos, bslot = (torch.full((1,), n, dtype=torch.int64, device="cuda") for n in (0, -1))
     stream = torch.cuda.Stream()
     with torch.cuda.stream(stream):
         step(bx, bres, bpos, bslot)
