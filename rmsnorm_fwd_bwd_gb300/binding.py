@@ -126,13 +126,16 @@ def _addr(p):
         raise TypeError(f"cannot take the address of {type(p)}") from None
 
 
+_codes = {}  # dtype -> code, as they are asked for
+
+
 def _dtype_code(dt) -> int:
     if isinstance(dt, int):
         return dt
-    if isinstance(dt, str):
-        return DTYPE_CODES[dt]
-    name = str(dt).replace("torch.", "")
-    return DTYPE_CODES[name]
+    code = _codes.get(dt)
+    if code is None:
+        code = _codes[dt] = DTYPE_CODES[str(dt).replace("torch.", "")]
+    return code
 
 
 _raw_stream = None  # () -> the current stream's handle on the current device

@@ -96,26 +96,38 @@ bool tile_map(CUtensorMap& map, const void* p, int64_t ld, int64_t rows, int64_t
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Clusters of 1, 2, ... blocks that the device holds at a time.
+struct ClusterFits {
+    int of[kMatmulMostSplit + 1] = {};
+};
 std::mutex g_serving_mu;
-std::map<std::pair<const void*, std::pair<int, int>>, int> g_clusters;  // by (kernel, (device, blocks of a cluster))
+std::map<std::pair<const void*, int>, ClusterFits> g_clusters;  // by (kernel, device)
 
-// Clusters of the plan's blocks that the device holds at a time; 0 on failure. Fewer than its
-// SMs would hold where their groups are no multiple of a cluster: 48 clusters of 6 blocks,
-// two to an SM, do not fit 152 SMs.
-int active_clusters(const MatmulPlan& p, int dev) {
+// Those of the plan's blocks; false on failure. Fewer than the SMs would hold where their groups
+// are no multiple of a cluster: 48 clusters of 6 blocks, two to an SM, do not fit 152 SMs.
+bool cluster_fits(const MatmulPlan& p, int dev, ClusterFits& fits) {
     const void* k = matmul_kernel(p);
-    if (!k || resident_blocks(k, dev, p.threads, p.smem) < 1) return 0;
+    if (!k) return false;
     try {
-        std::lock_guard<std::mutex> lock(g_serving_mu);
-        int& n = g_clusters[{k, {dev, p.cluster}}];
-        if (n == 0) {
-            cudaLaunchAttribute attr[1];
-            const cudaLaunchConfig_t cfg = launch_config(p.cluster, p.threads, p.smem, p.cluster, nullptr, attr);
-            if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess) n = 0;
+        {
+            std::lock_guard<std::mutex> lock(g_serving_mu);
+            const auto found = g_clusters.find({k, dev});
+            if (found != g_clusters.end()) {
+                fits = found->second;
+                return true;
+            }
         }
-        return n;
+        if (resident_blocks(k, dev, p.threads, p.smem) < 1) return false;
+        for (int n = 2; n <= kMatmulMostSplit; ++n) {
+            cudaLaunchAttribute attr[1];
+            const cudaLaunchConfig_t cfg = launch_config(n, p.threads, p.smem, n, nullptr, attr);
+            if (cudaOccupancyMaxActiveClusters(&fits.of[n], k, &cfg) != cudaSuccess) return false;
+        }
+        std::lock_guard<std::mutex> lock(g_serving_mu);
+        g_clusters[{k, dev}] = fits;
+        return true;
     } catch (...) {
-        return 0;
+        return false;
     }
 }
 
@@ -144,11 +156,10 @@ bool matmul_plan(int64_t M, int64_t N, int64_t K, bool tma, int dtype, int dev, 
     // (four blocks of K at least to each in tiles of 128 x 128, whose sums take longer to meet)
     const int64_t parts = p.how == kMatmulThin ? ceil_div(K, kBlock) : std::max<int64_t>(1, K / (4 * kBlock));
     p.cluster = static_cast<int>(std::min<int64_t>(kMatmulMostSplit, parts));
-    while (p.cluster > 1) {
-        const int fit = active_clusters(p, dev);
-        if (fit < 1) return false;
-        if (tiles <= fit) break;
-        --p.cluster;
+    if (p.cluster > 1) {
+        ClusterFits fits;
+        if (!cluster_fits(p, dev, fits)) return false;
+        while (p.cluster > 1 && tiles > fits.of[p.cluster]) --p.cluster;
     }
     p.blocks = p.cluster > 1 || p.how == kMatmulThin ? tiles * p.cluster : std::min<int64_t>(tiles, sms);
     return true;
