@@ -18,7 +18,8 @@
 // an 8-bit cache 134 us (5.5 TB/s), 16384 x (16 + 2 x 4) x 256 fp16 67 us (6.0), 16384 x (32 + 2 x 8) x 128
 // bf16 67 us (6.0), 8191 x (28 + 2 x 4) x 80 bf16, a padded batch, 24 us (3.9: five of a group's eight
 // lanes have entries), 64 x (32 + 2 x 8) x 128 2.8 us in a graph; partners through shared memory (24 of 128 entries
-// rotated) 16384 x 48 heads 100 us (3.7), entry by entry 8192 x 48 x 90 92 us (1.4).
+// rotated) 16384 x 48 heads 100 us (3.7), entry by entry 8192 x 48 x 90 80 us (1.6; 92 with
+// a head's loads when its turn comes).
 #include "launch.h"
 #include "quant.cuh"
 #include "rope.cuh"
@@ -349,17 +350,26 @@ __global__ void __launch_bounds__(kFusedGroupThreads) append_pairs(const __grid_
         const int col = j & 1 ? cb[j / 2] : ca[j / 2];
         g[j] = gb && col >= 0 ? entry<DT>(gb, col) + a.one : 1.f;
     }
-    for (int h = 0; h < a.chunk; ++h) {
-        const bool live = h < w.n;
-        const char* xr = static_cast<const char*>(set.x) + (w.token * set.x_token + (w.from + h) * set.x_head) * EB;
+    const char* xr = static_cast<const char*>(set.x) + (w.token * set.x_token + w.from * set.x_head) * EB;
+    const int64_t x_step = set.x_head * EB;
+    float ahead[2 * PK];  // the next head's entries
+    const auto load = [&](const char* row, bool live) {
+#pragma unroll
+        for (int j = 0; j < 2 * PK; ++j) {
+            const int col = j & 1 ? cb[j / 2] : ca[j / 2];
+            ahead[j] = live && col >= 0 ? entry<DT>(row, col) : 0.f;
+        }
+    };
+    load(xr, w.n > 0);
+    for (int h = 0; h < a.chunk; ++h, xr += x_step) {
         float x[2 * PK];
         float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < 2 * PK; ++j) {
-            const int col = j & 1 ? cb[j / 2] : ca[j / 2];
-            x[j] = live && col >= 0 ? entry<DT>(xr, col) : 0.f;
+            x[j] = ahead[j];
             ss = fmaf(x[j], x[j], ss);
         }
+        load(xr + x_step, h + 1 < w.n);
         const float r = gb ? row_rsqrt(group_sum<L>(ss), inv_d, a.eps) : 1.f;
         float amax = 0.f;
 #pragma unroll
