@@ -137,17 +137,18 @@ class QuantLinear(torch.nn.Module):
         super().__init__()
         self.out_dtype = dtype
         self.register_buffer("weight", torch.zeros((out_features, in_features), device=device).to(CODES))
-        self.register_buffer("weight_scales", torch.ones((_blocks(out_features), _blocks(in_features)), device=device))
+        scales = torch.ones((_blocks(out_features), _blocks(in_features)), dtype=torch.float32, device=device)
+        self.register_buffer("weight_scales", scales)
         self.register_buffer("bias", torch.zeros(out_features, dtype=dtype, device=device) if bias else None)
 
     def _apply(self, fn, *args, **kwargs):
         # a change of the module's dtype is one of its output's: codes and scales keep theirs
-        keep = self.weight.dtype, self.weight_scales
+        scales = self.weight_scales
         super()._apply(lambda t: fn(t) if t.dtype != CODES else fn(t.view(torch.uint8)).view(CODES), *args, **kwargs)
         if self.weight_scales.dtype != torch.float32:
-            self.weight_scales = keep[1].to(self.weight_scales.device)
-        if self.bias is not None:
-            self.out_dtype = self.bias.dtype
+            self.weight_scales = scales.to(self.weight_scales.device)
+        # (an empty tensor of the output's dtype goes the way of the bias, which there may not be)
+        self.out_dtype = fn(torch.empty(0, dtype=self.out_dtype, device=scales.device)).dtype
         return self
 
     @classmethod

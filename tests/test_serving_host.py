@@ -177,6 +177,29 @@ def test_quant_linear_keeps_codes_and_scales_through_changes_of_type():
         serving.RMSNormQuantLinear(torch.ones(200), lin, group=64)
 
 
+def test_quant_linear_without_a_bias_changes_its_outputs_type():
+    import torch
+    from rmsnorm_fwd_bwd_gb300 import serving
+    lin = torch.nn.Sequential(serving.QuantLinear(200, 130, device="cpu"))
+    assert lin[0].out_dtype == torch.bfloat16
+    for dtype in (torch.float16, torch.float32):
+        assert lin.to(dtype)[0].out_dtype == dtype
+        assert lin[0].weight_scales.dtype == torch.float32 and lin[0].weight.dtype == serving.CODES
+    assert lin.to("meta")[0].out_dtype == torch.float32 and lin[0].weight.device.type == "meta"
+    assert lin.to_empty(device="cpu").share_memory()[0].weight.device.type == "cpu"
+
+
+def test_quant_linear_scales_are_float32_whatever_the_default_is():
+    import torch
+    from rmsnorm_fwd_bwd_gb300 import serving
+    torch.set_default_dtype(torch.bfloat16)
+    try:
+        lin, cache = serving.QuantLinear(200, 130, device="cpu"), serving.PagedCache(3, 5, 2, 8, bits8=True, device="cpu")
+    finally:
+        torch.set_default_dtype(torch.float32)
+    assert lin.weight_scales.dtype == torch.float32 and cache.k_scales.dtype == torch.float32
+
+
 def test_paged_cache_shapes():
     import torch
     from rmsnorm_fwd_bwd_gb300 import serving
