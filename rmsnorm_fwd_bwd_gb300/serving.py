@@ -144,7 +144,15 @@ class QuantLinear(torch.nn.Module):
     def _apply(self, fn, *args, **kwargs):
         # a change of the module's dtype is one of its output's: codes and scales keep theirs
         scales = self.weight_scales
-        super()._apply(lambda t: fn(t) if t.dtype != CODES else fn(t.view(torch.uint8)).view(CODES), *args, **kwargs)
+
+        def moved(t):
+            if t.dtype != CODES:
+                return fn(t)
+            codes = t.view(torch.uint8)
+            out = fn(codes)
+            # (type() turns whole numbers into another type too: the codes only follow its device)
+            return (out if out.dtype == torch.uint8 else codes.to(out.device)).view(CODES)
+        super()._apply(moved, *args, **kwargs)
         if self.weight_scales.dtype != torch.float32:
             self.weight_scales = scales.to(self.weight_scales.device)
         # (an empty tensor of the output's dtype goes the way of the bias, which there may not be)

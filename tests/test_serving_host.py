@@ -177,6 +177,23 @@ def test_quant_linear_keeps_codes_and_scales_through_changes_of_type():
         serving.RMSNormQuantLinear(torch.ones(200), lin, group=64)
 
 
+@pytest.mark.parametrize("bias", [False, True])
+def test_quant_linear_keeps_codes_and_scales_through_type(bias):
+    # Module.type converts every tensor, whole numbers too
+    import torch
+    from rmsnorm_fwd_bwd_gb300 import serving
+    for dtype in (torch.float16, torch.float32, torch.bfloat16):
+        lin = serving.QuantLinear(201, 130, bias, device="cpu")
+        lin.weight.view(torch.uint8).copy_(torch.arange(130 * 201).remainder(120).view(130, 201))
+        lin.weight_scales.copy_(torch.rand(2, 2))
+        before = lin.weight.clone().view(torch.uint8), lin.weight_scales.clone()
+        lin.type(dtype)
+        assert lin.weight.dtype == serving.CODES and lin.weight.shape == (130, 201)
+        assert torch.equal(lin.weight.view(torch.uint8), before[0])
+        assert lin.weight_scales.dtype == torch.float32 and torch.equal(lin.weight_scales, before[1])
+        assert lin.out_dtype == dtype and (lin.bias is None or lin.bias.dtype == dtype)
+
+
 def test_quant_linear_without_a_bias_changes_its_outputs_type():
     import torch
     from rmsnorm_fwd_bwd_gb300 import serving
