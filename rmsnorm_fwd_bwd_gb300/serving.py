@@ -20,7 +20,7 @@ import torch
 
 from . import binding, fused
 from .autograd import _after_op, _row_view, _rows
-from .fused import _eager, _no_tangents, _on, _tokens
+from .fused import _eager, _no_tangents, _on, _tokens, _wants_grad
 
 CALLS = {"quant_weight": 0, "quant_matmul": 0, "rope_append": 0}
 CODES = torch.float8_e4m3fn
@@ -65,7 +65,8 @@ def _(weight, pow2):
 def quant_weight(weight: torch.Tensor, pow2: bool = False) -> tuple[torch.Tensor, torch.Tensor]:
     """(codes, scales) of a weight [N, K]: float8_e4m3fn codes [N, K] with a float32 scale per
     block of 128 x 128, [ceil(N / 128), ceil(K / 128)]; ``pow2`` rounds the scales up to powers
-    of two. The values are codes * scales."""
+    of two. The values are codes * scales. They are those of the weight as it is, a parameter too:
+    no gradient goes back to it."""
     if weight.dim() != 2 or weight.shape[1] < 1:
         raise ValueError("quant_weight: weight must be 2-D with at least one column")
     _no_tangents("quant_weight", weight)
@@ -107,7 +108,7 @@ def quant_matmul(codes: torch.Tensor, scales: torch.Tensor, weight: torch.Tensor
                  bias: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """[..., N] in ``dtype``: the rows codes * scales times the weight [N, K] of ``quant_weight``,
     plus bias [N] (of ``dtype``). codes [..., K] and scales [..., ceil(K / 128)] or [..., 1] are
-    what ``rms_norm_quant`` returns with ``group`` 128 or 0. Sums in fp32."""
+    what ``rms_norm_quant`` returns with ``group`` 128 or 0. Sums in fp32. Not differentiable."""
     if codes.dtype != CODES or weight.dtype != CODES:
         raise ValueError("quant_matmul: codes and weight must be float8_e4m3fn")
     if scales.dtype != torch.float32 or weight_scales.dtype != torch.float32:
@@ -123,6 +124,8 @@ def quant_matmul(codes: torch.Tensor, scales: torch.Tensor, weight: torch.Tensor
         raise ValueError("quant_matmul: bias must be [N] of the output's dtype")
     if any(t is not None and t.device != codes.device for t in (scales, weight, weight_scales, bias)):
         raise ValueError("quant_matmul: all tensors must share a device")
+    if _wants_grad(codes, scales, weight, weight_scales, bias):
+        raise ValueError("quant_matmul is not differentiable: use torch.no_grad()")
     _no_tangents("quant_matmul", scales, weight_scales, bias)
     args = (codes, scales.detach(), weight, weight_scales.detach(), None if bias is None else bias.detach(), dtype)
     return _quant_matmul_run(*args) if _eager(codes, scales, weight, weight_scales, bias) \
@@ -309,7 +312,7 @@ def rms_norm_rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: Optional
     if any(t.device != k.device for t in changed):
         raise ValueError("rms_norm_rope_append: the caches must be on k's device")
     tensors = (q, k, v, q_weight, k_weight, inv_freq, *changed)
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+    if _wants_grad(*tensors):
         raise ValueError("rms_norm_rope_append is not differentiable: use torch.no_grad()")
     _no_tangents("rms_norm_rope_append", *(t for t in (q, k, v, q_weight, k_weight, inv_freq) if t is not None))
     args = (q, k, v, q_weight, k_weight, positions, slots, inv_freq, k_cache, v_cache, k_scales, v_scales,

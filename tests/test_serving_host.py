@@ -137,6 +137,22 @@ def test_quant_matmul_front_checks():
             serving.quant_matmul(**dict(good, **bad))
 
 
+def test_quant_matmul_wants_no_gradient(monkeypatch):
+    import torch
+    from rmsnorm_fwd_bwd_gb300 import serving
+    monkeypatch.setattr(serving, "_quant_matmul_run", lambda codes, scales, weight, *rest: torch.zeros(3, weight.shape[0]))
+    f8 = torch.float8_e4m3fn
+    good = dict(codes=torch.zeros(3, 200).to(f8), scales=torch.ones(3, 2), weight=torch.zeros(130, 200).to(f8),
+                weight_scales=torch.ones(2, 2), bias=torch.zeros(130, dtype=torch.bfloat16))
+    assert serving.quant_matmul(**good).shape == (3, 130)
+    for name in good:
+        bad = dict(good, **{name: good[name].clone().requires_grad_()})
+        with pytest.raises(ValueError, match="not differentiable"):
+            serving.quant_matmul(**bad)
+        with torch.no_grad():
+            assert not serving.quant_matmul(**bad).requires_grad
+
+
 def test_rope_append_front_checks():
     import torch
     from rmsnorm_fwd_bwd_gb300 import serving
