@@ -90,8 +90,9 @@ typedef struct {
  * rotated all the same. A slot behind the last stores nothing and sets bit 2 of the device
  * error word (rmsnorm_device_error). Slots of one call that are not negative must be
  * distinct: of rows that share one, what remains is unspecified. Rows that no slot names
- * are not touched. slots: int64[T]. q may be NULL (a prompt's keys alone), and v may be
- * (keys that serve as values). The caches may be interleaved parts of one tensor of
+ * are not touched. The queries' output may be the queries (pointer and strides) or lie between
+ * the rows of other heads; one that meets them otherwise is refused. slots: int64[T]. q may be NULL
+ * (a prompt's keys alone), and v may be (keys that serve as values). The caches may be interleaved parts of one tensor of
  * the same strides; they must not overlap the heads, the weights or each other otherwise. Values
  * are copied bit by bit where their cache has no scales.
  */

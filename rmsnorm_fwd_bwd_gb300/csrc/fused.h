@@ -138,6 +138,17 @@ void rope_lanes(int64_t D, int64_t R, int interleaved, bool wide, RopePlan& p);
 // whose rows must not overlap (tokens outside heads, or heads outside tokens); the numbers.
 bool strides_ok(int64_t token, int64_t head, int64_t heads, int64_t T, int64_t D);
 bool output_strides_ok(int64_t token, int64_t head, int64_t heads, int64_t T, int64_t D);
+// Heads [T, heads, D] in memory: where the first starts, and strides in elements.
+struct HeadsAt {
+    const void* p;
+    int64_t token, head, heads;
+};
+// Whether no two head rows of p and q (elements of `s` bytes) share a byte. Heads that lie between one
+// another are told apart by their distance within what the strides are multiples of; where that does
+// not show it, false.
+bool heads_apart(const HeadsAt& p, const HeadsAt& q, int64_t T, int64_t D, int64_t s);
+// Whether p is q: the same first row and strides.
+bool heads_same(const HeadsAt& p, const HeadsAt& q, int64_t T);
 rmsnorm_status check_rope(int nsets, int64_t T, int64_t D, int64_t R, int interleaved, float mscale, float eps,
                           rmsnorm_dtype dtype, int offset);
 

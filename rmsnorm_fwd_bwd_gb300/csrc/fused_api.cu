@@ -4,6 +4,7 @@
 #include <cmath>
 #include <map>
 #include <mutex>
+#include <numeric>
 #include <utility>
 
 #include "../../include/rmsnorm_fused.h"
@@ -298,6 +299,54 @@ bool strides_ok(int64_t token, int64_t head, int64_t heads, int64_t T, int64_t D
 bool output_strides_ok(int64_t token, int64_t head, int64_t heads, int64_t T, int64_t D) {
     return strides_ok(token, head, heads, T, D) &&
            (T <= 1 || heads <= 1 || token >= (heads - 1) * head + D || head >= (T - 1) * token + D);
+}
+
+namespace {
+
+// n pieces of `bytes`, `step` bytes apart.
+struct Pieces {
+    int64_t n, step, bytes;
+    int64_t extent() const { return (n - 1) * step + bytes; }
+    int64_t period() const { return n > 1 ? step : 0; }
+};
+
+// Whether two pieces never meet, the second `d` bytes behind the first, when both recur every g bytes.
+bool recurring_apart(int64_t p, int64_t q, int64_t d, int64_t g) {
+    const int64_t r = (d % g + g) % g;
+    return r >= p && r + q <= g;
+}
+
+bool pieces_apart(const Pieces& p, const Pieces& q, int64_t d) {
+    if (d >= p.extent() || d + q.extent() <= 0) return true;
+    const int64_t g = std::gcd(p.period(), q.period());
+    return g > 0 && recurring_apart(p.bytes, q.bytes, d, g);
+}
+
+// The same of rows of pieces, np of them p_step apart and nq q_step apart. Where a row is no longer than the
+// steps' common divisor g, a row of p can meet two rows of q alone: those at d modulo g and g before.
+bool rows_apart(int64_t np, int64_t p_step, const Pieces& p, int64_t nq, int64_t q_step, const Pieces& q, int64_t d) {
+    const int64_t g = std::gcd(np > 1 ? p_step : 0, nq > 1 ? q_step : 0);
+    if (g == 0) return pieces_apart(p, q, d);
+    if (p.extent() > g || q.extent() > g) return false;
+    const int64_t r = (d % g + g) % g;
+    return pieces_apart(p, q, r) && pieces_apart(p, q, r - g);
+}
+
+}  // namespace
+
+bool heads_apart(const HeadsAt& p, const HeadsAt& q, int64_t T, int64_t D, int64_t s) {
+    const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(q.p) - reinterpret_cast<uintptr_t>(p.p));
+    const Pieces pt = {T, p.token * s, D * s}, ph = {p.heads, p.head * s, D * s};
+    const Pieces qt = {T, q.token * s, D * s}, qh = {q.heads, q.head * s, D * s};
+    if (d >= pt.extent() + ph.extent() - D * s || d + qt.extent() + qh.extent() - D * s <= 0) return true;
+    // heads within tokens, tokens within heads, or both at once
+    if (rows_apart(T, pt.step, ph, T, qt.step, qh, d) || rows_apart(p.heads, ph.step, pt, q.heads, qh.step, qt, d)) return true;
+    const int64_t g = std::gcd(std::gcd(pt.period(), ph.period()), std::gcd(qt.period(), qh.period()));
+    return g > 0 && recurring_apart(D * s, D * s, d, g);
+}
+
+bool heads_same(const HeadsAt& p, const HeadsAt& q, int64_t T) {
+    return p.p == q.p && p.heads == q.heads && (T <= 1 || p.token == q.token) && (p.heads <= 1 || p.head == q.head);
 }
 
 rmsnorm_status check_rope(int nsets, int64_t T, int64_t D, int64_t R, int interleaved, float mscale, float eps,

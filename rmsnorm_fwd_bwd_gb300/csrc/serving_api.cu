@@ -377,9 +377,18 @@ extern "C" rmsnorm_status rmsnorm_rope_append(const rmsnorm_rope_heads* q, const
         wide = wide && aligned(t.x, 16) && aligned(t.gamma, 16) && t.x_token % words == 0 && t.x_head % words == 0 &&
                aligned(t.y, t.scales ? 8 : 16) && t.y_page % w == 0 && t.y_token % w == 0 && t.y_head % w == 0;
     }
+    // the queries' output may be the queries, or lie between other heads of their rows
+    if (q) {
+        const HeadsAt out = {q->y, q->y_token, q->y_head, q->heads};
+        for (int j = 0; j < 3; ++j) {
+            const AppendSet& t = a.sets[j];
+            const HeadsAt in = {t.x, t.x_token, t.x_head, t.heads};
+            if (t.heads && !(j == 0 && heads_same(out, in, T)) && !heads_apart(out, in, T, D, s)) return RMSNORM_ERR_ARG;
+        }
+    }
     if (!slots || !positions || !inv_freq) return RMSNORM_ERR_NULL;
     if (!aligned(slots, 8) || !aligned(positions, 8) || !aligned(inv_freq, 8)) return RMSNORM_ERR_ALIGN;
-    // what is written against what is read and written: the queries' output may be the queries
+    // what else is written against what is read and written
     for (int i = 0; i < 3; ++i) {
         const AppendSet& o = a.sets[i];
         if (!o.heads) continue;
@@ -387,10 +396,7 @@ extern "C" rmsnorm_status rmsnorm_rope_append(const rmsnorm_rope_heads* q, const
             const AppendSet& t = a.sets[j];
             if (!t.heads) continue;
             const int64_t read = ((T - 1) * t.x_token + (t.heads - 1) * t.x_head + D) * s;
-            // the queries' output may be the queries, or lie between other heads of their rows
-            if (i > 0 ? overlap(o.y, extent[i] * bytes[i], t.x, read)
-                      : o.y == t.x && !(j == 0 && (T <= 1 || o.y_token == t.x_token) && (t.heads <= 1 || o.y_head == t.x_head)))
-                return RMSNORM_ERR_ARG;
+            if (i > 0 && overlap(o.y, extent[i] * bytes[i], t.x, read)) return RMSNORM_ERR_ARG;
             if (overlap(o.y, extent[i] * bytes[i], t.gamma, D * s) || overlap(o.scales, scale_extent[i] * 4, t.x, read) ||
                 overlap(o.scales, scale_extent[i] * 4, t.gamma, D * s) ||
                 overlap(o.scales, scale_extent[i] * 4, t.y, extent[j] * bytes[j]))

@@ -96,6 +96,69 @@ def test_append_refusals(want, kw):
     assert append(**kw) == want
 
 
+@pytest.mark.parametrize("y,strides", [(0x2000000 + 2, {}), (0x2000000 + 128, {}), (0x1000000 + 128, {}), (0x1000000 + 2, {}),
+                                       (0x1000000 - 2, {}), (0x4000000 - 2, {}), (0x4000000 + 510, {}),
+                                       (0x2000000 - 4 * 256 * 2 + 2, {}), (0x1000000 + 2, dict(T=1, q_heads=1))])
+def test_append_refuses_queries_written_on_parts_of_heads(y, strides):
+    assert append(q_y=y, **strides) == ARG
+
+
+def test_append_takes_queries_written_between_the_heads_of_their_rows():
+    # (all that is wrong with these calls is that there are no positions)
+    base = 0x1000000
+
+    def rows(token, head, at, **kw):
+        """q, k and v at `at` elements of one tensor."""
+        a = {f"{n}_{f}": x for n, first in zip("qkv", at)
+             for f, x in (("x", base + 2 * first), ("x_token", token), ("x_head", head))}
+        return append(**dict(a, q_y=base + 2 * at[0], q_y_token=token, q_y_head=head, positions=None, **kw))
+    assert rows(512, 64, (0, 256, 384)) == NULL                                   # a fused projection's rows, in place
+    assert rows(512 + 40, 64, (0, 256, 384)) == NULL
+    assert rows(4 * 192, 192, (0, 64, 128), k_heads=4, v_heads=4, k_row=256, v_row=256, k_page=4096, v_page=4096) == NULL
+    assert rows(4 * 192 + 24, 192, (0, 64, 128), k_heads=4, v_heads=4, k_row=256, v_row=256, k_page=4096, v_page=4096) == NULL
+    assert rows(128, 4 * 128, (0, 64, 64 + 512)) == NULL                          # heads outside of tokens
+    assert rows(512, 64, (0, 192, 384)) == ARG
+    assert rows(4 * 192, 192, (0, 65, 128), k_heads=4, v_heads=4, k_row=256, v_row=256, k_page=4096, v_page=4096) == NULL
+    assert rows(4 * 192, 192, (0, 63, 128), k_heads=4, v_heads=4, k_row=256, v_row=256, k_page=4096, v_page=4096) == ARG
+    # the output in a gap of the queries' own rows, and behind the last row
+    assert append(q_x=base, q_x_token=1024, q_y=base + 512, q_y_token=1024, positions=None) == NULL
+    assert append(q_x=base, q_x_token=1024, q_y=base + 510, q_y_token=1024, positions=None) == ARG
+    assert append(q_y=0x1000000 + 4 * 256 * 2, positions=None) == NULL
+    assert append(q_y=0x1000000 + 4 * 256 * 2 - 2, positions=None) == ARG
+
+
+def test_append_refuses_every_output_of_the_queries_that_meets_other_heads():
+    import random
+    rng, D, base = random.Random(5), 8, 0x1000000
+
+    def lies(p, token, head, heads, T):
+        return {p + 2 * (t * token + h * head + d) for t in range(T) for h in range(heads) for d in range(D)}
+    met = 0
+    for _ in range(4000):
+        T, Hq, Hk = rng.randint(1, 5), rng.randint(1, 4), rng.randint(1, 3)
+        tok = D * rng.randint(1, 14) + rng.choice([0, 0, 1, 4])
+
+        def strides():
+            return rng.choice([(tok, rng.choice([D, 2 * D, 3 * D, D + 1])), (rng.choice([D, 2 * D]), D * T * 2 + rng.choice([0, 3])),
+                               (D * rng.randint(1, 14), rng.choice([D, 3 * D]))])
+        sy = strides()
+        sx, sk = (sy if rng.random() < 0.5 else strides() for _ in range(2))
+        y = base
+        x, k = (base + 2 * rng.choice([0, rng.randint(-150, 150), D * rng.randint(-20, 20)]) for _ in range(2))
+        st = append(v=False, T=T, D=D, rotary_dim=D, q_x=x, q_x_token=sx[0], q_x_head=sx[1], q_heads=Hq, q_y=y, q_y_token=sy[0],
+                    q_y_head=sy[1], k_x=k, k_x_token=sk[0], k_x_head=sk[1], k_heads=Hk, k_head=D, k_row=D * Hk,
+                    k_page=D * Hk * 16, positions=None)
+        if st == SHAPE:
+            continue
+        assert st in (ARG, NULL)
+        out = lies(y, *sy, Hq, T)
+        in_place = x == y and (T == 1 or sx[0] == sy[0]) and (Hq == 1 or sx[1] == sy[1])
+        if (not in_place and out & lies(x, *sx, Hq, T)) or out & lies(k, *sk, Hk, T):
+            met += 1
+            assert st == ARG, (T, Hq, Hk, sy, sx, sk, x - y, k - y)
+    assert met > 500
+
+
 def test_append_wants_keys():
     assert B.rmsnorm_rope_append(None, None, None, 0x1000, 1, 1, 0x2000, 1, 64, 64, 0x3000, 0, 1.0, 1e-6, 2, 0, 0) == NULL
 
