@@ -19,7 +19,8 @@
  * dy or dh, rotated heads on the heads). No other overlap is allowed; two outputs at
  * one address whose values differ are refused, and so are an output's rows that overlap
  * and an output that starts where an input of another pitch, the weight (of several rows) or
- * another set's heads do.
+ * another set's heads do. Outputs of heads that meet an input or another output in part are
+ * refused wherever they start; those that lie between other heads' rows are not.
  */
 #ifndef RMSNORM_FUSED_H
 #define RMSNORM_FUSED_H

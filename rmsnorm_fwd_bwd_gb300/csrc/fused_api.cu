@@ -376,17 +376,21 @@ void rope_lanes(int64_t D, int64_t R, int interleaved, bool wide, RopePlan& p) {
 
 namespace {
 
-// Whether a set's output, where it lies on an input of a set, is that set's heads, of the same
-// strides.
-bool same_heads(const RopeArgs& a, int64_t T, int nsets) {
-    for (int i = 0; i < nsets; ++i)
+// Whether a set's output, where it meets an input of a set, is that set's heads, of the same
+// strides (or its weight, of one row), and whether it keeps out of the other set's output.
+bool outputs_ok(const RopeArgs& a, int64_t T, int64_t D, int64_t bytes, int nsets) {
+    for (int i = 0; i < nsets; ++i) {
+        const RopeSet& o = a.set[i];
+        const HeadsAt out = {o.y, o.y_token, o.y_head, o.heads};
         for (int j = 0; j < nsets; ++j) {
-            const RopeSet &o = a.set[i], &s = a.set[j];
-            if ((o.y == s.gamma && !(i == j && T <= 1 && s.heads <= 1)) ||
-                (o.y == s.x && !(i == j && (T <= 1 || o.y_token == s.x_token) && (s.heads <= 1 || o.y_head == s.x_head))) ||
-                (o.y == s.dy && !(i == j && (T <= 1 || o.y_token == s.dy_token) && (s.heads <= 1 || o.y_head == s.dy_head))))
-                return false;
+            const RopeSet& s = a.set[j];
+            const HeadsAt x = {s.x, s.x_token, s.x_head, s.heads}, dy = {s.dy, s.dy_token, s.dy_head, s.heads};
+            const HeadsAt gamma = {s.gamma, 0, 0, 1}, other = {s.y, s.y_token, s.y_head, s.heads};
+            for (const HeadsAt* in : {&x, &dy, &gamma})
+                if (in->p && !(i == j && heads_same(out, *in, T)) && !heads_apart(out, *in, T, D, bytes)) return false;
+            if (i < j && !heads_apart(out, other, T, D, bytes)) return false;
         }
+    }
     return true;
 }
 
@@ -659,7 +663,7 @@ extern "C" rmsnorm_status rmsnorm_rope_fwd(const rmsnorm_rope_heads* sets, int n
     }
     if (heads > RMSNORM_ROPE_MAX_HEADS) return RMSNORM_ERR_SHAPE;
     if (T == 0) return RMSNORM_OK;
-    if (!distinct({a.set[0].y, a.set[1].y}) || !same_heads(a, T, nsets)) return RMSNORM_ERR_ARG;
+    if (!outputs_ok(a, T, D, s, nsets)) return RMSNORM_ERR_ARG;
     if (!positions || !inv_freq) return RMSNORM_ERR_NULL;
     if (!aligned(positions, 8) || !aligned(inv_freq, 8)) return RMSNORM_ERR_ALIGN;
     a.nsets = nsets;
@@ -729,7 +733,7 @@ extern "C" rmsnorm_status rmsnorm_rope_bwd(const rmsnorm_rope_heads_bwd* sets, i
     }
     if (heads > RMSNORM_ROPE_MAX_HEADS) return RMSNORM_ERR_SHAPE;
     if (nsets == 2 && sets[0].gamma && sets[1].gamma && sets[0].dgamma == sets[1].dgamma) return RMSNORM_ERR_ARG;
-    if (T > 0 && (!distinct({a.set[0].y, a.set[1].y}) || !same_heads(a, T, nsets))) return RMSNORM_ERR_ARG;
+    if (T > 0 && !outputs_ok(a, T, D, s, nsets)) return RMSNORM_ERR_ARG;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     a.nsets = nsets;
     a.heads = static_cast<int>(heads);

@@ -458,3 +458,61 @@ def test_rope_module_from_the_meta_device():
     assert m.inv_freq.is_meta
     m = m.to_empty(device="cpu")
     assert m.inv_freq.tolist() == fused.rope_frequencies(8, 500.0, device="cpu")[0].tolist()
+
+
+def test_rotated_heads_refuse_outputs_on_parts_of_heads():
+    base, far = 0x100000, 0x900000
+
+    def fwd(*sets, T=4):
+        sets = (B.RopeHeads * len(sets))(*(B.RopeHeads(*s) for s in sets))
+        return B.rmsnorm_rope_fwd(sets, None, T, 64, 64, 0x7000, 0, 1.0, 1e-6, 2, 0)
+
+    def bwd(*sets, T=4):
+        sets = (B.RopeHeadsBwd * len(sets))(*(B.RopeHeadsBwd(*s) for s in sets))
+        return B.rmsnorm_rope_bwd(sets, None, T, 64, 64, 0x7000, 0, 1.0, 1e-6, 2, 0, 0x8000000, 1 << 24)
+    # (x, strides, weight, y, strides, heads); all that is wrong with what is taken is that there are no positions
+    for at, want in ((0, NULL), (2, ARG), (-2, ARG), (128, ARG), (1022, ARG), (1024, NULL), (-1024, NULL), (-1022, ARG)):
+        assert fwd((base, 128, 64, None, base + at, 128, 64, 2)) == want
+        assert bwd((base, 128, 64, far, 128, 64, far + 0x1000, base + at, 128, 64, far + 0x2000, 2)) == want       # on dy
+        assert bwd((far, 128, 64, base, 128, 64, far + 0x1000, base + at, 128, 64, far + 0x2000, 2)) == want       # on x
+    assert fwd((far, 128, 64, base, base - 64, 128, 64, 2)) == ARG                                            # on the weight
+    assert fwd((far, 64, 64, base, base, 64, 64, 1), T=1) == NULL and fwd((far, 64, 64, base, base + 2, 64, 64, 1), T=1) == ARG
+    # queries and keys of one tensor, in place: side by side, interleaved, heads outside of tokens; and not quite so
+    for token, head, k, want in ((256, 64, 128, NULL), (260, 64, 128, NULL), (256, 64, 127, ARG), (256, 128, 64, NULL),
+                                 (264, 128, 64, NULL), (264, 128, 63, ARG), (64, 256, 512, NULL), (128, 512, 64, NULL),
+                                 (128, 512, 63, ARG)):
+        q, k = (base, token, head), (base + 2 * k, token, head)
+        assert fwd((*q, None, *q, 2), (*k, None, *k, 2)) == want
+        assert bwd((*q, None, 0, 0, None, *q, None, 2), (*k, None, 0, 0, None, *k, None, 2)) == want
+        # out of place, into a tensor of the same strides
+        assert fwd((far, 128, 64, None, *q, 2), (far + 0x1000, 128, 64, None, *k, 2)) == want
+
+
+def test_rotated_heads_refuse_every_output_that_meets_other_heads():
+    import random
+    rng, D, base = random.Random(6), 8, 0x1000000
+
+    def lies(p, token, head, heads, T):
+        return {p + 2 * (t * token + h * head + d) for t in range(T) for h in range(heads) for d in range(D)}
+    met = 0
+    for _ in range(3000):
+        T, H = rng.randint(1, 5), rng.randint(1, 4)
+        tok = D * rng.randint(1, 14) + rng.choice([0, 0, 1, 4])
+
+        def strides():
+            return rng.choice([(tok, rng.choice([D, 2 * D, 3 * D, D + 1])), (rng.choice([D, 2 * D]), D * T * 2 + rng.choice([0, 3])),
+                               (D * rng.randint(1, 14), rng.choice([D, 3 * D]))])
+        sy = strides()
+        sx = sy if rng.random() < 0.5 else strides()
+        x = base + 2 * rng.choice([0, rng.randint(-150, 150), D * rng.randint(-20, 20)])
+        sets = (B.RopeHeads * 1)(B.RopeHeads(x, *sx, None, base, *sy, H))
+        st = B.rmsnorm_rope_fwd(sets, None, T, D, D, 0x7000, 0, 1.0, 1e-6, 2, 0)
+        if st == SHAPE:
+            continue
+        in_place = x == base and (T == 1 or sx[0] == sy[0]) and (H == 1 or sx[1] == sy[1])
+        if in_place:
+            assert st == NULL
+        elif lies(base, *sy, H, T) & lies(x, *sx, H, T):
+            met += 1
+            assert st == ARG, (T, H, sy, sx, x - base)
+    assert met > 300
