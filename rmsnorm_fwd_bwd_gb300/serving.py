@@ -215,13 +215,19 @@ class PagedCache:
         self.k_scales, self.v_scales = (rows(dtype=torch.float32) if bits8 else None for _ in range(2))
 
     def rows(self, slots: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
-        """Keys and values [..., heads, D] of the given slots, in float32 of an 8-bit cache."""
-        page, row = slots // self.k.shape[1], slots % self.k.shape[1]
+        """Keys and values [..., heads, D] of the given slots, in float32 of an 8-bit cache. Slots
+        below 0 (padded tokens) and behind the last, which have no row, give zeros."""
+        none = (slots < 0) | (slots >= self.k.shape[0] * self.k.shape[1])
+        at = slots.masked_fill(none, 0)
+        page, row = at // self.k.shape[1], at % self.k.shape[1]
+        none = none.unsqueeze(-1).unsqueeze(-1)
 
         def read(cache, scales):
             if scales is None:
-                return cache[page, row]
-            return cache.view(torch.uint8)[page, row].view(CODES).float() * scales[page, row].unsqueeze(-1)
+                got = cache[page, row]
+            else:
+                got = cache.view(torch.uint8)[page, row].view(CODES).float() * scales[page, row].unsqueeze(-1)
+            return got.masked_fill(none, 0.0)
         return read(self.k, self.k_scales), read(self.v, self.v_scales)
 
 

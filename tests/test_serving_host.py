@@ -309,3 +309,27 @@ def test_paged_cache_shapes():
         assert (k[0] == 3.0).all() and (k[1] == 0.0).all() and (v == 0.0).all()
     c = serving.PagedCache(3, 5, 2, 8, dtype=torch.float16, device="cpu")
     assert c.k.dtype == torch.float16 and c.k_scales is None
+
+
+@pytest.mark.parametrize("bits8", [False, True])
+@pytest.mark.parametrize("first", [False, True])
+def test_paged_cache_rows_of_slots_without_one_are_zeros(bits8, first):
+    import torch
+    from rmsnorm_fwd_bwd_gb300 import serving
+    c = serving.PagedCache(3, 5, 2, 8, dtype=torch.float32, bits8=bits8, heads_first=first, device="cpu")
+    for cache, scales, value in ((c.k, c.k_scales, 1.0), (c.v, c.v_scales, 2.0)):
+        if bits8:
+            cache.view(torch.uint8).fill_(0x38)             # 1.0
+            scales.fill_(value)
+            scales[2, 4] = float("nan")
+        else:
+            cache.fill_(value)
+            cache[2, 4] = float("nan")
+    slots = torch.tensor([[0, -1, 13], [15, -(1 << 40), 1 << 40]])
+    for rows, value in zip(c.rows(slots), (1.0, 2.0)):
+        assert rows.shape == (2, 3, 2, 8)
+        assert (rows[0, 0] == value).all() and (rows[0, 2] == value).all()
+        assert (rows[0, 1] == 0.0).all() and (rows[1] == 0.0).all()
+    k, _ = c.rows(torch.tensor(-1))
+    assert k.shape == (2, 8) and (k == 0.0).all()
+    assert torch.isnan(c.rows(torch.tensor([14]))[0]).all() and c.rows(torch.zeros(0, dtype=torch.int64))[0].shape == (0, 2, 8)
