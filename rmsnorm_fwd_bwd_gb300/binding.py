@@ -77,6 +77,7 @@ def _load():
                                              ctypes.POINTER(ctypes.c_int64)]),
             "rmsnorm_bwd_static_scratch": (I, [P, P, P, P, P, P, I64, I64, I, I, P]),
             "rmsnorm_selftest_wait_timeout": (I, [ctypes.c_uint32, P]),
+            "rmsnorm_selftest_matmul_gives_up": (I, [I]),
             "rmsnorm_fwd_strided": (I, [P, I64, P, P, I64, P, I64, I64, F, I, I, P]),
             "rmsnorm_bwd_strided": (I, [P, I64, P, I64, P, P, P, I64, P, I64, I64, I, I, P, SZ, P]),
             "layernorm_fwd": (I, [P, I64, P, P, P, I64, P, P, I64, I64, F, I, P]),
@@ -377,6 +378,11 @@ def rmsnorm_device_error(clear: bool = False) -> int:
 
 def rmsnorm_selftest_wait_timeout(polls, stream=None) -> int:
     return _load().rmsnorm_selftest_wait_timeout(int(polls), _stream(stream))
+
+
+def rmsnorm_selftest_matmul_gives_up(rank) -> int:
+    """Debug builds: the block of each cluster that acts as if a wait had given up (see csrc/tuning.h)."""
+    return _load().rmsnorm_selftest_matmul_gives_up(int(rank))
 
 
 def rmsnorm_describe_plan(pass_, M, N, dtype, aligned16=True) -> str:

@@ -77,10 +77,11 @@ template <int N> struct Ring {
 };
 
 // The barriers of a block: ring places filled and emptied, accumulators filled and emptied,
-// and one for the instructions under way when a wait has given up.
+// and one for the instructions under way when a wait has given up; and whether one of the warps that
+// add up has, for the other blocks of a cluster.
 template <int STAGES, int BUFFERS> struct Bars {
     uint64_t full[STAGES], empty[STAGES], done[BUFFERS], taken[BUFFERS], drain;
-    uint32_t tmem;
+    uint32_t tmem, gave_up;
     __device__ __forceinline__ void init(int producers, int takers) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(smem_u32(&full[i]), producers);
@@ -91,7 +92,18 @@ template <int STAGES, int BUFFERS> struct Bars {
             mbar_init(smem_u32(&taken[i]), takers);
         }
         mbar_init(smem_u32(&drain), 1);
+        gave_up = 0;
         fence_mbar_init();
+    }
+    // Before the cluster's sums meet: whether this warp's are whole. In debug builds those of a
+    // chosen block's first warp never are.
+    __device__ __forceinline__ bool whole(const MatmulArgs& a, int rank, int warp, bool ok) {
+        if (kDebugReads && rank == a.give_up && warp == 0) {
+            if ((threadIdx.x & 31) == 0) atomicOr(a.err, kDevErrWaitTimeout);
+            ok = false;
+        }
+        if (!ok && (threadIdx.x & 31) == 0) gave_up = 1;
+        return ok;
     }
 };
 
@@ -438,12 +450,14 @@ struct Share {
 // The cluster's sums [rows][PITCH], at one place in its blocks' shared memory, added in the blocks'
 // order and stored, four warps of a block to every split-th four rows: row r is row0 + r of y,
 // its 128 columns are those from col0 on, four to a lane. Four rows and four blocks at a time,
-// whose loads are under way together.
+// whose loads are under way together. Nothing is stored where a block's `gave_up` is set: its sums
+// lack blocks of K.
 template <int DT, int PITCH>
-__device__ __forceinline__ void store_cluster(const MatmulArgs& a, uint32_t sums, int64_t row0, int rows, int col0, int rank,
-                                              int split, int warp) {
+__device__ __forceinline__ void store_cluster(const MatmulArgs& a, uint32_t gave_up, uint32_t sums, int64_t row0, int rows,
+                                              int col0, int rank, int split, int warp) {
     constexpr int EB = Elem<DT>::kBytes, B = 4;
     const int lane = threadIdx.x & 31, col = col0 + 4 * lane;
+    const uint32_t lacking = lane < split ? dsmem_ld_u32(dsmem_map(gave_up, lane)) : 0u;
     float bias[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) bias[i] = a.bias && col + i < a.N ? Elem<DT>::ld(a.bias, col + i) : 0.f;
@@ -475,6 +489,7 @@ __device__ __forceinline__ void store_cluster(const MatmulArgs& a, uint32_t sums
                     v[i][3] += part[i][k].w;
                 }
         }
+        if (__any_sync(0xffffffffu, lacking != 0u)) return;
 #pragma unroll
         for (int i = 0; i < B; ++i) {
             if (first + i * step >= rows) break;
@@ -646,10 +661,12 @@ __global__ void __launch_bounds__(tile_threads(TMA), 1)
             __syncwarp();
         }
         if (split > 1) {
+            ok = bars.whole(a, rank, warp, ok);
+            __syncwarp();
             cluster_sync();
             const int64_t row0 = static_cast<int64_t>(m) * 128;
             const int rows = static_cast<int>(min(int64_t(128), a.M - row0));
-            if (ok) store_cluster<DT, kWidePitch>(a, smem_u32(sums), row0, rows, n * 128, rank, split, warp);
+            if (ok) store_cluster<DT, kWidePitch>(a, smem_u32(&bars.gave_up), smem_u32(sums), row0, rows, n * 128, rank, split, warp);
             __syncwarp();
             cluster_sync();
         }
@@ -877,9 +894,10 @@ __global__ void __launch_bounds__(tile_threads(TMA), thin_blocks(TMA))
         } else {
 #pragma unroll
             for (int j = 0; j < NT; ++j) sums[j * 128 + threadIdx.x] = acc[j];
+            ok = bars.whole(a, rank, warp, ok);
             __syncwarp();
             cluster_sync();
-            if (ok) store_cluster<DT, 128>(a, smem_u32(sums), t0, rows, n * 128, rank, split, warp);
+            if (ok) store_cluster<DT, 128>(a, smem_u32(&bars.gave_up), smem_u32(sums), t0, rows, n * 128, rank, split, warp);
             __syncwarp();
             cluster_sync();
         }

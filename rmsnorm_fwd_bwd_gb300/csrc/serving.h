@@ -28,6 +28,7 @@ struct MatmulArgs {
     int wide_y;        // y's rows on 16-byte boundaries
     int wide_bias;     // there is a bias, and it starts on one
     uint32_t* err;     // device error word
+    int give_up;       // debug builds: block of each cluster that acts as if a wait had given up, or -1
 };
 
 // Most blocks that share K: the portable size of a cluster.

@@ -1,6 +1,7 @@
 // serving_api.cu -- the entry points of include/rmsnorm_serving.h: argument checks, launch
 // shapes and launches of the kernels in matmul.cu, weight.cu and append.cu.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <map>
 #include <mutex>
@@ -11,6 +12,7 @@
 #include "fused.h"
 #include "launch.h"
 #include "serving.h"
+#include "tuning.h"
 
 namespace rmsnorm {
 namespace {
@@ -130,6 +132,8 @@ bool cluster_fits(const MatmulPlan& p, int dev, ClusterFits& fits) {
         return false;
     }
 }
+
+std::atomic<int> g_give_up{-1};  // rmsnorm_selftest_matmul_gives_up
 
 // How a product is cut; false on failure. Few rows of a: b's rows in the accumulators' lanes.
 // More: 128 x 128 by single blocks or 256 x 256 by pairs, whichever takes less, a turn of
@@ -299,6 +303,7 @@ extern "C" rmsnorm_status rmsnorm_quant_matmul(const void* a, int64_t lda, const
     t.n_tiles = static_cast<int>(ceil_div(N, tile_rows_b(p)));
     t.wide_y = aligned(y, 16) && ldy * static_cast<int64_t>(s) % 16 == 0;
     t.wide_bias = bias && aligned(bias, 16);
+    t.give_up = g_give_up.load(std::memory_order_relaxed);
     t.err = device_error_word();
     if (!t.err) return RMSNORM_ERR_CUDA;
     CUtensorMap amap = {}, bmap = {};
@@ -306,6 +311,17 @@ extern "C" rmsnorm_status rmsnorm_quant_matmul(const void* a, int64_t lda, const
         return RMSNORM_ERR_CUDA;
     void* params[] = {&t, &amap, &bmap};
     return run(matmul_kernel(p), p.blocks, p.threads, p.smem, p.cluster, params, stream);
+}
+
+extern "C" rmsnorm_status rmsnorm_selftest_matmul_gives_up(int rank) {
+#ifdef RMSNORM_DEBUG
+    if (rank < -1 || rank >= kMatmulMostSplit) return RMSNORM_ERR_ARG;
+    g_give_up.store(rank, std::memory_order_relaxed);
+    return RMSNORM_OK;
+#else
+    (void)rank;
+    return RMSNORM_ERR_UNSUPPORTED;
+#endif
 }
 
 extern "C" rmsnorm_status rmsnorm_rope_append(const rmsnorm_rope_heads* q, const rmsnorm_cache_heads* k,

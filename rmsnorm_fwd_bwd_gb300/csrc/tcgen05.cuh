@@ -94,6 +94,11 @@ __device__ __forceinline__ float4 dsmem_ld_f4(uint32_t addr) {
                  : "memory");
     return v;
 }
+__device__ __forceinline__ uint32_t dsmem_ld_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
 
 // An arrival on a barrier of another block of the cluster (or this one) that hands no memory
 // over but tensor memory whose loads are done, and so is relaxed: a release to the cluster waits for

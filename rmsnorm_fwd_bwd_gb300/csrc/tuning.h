@@ -49,6 +49,13 @@ rmsnorm_status rmsnorm_set_row_pool_shape(int head_pct, int head_pct_few, int le
 rmsnorm_status rmsnorm_row_pool_layout(int64_t M, int64_t G, int64_t* head, int64_t* nseg);
 rmsnorm_status rmsnorm_row_pool_segment(int64_t M, int64_t G, int64_t k, int64_t* first, int64_t* last);
 
+/*
+ * Debug builds (RMSNORM_ERR_UNSUPPORTED in others): in later products whose blocks of a cluster
+ * share K, the block of this rank in each cluster acts as if one of its warps had given up a
+ * wait: the error word's bit 0, sums that do not count. -1 (the default): none. Process-wide.
+ */
+rmsnorm_status rmsnorm_selftest_matmul_gives_up(int rank);
+
 #ifdef __cplusplus
 }
 #endif

@@ -159,6 +159,10 @@ def test_append_refuses_every_output_of_the_queries_that_meets_other_heads():
     assert met > 500
 
 
+def test_only_debug_builds_let_a_product_give_up():
+    assert B.rmsnorm_selftest_matmul_gives_up(0) == B.rmsnorm_selftest_matmul_gives_up(-1) == 7   # RMSNORM_ERR_UNSUPPORTED
+
+
 def test_append_wants_keys():
     assert B.rmsnorm_rope_append(None, None, None, 0x1000, 1, 1, 0x2000, 1, 64, 64, 0x3000, 0, 1.0, 1e-6, 2, 0, 0) == NULL
 
