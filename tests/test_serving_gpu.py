@@ -635,3 +635,20 @@ def test_matmul_and_append_from_two_threads():
     for t in threads:
         t.join()
     assert not failed and all(same(st, w) for (_, st), w in zip(made, want))
+
+
+@pytest.mark.parametrize("M,N,side,pitch", [(130, 300, "a", (1 << 25) + 3), (20, 200, "b", (1 << 25) + 3),   # the loaders' rows
+                                            (9, 130, "b", 1 << 25), (130, 300, "a", 1 << 25),                 # by TMA
+                                            (1300, 2000, "a", 1 << 22)])                                      # pairs
+def test_matmul_of_an_operand_of_more_than_2_to_the_32_bytes(M, N, side, pitch):
+    K = 260
+    a, lda, b, ldb, sa, sb = product_inputs(M, N, K, 128, 71, "padded")
+    dense = a if side == "a" else b
+    rows = dense.shape[0]
+    assert (rows - 1) * pitch > 1 << 32
+    far = torch.empty(rows * pitch, dtype=torch.uint8, device="cuda").as_strided((rows, K), (pitch, 1))
+    far.copy_(dense.view(torch.uint8))
+    far = far.view(F8)
+    y = product(far, pitch, b, ldb, sa, sb, "float32", 128) if side == "a" \
+        else product(a, lda, far, pitch, sa, sb, "float32", 128)
+    check_product(a, b, sa, sb, "float32", 128, y)

@@ -211,3 +211,74 @@ def test_from_the_residual_stream_to_the_cache_and_an_attention(group, bits8):
     att = torch.einsum("qhd,khd->hqk", queries.double(), rk) * D ** -0.5
     att = att.masked_fill(torch.ones(total, total, device="cuda").triu(1).bool(), float("-inf")).softmax(-1)
     assert torch.isfinite(torch.einsum("hqk,khd->qhd", att, rv)).all()
+
+
+@pytest.mark.parametrize("group", [0, 128])
+def test_the_product_passes_opcheck_and_compiles_without_breaks(group):
+    a, _, b, _, sa, sb = product_inputs(24, 130, 384, group, 90)
+    a, b = a.contiguous(), b.contiguous()
+    bias = randn(130, dtype="bfloat16", seed=91).cuda()
+    before = [t.view(torch.uint8).clone() for t in (a, sa, b, sb, bias)]
+    for extra in (None, bias):
+        # (the check of the schema multiplies its tensors, which torch does not do in e4m3: by hand below)
+        torch.library.opcheck(torch.ops.rmsnorm_gb300.quant_matmul, (a, sa, b, sb, extra, torch.bfloat16),
+                              test_utils=("test_faketensor",))
+    assert all(torch.equal(t.view(torch.uint8), u) for t, u in zip((a, sa, b, sb, bias), before))
+
+    def f(codes, scales):
+        return serving.quant_matmul(codes, scales, b, sb, bias) + 1
+    compiled = torch.compile(f, backend="aot_eager", fullgraph=True)
+    assert torch.equal(compiled(a, sa), f(a, sa))
+    lead = a.view(4, 6, 384), sa.view(4, 6, -1)
+    assert torch.equal(compiled(*lead), f(*lead))
+
+
+def test_a_weight_compiles_without_breaks():
+    w = randn(130, 200, dtype="bfloat16", seed=92).cuda()
+
+    def f(w):
+        codes, scales = serving.quant_weight(w * 2)
+        return codes.view(torch.uint8), scales + 1
+    for got, want in zip(torch.compile(f, backend="aot_eager", fullgraph=True)(w), f(w)):
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("bits8", [False, True])
+@pytest.mark.parametrize("heads_first", [False, True])
+def test_an_append_through_modules_compiles_without_breaks(bits8, heads_first):
+    N, Hq, Hk, D = 256, 4, 2, 64
+    torch.manual_seed(4)
+    lin = serving.QuantLinear.from_linear(torch.nn.Linear(N, (Hq + 2 * Hk) * D, device="cuda", dtype=torch.bfloat16))
+    layer = serving.RMSNormQuantLinear(torch.ones(N, dtype=torch.bfloat16, device="cuda"), lin)
+    rope = fused.RMSNormRope(D, 32, dtype=torch.bfloat16, device="cuda")
+    caches = [serving.PagedCache(4, 10, Hk, D, bits8=bits8, heads_first=heads_first) for _ in range(2)]
+
+    def step(x, pos, slots, cache):
+        y, h = layer(x)
+        q, k, v = (t.unflatten(-1, (-1, D)) for t in y.split([Hq * D, Hk * D, Hk * D], dim=-1))
+        return rope.append(q, k, v, pos, slots, cache) + 1, h
+    compiled = torch.compile(step, backend="aot_eager", fullgraph=True)
+    x, pos = randn(7, N, dtype="bfloat16", seed=93).cuda(), torch.arange(7).cuda() * 3
+    with torch.no_grad():
+        for shift in (0, 9):                                # the second call into what the first has left
+            slots = torch.tensor([3, -1, 39, 12, 0, 11, 25]).cuda()
+            slots = torch.where(slots < 0, slots, (slots + shift) % 40)
+            want, got = (f(x + shift, pos, slots, c) for f, c in ((step, caches[0]), (compiled, caches[1])))
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+    one, two = caches
+    bits = lambda t: t.view(torch.uint8) if bits8 else t
+    assert torch.equal(bits(one.k), bits(two.k)) and torch.equal(bits(one.v), bits(two.v))
+    assert (bits(one.k) != 0).any()
+    if bits8:
+        assert torch.equal(one.k_scales, two.k_scales) and torch.equal(one.v_scales, two.v_scales)
+
+
+def test_rows_of_slots_without_one_are_zeros_on_the_gpu():
+    T, q, k, v = step_inputs()
+    cache = serving.PagedCache(4, 10, 2, 64)
+    pos = torch.arange(T).cuda()
+    slots = torch.where(pos % 3 == 1, -1, pos + 40 - T)     # the last row holds a token
+    serving.rms_norm_rope_append(None, k.cuda(), v.cuda(), None, None, pos, slots, freqs(64).cuda(), cache.k, cache.v)
+    rk, rv = cache.rows(torch.cat([slots, torch.tensor([40, 1 << 40]).cuda()]))
+    stored = torch.cat([slots >= 0, torch.zeros(2, dtype=torch.bool, device="cuda")])
+    assert torch.equal(rv[stored].cpu(), v[(slots >= 0).cpu()]) and (rk[~stored] == 0).all() and (rv[~stored] == 0).all()
