@@ -160,8 +160,8 @@ rmsnorm_status rmsnorm_bwd_static_scratch(const void* dy, const void* x, const v
 
 /*
  * Strided forms: the same operations on row-major tensors whose consecutive
- * rows are ld* elements apart (ld* >= N; the gaps between rows are neither read
- * nor written), e.g. a view of the first N columns of a wider matrix. With
+ * rows are ld* elements apart (ld* >= N; the gaps between rows are not written and
+ * what they hold does not matter), e.g. a view of the first N columns of a wider matrix. With
  * ld* = N they are rmsnorm_fwd / rmsnorm_bwd. The fast paths need every row to
  * start on the same 16-byte boundary pattern: 16-byte aligned rows and pitches
  * take the TMA (or, up to 2 KB, the lane-group) path; x and dy rows at equal

@@ -9,10 +9,10 @@
  * Conventions are those of rmsnorm.h: device pointers on the current device, the
  * caller owns every buffer and the stream, no allocation, all checks on the host
  * before any launch, fp32 arithmetic whatever the I/O dtype, status codes. Rows
- * are ld* elements apart (ld* >= N; the gaps are neither read nor written). Any
- * element-aligned pointer and pitch works; the wide path wants every row to start
- * on a 16-byte boundary and N to be a multiple of 8, other rows are moved in
- * 16-byte words that are shifted together.
+ * are ld* elements apart (ld* >= N; the gaps are not written and what they hold does not
+ * matter). Any element-aligned pointer and pitch works; the wide path wants every row to start
+ * on a 16-byte boundary and N to be a multiple of 8, other rows are moved in 16-byte words (read
+ * whole where they have a byte of the row) that are shifted together.
  *
  * In place: every row is read before it is written, so an output may be an input
  * of the same shape, dtype, pointer and pitch (h on residual, y on x, dresidual on

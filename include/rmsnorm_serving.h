@@ -10,8 +10,9 @@
  * Conventions are those of rmsnorm.h: device pointers on the current device, the caller owns
  * every buffer and the stream, no allocation, no workspace, all checks on the host before any
  * launch, status codes. None of them has a gradient. Rows are ld* elements apart (ld* >= the
- * row; the gaps are neither read nor written), and any element-aligned pointer and pitch
- * works; the fast paths want rows on 16-byte boundaries.
+ * row; the gaps are not written and what they hold does not matter), and any element-aligned
+ * pointer and pitch works; the fast paths want rows on 16-byte boundaries. Other rows are read in
+ * whole 16-byte words, each with a byte of the row at least.
  */
 #ifndef RMSNORM_SERVING_H
 #define RMSNORM_SERVING_H

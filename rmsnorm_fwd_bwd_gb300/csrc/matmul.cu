@@ -17,13 +17,13 @@
 // take, are copied as they lie by eight warps, which shift them into the tiles.
 //
 // Measured on GB300 (device copy 6.79 TB/s; bf16 products of the library 1.94 PFLOP/s, 1.73 under
-// the power limit): 16384 x 8192 x 8192 into bf16 780-815 us (2.7 PFLOP/s at 1350 W, the power
+// the power limit): 16384 x 8192 x 8192 into bf16 830-850 us (2.6 PFLOP/s at 1350 W, the power
 // limit; the tensor cores are busy for half of the time, and the sums, 128 multiply-adds a
 // thread and block, bound the rest), 2048 x 4096 x 5120 into fp32 with a bias 41 us (128 tiles
 // are two turns of 76 pairs), 512 x 4096 x 4096 12.5 us, 64 x 8192 x 8192 17.3 us and 8 x 6144 x
 // 4096 8 us (the weight's bytes in 11 and 3.4 us of it, at 6 to 7 TB/s; the rest is the start
 // of a ring, 1.2 us, and the meeting of a cluster's sums, 1.5 to 2.5), 1001 x 5120 x 4099, rows off 16
-// bytes, 107 us.
+// bytes, 108 us.
 #include "octet.cuh"
 #include "serving.h"
 #include "tcgen05.cuh"
@@ -160,7 +160,7 @@ __device__ __forceinline__ void issue(Bars<STAGES, BUFFERS>& bars, uint32_t tile
 // pieces, shifted from two words, to their swizzled places in the tile. No warp waits for
 // another's rows. Bound by the L1's pipeline: a row of 144 bytes touches two lines (without the copies
 // 83 us, without the shifts 68, without both 33), and a tile goes through shared memory three times.
-// 1001 x 5120 x 4099 107 us; 574 with single loads and the shift in between, 126 with all loaders'
+// 1001 x 5120 x 4099 108 us; 574 with single loads and the shift in between, 126 with all loaders'
 // rows behind one barrier, 129 with twice the loaders in two groups that take the blocks in turn, 207 with a
 // bulk copy of each row.
 constexpr int kLoaders = 256, kLoaderWarps = kLoaders / 32;

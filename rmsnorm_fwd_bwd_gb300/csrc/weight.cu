@@ -5,7 +5,9 @@
 // a checkpoint is turned into them. A block of 512 threads holds one block of the weight in
 // registers (four octets a thread), so that the weight is read once. Bound by the blocks' phases,
 // loads, maximum, stores, three blocks to an SM: 8192 x 8192 bf16 40.6 us (5.0 TB/s; 46.6 with two
-// blocks, 54 with persistent ones that load ahead), 4099 x 5000 fp32 18.0 (5.7 TB/s).
+// blocks, 54 with persistent ones that load ahead), 4099 x 5000 fp32 17.8 (5.8 TB/s). Rows off 16 bytes,
+// whose words are shifted together: 8192 x 8191 bf16 76.5 us (2.6 TB/s), 4099 x 4999 fp32 32.7 (3.1). Three
+// blocks leave 40 registers a thread: fp32 spills 44 bytes, off 16 bytes 152 of them.
 #include "octet.cuh"
 #include "quant.cuh"
 #include "serving.h"
