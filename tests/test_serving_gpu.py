@@ -652,3 +652,19 @@ def test_matmul_of_an_operand_of_more_than_2_to_the_32_bytes(M, N, side, pitch):
     y = product(far, pitch, b, ldb, sa, sb, "float32", 128) if side == "a" \
         else product(a, lda, far, pitch, sa, sb, "float32", 128)
     check_product(a, b, sa, sb, "float32", 128, y)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_weight_scales_that_are_powers_of_two_stay(dtype):
+    # largest entries of 7 * 2^k: 7 / 448 = 2^-6 exactly, and a step of the type above it the next power
+    w = randn(5 * 128, 300, dtype=dtype, seed=95, scale=0.5).clamp(-1, 1)
+    step = torch.finfo(w.dtype).eps * 4                     # between 4 and 8
+    tops = [7.0, 7.0 + step, 3.5, 7.0 * 2.0 ** -3, 14.0 - 2 * step]
+    for i, top in enumerate(tops):
+        w[128 * i:128 * (i + 1)] *= 2.0 ** -3
+        w[128 * i + 9, ::128] = -top
+    c, s = quant_weight(w.cuda(), 300, *w.shape, dtype, True)
+    want = torch.tensor([2.0 ** -6, 2.0 ** -5, 2.0 ** -7, 2.0 ** -9, 2.0 ** -5]).unsqueeze(1).expand(5, 3)
+    assert torch.equal(s.cpu(), want)
+    v = w.double() / spread(want, *w.shape)                 # exact: by powers of two
+    assert torch.equal(c.cpu().view(torch.uint8), v.float().to(F8).view(torch.uint8))
