@@ -336,8 +336,9 @@ bool rows_apart(int64_t np, int64_t p_step, const Pieces& p, int64_t nq, int64_t
 
 bool heads_apart(const HeadsAt& p, const HeadsAt& q, int64_t T, int64_t D, int64_t s) {
     const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(q.p) - reinterpret_cast<uintptr_t>(p.p));
-    const Pieces pt = {T, p.token * s, D * s}, ph = {p.heads, p.head * s, D * s};
-    const Pieces qt = {T, q.token * s, D * s}, qh = {q.heads, q.head * s, D * s};
+    // (the stride of a single token or head may be any number)
+    const auto pieces = [&](int64_t n, int64_t stride) { return Pieces{n, n > 1 ? stride * s : 0, D * s}; };
+    const Pieces pt = pieces(T, p.token), ph = pieces(p.heads, p.head), qt = pieces(T, q.token), qh = pieces(q.heads, q.head);
     if (d >= pt.extent() + ph.extent() - D * s || d + qt.extent() + qh.extent() - D * s <= 0) return true;
     // heads within tokens, tokens within heads, or both at once
     if (rows_apart(T, pt.step, ph, T, qt.step, qh, d) || rows_apart(p.heads, ph.step, pt, q.heads, qh.step, qt, d)) return true;

@@ -516,3 +516,10 @@ def test_rotated_heads_refuse_every_output_that_meets_other_heads():
             met += 1
             assert st == ARG, (T, H, sy, sx, x - base)
     assert met > 300
+
+
+def test_strides_of_a_single_token_or_head_do_not_matter():
+    any_stride = (1 << 62) + 12345
+    for y, want in ((0x100000, NULL), (0x100000 + 2, ARG), (0x100000 + 128, NULL)):
+        sets = (B.RopeHeads * 1)(B.RopeHeads(0x100000, any_stride, any_stride, None, y, any_stride - 7, any_stride, 1))
+        assert B.rmsnorm_rope_fwd(sets, None, 1, 64, 64, 0x7000, 0, 1.0, 1e-6, 2, 0) == want
